@@ -15,6 +15,11 @@ g = h // (h_s // h_n),
 
 Layouts: q_sig, k_sig [B, L, h_s, d]; q_noise, k_noise [B, L, h_n, d];
 v and the output [B, L, h_s, dv]; lambda [h_s] float32.
+
+Around the attention: ``gda_qk_norm_rope`` (per-head norm and rotation of the
+four projections, with gradients), ``gda_block_tables`` (block table, slots and
+positions of a serving step), and a 4-bit cache (``gda_cache_append_fp4``,
+``gda_cache_read_fp4``, ``gda_attn_decode_fp4``, ``gda_attn_decode_paged_fp4``).
 """
 from __future__ import annotations
 
@@ -32,6 +37,9 @@ __all__ = [
     "gda_attn_bwd", "gda_attn_bwd_workspace_size", "gda_attn_fwd_2pass",
     "gda_attn_fwd_2pass_workspace_size", "gda_attn_bwd_bf16", "gda_attn_bwd_bf16_workspace_size",
     "gda_attn_decode_paged_fp8", "gda_attn_fwd_chunk", "gda_attn_fwd_chunk_2pass",
+    "gda_qk_norm_rope", "gda_qk_norm_rope_bwd", "gda_qk_norm_rope_bwd_workspace_size", "gda_block_tables",
+    "gda_cache_append_fp4", "gda_cache_read_fp4", "gda_attn_decode_fp4", "gda_attn_decode_paged_fp4",
+    "gda_attn_decode_fp4_workspace_size", "GDA_FLAG_ROPE_INTERLEAVED",
 ]
 
 GDA_OK = 0
@@ -43,10 +51,12 @@ GDA_ERR_CUDA = -5
 GDA_ERR_DEVICE_TIMEOUT = -6
 GDA_FLAG_NO_NORM = 0x1
 GDA_FLAG_SINGLE_PASS = 0x2
+GDA_FLAG_ROPE_INTERLEAVED = 0x4
 GDA_DEVERR_PREFILL_TIMEOUT = 0x1
 GDA_DEVERR_BAD_LENGTH = 0x2
 GDA_DEVERR_DECODE_TIMEOUT = 0x4
 GDA_DEVERR_BAD_PAGE = 0x8
+GDA_DEVERR_NO_PAGES = 0x10
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "_build", "libgda.so")
@@ -120,6 +130,27 @@ def _load():
             lib.gda_attn_bwd.restype = I
             lib.gda_attn_bwd_workspace_size.argtypes = [I, I, I, I, I]
             lib.gda_attn_bwd_workspace_size.restype = Z
+            X = ctypes.c_longlong
+            for name in ("gda_qk_norm_rope", "gda_qk_norm_rope_f32"):
+                getattr(lib, name).argtypes = [P] * 11 + [I] * 5 + [X] * 4 + [F, U, P]
+                getattr(lib, name).restype = I
+            for name in ("gda_qk_norm_rope_bwd", "gda_qk_norm_rope_bwd_f32"):
+                getattr(lib, name).argtypes = [P] * 16 + [I] * 5 + [P, F, U, P, Z, P]
+                getattr(lib, name).restype = I
+            lib.gda_qk_norm_rope_bwd_workspace_size.argtypes = [I] * 4
+            lib.gda_qk_norm_rope_bwd_workspace_size.restype = Z
+            lib.gda_block_tables.argtypes = [P] * 10 + [I] * 6 + [P]
+            lib.gda_block_tables.restype = I
+            lib.gda_cache_append_fp4.argtypes = [P] * 13 + [I] * 7 + [X] * 3 + [P]
+            lib.gda_cache_append_fp4.restype = I
+            lib.gda_cache_read_fp4.argtypes = [P] * 13 + [I] * 7 + [P]
+            lib.gda_cache_read_fp4.restype = I
+            lib.gda_attn_decode_fp4.argtypes = [P] * 13 + [F, P] + [I] * 6 + [F, P, Z, P]
+            lib.gda_attn_decode_fp4.restype = I
+            lib.gda_attn_decode_paged_fp4.argtypes = [P] * 14 + [F, P] + [I] * 8 + [F, P, Z, P]
+            lib.gda_attn_decode_paged_fp4.restype = I
+            lib.gda_attn_decode_fp4_workspace_size.argtypes = [I] * 5
+            lib.gda_attn_decode_fp4_workspace_size.restype = Z
             lib.gda_device_error.argtypes = [I]
             lib.gda_last_cuda_error.argtypes = []
             lib.gda_last_cuda_error.restype = I
@@ -589,6 +620,312 @@ def gda_attn_decode_noalloc(q_sig, q_noise, k_sig_cache, k_noise_cache, v_cache,
             float(eps), _stream(dev))
     _check(rc, "gda decode (no allocation)")
     return out
+
+
+def _token_stride(t, name, dtype, shape, device):
+    """Checks t [*tokens, heads, dim] and returns the elements between its tokens.
+
+    A token's heads are dense; the tokens are a constant number of elements
+    apart (a slice of a fused projection, or a dense tensor).
+    """
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    heads, dim = shape[-2:]
+    if t.stride(-1) != 1 or (heads > 1 and t.stride(-2) != dim):
+        raise ValueError(f"{name}: the heads of a token must be dense")
+    step, expect = heads * dim, None
+    for size, stride in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):
+        if size == 1:
+            continue
+        if expect is None:
+            step = expect = stride
+        if stride != expect:
+            raise ValueError(f"{name}: its tokens must be a constant number of elements apart")
+        expect *= size
+    return step
+
+
+def _norm_rope_sizes(q_sig, q_noise, weight, positions, inv_freq):
+    dev = q_sig.device
+    if dev.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    if q_sig.dim() < 3 or q_noise.dim() != q_sig.dim():
+        raise ValueError("projections must be [*tokens, heads, d]")
+    if q_sig.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"q_sig has dtype {q_sig.dtype}, expected bfloat16 or float32")
+    lead = tuple(q_sig.shape[:-2])
+    hs, d = q_sig.shape[-2:]
+    hn = q_noise.shape[-2]
+    _expect(weight, "weight", torch.float32, (4, d), dev)
+    _expect(positions, "positions", torch.int32, lead, dev)
+    _expect(inv_freq, "inv_freq", torch.float32, (inv_freq.numel(),), dev)
+    shapes = (lead + (hs, d),) * 2 + (lead + (hn, d),) * 2
+    return dev, q_sig.dtype, positions.numel(), hs, hn, d, 2 * inv_freq.numel(), shapes
+
+
+_PROJECTIONS = ("q_sig", "k_sig", "q_noise", "k_noise")
+
+
+def gda_qk_norm_rope(q_sig, k_sig, q_noise, k_noise, weight, positions, inv_freq, *, eps: float = 1e-5,
+                     interleaved: bool = False, out=None):
+    """Per-head RMSNorm and rotation by position of the four projections, in one pass.
+
+    q_sig, k_sig [*tokens, h_s, d] and q_noise, k_noise [*tokens, h_n, d]
+    (bf16 or float32; one or two token dims, dense or slices of a fused
+    projection), weight [4, d] float32 (the rows of the four), positions
+    [*tokens] int32, inv_freq [rot / 2] float32: the first rot dims of a head
+    rotate, in pairs (i, i + rot / 2), or (2i, 2i + 1) with ``interleaved``.
+    Returns the four dense outputs (``out`` may hold them; a dense input may
+    be its own output).
+    """
+    dev, dt, T, hs, hn, d, rot, shapes = _norm_rope_sizes(q_sig, q_noise, weight, positions, inv_freq)
+    x = (q_sig, k_sig, q_noise, k_noise)
+    strides = [_token_stride(t, n, dt, s, dev) for t, n, s in zip(x, _PROJECTIONS, shapes)]
+    if out is None:
+        out = tuple(torch.empty(s, dtype=dt, device=dev) for s in shapes)
+    for t, n, s in zip(out, _PROJECTIONS, shapes):
+        _expect(t, "out " + n, dt, s, dev)
+    entry = _load().gda_qk_norm_rope if dt == torch.bfloat16 else _load().gda_qk_norm_rope_f32
+    with torch.cuda.device(dev):
+        rc = entry(*[_ptr(t) for t in x], _ptr(weight), _ptr(positions), _ptr(inv_freq), *[_ptr(t) for t in out], T,
+                   hs, hn, d, rot, *strides, float(eps), GDA_FLAG_ROPE_INTERLEAVED if interleaved else 0, _stream(dev))
+    _check(rc, "gda norm and rotation")
+    return tuple(out)
+
+
+def gda_qk_norm_rope_bwd_workspace_size(T: int, h_s: int, h_n: int, d: int) -> int:
+    return int(_load().gda_qk_norm_rope_bwd_workspace_size(T, h_s, h_n, d))
+
+
+def gda_qk_norm_rope_bwd(q_sig, k_sig, q_noise, k_noise, weight, positions, inv_freq, dq_sig, dk_sig, dq_noise,
+                         dk_noise, *, eps: float = 1e-5, interleaved: bool = False, grads=None, workspace=None):
+    """Gradients of ``gda_qk_norm_rope``: (dq_sig, dk_sig, dq_noise, dk_noise, dweight).
+
+    Inputs as for the forward call plus the float32 gradients of its outputs
+    (dense, as ``gda_attn_bwd`` and ``gda_attn_bwd_bf16`` return them).  The
+    input gradients have the inputs' type, dweight [4, d] is float32.
+    ``grads`` may hold the five to overwrite (the first four may be slices of
+    one fused gradient).
+    """
+    dev, dt, T, hs, hn, d, rot, shapes = _norm_rope_sizes(q_sig, q_noise, weight, positions, inv_freq)
+    x, dy = (q_sig, k_sig, q_noise, k_noise), (dq_sig, dk_sig, dq_noise, dk_noise)
+    if grads is None:
+        grads = tuple(torch.empty(s, dtype=dt, device=dev) for s in shapes) + (
+            torch.empty((4, d), dtype=torch.float32, device=dev),)
+    strides = [_token_stride(t, n, dt, s, dev) for t, n, s in zip(x, _PROJECTIONS, shapes)]
+    strides += [_token_stride(t, "grads " + n, dt, s, dev) for t, n, s in zip(grads, _PROJECTIONS, shapes)]
+    for t, n, s in zip(dy, _PROJECTIONS, shapes):
+        _expect(t, "d" + n, torch.float32, s, dev)
+    _expect(grads[4], "dweight", torch.float32, (4, d), dev)
+    need = gda_qk_norm_rope_bwd_workspace_size(T, hs, hn, d)
+    if workspace is None:
+        workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=dev)
+    _expect(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
+    entry = _load().gda_qk_norm_rope_bwd if dt == torch.bfloat16 else _load().gda_qk_norm_rope_bwd_f32
+    with torch.cuda.device(dev):
+        rc = entry(*[_ptr(t) for t in x], _ptr(weight), _ptr(positions), _ptr(inv_freq), *[_ptr(t) for t in dy],
+                   *[_ptr(t) for t in grads], T, hs, hn, d, rot, (ctypes.c_longlong * 8)(*strides), float(eps),
+                   GDA_FLAG_ROPE_INTERLEAVED if interleaved else 0, _ptr(workspace), workspace.numel(), _stream(dev))
+    _check(rc, "gda norm and rotation backward")
+    return tuple(grads)
+
+
+def gda_block_tables(cache_lens, new_lens, block_table, free_pages, free_count, page_size: int, num_pages: int,
+                     max_rows: int, *, out=None):
+    """Block table, slots and positions of a step's new tokens, from the sequences' lengths.
+
+    int32 CUDA tensors: cache_lens [B] (positions held), new_lens [B] (tokens
+    to add, 0 for none), block_table [B, max_pages] (updated in place),
+    free_pages [F] and free_count [1] (a stack, its top at free_count - 1).
+    Returns (slot_map [max_rows], positions [max_rows], row_starts [B + 1],
+    lens [B], free_left [1]): the new tokens' rows follow sequence after
+    sequence, rows past the last one and rows of a refused sequence have slot
+    -1.  ``out`` may hold the five; its lens may be cache_lens and its
+    free_left free_count.  See include/gda.h for refusals.
+    """
+    dev = cache_lens.device
+    if dev.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    if block_table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("block_table must be [B, max_pages] and free_pages 1-D")
+    i32 = torch.int32
+    B, max_pages = block_table.shape
+    _expect(cache_lens, "cache_lens", i32, (B,), dev)
+    _expect(new_lens, "new_lens", i32, (B,), dev)
+    _expect(block_table, "block_table", i32, (B, max_pages), dev)
+    _expect(free_pages, "free_pages", i32, (free_pages.numel(),), dev)
+    _expect(free_count, "free_count", i32, (1,), dev)
+    shapes = ((max_rows,), (max_rows,), (B + 1,), (B,), (1,))
+    if out is None:
+        out = tuple(torch.empty(s, dtype=i32, device=dev) for s in shapes)
+    for t, n, s in zip(out, ("slot_map", "positions", "row_starts", "lens", "free_left"), shapes):
+        _expect(t, n, i32, s, dev)
+    with torch.cuda.device(dev):
+        rc = _load().gda_block_tables(
+            _ptr(cache_lens), _ptr(new_lens), _ptr(block_table), _ptr(free_pages), _ptr(free_count),
+            *[_ptr(t) for t in out], B, max_pages, int(page_size), int(num_pages), free_pages.numel(), int(max_rows),
+            _stream(dev))
+    _check(rc, "gda block tables")
+    return tuple(out)
+
+
+_FP4_TYPES = (torch.uint8,) + ((torch.float4_e2m1fn_x2,) if hasattr(torch, "float4_e2m1fn_x2") else ())
+
+
+def _fp4_cache(pools, blocks, scales, rows, heads, dims, device):
+    """Checks the nine tensors of a 4-bit cache; returns their pointers in the order of the C entries."""
+    names = ("k_sig", "k_noise", "v")
+    for t, n, h, dim in zip(pools, names, heads, dims):
+        if isinstance(t, torch.Tensor) and t.dtype in _FP4_TYPES[1:]:
+            t = t.view(torch.uint8)
+        _expect(t, n + " codes", torch.uint8, rows + (h, dim // 2), device)
+    for t, n, h, dim in zip(blocks, names, heads, dims):
+        if isinstance(t, torch.Tensor) and t.dtype == torch.float8_e4m3fn:
+            t = t.view(torch.uint8)
+        _expect(t, n + "_block_scale", torch.uint8, rows + (h, dim // 16), device)
+    for t, n, h in zip(scales, names, heads):
+        _expect(t, n + "_scale", torch.float32, (h,), device)
+    return [_ptr(t) for t in (*pools, *blocks, *scales)]
+
+
+def gda_cache_append_fp4(k_sig, k_noise, v, slot_map, k_sig_pool, k_noise_pool, v_pool, k_sig_block_scale,
+                         k_noise_block_scale, v_block_scale, k_sig_scale, k_noise_scale, v_scale):
+    """Writes tokens' K and V rows (bf16 [T, heads, dim]) into a 4-bit cache, in place.
+
+    slot_map [T] int32: the slot of each token (page * page_size + offset, as
+    ``gda_block_tables`` gives them), negative to leave it out; the slots of a
+    call differ.  Pools [num_pages, page_size, heads, dim / 2] uint8 (e2m1, two
+    to a byte; a contiguous cache [B, Lcap, ...] is B pages of Lcap), block
+    scales [num_pages, page_size, heads, dim / 16] float8_e4m3fn (or uint8),
+    head scales [heads] float32.  The rows may be slices of a fused projection.
+    """
+    dev = k_sig.device
+    if dev.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    if k_sig.dim() != 3 or k_noise.dim() != 3 or v.dim() != 3 or k_sig_pool.dim() != 4:
+        raise ValueError("rows must be [T, heads, dim] and pools [num_pages, page_size, heads, dim / 2]")
+    T, hs, d = k_sig.shape
+    hn, dv = k_noise.shape[1], v.shape[2]
+    rows = tuple(k_sig_pool.shape[:2])
+    bf = torch.bfloat16
+    strides = [_token_stride(t, n, bf, (T, h, dim), dev)
+               for t, n, h, dim in ((k_sig, "k_sig", hs, d), (k_noise, "k_noise", hn, d), (v, "v", hs, dv))]
+    _expect(slot_map, "slot_map", torch.int32, (T,), dev)
+    cache = _fp4_cache((k_sig_pool, k_noise_pool, v_pool), (k_sig_block_scale, k_noise_block_scale, v_block_scale),
+                       (k_sig_scale, k_noise_scale, v_scale), rows, (hs, hn, hs), (d, d, dv), dev)
+    with torch.cuda.device(dev):
+        rc = _load().gda_cache_append_fp4(_ptr(k_sig), _ptr(k_noise), _ptr(v), _ptr(slot_map), *cache, T, *rows, hs,
+                                          hn, d, dv, *strides, _stream(dev))
+    _check(rc, "gda 4-bit cache append")
+
+
+def gda_cache_read_fp4(slot_map, k_sig_pool, k_noise_pool, v_pool, k_sig_block_scale, k_noise_block_scale,
+                       v_block_scale, k_sig_scale, k_noise_scale, v_scale, *, out=None):
+    """The rows of a 4-bit cache at slot_map [T] as bf16: (k_sig, k_noise, v), each [T, heads, dim].
+
+    Zero rows for negative slots.  ``out`` may hold the three tensors.  The
+    cache is as in ``gda_cache_append_fp4``; the rows of a sequence's slots, in
+    order, are the keys and values of a prefix for ``gda_attn_fwd_chunk``.
+    """
+    dev = slot_map.device
+    if dev.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    if slot_map.dim() != 1 or k_sig_pool.dim() != 4 or k_noise_pool.dim() != 4 or v_pool.dim() != 4:
+        raise ValueError("slot_map must be 1-D and pools [num_pages, page_size, heads, dim / 2]")
+    T = slot_map.numel()
+    rows = tuple(k_sig_pool.shape[:2])
+    hs, d = k_sig_pool.shape[2], 2 * k_sig_pool.shape[3]
+    hn, dv = k_noise_pool.shape[2], 2 * v_pool.shape[3]
+    _expect(slot_map, "slot_map", torch.int32, (T,), dev)
+    cache = _fp4_cache((k_sig_pool, k_noise_pool, v_pool), (k_sig_block_scale, k_noise_block_scale, v_block_scale),
+                       (k_sig_scale, k_noise_scale, v_scale), rows, (hs, hn, hs), (d, d, dv), dev)
+    shapes = ((T, hs, d), (T, hn, d), (T, hs, dv))
+    if out is None:
+        out = tuple(torch.empty(s, dtype=torch.bfloat16, device=dev) for s in shapes)
+    for t, n, s in zip(out, ("k_sig", "k_noise", "v"), shapes):
+        _expect(t, n, torch.bfloat16, s, dev)
+    with torch.cuda.device(dev):
+        rc = _load().gda_cache_read_fp4(_ptr(slot_map), *cache, *[_ptr(t) for t in out], T, *rows, hs, hn, d, dv,
+                                        _stream(dev))
+    _check(rc, "gda 4-bit cache read")
+    return tuple(out)
+
+
+def gda_attn_decode_fp4_workspace_size(B: int, h_s: int, h_n: int, d: int, dv: int) -> int:
+    return int(_load().gda_attn_decode_fp4_workspace_size(B, h_s, h_n, d, dv))
+
+
+def _decode_fp4(q_sig, q_noise, pools, blocks, scales, block_table, cache_lens, lam, lambda_init, eps, out, workspace):
+    dev = q_sig.device
+    if dev.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    if q_sig.dim() != 3 or q_noise.dim() != 3 or any(t.dim() != 4 for t in pools):
+        raise ValueError("bad ranks: q [B, heads, d], caches [.., .., heads, dim / 2]")
+    B, hs, d = q_sig.shape
+    hn, dv = q_noise.shape[1], 2 * pools[2].shape[3]
+    rows = tuple(pools[0].shape[:2])
+    bf = torch.bfloat16
+    _expect(q_sig, "q_sig", bf, (B, hs, d), dev)
+    _expect(q_noise, "q_noise", bf, (B, hn, d), dev)
+    cache = _fp4_cache(pools, blocks, scales, rows, (hs, hn, hs), (d, d, dv), dev)
+    _expect(cache_lens, "cache_lens", torch.int32, (B,), dev)
+    _expect(lam, "lam", torch.float32, (hs,), dev)
+    if out is None:
+        out = torch.empty((B, hs, dv), dtype=bf, device=dev)
+    _expect(out, "out", bf, (B, hs, dv), dev)
+    if workspace is None:
+        need = gda_attn_decode_fp4_workspace_size(B, hs, hn, d, dv)
+        workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=dev)
+    _expect(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
+    tail = (hs, hn, d, dv, float(eps), _ptr(workspace), workspace.numel())
+    with torch.cuda.device(dev):
+        if block_table is None:
+            if rows[0] != B:
+                raise ValueError(f"caches hold {rows[0]} sequences, expected {B}")
+            rc = _load().gda_attn_decode_fp4(_ptr(q_sig), _ptr(q_noise), *cache, _ptr(cache_lens), _ptr(lam),
+                                             float(lambda_init), _ptr(out), B, rows[1], *tail, _stream(dev))
+        else:
+            if block_table.dim() != 2:
+                raise ValueError("block_table must be [B, max_pages]")
+            max_pages = block_table.shape[1]
+            _expect(block_table, "block_table", torch.int32, (B, max_pages), dev)
+            rc = _load().gda_attn_decode_paged_fp4(
+                _ptr(q_sig), _ptr(q_noise), *cache, _ptr(block_table), _ptr(cache_lens), _ptr(lam),
+                float(lambda_init), _ptr(out), B, max_pages, rows[1], rows[0], *tail, _stream(dev))
+    _check(rc, "gda decode (4-bit cache)")
+    return out
+
+
+def gda_attn_decode_fp4(q_sig, q_noise, k_sig_cache, k_noise_cache, v_cache, k_sig_block_scale, k_noise_block_scale,
+                        v_block_scale, k_sig_scale, k_noise_scale, v_scale, cache_lens, lam, lambda_init: float, *,
+                        eps: float = 1e-5, out=None, workspace=None):
+    """bf16 decode over 4-bit caches: cached value = e2m1 code * block scale * head scale.
+
+    Caches [B, Lcap, heads, dim / 2] uint8, block scales [B, Lcap, heads,
+    dim / 16] float8_e4m3fn (or uint8), head scales [heads] float32, as
+    ``gda_cache_append_fp4`` writes them.  A cache length of 0 gives a zero row.
+    """
+    return _decode_fp4(q_sig, q_noise, (k_sig_cache, k_noise_cache, v_cache),
+                       (k_sig_block_scale, k_noise_block_scale, v_block_scale), (k_sig_scale, k_noise_scale, v_scale),
+                       None, cache_lens, lam, lambda_init, eps, out, workspace)
+
+
+def gda_attn_decode_paged_fp4(q_sig, q_noise, k_sig_pool, k_noise_pool, v_pool, k_sig_block_scale,
+                              k_noise_block_scale, v_block_scale, k_sig_scale, k_noise_scale, v_scale, block_table,
+                              cache_lens, lam, lambda_init: float, *, eps: float = 1e-5, out=None, workspace=None):
+    """``gda_attn_decode_fp4`` over page pools [num_pages, page_size, heads, ..] and a block table
+    [B, max_pages] int32 (position j of sequence b is row j % page_size of page block_table[b, j // page_size])."""
+    if not isinstance(block_table, torch.Tensor):
+        raise TypeError("block_table must be a torch.Tensor")
+    return _decode_fp4(q_sig, q_noise, (k_sig_pool, k_noise_pool, v_pool),
+                       (k_sig_block_scale, k_noise_block_scale, v_block_scale), (k_sig_scale, k_noise_scale, v_scale),
+                       block_table, cache_lens, lam, lambda_init, eps, out, workspace)
 
 
 def gda_device_error(clear: bool = True) -> int:

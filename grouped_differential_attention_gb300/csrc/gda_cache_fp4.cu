@@ -1,0 +1,147 @@
+// Rows of K and V written into a 4-bit paged cache, and read back as bf16.
+//
+// Format (gda_fp4.cuh): for each block of 16 elements x of a head row, with
+// the head's float32 scale g,
+//   s = e4m3(max |x| / (6 g))            6 is the largest e2m1 magnitude
+//   code_i = e2m1(x_i * (1 / (s g)))     0 where s rounds to 0
+// in float32, each conversion to the nearest with ties to even and
+// saturating; a NaN in the block makes s NaN, so that reading gives NaN for
+// the whole block.  Reading gives bf16(code * s * g): the product code * s
+// has at most six significant bits and is exact.
+//
+// One thread handles one block: 32 bytes of bf16 on one side, 8 bytes of
+// codes and one scale byte on the other, so a warp touches 1 KB of
+// consecutive bf16 whatever the head layout.  Memory-bound: 2.5625 bytes an
+// element in each direction.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "gda.h"
+#include "gda_device.cuh"
+#include "gda_fp4.cuh"
+#include "gda_internal.h"
+
+namespace gda {
+namespace {
+
+constexpr int kThreads = 256;
+
+// Which tensor a block of 16 elements belongs to, and its place in the token's row there.
+struct Place {
+    int t;            // tensor: 0 K_sig, 1 K_noise, 2 V
+    int in_row;       // block within the token's row of that tensor
+};
+
+__device__ __forceinline__ Place place_of(const CacheFp4Args &a, int blk) {
+    if (blk < a.nb[0]) return {0, blk};
+    blk -= a.nb[0];
+    if (blk < a.nb[1]) return {1, blk};
+    return {2, blk - a.nb[1]};
+}
+
+// Slot of token t: negative for a token to leave out.  A slot outside the pool is reported.
+__device__ __forceinline__ int slot_of(const CacheFp4Args &a, long long t) {
+    const int slot = a.slot_map[t];
+    if (slot >= a.slots) {
+        atomicOr(a.dev_err, GDA_DEVERR_BAD_PAGE);
+        return -1;
+    }
+    return slot;
+}
+
+__global__ void __launch_bounds__(kThreads) gda_cache_append_fp4_kernel(const CacheFp4Args a) {
+    const int per_token = a.nb[0] + a.nb[1] + a.nb[2];
+    const long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
+    const long long tok = i / per_token;
+    if (tok >= a.T) return;
+    const Place pl = place_of(a, static_cast<int>(i - tok * per_token));
+    const int slot = slot_of(a, tok);
+    if (slot < 0) return;
+    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.rows[pl.t]) +
+                                                       tok * a.ld[pl.t] + pl.in_row * kFp4Block);
+    const uint4 lo = src[0], hi = src[1];
+    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    // magnitudes of bf16 order like their bits, and a NaN's are above infinity's
+    uint32_t most = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) most = __vmaxu2(most, w[j] & 0x7fff7fffu);
+    most = max(most & 0xffffu, most >> 16);
+    const float g = a.scale[pl.t][pl.in_row * kFp4Block / a.dim[pl.t]];
+    uint8_t s8 = 0x7f;
+    float r = 0.f;
+    if (most <= 0x7f80u) {
+        s8 = float_to_e4m3(fminf(__fdiv_rn(__uint_as_float(most << 16), __fmul_rn(6.f, g)), 448.f));
+        const float s = e4m3_to_float(s8);
+        if (s > 0.f) r = __frcp_rn(__fmul_rn(s, g));
+    }
+    uint2 codes = {0u, 0u};
+    if (r > 0.f) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t b = float2_to_e2m1x2(__fmul_rn(bf16_lo(w[j]), r), __fmul_rn(bf16_hi(w[j]), r));
+            (j < 4 ? codes.x : codes.y) |= b << (8 * (j & 3));
+        }
+    }
+    const size_t at = static_cast<size_t>(slot) * a.nb[pl.t] + pl.in_row;
+    reinterpret_cast<uint2 *>(a.codes[pl.t])[at] = codes;
+    a.blocks[pl.t][at] = s8;
+}
+
+__global__ void __launch_bounds__(kThreads) gda_cache_read_fp4_kernel(const CacheFp4Args a) {
+    const int per_token = a.nb[0] + a.nb[1] + a.nb[2];
+    const long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
+    const long long tok = i / per_token;
+    if (tok >= a.T) return;
+    const Place pl = place_of(a, static_cast<int>(i - tok * per_token));
+    const int slot = slot_of(a, tok);
+    uint32_t o[8] = {};
+    if (slot >= 0) {
+        const size_t at = static_cast<size_t>(slot) * a.nb[pl.t] + pl.in_row;
+        const uint2 codes = reinterpret_cast<const uint2 *>(a.codes[pl.t])[at];
+        const float s = e4m3_to_float(a.blocks[pl.t][at]);
+        const float g = a.scale[pl.t][pl.in_row * kFp4Block / a.dim[pl.t]];
+        uint32_t h[2][4];
+        e2m1x8_to_half2x4(h[0], codes.x);
+        e2m1x8_to_half2x4(h[1], codes.y);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float2 v = half2_bits_to_float2(h[j / 4][j % 4]);
+            o[j] = pack_bf16x2(__fmul_rn(__fmul_rn(v.x, s), g), __fmul_rn(__fmul_rn(v.y, s), g));
+        }
+    }
+    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(const_cast<void *>(a.rows[pl.t])) +
+                                           tok * a.ld[pl.t] + pl.in_row * kFp4Block);
+    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+int grid_of(const CacheFp4Args &a, unsigned *grid) {
+    const long long n = a.T * (a.nb[0] + a.nb[1] + a.nb[2]);
+    const long long g = (n + kThreads - 1) / kThreads;
+    if (g > 0x7fffffffLL) return GDA_ERR_UNSUPPORTED;
+    *grid = static_cast<unsigned>(g);
+    return GDA_OK;
+}
+
+}  // namespace
+
+int launch_cache_append_fp4(const CacheFp4Args &a, cudaStream_t stream) {
+    unsigned grid = 0;
+    const int st = grid_of(a, &grid);
+    if (st != GDA_OK) return st;
+    gda_cache_append_fp4_kernel<<<grid, kThreads, 0, stream>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? GDA_OK : record_cuda_error(e);
+}
+
+int launch_cache_read_fp4(const CacheFp4Args &a, cudaStream_t stream) {
+    unsigned grid = 0;
+    const int st = grid_of(a, &grid);
+    if (st != GDA_OK) return st;
+    gda_cache_read_fp4_kernel<<<grid, kThreads, 0, stream>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? GDA_OK : record_cuda_error(e);
+}
+
+}  // namespace gda

@@ -64,6 +64,63 @@ struct BackwardTcArgs {
     unsigned *dev_err;
 };
 
+// Rows of the three cached tensors (K_sig, K_noise, V) and the 4-bit pools they go to or come from.
+struct CacheFp4Args {
+    const void *rows[3];            // bf16 [T, heads, dim]
+    long long ld[3];                // elements between tokens
+    const int *slot_map;            // [T], negative: leave the token out
+    uint8_t *codes[3], *blocks[3];  // [slots, heads, dim / 2], [slots, heads, dim / 16]
+    const float *scale[3];          // [heads]
+    int nb[3], dim[3];              // blocks of 16 elements in a token's row; elements of a head row
+    long long T;
+    int slots;
+    unsigned *dev_err;
+};
+
+struct NormRopeArgs {
+    const void *x[4];               // q_sig, k_sig, q_noise, k_noise
+    long long ld[4];                // elements between tokens
+    const float *weight;            // [4, d]
+    const int *positions;           // [T]
+    const float *inv_freq;          // [rot / 2]
+    void *y[4];                     // outputs, or the gradients of x
+    long long ldy[4];               // elements between tokens of the gradients
+    const float *dy[4];             // gradients of the outputs
+    float *partial, *dweight;
+    long long T;
+    int hs, hn, d, rot;
+    bool interleaved, f32;
+    float eps;
+};
+constexpr int kNormRopeBlocks = 608;   // blocks of the backward kernel at most (four for each of 152 SMs)
+
+struct BlockTablesArgs {
+    const int *cache_lens, *new_lens;
+    int *block_table;
+    const int *free_pages, *free_count;
+    int *slot_map, *positions, *row_starts, *lens_out, *free_out;
+    int B, max_pages, page_size, num_pages, free_capacity, max_rows;
+    unsigned *dev_err;
+};
+constexpr int kBlockTablesMaxB = 8192;
+
+struct DecodeFp4Args {
+    const void *q1, *q2;                                   // bf16 [B, heads, d]
+    const uint8_t *k1c, *k2c, *vc;                         // e2m1 codes, two to a byte
+    const uint8_t *k1b, *k2b, *vb;                         // e4m3 block scales
+    const float *k1_scale, *k2_scale, *v_scale;            // per head
+    const int *lens;
+    const float *lambda;
+    float lambda_init;
+    void *out;
+    int B, Lcap, hs, hn, d, dv;
+    float eps;
+    void *workspace;
+    unsigned *dev_err;
+    const int *block_table = nullptr;                      // nullptr: contiguous caches [B, Lcap, heads, dim]
+    int page_size = 0, max_pages = 0, num_pages = 0;
+};
+
 // Remembers `e` as this thread's last CUDA error (see gda_last_cuda_error),
 // clears the runtime's sticky-free error state and returns GDA_ERR_CUDA.
 int record_cuda_error(cudaError_t e);
@@ -91,6 +148,14 @@ size_t backward_tc_workspace_bytes(int B, int L, int hs, int hn, int dv);
 size_t backward_f32_workspace_bytes(int B, int L, int hs, int d, int dv);
 int launch_lambda_reparam(const float *lq1, const float *lk1, const float *lq2, const float *lk2,
                           float lambda_init, float *out, int hs, int d, cudaStream_t stream);
+
+int launch_cache_append_fp4(const CacheFp4Args &a, cudaStream_t stream);
+int launch_cache_read_fp4(const CacheFp4Args &a, cudaStream_t stream);
+int launch_qk_norm_rope(const NormRopeArgs &a, cudaStream_t stream);
+int launch_qk_norm_rope_bwd(const NormRopeArgs &a, cudaStream_t stream);
+int launch_block_tables(const BlockTablesArgs &a, cudaStream_t stream);
+int launch_decode_fp4(const DecodeFp4Args &a, cudaStream_t stream);
+size_t decode_fp4_workspace_bytes(int B, int hs, int hn, int d, int dv);
 
 // Split plan of the decode kernel (positions per split and split count).
 struct DecodePlan {

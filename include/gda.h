@@ -72,6 +72,7 @@ typedef enum {
 /* Flags for the *_ex entry points. */
 #define GDA_FLAG_NO_NORM 0x1u    /* return o_h (pre-norm, float32 difference) instead of y_h */
 #define GDA_FLAG_SINGLE_PASS 0x2u /* gda_attn_fwd_ex, gda_attn_fwd_chunk: run the per-signal-head single-pass kernel */
+#define GDA_FLAG_ROPE_INTERLEAVED 0x4u /* gda_qk_norm_rope*: rotated pairs are dims 2i, 2i + 1 (default: i, i + rot/2) */
 
 /*
  * Prefill / full-sequence forward, bf16 I/O, float32 accumulation.
@@ -378,6 +379,174 @@ int gda_lambda_reparam(const float *lambda_q1, const float *lambda_k1, const flo
                        const float *lambda_k2, float lambda_init, float *lambda_out, int h_s, int d,
                        gda_stream_t stream);
 
+/*
+ * Norm of queries and keys for each head, and their rotation by position, in
+ * one pass over the four projections (what a model puts between its
+ * projections and the attention calls above).  For a head row x of d values,
+ * its tensor's weight row w and the token's position:
+ *     n = w * x / sqrt(mean(x^2) + eps)
+ *     y_a = n_a cos(t) - n_b sin(t),  y_b = n_b cos(t) + n_a sin(t),
+ *           t = position * inv_freq[i], for the pairs i = 0 .. rot/2 - 1;
+ *     y = n for the dims from rot on.
+ * Pair i is dims (i, i + rot/2), or (2i, 2i + 1) with
+ * GDA_FLAG_ROPE_INTERLEAVED.
+ *   q_sig, k_sig [T, h_s, d], q_noise, k_noise [T, h_n, d]: bf16 (float32 in
+ *   the _f32 entry) with `*_stride` elements between tokens (h * d when
+ *   dense; wider for a slice of a fused projection), a multiple of 16 bytes.
+ *   weight [4, d] float32: the rows of q_sig, k_sig, q_noise, k_noise.
+ *   positions [T] int32 (any value), inv_freq [rot/2] float32.
+ *   Outputs: dense [T, h, d] of the inputs' type; an output may be its own
+ *   input when that is dense, and overlaps nothing else.
+ * Float32 arithmetic, one rounding at the end; angles keep float32 accuracy
+ * at any position.  Supported: d in {64, 128}; rot a multiple of 16, at most
+ * d; h_s % h_n == 0, h_s + h_n <= 1024.  No workspace, no allocation.
+ */
+int gda_qk_norm_rope(const void *q_sig, const void *k_sig, const void *q_noise, const void *k_noise,
+                     const float *weight, const int *positions, const float *inv_freq, void *q_sig_out,
+                     void *k_sig_out, void *q_noise_out, void *k_noise_out, int T, int h_s, int h_n, int d, int rot,
+                     long long q_sig_stride, long long k_sig_stride, long long q_noise_stride,
+                     long long k_noise_stride, float eps, unsigned flags, gda_stream_t stream);
+int gda_qk_norm_rope_f32(const float *q_sig, const float *k_sig, const float *q_noise, const float *k_noise,
+                         const float *weight, const int *positions, const float *inv_freq, float *q_sig_out,
+                         float *k_sig_out, float *q_noise_out, float *k_noise_out, int T, int h_s, int h_n, int d,
+                         int rot, long long q_sig_stride, long long k_sig_stride, long long q_noise_stride,
+                         long long k_noise_stride, float eps, unsigned flags, gda_stream_t stream);
+
+/*
+ * Gradients of gda_qk_norm_rope (of the _f32 entry): given the gradients of
+ * its outputs, dense float32 [T, h, d] as gda_attn_bwd* returns them, the
+ * gradients of its inputs (their type) and of weight (float32 [4, d], summed
+ * over tokens and heads).  Outputs are overwritten.
+ *   strides: host array of 8: elements between tokens of q_sig, k_sig,
+ *   q_noise, k_noise and of the four input gradients (which may be slices of
+ *   one fused gradient); read before the call returns.  Input gradients
+ *   overlap neither the inputs nor one another.
+ *   workspace: device memory of at least gda_qk_norm_rope_bwd_workspace_size
+ *   bytes, 16-byte aligned, owned by the caller.
+ * No atomics; results repeat bit for bit.  Support and errors as
+ * gda_qk_norm_rope, plus GDA_ERR_WORKSPACE.
+ */
+int gda_qk_norm_rope_bwd(const void *q_sig, const void *k_sig, const void *q_noise, const void *k_noise,
+                         const float *weight, const int *positions, const float *inv_freq, const float *dq_sig,
+                         const float *dk_sig, const float *dq_noise, const float *dk_noise, void *dq_sig_out,
+                         void *dk_sig_out, void *dq_noise_out, void *dk_noise_out, float *dweight, int T, int h_s,
+                         int h_n, int d, int rot, const long long *strides, float eps, unsigned flags,
+                         void *workspace, size_t workspace_bytes, gda_stream_t stream);
+int gda_qk_norm_rope_bwd_f32(const float *q_sig, const float *k_sig, const float *q_noise, const float *k_noise,
+                             const float *weight, const int *positions, const float *inv_freq, const float *dq_sig,
+                             const float *dk_sig, const float *dq_noise, const float *dk_noise, float *dq_sig_out,
+                             float *dk_sig_out, float *dq_noise_out, float *dk_noise_out, float *dweight, int T,
+                             int h_s, int h_n, int d, int rot, const long long *strides, float eps, unsigned flags,
+                             void *workspace, size_t workspace_bytes, gda_stream_t stream);
+
+/* Bytes of workspace gda_qk_norm_rope_bwd* needs (0 for invalid sizes). */
+size_t gda_qk_norm_rope_bwd_workspace_size(int T, int h_s, int h_n, int d);
+
+/*
+ * Block table, slots and positions of a step's new tokens, from the
+ * sequences' lengths, for the paged decodes and gda_cache_append_fp4.
+ * Sequence b holds cache_lens[b] positions and gets new_lens[b] more (0: none
+ * this step).  The new tokens' rows follow sequence after sequence; the pages
+ * a sequence lacks come off the top of the stack free_pages[0 .. free_count)
+ * (free_pages[free_count - 1] first), in the order of the sequences.
+ *   cache_lens, new_lens [B]; block_table [B, max_pages] (entries of new
+ *   pages are written, all others left as they are); free_pages
+ *   [free_capacity]; free_count [1].
+ *   slot_map, positions [max_rows]: of row r, page * page_size + offset and
+ *   the position in its sequence; -1 and 0 for rows past the last token and
+ *   for those of a refused sequence.
+ *   row_starts [B + 1]: first row of each sequence, and the number of rows.
+ *   lens_out [B], free_count_out [1]: lengths and free pages after the step;
+ *   they may be cache_lens and free_count themselves.  Nothing else overlaps.
+ * A sequence that cannot be served is refused as a whole: its length and its
+ * block table stay as they are, its rows get slot -1, and the device error
+ * word says why: GDA_DEVERR_BAD_LENGTH (a negative length; more positions
+ * than max_pages * page_size; rows past max_rows) or GDA_DEVERR_NO_PAGES (the
+ * stack is too short for it; later sequences that need a page are refused
+ * too).  A page id outside [0, num_pages) gives its rows slot -1, and a
+ * free_count outside [0, free_capacity] is clamped; both report
+ * GDA_DEVERR_BAD_PAGE.
+ * All int32 device arrays, 4-byte aligned.  Supported: B <= 8192;
+ * max_pages * page_size and num_pages * page_size below 2^31.  One launch, no
+ * workspace; can be captured into a graph and replayed.
+ */
+int gda_block_tables(const int *cache_lens, const int *new_lens, int *block_table, const int *free_pages,
+                     const int *free_count, int *slot_map, int *positions, int *row_starts, int *lens_out,
+                     int *free_count_out, int B, int max_pages, int page_size, int num_pages, int free_capacity,
+                     int max_rows, gda_stream_t stream);
+
+/*
+ * 4-bit cache.  A cached tensor (K_sig [slots, h_s, d], K_noise [slots, h_n,
+ * d], V [slots, h_s, dv]; slots = num_pages * page_size, or B * Lcap of a
+ * contiguous cache) is held as
+ *   codes  [slots, heads, dim/2]  e2m1, two to a byte, the even element in
+ *                                 the low half: 0 .5 1 1.5 2 3 4 6 and sign
+ *   blocks [slots, heads, dim/16] e4m3, a scale for 16 consecutive elements
+ *   scale  [heads] float32 > 0, of the caller's choice (1, or a head's amax
+ *                                 over 2688 to use the e4m3 range)
+ * and stands for code * block * scale.  9/16 byte an element.
+ *
+ * gda_cache_append_fp4 writes T tokens' rows (bf16, `*_stride` elements
+ * between tokens, a multiple of 8) to the slots slot_map[T] (int32; negative:
+ * the token is left out; past the pool: left out and reported through
+ * gda_device_error as GDA_DEVERR_BAD_PAGE).  Per block of 16 values x, in
+ * float32: s = e4m3(amax / (6 scale)), code = e2m1(x * (1 / (s scale))), to
+ * the nearest, ties to even, saturating; all codes 0 where s is 0; a NaN
+ * makes s NaN, so the whole block reads as NaN.  Slots of one call differ.
+ *
+ * gda_cache_read_fp4 is the reverse: rows of the slots as dense bf16 [T,
+ * heads, dim], rounded once (zero rows for slots that append leaves out): the
+ * keys and values of a cached prefix for gda_attn_fwd_chunk.
+ *
+ * Supported: d in {64, 128}; dv in {64, 128, 256}; h_s + h_n <= 128; fewer
+ * than 2^31 slots.  Pointers 16-byte aligned, slot_map and scales 4-byte.
+ */
+int gda_cache_append_fp4(const void *k_sig, const void *k_noise, const void *v, const int *slot_map,
+                         void *k_sig_pool, void *k_noise_pool, void *v_pool, void *k_sig_block_scale,
+                         void *k_noise_block_scale, void *v_block_scale, const float *k_sig_scale,
+                         const float *k_noise_scale, const float *v_scale, int T, int num_pages, int page_size,
+                         int h_s, int h_n, int d, int dv, long long k_sig_stride, long long k_noise_stride,
+                         long long v_stride, gda_stream_t stream);
+int gda_cache_read_fp4(const int *slot_map, const void *k_sig_pool, const void *k_noise_pool, const void *v_pool,
+                       const void *k_sig_block_scale, const void *k_noise_block_scale, const void *v_block_scale,
+                       const float *k_sig_scale, const float *k_noise_scale, const float *v_scale, void *k_sig_out,
+                       void *k_noise_out, void *v_out, int T, int num_pages, int page_size, int h_s, int h_n, int d,
+                       int dv, gda_stream_t stream);
+
+/*
+ * Decode over a 4-bit cache: the operation of gda_attn_decode on the values
+ * the format above stands for.  Contiguous: codes [B, Lcap, heads, dim/2] and
+ * blocks [B, Lcap, heads, dim/16]; paged: page pools and a block table as in
+ * gda_attn_decode_paged.  Queries, lambda and the output as in
+ * gda_attn_decode, except that cache_lens[b] may be 0: that sequence's output
+ * row is zero (an idle place of a batch), and nothing of its cache is read.
+ * A length outside [0, Lcap] is clamped and reported (GDA_DEVERR_BAD_LENGTH);
+ * a block-table entry outside the pool is read as page 0 and reported
+ * (GDA_DEVERR_BAD_PAGE).  Cache rows past a sequence's length are never used.
+ *   workspace: device memory of at least
+ *   gda_attn_decode_fp4_workspace_size(B, h_s, h_n, d, dv) bytes, 16-byte
+ *   aligned, owned by the caller; needs no initialisation.  Calls in flight
+ *   at the same time need a workspace each.
+ * Supported: d in {64, 128}; dv in {64, 128, 256}; h_s + h_n <= 128;
+ * B <= 65535; page_size >= 1.
+ */
+int gda_attn_decode_fp4(const void *q_sig, const void *q_noise, const void *k_sig_cache,
+                        const void *k_noise_cache, const void *v_cache, const void *k_sig_block_scale,
+                        const void *k_noise_block_scale, const void *v_block_scale, const float *k_sig_scale,
+                        const float *k_noise_scale, const float *v_scale, const int *cache_lens,
+                        const float *lambda, float lambda_init, void *out, int B, int Lcap, int h_s, int h_n,
+                        int d, int dv, float eps, void *workspace, size_t workspace_bytes, gda_stream_t stream);
+int gda_attn_decode_paged_fp4(const void *q_sig, const void *q_noise, const void *k_sig_pool,
+                              const void *k_noise_pool, const void *v_pool, const void *k_sig_block_scale,
+                              const void *k_noise_block_scale, const void *v_block_scale, const float *k_sig_scale,
+                              const float *k_noise_scale, const float *v_scale, const int *block_table,
+                              const int *cache_lens, const float *lambda, float lambda_init, void *out, int B,
+                              int max_pages, int page_size, int num_pages, int h_s, int h_n, int d, int dv,
+                              float eps, void *workspace, size_t workspace_bytes, gda_stream_t stream);
+
+/* Bytes of workspace gda_attn_decode_fp4 and gda_attn_decode_paged_fp4 need (0 for invalid sizes). */
+size_t gda_attn_decode_fp4_workspace_size(int B, int h_s, int h_n, int d, int dv);
+
 /* Static English description of a gda_status value. */
 const char *gda_status_string(int status);
 
@@ -389,9 +558,10 @@ int gda_last_cuda_error(void);
 
 /* Bits of the device error word. */
 #define GDA_DEVERR_PREFILL_TIMEOUT 0x1u  /* a prefill pipeline wait ran out */
-#define GDA_DEVERR_BAD_LENGTH      0x2u  /* a decode cache length was outside [1, Lcap] */
+#define GDA_DEVERR_BAD_LENGTH      0x2u  /* a cache length or a step's new length was out of range */
 #define GDA_DEVERR_DECODE_TIMEOUT  0x4u  /* a decode cache-streaming wait ran out */
-#define GDA_DEVERR_BAD_PAGE        0x8u  /* a paged decode's block table named a page outside the pool */
+#define GDA_DEVERR_BAD_PAGE        0x8u  /* a block table, free page stack or slot map named a page outside the pool */
+#define GDA_DEVERR_NO_PAGES        0x10u /* gda_block_tables: a sequence was refused, the free pages do not suffice */
 
 /*
  * Reads the error word of the current device (synchronises the device
