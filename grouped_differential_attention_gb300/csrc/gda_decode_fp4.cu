@@ -3,14 +3,36 @@
 // the cache length, plus a combine pass.
 //
 // The batch's cache positions, concatenated sequence after sequence, are cut
-// into equal contiguous ranges.  A warp takes one range for one signal head
-// and the noise head it shares: online softmax of both maps (exp2 units) and
-// the two accumulators O1, O2.  Each part of a range that lies in one
-// sequence leaves (m, l) of both maps and (O1, O2) in workspace slot
-// (range + sequence), which is unique because along the position axis
-// neither index falls and one grows from part to part.  The combine kernel
-// joins the parts of a sequence and applies the difference and the
-// (1 - lambda_init) RMSNorm.
+// into equal contiguous ranges.  A warp takes one range for one noise head
+// and up to RH signal heads that share it, on its own: it copies 16 positions
+// at a time into a ring of its own in shared memory (cp.async, RING - 1 tiles
+// ahead, so no thread of another warp is ever waited for), and keeps the
+// online softmax of all its maps and the accumulators O1, O2 in registers.
+// Each part of a range that lies in one sequence leaves (m, l) of both maps
+// and (O1, O2) in workspace slot (range + sequence), which is unique because
+// along the position axis neither index falls and one grows from part to
+// part.  The combine kernel joins the parts of a sequence and applies the
+// difference and the (1 - lambda_init) RMSNorm.
+//
+// Bytes are few (9/16 per element), so the arithmetic decides.  On the CUDA
+// cores every element costs a widening and one (K) or two (V) multiply-adds:
+// at the copy rate that is more than they can do (the fp8 decode, with half
+// the elements per byte, already is bound by them).  Here the tensor cores
+// multiply (mma.sync m16n8k16, f16 in, float32 out; a tile of a decode has
+// one row of queries, so the 128-row tcgen05 forms would sit idle for 127),
+// and the work left per element is half a conversion.  An mma has eight
+// columns where a decode needs one or two, and the others take the block
+// scales out of the inner loop:
+//   - scores: A = codes of 16 positions, B column n = the query with all but
+//     its n-th block of 16 dims zeroed, so C holds the dot product of every
+//     block by itself, and a score is sum_n scale[n] * C[n];
+//   - values: A = codes of 16 dims x 16 positions, B column (n, map) =
+//     weight of the map * scale of block n, for the four blocks of a 64-dim
+//     slab and both maps; each dim is read from its own block's column.
+// e2m1 codes, e4m3 scales and their products are exact in f16; the query is
+// too, after a power of two; a weight times a scale is rounded to 11 bits.
+// The weights are 2^7 exp2(score - maximum) so that a small one times a small
+// scale stays clear of f16's end; numerator and denominator share the factor.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <algorithm>
@@ -26,17 +48,40 @@ namespace gda {
 namespace {
 
 constexpr int kWarpsPerBlock = 4;
-constexpr int kMaxWarps = 2048;        // warps of the split kernel at most
+constexpr int kTile = 16;              // positions of a tile
 constexpr int kMinRange = 32;          // fewest positions of a range
+constexpr int kSms = 152;              // SMs that the plan counts on
+constexpr float kWeightBits = 7.f;     // weights carry a factor 2^7
+
+// Signal heads of a warp: a noise head's group in equal parts of at most
+// three (two where the accumulators of three would not fit the registers).
+struct Heads {
+    int parts, each;   // parts of a group; signal heads of the largest part
+};
+Heads heads_of(int hs, int hn, int dv) {
+    const int r = hs / hn, most = dv == 256 ? 2 : 3;
+    Heads h;
+    h.parts = (r + most - 1) / most;
+    h.each = (r + h.parts - 1) / h.parts;
+    return h;
+}
+
+// Blocks that share an SM, by the accumulator registers of a thread (DV / 4
+// for each signal head): as many as leave room for those and about 70 more.
+__host__ __device__ constexpr int blocks_per_sm(int rh, int dv) {
+    return rh * dv / 4 <= 32 ? 5 : (rh * dv / 4 <= 64 ? 4 : (rh * dv / 4 <= 96 ? 3 : 2));
+}
 
 struct Fp4Plan {
+    Heads heads;
     int splits;        // ranges at most
     size_t ml_at, seg_at, bytes;
 };
 
-Fp4Plan plan_of(int B, int hs, int dv) {
+Fp4Plan plan_of(int B, int hs, int hn, int dv) {
     Fp4Plan p;
-    p.splits = std::max(1, kMaxWarps / hs);
+    p.heads = heads_of(hs, hn, dv);
+    p.splits = std::max(1, kSms * blocks_per_sm(p.heads.each, dv) * kWarpsPerBlock / (hn * p.heads.parts));
     const size_t slots = static_cast<size_t>(p.splits) + B;
     p.ml_at = (slots * hs * 2 * dv * sizeof(float) + 255) / 256 * 256;
     p.seg_at = p.ml_at + (slots * hs * 4 * sizeof(float) + 255) / 256 * 256;
@@ -57,7 +102,7 @@ struct Params {
     unsigned *err;
     float lambda_init, eps, scale_log2;
     int B, Lcap, hs, hn;
-    int splits;
+    int splits, parts;   // ranges; parts of a noise head's group
     const int *block_table;
     int page_size, max_pages, num_pages;
 };
@@ -70,16 +115,17 @@ __device__ __forceinline__ int length_of(const Params &p, int b) {
     return len < 0 ? 0 : p.Lcap;
 }
 
-// Cache row of position pos of sequence b.  A page outside the pool is read as page 0 and reported.
-__device__ __forceinline__ size_t row_of(const Params &p, int b, int pos) {
-    if (p.block_table == nullptr) return static_cast<size_t>(b) * p.Lcap + pos;
+// Cache row of position pos of sequence b.  A page outside the pool is read
+// as page 0 and reported.  (2^32 rows of the smallest cache are 464 GB.)
+__device__ __forceinline__ uint32_t row_of(const Params &p, int b, int pos) {
+    if (p.block_table == nullptr) return static_cast<uint32_t>(b) * static_cast<uint32_t>(p.Lcap) + pos;
     const int pg = pos / p.page_size;
     int phys = p.block_table[static_cast<size_t>(b) * p.max_pages + pg];
     if (phys < 0 || phys >= p.num_pages) {
         atomicOr(p.err, GDA_DEVERR_BAD_PAGE);
         phys = 0;
     }
-    return static_cast<size_t>(phys) * p.page_size + (pos - pg * p.page_size);
+    return static_cast<uint32_t>(phys) * p.page_size + (pos - pg * p.page_size);
 }
 
 // The range [start, end) of a split in the concatenated positions, and where it begins.
@@ -123,92 +169,401 @@ __device__ __forceinline__ bool range_of(const Params &p, int split, Range &r) {
     return false;                         // not reached: start < total
 }
 
-// The N = D / 32 consecutive elements of a head row that belong to this lane.
-template <int N>
-__device__ __forceinline__ void load_lane(float (&x)[N], const uint8_t *codes, const uint8_t *blocks, int lane) {
-    const float s = e4m3_to_float(blocks[lane * N / kFp4Block]);
-    uint32_t w = 0;
-    if constexpr (N == 2) w = codes[lane];
-    if constexpr (N == 4) w = reinterpret_cast<const uint16_t *>(codes)[lane];
-    if constexpr (N == 8) w = reinterpret_cast<const uint32_t *>(codes)[lane];
-    uint32_t h[4];
-    e2m1x8_to_half2x4(h, w);
+// Copies into shared memory, asynchronous; zeros in place of what `ok` leaves out.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const uint8_t *src, bool ok) {
+    const int n = ok ? BYTES : 0;
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n) : "memory");
+}
+
+// c += a * b: 16 x 16 (f16) times 16 x 8 (f16).
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
+
+// A place in a warp's range: sequence b, positions [pos, hi) of it, and the positions of the range after those.
+struct Cursor {
+    int b, pos, hi, left;
+};
+
+__device__ __forceinline__ void enter(const Params &p, Cursor &c, int pos, int len) {
+    const int n = min(len - pos, c.left);
+    c.pos = pos;
+    c.hi = pos + n;
+    c.left -= n;
+}
+
+// To the next sequence with positions; there is one while left > 0.  Returns its length.
+__device__ __forceinline__ int next_sequence(const Params &p, Cursor &c) {
+    int len = 0;
+    do len = length_of(p, ++c.b);
+    while (len == 0);
+    enter(p, c, 0, len);
+    return len;
+}
+
+// Sizes of a warp's tile in shared memory, in bytes.
+template <int D, int DV, int RH>
+struct Tile {
+    static constexpr int NH = RH + 1;                    // heads with scores; the noise head is the last
+    static constexpr int KC = D / 2, KS = D / 16, VC = DV / 2, VS = DV / 16;   // codes and scales of a head row
+    static constexpr int k_codes = 0;
+    static constexpr int v_codes = k_codes + NH * kTile * KC;
+    static constexpr int k_scales = v_codes + RH * kTile * VC;
+    static constexpr int v_scales = k_scales + NH * kTile * KS;
+    static constexpr int bytes = (v_scales + RH * kTile * VS + 15) / 16 * 16;
+    static constexpr int queries = NH * D * 2 + 32;      // f16, and 32 bytes of zeros
+    static constexpr int blocks = blocks_per_sm(RH, DV);
+    static constexpr int room = (227 * 1024 / blocks - 1024) / kWarpsPerBlock;
+    static constexpr int fit = (room - queries) / bytes;
+    static constexpr int ring = fit > 6 ? 6 : fit;       // tiles of the ring
+    static_assert(ring >= 2, "a tile must be copied while another is used");
+    static constexpr int warp_bytes = ring * bytes + queries;
+};
+
+// V codes: row order and 16-byte chunk order that keep the four rows a load
+// reads at once (positions 2t + const) in different banks.
+template <int DV>
+__device__ __forceinline__ int v_row(int pos) { return (pos >> 1) | ((pos & 1) << 3); }
+template <int DV>
+__device__ __forceinline__ int v_chunk(int row, int chunk) {
+    if constexpr (DV == 128) return chunk ^ (((row >> 1) & 1) << 1);
+    if constexpr (DV == 256) return chunk ^ ((row & 3) << 1);
+    return chunk;
+}
+
+// Starts the copies of a tile: positions whose cache rows are `row` of lanes
+// 0 .. 15 (and again 16 .. 31), the first n of them; nh signal heads from h0 on.
+template <int D, int DV, int RH>
+__device__ __forceinline__ void issue_tile(const Params &p, uint32_t tile, uint32_t row, int n, int h0, int nh, int g) {
+    using T = Tile<D, DV, RH>;
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < N; i += 2) {
-        const float2 v = half2_bits_to_float2(h[i / 2]);
-        x[i] = v.x * s;
-        x[i + 1] = v.y * s;
+    for (int i = 0; i < D / 64; ++i) {                   // K codes: D / 32 chunks a row
+        const int at = lane + 32 * i, pos = at / (D / 32), ch = at % (D / 32);
+        const size_t r = __shfl_sync(0xffffffffu, row, pos);
+        const uint8_t *s1 = p.k1c + (r * p.hs + h0) * T::KC + ch * 16;
+        const uint32_t dst = tile + T::k_codes + pos * T::KC + ch * 16;
+#pragma unroll
+        for (int j = 0; j < RH; ++j)
+            if (j < nh) copy_async<16>(dst + j * kTile * T::KC, s1 + j * T::KC, pos < n);
+        copy_async<16>(dst + RH * kTile * T::KC, p.k2c + (r * p.hn + g) * T::KC + ch * 16, pos < n);
+    }
+#pragma unroll
+    for (int i = 0; i < DV / 64; ++i) {                  // V codes: DV / 32 chunks a row
+        const int at = lane + 32 * i, pos = at / (DV / 32), ch = at % (DV / 32);
+        const size_t r = __shfl_sync(0xffffffffu, row, pos);
+        const uint8_t *s = p.vc + (r * p.hs + h0) * T::VC + ch * 16;
+        const int vr = v_row<DV>(pos);
+        const uint32_t dst = tile + T::v_codes + vr * T::VC + v_chunk<DV>(vr, ch) * 16;
+#pragma unroll
+        for (int j = 0; j < RH; ++j)
+            if (j < nh) copy_async<16>(dst + j * kTile * T::VC, s + j * T::VC, pos < n);
+    }
+    const int pos = lane & 15, odd = lane >> 4;
+    const size_t r = row;
+#pragma unroll
+    for (int i = 0; i < (T::NH + 1) / 2; ++i) {          // scales: a lane takes a row of every other head
+        const int j = 2 * i + odd;
+        if (j < nh || j == RH) {
+            const uint8_t *s = j == RH ? p.k2b + (r * p.hn + g) * T::KS : p.k1b + (r * p.hs + h0 + j) * T::KS;
+            copy_async<T::KS>(tile + T::k_scales + (j * kTile + pos) * T::KS, s, pos < n);
+        }
+        if (j < nh)
+            copy_async<T::VS>(tile + T::v_scales + (j * kTile + pos) * T::VS, p.vb + (r * p.hs + h0 + j) * T::VS, pos < n);
     }
 }
 
-template <int D, int DV>
-__global__ void __launch_bounds__(kWarpsPerBlock * 32) gda_decode_fp4_split_kernel(const Params p) {
-    constexpr int NK = D / 32, NV = DV / 32;
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+    return v;
+}
+
+// The query rows of the warp's heads as f16 in shared memory, scaled by a
+// power of two that brings their largest element to [2^14, 2^15) (f16 then
+// holds all of bf16's digits down to 2^-31 of that).  Returns this lane's
+// factor from a score head to exp2 units: that of head lane % 4.
+template <int D, int RH>
+__device__ __forceinline__ float load_queries(const Params &p, uint32_t dst, int b, int h0, int nh, int g) {
     const int lane = threadIdx.x & 31;
-    const int unit = blockIdx.x * kWarpsPerBlock + (threadIdx.x >> 5);
-    const int split = unit / p.hs, h = unit % p.hs, g = h / (p.hs / p.hn);
+    float mine = 0.f;
+#pragma unroll
+    for (int j = 0; j <= RH; ++j) {
+        if (j >= nh && j != RH) continue;
+        const __nv_bfloat16 *q = j == RH ? p.q2 + (static_cast<size_t>(b) * p.hn + g) * D
+                                         : p.q1 + (static_cast<size_t>(b) * p.hs + h0 + j) * D;
+        uint32_t w[D / 64], most = 0;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+            w[i] = reinterpret_cast<const uint32_t *>(q)[lane + 32 * i];
+            most = max(most, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+        }
+        most = __reduce_max_sync(0xffffffffu, most);
+        const int up = min(268 - static_cast<int>(most >> 7), 254);       // biased exponent of the factor
+        const float f = __uint_as_float(static_cast<uint32_t>(up) << 23);
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i)
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + j * D * 2 + (lane + 32 * i) * 4),
+                         "r"(pack_half2(bf16_lo(w[i]) * f, bf16_hi(w[i]) * f)) : "memory");
+        const float back = __uint_as_float(static_cast<uint32_t>(254 - up) << 23);
+        const float k = j == RH ? p.k2_scale[g] : p.k1_scale[h0 + j];
+        if ((lane & 3) == j) mine = p.scale_log2 * k * back;
+    }
+    return mine;
+}
+
+// One warp: split u / units of the range, unit u % units = (noise head, part of its group).
+template <int D, int DV, int RH>
+__global__ void __launch_bounds__(kWarpsPerBlock * 32, (Tile<D, DV, RH>::blocks)) gda_decode_fp4_split_kernel(const Params p) {
+    using T = Tile<D, DV, RH>;
+    constexpr int NH = T::NH, SLABS = DV / 64, S = T::ring;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int lane = threadIdx.x & 31, quad = lane >> 2, t = lane & 3;
+    const uint32_t ring = smem_u32(smem) + (threadIdx.x >> 5) * T::warp_bytes;
+    const uint32_t queries = ring + S * T::bytes, zeros = queries + NH * D * 2;
+    const int units = p.hn * p.parts;
+    const int u = blockIdx.x * kWarpsPerBlock + (threadIdx.x >> 5);
+    const int split = u / units, g = (u % units) / p.parts, part = u % p.parts;
     if (split >= p.splits) return;
-    Range r;
-    if (!range_of(p, split, r)) return;
-    long long at = r.start;
-    while (at < r.end) {
-        const int len = length_of(p, r.b);
-        const int pos0 = static_cast<int>(at - r.before);
-        const int pos1 = static_cast<int>(min(static_cast<long long>(len), r.end - r.before));
-        float q1[NK], q2[NK], o1[NV] = {}, o2[NV] = {};
-        const float f1 = p.scale_log2 * p.k1_scale[h], f2 = p.scale_log2 * p.k2_scale[g];
+    const int r = p.hs / p.hn;
+    const int first = part * r / p.parts, h0 = g * r + first, nh = (part + 1) * r / p.parts - first;
+    Range range;
+    if (!range_of(p, split, range)) return;
+
+    Cursor use{range.b, 0, 0, static_cast<int>(range.end - range.start)};
+    int len = length_of(p, range.b);
+    enter(p, use, static_cast<int>(range.start - range.before), len);
+    Cursor get = use;                                    // the copies' place, ahead of the arithmetic's
+    bool more = true;
+    uint32_t row = 0;
+    int n = 0;
+    // the rows of the next tile to copy, and the place behind it
+    auto find = [&]() {
+        n = min(kTile, get.hi - get.pos);
+        row = row_of(p, get.b, get.pos + min(lane & 15, n - 1));
+    };
+    auto step = [&]() {
+        get.pos += kTile;
+        if (get.pos < get.hi) return;
+        if (get.left > 0) next_sequence(p, get); else more = false;
+    };
+    if (lane < 8) asm volatile("st.shared.u32 [%0], %1;" ::"r"(zeros + lane * 4), "r"(0) : "memory");
+    find();
 #pragma unroll
-        for (int i = 0; i < NK; ++i) {
-            q1[i] = f1 * __bfloat162float(p.q1[(static_cast<size_t>(r.b) * p.hs + h) * D + lane * NK + i]);
-            q2[i] = f2 * __bfloat162float(p.q2[(static_cast<size_t>(r.b) * p.hn + g) * D + lane * NK + i]);
+    for (int s = 0; s < S - 1; ++s) {
+        if (more) {
+            issue_tile<D, DV, RH>(p, ring + s * T::bytes, row, n, h0, nh, g);
+            step();
+            if (more) find();
         }
-        float m1 = -INFINITY, m2 = -INFINITY, l1 = 0.f, l2 = 0.f;
-        for (int pos = pos0; pos < pos1; ++pos) {
-            const size_t row = row_of(p, r.b, pos);
-            float k1[NK], k2[NK], v[NV];
-            load_lane<NK>(k1, p.k1c + (row * p.hs + h) * (D / 2), p.k1b + (row * p.hs + h) * (D / 16), lane);
-            load_lane<NK>(k2, p.k2c + (row * p.hn + g) * (D / 2), p.k2b + (row * p.hn + g) * (D / 16), lane);
-            load_lane<NV>(v, p.vc + (row * p.hs + h) * (DV / 2), p.vb + (row * p.hs + h) * (DV / 16), lane);
-            float s1 = 0.f, s2 = 0.f;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    int to = S - 1, from = 0;
+
+    float acc[RH][SLABS][4][4];
+    float m = -INFINITY, l = 0.f;                        // of head t (both its lanes' positions; l of this lane's only)
+    float factor = load_queries<D, RH>(p, queries, use.b, h0, nh, g);
 #pragma unroll
-            for (int i = 0; i < NK; ++i) {
-                s1 = fmaf(q1[i], k1[i], s1);
-                s2 = fmaf(q2[i], k2[i], s2);
+    for (int j = 0; j < RH; ++j)
+#pragma unroll
+        for (int s = 0; s < SLABS; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[j][s][i][k] = 0.f;
+
+    for (;;) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+        __syncwarp();                                    // every lane's copies have landed; the oldest tile is free
+        if (more) {
+            issue_tile<D, DV, RH>(p, ring + to * T::bytes, row, n, h0, nh, g);
+            step();
+            if (more) find();
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        to = to + 1 == S ? 0 : to + 1;
+        const uint32_t tile = ring + from * T::bytes;
+        from = from + 1 == S ? 0 : from + 1;
+
+        // ---- scores: lane (quad, t) ends up with positions quad, quad + 8 of head t
+        float x0[4] = {}, x1[4] = {};
+#pragma unroll
+        for (int j = 0; j < NH; ++j) {
+            if (j >= nh && j != RH) continue;
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
+            const uint32_t q = queries + j * D * 2;
+#pragma unroll
+            for (int half = 0; half < D / 64; ++half) {  // 16 dims of this lane: block `blk`
+                const int blk = D == 64 ? t : 2 * t + half;
+                const uint32_t qa = quad == blk ? q + blk * 32 : zeros;
+                const uint4 b0 = lds128(qa), b1 = lds128(qa + 16);
+                const uint32_t ka = tile + T::k_codes + (j * kTile + quad) * T::KC + blk * 8;
+                const uint2 lo = lds64(ka), hi = lds64(ka + 8 * T::KC);
+                uint32_t a0[4], a1[4];
+                e2m1x8_to_half2x4(a0, lo.x);
+                e2m1x8_to_half2x4(a1, hi.x);
+                mma_16816(c, a0[0], a1[0], a0[1], a1[1], b0.x, b0.y);
+                mma_16816(c, a0[2], a1[2], a0[3], a1[3], b0.z, b0.w);
+                e2m1x8_to_half2x4(a0, lo.y);
+                e2m1x8_to_half2x4(a1, hi.y);
+                mma_16816(c, a0[0], a1[0], a0[1], a1[1], b1.x, b1.y);
+                mma_16816(c, a0[2], a1[2], a0[3], a1[3], b1.z, b1.w);
             }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                s1 += __shfl_xor_sync(0xffffffffu, s1, o);
-                s2 += __shfl_xor_sync(0xffffffffu, s2, o);
-            }
-            const float n1 = fmaxf(m1, s1), n2 = fmaxf(m2, s2);
-            const float a1 = exp2f(m1 - n1), a2 = exp2f(m2 - n2), w1 = exp2f(s1 - n1), w2 = exp2f(s2 - n2);
-            m1 = n1, m2 = n2;
-            l1 = l1 * a1 + w1, l2 = l2 * a2 + w2;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                o1[i] = fmaf(w1, v[i], o1[i] * a1);
-                o2[i] = fmaf(w2, v[i], o2[i] * a2);
+            if (D == 128 || t < 2) {                     // columns 2t, 2t + 1 are blocks
+                const uint32_t sa = tile + T::k_scales + (j * kTile + quad) * T::KS + 2 * t;
+                const float2 s0 = half2_bits_to_float2(e4m3x2_to_half2(lds16(sa)));
+                const float2 s1 = half2_bits_to_float2(e4m3x2_to_half2(lds16(sa + 8 * T::KS)));
+                // the noise head goes to place RH of the four
+                x0[j] = fmaf(c[1], s0.y, c[0] * s0.x);
+                x1[j] = fmaf(c[3], s1.y, c[2] * s1.x);
             }
         }
-        const size_t slot = static_cast<size_t>(split) + r.b;
-        float *o = p.ws_o + (slot * p.hs + h) * 2 * DV;
-        const float vs = p.v_scale[h];
+        auto gather = [&](const float (&x)[4]) {         // sum over the quad's lanes, head t to lane t
+            const float a = (t < 2 ? x[0] : x[2]) + __shfl_xor_sync(0xffffffffu, t < 2 ? x[2] : x[0], 2);
+            const float b = (t < 2 ? x[1] : x[3]) + __shfl_xor_sync(0xffffffffu, t < 2 ? x[3] : x[1], 2);
+            return (t & 1 ? b : a) + __shfl_xor_sync(0xffffffffu, t & 1 ? a : b, 1);
+        };
+        const int have = use.hi - use.pos;               // positions of the tile, if below 16
+        float sc0 = gather(x0) * factor, sc1 = gather(x1) * factor;   // every lane takes part in the shuffles
+        if (quad >= have) sc0 = -INFINITY;
+        if (quad + 8 >= have) sc1 = -INFINITY;
+        float mt = max3f(m, sc0, sc1);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            o[lane * NV + i] = o1[i] * vs;
-            o[DV + lane * NV + i] = o2[i] * vs;
-        }
-        if (lane == 0) {
-            reinterpret_cast<float4 *>(p.ws_ml)[slot * p.hs + h] = make_float4(m1, l1, m2, l2);
-            if (pos0 == 0 && h == 0) {
-                p.ws_seg[2 * r.b] = split;
-                p.ws_seg[2 * r.b + 1] = static_cast<int>((r.before + len - 1) / r.per);
+        for (int o = 4; o < 32; o <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+        const float scale = fast_exp2(m - mt);           // m = -inf gives 0
+        const float p0 = fast_exp2(sc0 - mt + kWeightBits), p1 = fast_exp2(sc1 - mt + kWeightBits);
+        m = mt;
+        l = fmaf(l, scale, p0 + p1);
+        const uint32_t weights = pack_half2(p0, p1);
+        if (__any_sync(0xffffffffu, scale != 1.f)) {
+            const float sn = __shfl_sync(0xffffffffu, scale, RH);
+#pragma unroll
+            for (int j = 0; j < RH; ++j) {
+                const float sj = __shfl_sync(0xffffffffu, scale, j);
+#pragma unroll
+                for (int s = 0; s < SLABS; ++s)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        acc[j][s][i][0] *= sj, acc[j][s][i][2] *= sj;
+                        acc[j][s][i][1] *= sn, acc[j][s][i][3] *= sn;
+                    }
             }
         }
-        at = r.before + pos1;
-        r.before += len;
-        ++r.b;
-        while (at < r.end && length_of(p, r.b) == 0) ++r.b;
+
+        // ---- values: k slots (2t, 2t + 1) are positions 2t, 2t + 8 and (2t + 8, 2t + 9) are 2t + 1, 2t + 9;
+        // column 2 n + map, n the block within the slab; row `quad` of tile i is dim 8 quad + 2 i, row quad + 8 the next
+        const uint32_t pick = 0x40u + 0x11u * (quad >> 1);   // byte of block quad / 2 from either word
+#pragma unroll
+        for (int j = 0; j < RH; ++j) {
+            if (j >= nh) continue;
+            const int src = 8 * t + (quad & 1 ? RH : j);
+            const uint32_t w0 = __shfl_sync(0xffffffffu, weights, src), w1 = __shfl_sync(0xffffffffu, weights, src + 4);
+            const uint32_t vs = tile + T::v_scales + (j * kTile + 2 * t) * T::VS;
+            const uint32_t vc = tile + T::v_codes + j * kTile * T::VC;
+#pragma unroll
+            for (int s = 0; s < SLABS; ++s) {
+                // scales of positions 2t, 2t + 1 and 2t + 8, 2t + 9: four blocks to a word
+                const uint32_t e0 = prmt(lds32(vs + 4 * s), lds32(vs + 8 * T::VS + 4 * s), pick);
+                const uint32_t e1 = prmt(lds32(vs + T::VS + 4 * s), lds32(vs + 9 * T::VS + 4 * s), pick);
+                const uint32_t b0 = half2_mul(w0, e4m3x2_to_half2(e0)), b1 = half2_mul(w1, e4m3x2_to_half2(e1));
+                auto word = [&](int vr) {                // codes of 8 dims in row vr of the tile
+                    return lds32(vc + vr * T::VC + v_chunk<DV>(vr, 2 * s + (quad >> 2)) * 16 + (quad & 3) * 4);
+                };
+                const uint32_t p0w = word(t), p8w = word(t + 4), p1w = word(t + 8), p9w = word(t + 12);
+                uint32_t a0[4], a1[4], a2[4], a3[4];
+                // two positions' codes of one dim side by side in a byte: even dims, odd dims
+                e2m1x8_to_half2x4(a0, (p0w & 0x0f0f0f0fu) | ((p8w << 4) & 0xf0f0f0f0u));
+                e2m1x8_to_half2x4(a1, ((p0w >> 4) & 0x0f0f0f0fu) | (p8w & 0xf0f0f0f0u));
+                e2m1x8_to_half2x4(a2, (p1w & 0x0f0f0f0fu) | ((p9w << 4) & 0xf0f0f0f0u));
+                e2m1x8_to_half2x4(a3, ((p1w >> 4) & 0x0f0f0f0fu) | (p9w & 0xf0f0f0f0u));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mma_16816(acc[j][s][i], a0[i], a1[i], a2[i], a3[i], b0, b1);
+            }
+        }
+
+        use.pos += kTile;
+        if (use.pos < use.hi) continue;
+
+        // ---- end of the part that lies in sequence use.b
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        const float mn = __shfl_sync(0xffffffffu, m, RH), ln = __shfl_sync(0xffffffffu, l, RH);
+        const size_t slot = static_cast<size_t>(split) + use.b;
+#pragma unroll
+        for (int j = 0; j < RH; ++j) {
+            if (j >= nh) continue;
+            const float mj = __shfl_sync(0xffffffffu, m, j), lj = __shfl_sync(0xffffffffu, l, j);
+            const size_t at = slot * p.hs + h0 + j;
+            if (lane == 0) reinterpret_cast<float4 *>(p.ws_ml)[at] = make_float4(mj, lj, mn, ln);
+            if (t == quad >> 1) {                        // the lanes whose columns are their own block
+                const float v = p.v_scale[h0 + j];
+                float4 *o1 = reinterpret_cast<float4 *>(p.ws_o + at * 2 * DV), *o2 = o1 + DV / 4;
+#pragma unroll
+                for (int s = 0; s < SLABS; ++s)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float(&c)[4] = acc[j][s][2 * i], (&d)[4] = acc[j][s][2 * i + 1];
+                        o1[16 * s + 2 * quad + i] = make_float4(c[0] * v, c[2] * v, d[0] * v, d[2] * v);
+                        o2[16 * s + 2 * quad + i] = make_float4(c[1] * v, c[3] * v, d[1] * v, d[3] * v);
+                    }
+            }
+        }
+        if (lane == 0 && h0 == 0 && range.before >= range.start) {
+            // the part begins with the sequence: the ranges that meet it
+            p.ws_seg[2 * use.b] = split;
+            p.ws_seg[2 * use.b + 1] = static_cast<int>((range.before + len - 1) / range.per);
+        }
+        if (use.left == 0) return;
+        range.before += len;
+        len = next_sequence(p, use);
+        m = -INFINITY, l = 0.f;
+        __syncwarp();                                    // the queries' last readers are done
+        factor = load_queries<D, RH>(p, queries, use.b, h0, nh, g);
+#pragma unroll
+        for (int j = 0; j < RH; ++j)
+#pragma unroll
+            for (int s = 0; s < SLABS; ++s)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) acc[j][s][i][k] = 0.f;
     }
 }
 
@@ -251,16 +606,35 @@ __global__ void __launch_bounds__(256) gda_decode_fp4_combine_kernel(const Param
     *out = __float2bfloat16_rn((1.f - p.lambda_init) * o * rsqrtf(tot / static_cast<float>(dv) + p.eps));
 }
 
+template <int D, int DV, int RH>
+cudaError_t launch_split(const Params &p, cudaStream_t stream) {
+    using T = Tile<D, DV, RH>;
+    auto kern = gda_decode_fp4_split_kernel<D, DV, RH>;
+    const int smem = T::warp_bytes * kWarpsPerBlock;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int warps = p.splits * p.hn * p.parts;
+    kern<<<(warps + kWarpsPerBlock - 1) / kWarpsPerBlock, kWarpsPerBlock * 32, smem, stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <int D, int DV>
+cudaError_t launch_split(const Params &p, int rh, cudaStream_t stream) {
+    if (rh == 1) return launch_split<D, DV, 1>(p, stream);
+    if constexpr (DV < 256)
+        if (rh == 3) return launch_split<D, DV, 3>(p, stream);
+    return launch_split<D, DV, 2>(p, stream);
+}
+
 }  // namespace
 
 size_t decode_fp4_workspace_bytes(int B, int hs, int hn, int d, int dv) {
-    (void)hn;
     (void)d;
-    return plan_of(B, hs, dv).bytes;
+    return plan_of(B, hs, hn, dv).bytes;
 }
 
 int launch_decode_fp4(const DecodeFp4Args &a, cudaStream_t stream) {
-    const Fp4Plan pl = plan_of(a.B, a.hs, a.dv);
+    const Fp4Plan pl = plan_of(a.B, a.hs, a.hn, a.dv);
     char *ws = static_cast<char *>(a.workspace);
     const Params p{static_cast<const __nv_bfloat16 *>(a.q1),
                    static_cast<const __nv_bfloat16 *>(a.q2),
@@ -271,21 +645,18 @@ int launch_decode_fp4(const DecodeFp4Args &a, cudaStream_t stream) {
                    reinterpret_cast<int *>(ws + pl.seg_at),
                    a.dev_err, a.lambda_init, a.eps,
                    static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(a.d))),
-                   a.B, a.Lcap, a.hs, a.hn, pl.splits, a.block_table, a.page_size, a.max_pages, a.num_pages};
-    const int units = pl.splits * a.hs;
-    const int grid = (units + kWarpsPerBlock - 1) / kWarpsPerBlock;
-    void (*kern)(Params) = nullptr;
+                   a.B, a.Lcap, a.hs, a.hn, pl.splits, pl.heads.parts, a.block_table, a.page_size, a.max_pages,
+                   a.num_pages};
+    cudaError_t e = cudaErrorInvalidValue;
     switch (a.d * 1000 + a.dv) {
-        case 64064: kern = gda_decode_fp4_split_kernel<64, 64>; break;
-        case 64128: kern = gda_decode_fp4_split_kernel<64, 128>; break;
-        case 64256: kern = gda_decode_fp4_split_kernel<64, 256>; break;
-        case 128064: kern = gda_decode_fp4_split_kernel<128, 64>; break;
-        case 128128: kern = gda_decode_fp4_split_kernel<128, 128>; break;
-        case 128256: kern = gda_decode_fp4_split_kernel<128, 256>; break;
+        case 64064: e = launch_split<64, 64>(p, pl.heads.each, stream); break;
+        case 64128: e = launch_split<64, 128>(p, pl.heads.each, stream); break;
+        case 64256: e = launch_split<64, 256>(p, pl.heads.each, stream); break;
+        case 128064: e = launch_split<128, 64>(p, pl.heads.each, stream); break;
+        case 128128: e = launch_split<128, 128>(p, pl.heads.each, stream); break;
+        case 128256: e = launch_split<128, 256>(p, pl.heads.each, stream); break;
         default: return GDA_ERR_UNSUPPORTED;
     }
-    kern<<<grid, kWarpsPerBlock * 32, 0, stream>>>(p);
-    cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return record_cuda_error(e);
     gda_decode_fp4_combine_kernel<<<dim3(a.hs, a.B), a.dv, 0, stream>>>(p);
     e = cudaGetLastError();
