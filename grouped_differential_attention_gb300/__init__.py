@@ -24,6 +24,7 @@ positions of a serving step), and a 4-bit cache (``gda_cache_append_fp4``,
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -79,6 +80,8 @@ def library_path() -> str:
 
 def _load():
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(_LIB_PATH):
@@ -622,6 +625,38 @@ def gda_attn_decode_noalloc(q_sig, q_noise, k_sig_cache, k_noise_cache, v_cache,
     return out
 
 
+# The raw handle of a device's current stream, without a Stream object around it (2 us of a call's 10).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _enqueue(entry, what, device, *args):
+    """Calls entry(*args, stream) with `device` current, on its current stream."""
+    index = device.index
+    if torch.cuda.current_device() == index:
+        rc = entry(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(device):
+            rc = entry(*args, _raw_stream(index))
+    if rc != GDA_OK:
+        raise GDAError(rc, what)
+
+
+def _workspace(workspace, need, device):
+    if workspace is None:
+        return torch.empty((max(need, 16),), dtype=torch.uint8, device=device)
+    _expect(workspace, "workspace", torch.uint8, (workspace.numel(),), device)
+    return workspace
+
+
+def _expect_bytes(t, name, other, shape, device):
+    """_expect for a tensor of bytes: uint8, or the one-byte type `other`."""
+    if isinstance(t, torch.Tensor) and t.dtype is other:
+        _expect(t, name, other, shape, device)
+    else:
+        _expect(t, name, torch.uint8, shape, device)
+
+
 def _token_stride(t, name, dtype, shape, device):
     """Checks t [*tokens, heads, dim] and returns the elements between its tokens.
 
@@ -634,20 +669,24 @@ def _token_stride(t, name, dtype, shape, device):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     heads, dim = shape[-2:]
-    if t.stride(-1) != 1 or (heads > 1 and t.stride(-2) != dim):
+    if t.is_contiguous():
+        return heads * dim
+    strides = t.stride()
+    if strides[-1] != 1 or (heads > 1 and strides[-2] != dim):
         raise ValueError(f"{name}: the heads of a token must be dense")
     step, expect = heads * dim, None
-    for size, stride in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):
+    for i in range(len(strides) - 3, -1, -1):
+        size, stride = shape[i], strides[i]
         if size == 1:
             continue
         if expect is None:
-            step = expect = stride
-        if stride != expect:
+            step = stride
+        elif stride != expect:
             raise ValueError(f"{name}: its tokens must be a constant number of elements apart")
-        expect *= size
+        expect = stride * size
     return step
 
 
@@ -659,13 +698,14 @@ def _norm_rope_sizes(q_sig, q_noise, weight, positions, inv_freq):
         raise ValueError("projections must be [*tokens, heads, d]")
     if q_sig.dtype not in (torch.bfloat16, torch.float32):
         raise TypeError(f"q_sig has dtype {q_sig.dtype}, expected bfloat16 or float32")
-    lead = tuple(q_sig.shape[:-2])
-    hs, d = q_sig.shape[-2:]
+    *lead, hs, d = q_sig.shape
+    lead = tuple(lead)
     hn = q_noise.shape[-2]
     _expect(weight, "weight", torch.float32, (4, d), dev)
     _expect(positions, "positions", torch.int32, lead, dev)
     _expect(inv_freq, "inv_freq", torch.float32, (inv_freq.numel(),), dev)
-    shapes = (lead + (hs, d),) * 2 + (lead + (hn, d),) * 2
+    sig, noise = lead + (hs, d), lead + (hn, d)
+    shapes = (sig, sig, noise, noise)
     return dev, q_sig.dtype, positions.numel(), hs, hn, d, 2 * inv_freq.numel(), shapes
 
 
@@ -688,17 +728,18 @@ def gda_qk_norm_rope(q_sig, k_sig, q_noise, k_noise, weight, positions, inv_freq
     x = (q_sig, k_sig, q_noise, k_noise)
     strides = [_token_stride(t, n, dt, s, dev) for t, n, s in zip(x, _PROJECTIONS, shapes)]
     if out is None:
-        out = tuple(torch.empty(s, dtype=dt, device=dev) for s in shapes)
-    for t, n, s in zip(out, _PROJECTIONS, shapes):
-        _expect(t, "out " + n, dt, s, dev)
-    entry = _load().gda_qk_norm_rope if dt == torch.bfloat16 else _load().gda_qk_norm_rope_f32
-    with torch.cuda.device(dev):
-        rc = entry(*[_ptr(t) for t in x], _ptr(weight), _ptr(positions), _ptr(inv_freq), *[_ptr(t) for t in out], T,
-                   hs, hn, d, rot, *strides, float(eps), GDA_FLAG_ROPE_INTERLEAVED if interleaved else 0, _stream(dev))
-    _check(rc, "gda norm and rotation")
+        out = tuple([torch.empty(s, dtype=dt, device=dev) for s in shapes])
+    else:
+        for t, n, s in zip(out, _PROJECTIONS, shapes):
+            _expect(t, "out " + n, dt, s, dev)
+    lib = _load()
+    _enqueue(lib.gda_qk_norm_rope if dt is torch.bfloat16 else lib.gda_qk_norm_rope_f32, "gda norm and rotation", dev,
+             *[t.data_ptr() for t in (*x, weight, positions, inv_freq, *out)], T, hs, hn, d, rot, *strides, float(eps),
+             GDA_FLAG_ROPE_INTERLEAVED if interleaved else 0)
     return tuple(out)
 
 
+@functools.lru_cache(maxsize=64)
 def gda_qk_norm_rope_bwd_workspace_size(T: int, h_s: int, h_n: int, d: int) -> int:
     return int(_load().gda_qk_norm_rope_bwd_workspace_size(T, h_s, h_n, d))
 
@@ -715,24 +756,23 @@ def gda_qk_norm_rope_bwd(q_sig, k_sig, q_noise, k_noise, weight, positions, inv_
     """
     dev, dt, T, hs, hn, d, rot, shapes = _norm_rope_sizes(q_sig, q_noise, weight, positions, inv_freq)
     x, dy = (q_sig, k_sig, q_noise, k_noise), (dq_sig, dk_sig, dq_noise, dk_noise)
-    if grads is None:
-        grads = tuple(torch.empty(s, dtype=dt, device=dev) for s in shapes) + (
-            torch.empty((4, d), dtype=torch.float32, device=dev),)
     strides = [_token_stride(t, n, dt, s, dev) for t, n, s in zip(x, _PROJECTIONS, shapes)]
-    strides += [_token_stride(t, "grads " + n, dt, s, dev) for t, n, s in zip(grads, _PROJECTIONS, shapes)]
+    if grads is None:
+        grads = (*[torch.empty(s, dtype=dt, device=dev) for s in shapes],
+                 torch.empty((4, d), dtype=torch.float32, device=dev))
+        strides += [hs * d, hs * d, hn * d, hn * d]
+    else:
+        strides += [_token_stride(t, "grads " + n, dt, s, dev) for t, n, s in zip(grads, _PROJECTIONS, shapes)]
+        _expect(grads[4], "dweight", torch.float32, (4, d), dev)
     for t, n, s in zip(dy, _PROJECTIONS, shapes):
         _expect(t, "d" + n, torch.float32, s, dev)
-    _expect(grads[4], "dweight", torch.float32, (4, d), dev)
-    need = gda_qk_norm_rope_bwd_workspace_size(T, hs, hn, d)
-    if workspace is None:
-        workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=dev)
-    _expect(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
-    entry = _load().gda_qk_norm_rope_bwd if dt == torch.bfloat16 else _load().gda_qk_norm_rope_bwd_f32
-    with torch.cuda.device(dev):
-        rc = entry(*[_ptr(t) for t in x], _ptr(weight), _ptr(positions), _ptr(inv_freq), *[_ptr(t) for t in dy],
-                   *[_ptr(t) for t in grads], T, hs, hn, d, rot, (ctypes.c_longlong * 8)(*strides), float(eps),
-                   GDA_FLAG_ROPE_INTERLEAVED if interleaved else 0, _ptr(workspace), workspace.numel(), _stream(dev))
-    _check(rc, "gda norm and rotation backward")
+    workspace = _workspace(workspace, gda_qk_norm_rope_bwd_workspace_size(T, hs, hn, d), dev)
+    lib = _load()
+    _enqueue(lib.gda_qk_norm_rope_bwd if dt is torch.bfloat16 else lib.gda_qk_norm_rope_bwd_f32,
+             "gda norm and rotation backward", dev,
+             *[t.data_ptr() for t in (*x, weight, positions, inv_freq, *dy, *grads)], T, hs, hn, d, rot,
+             (ctypes.c_longlong * 8)(*strides), float(eps), GDA_FLAG_ROPE_INTERLEAVED if interleaved else 0,
+             workspace.data_ptr(), workspace.numel())
     return tuple(grads)
 
 
@@ -763,35 +803,32 @@ def gda_block_tables(cache_lens, new_lens, block_table, free_pages, free_count, 
     _expect(free_count, "free_count", i32, (1,), dev)
     shapes = ((max_rows,), (max_rows,), (B + 1,), (B,), (1,))
     if out is None:
-        out = tuple(torch.empty(s, dtype=i32, device=dev) for s in shapes)
-    for t, n, s in zip(out, ("slot_map", "positions", "row_starts", "lens", "free_left"), shapes):
-        _expect(t, n, i32, s, dev)
-    with torch.cuda.device(dev):
-        rc = _load().gda_block_tables(
-            _ptr(cache_lens), _ptr(new_lens), _ptr(block_table), _ptr(free_pages), _ptr(free_count),
-            *[_ptr(t) for t in out], B, max_pages, int(page_size), int(num_pages), free_pages.numel(), int(max_rows),
-            _stream(dev))
-    _check(rc, "gda block tables")
+        out = tuple([torch.empty(s, dtype=i32, device=dev) for s in shapes])
+    else:
+        for t, n, s in zip(out, ("slot_map", "positions", "row_starts", "lens", "free_left"), shapes):
+            _expect(t, n, i32, s, dev)
+    _enqueue(_load().gda_block_tables, "gda block tables", dev,
+             *[t.data_ptr() for t in (cache_lens, new_lens, block_table, free_pages, free_count, *out)], B, max_pages,
+             page_size, num_pages, free_pages.numel(), max_rows)
     return tuple(out)
 
 
-_FP4_TYPES = (torch.uint8,) + ((torch.float4_e2m1fn_x2,) if hasattr(torch, "float4_e2m1fn_x2") else ())
+_FP4 = getattr(torch, "float4_e2m1fn_x2", torch.uint8)
+_FP8 = torch.float8_e4m3fn
 
 
-def _fp4_cache(pools, blocks, scales, rows, heads, dims, device):
-    """Checks the nine tensors of a 4-bit cache; returns their pointers in the order of the C entries."""
-    names = ("k_sig", "k_noise", "v")
-    for t, n, h, dim in zip(pools, names, heads, dims):
-        if isinstance(t, torch.Tensor) and t.dtype in _FP4_TYPES[1:]:
-            t = t.view(torch.uint8)
-        _expect(t, n + " codes", torch.uint8, rows + (h, dim // 2), device)
-    for t, n, h, dim in zip(blocks, names, heads, dims):
-        if isinstance(t, torch.Tensor) and t.dtype == torch.float8_e4m3fn:
-            t = t.view(torch.uint8)
-        _expect(t, n + "_block_scale", torch.uint8, rows + (h, dim // 16), device)
-    for t, n, h in zip(scales, names, heads):
-        _expect(t, n + "_scale", torch.float32, (h,), device)
-    return [_ptr(t) for t in (*pools, *blocks, *scales)]
+def _fp4_cache(pools, blocks, scales, rows, hs, hn, d, dv, dev):
+    """Checks the nine tensors of a 4-bit cache; returns their addresses in the order of the C entries."""
+    _expect_bytes(pools[0], "k_sig codes", _FP4, rows + (hs, d // 2), dev)
+    _expect_bytes(pools[1], "k_noise codes", _FP4, rows + (hn, d // 2), dev)
+    _expect_bytes(pools[2], "v codes", _FP4, rows + (hs, dv // 2), dev)
+    _expect_bytes(blocks[0], "k_sig_block_scale", _FP8, rows + (hs, d // 16), dev)
+    _expect_bytes(blocks[1], "k_noise_block_scale", _FP8, rows + (hn, d // 16), dev)
+    _expect_bytes(blocks[2], "v_block_scale", _FP8, rows + (hs, dv // 16), dev)
+    _expect(scales[0], "k_sig_scale", torch.float32, (hs,), dev)
+    _expect(scales[1], "k_noise_scale", torch.float32, (hn,), dev)
+    _expect(scales[2], "v_scale", torch.float32, (hs,), dev)
+    return [t.data_ptr() for t in (*pools, *blocks, *scales)]
 
 
 def gda_cache_append_fp4(k_sig, k_noise, v, slot_map, k_sig_pool, k_noise_pool, v_pool, k_sig_block_scale,
@@ -818,11 +855,9 @@ def gda_cache_append_fp4(k_sig, k_noise, v, slot_map, k_sig_pool, k_noise_pool, 
                for t, n, h, dim in ((k_sig, "k_sig", hs, d), (k_noise, "k_noise", hn, d), (v, "v", hs, dv))]
     _expect(slot_map, "slot_map", torch.int32, (T,), dev)
     cache = _fp4_cache((k_sig_pool, k_noise_pool, v_pool), (k_sig_block_scale, k_noise_block_scale, v_block_scale),
-                       (k_sig_scale, k_noise_scale, v_scale), rows, (hs, hn, hs), (d, d, dv), dev)
-    with torch.cuda.device(dev):
-        rc = _load().gda_cache_append_fp4(_ptr(k_sig), _ptr(k_noise), _ptr(v), _ptr(slot_map), *cache, T, *rows, hs,
-                                          hn, d, dv, *strides, _stream(dev))
-    _check(rc, "gda 4-bit cache append")
+                       (k_sig_scale, k_noise_scale, v_scale), rows, hs, hn, d, dv, dev)
+    _enqueue(_load().gda_cache_append_fp4, "gda 4-bit cache append", dev, k_sig.data_ptr(), k_noise.data_ptr(),
+             v.data_ptr(), slot_map.data_ptr(), *cache, T, *rows, hs, hn, d, dv, *strides)
 
 
 def gda_cache_read_fp4(slot_map, k_sig_pool, k_noise_pool, v_pool, k_sig_block_scale, k_noise_block_scale,
@@ -844,19 +879,19 @@ def gda_cache_read_fp4(slot_map, k_sig_pool, k_noise_pool, v_pool, k_sig_block_s
     hn, dv = k_noise_pool.shape[2], 2 * v_pool.shape[3]
     _expect(slot_map, "slot_map", torch.int32, (T,), dev)
     cache = _fp4_cache((k_sig_pool, k_noise_pool, v_pool), (k_sig_block_scale, k_noise_block_scale, v_block_scale),
-                       (k_sig_scale, k_noise_scale, v_scale), rows, (hs, hn, hs), (d, d, dv), dev)
+                       (k_sig_scale, k_noise_scale, v_scale), rows, hs, hn, d, dv, dev)
     shapes = ((T, hs, d), (T, hn, d), (T, hs, dv))
     if out is None:
-        out = tuple(torch.empty(s, dtype=torch.bfloat16, device=dev) for s in shapes)
-    for t, n, s in zip(out, ("k_sig", "k_noise", "v"), shapes):
-        _expect(t, n, torch.bfloat16, s, dev)
-    with torch.cuda.device(dev):
-        rc = _load().gda_cache_read_fp4(_ptr(slot_map), *cache, *[_ptr(t) for t in out], T, *rows, hs, hn, d, dv,
-                                        _stream(dev))
-    _check(rc, "gda 4-bit cache read")
+        out = tuple([torch.empty(s, dtype=torch.bfloat16, device=dev) for s in shapes])
+    else:
+        for t, n, s in zip(out, ("k_sig", "k_noise", "v"), shapes):
+            _expect(t, n, torch.bfloat16, s, dev)
+    _enqueue(_load().gda_cache_read_fp4, "gda 4-bit cache read", dev, slot_map.data_ptr(), *cache,
+             *[t.data_ptr() for t in out], T, *rows, hs, hn, d, dv)
     return tuple(out)
 
 
+@functools.lru_cache(maxsize=64)
 def gda_attn_decode_fp4_workspace_size(B: int, h_s: int, h_n: int, d: int, dv: int) -> int:
     return int(_load().gda_attn_decode_fp4_workspace_size(B, h_s, h_n, d, dv))
 
@@ -873,32 +908,29 @@ def _decode_fp4(q_sig, q_noise, pools, blocks, scales, block_table, cache_lens, 
     bf = torch.bfloat16
     _expect(q_sig, "q_sig", bf, (B, hs, d), dev)
     _expect(q_noise, "q_noise", bf, (B, hn, d), dev)
-    cache = _fp4_cache(pools, blocks, scales, rows, (hs, hn, hs), (d, d, dv), dev)
+    cache = _fp4_cache(pools, blocks, scales, rows, hs, hn, d, dv, dev)
     _expect(cache_lens, "cache_lens", torch.int32, (B,), dev)
     _expect(lam, "lam", torch.float32, (hs,), dev)
     if out is None:
         out = torch.empty((B, hs, dv), dtype=bf, device=dev)
-    _expect(out, "out", bf, (B, hs, dv), dev)
-    if workspace is None:
-        need = gda_attn_decode_fp4_workspace_size(B, hs, hn, d, dv)
-        workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=dev)
-    _expect(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
-    tail = (hs, hn, d, dv, float(eps), _ptr(workspace), workspace.numel())
-    with torch.cuda.device(dev):
-        if block_table is None:
-            if rows[0] != B:
-                raise ValueError(f"caches hold {rows[0]} sequences, expected {B}")
-            rc = _load().gda_attn_decode_fp4(_ptr(q_sig), _ptr(q_noise), *cache, _ptr(cache_lens), _ptr(lam),
-                                             float(lambda_init), _ptr(out), B, rows[1], *tail, _stream(dev))
-        else:
-            if block_table.dim() != 2:
-                raise ValueError("block_table must be [B, max_pages]")
-            max_pages = block_table.shape[1]
-            _expect(block_table, "block_table", torch.int32, (B, max_pages), dev)
-            rc = _load().gda_attn_decode_paged_fp4(
-                _ptr(q_sig), _ptr(q_noise), *cache, _ptr(block_table), _ptr(cache_lens), _ptr(lam),
-                float(lambda_init), _ptr(out), B, max_pages, rows[1], rows[0], *tail, _stream(dev))
-    _check(rc, "gda decode (4-bit cache)")
+    else:
+        _expect(out, "out", bf, (B, hs, dv), dev)
+    workspace = _workspace(workspace, gda_attn_decode_fp4_workspace_size(B, hs, hn, d, dv), dev)
+    head = (q_sig.data_ptr(), q_noise.data_ptr(), *cache)
+    tail = (hs, hn, d, dv, float(eps), workspace.data_ptr(), workspace.numel())
+    if block_table is None:
+        if rows[0] != B:
+            raise ValueError(f"caches hold {rows[0]} sequences, expected {B}")
+        _enqueue(_load().gda_attn_decode_fp4, "gda decode (4-bit cache)", dev, *head, cache_lens.data_ptr(),
+                 lam.data_ptr(), float(lambda_init), out.data_ptr(), B, rows[1], *tail)
+    else:
+        if block_table.dim() != 2:
+            raise ValueError("block_table must be [B, max_pages]")
+        max_pages = block_table.shape[1]
+        _expect(block_table, "block_table", torch.int32, (B, max_pages), dev)
+        _enqueue(_load().gda_attn_decode_paged_fp4, "gda decode (4-bit cache)", dev, *head, block_table.data_ptr(),
+                 cache_lens.data_ptr(), lam.data_ptr(), float(lambda_init), out.data_ptr(), B, max_pages, rows[1],
+                 rows[0], *tail)
     return out
 
 

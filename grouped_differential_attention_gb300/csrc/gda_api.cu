@@ -249,7 +249,7 @@ int norm_rope_bwd(const Four &x, const long long *strides, const float *weight, 
     }
     if (reinterpret_cast<uintptr_t>(dweight) & 3u) return GDA_ERR_MISALIGNED;
     if (!workspace || !aligned16(workspace) ||
-        workspace_bytes < static_cast<size_t>(kNormRopeBlocks) * 4 * d * sizeof(float))
+        workspace_bytes < qk_norm_rope_bwd_workspace_bytes(T, hs, hn, d))
         return GDA_ERR_WORKSPACE;
     a.weight = weight, a.positions = positions, a.inv_freq = inv_freq;
     a.partial = static_cast<float *>(workspace), a.dweight = dweight;
@@ -731,8 +731,8 @@ int gda_qk_norm_rope_f32(const float *q_sig, const float *k_sig, const float *q_
 }
 
 size_t gda_qk_norm_rope_bwd_workspace_size(int T, int h_s, int h_n, int d) {
-    if (T < 1 || h_s < 1 || h_n < 1 || d < 1 || d > 256) return 0;
-    return static_cast<size_t>(kNormRopeBlocks) * 4 * d * sizeof(float);
+    if (T < 1 || h_s < 1 || h_n < 1 || h_s % h_n != 0 || h_s + h_n > 1024 || !(d == 64 || d == 128)) return 0;
+    return qk_norm_rope_bwd_workspace_bytes(T, h_s, h_n, d);
 }
 
 int gda_qk_norm_rope_bwd(const void *q_sig, const void *k_sig, const void *q_noise, const void *k_noise,

@@ -567,43 +567,122 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32, (Tile<D, DV, RH>::blocks)
     }
 }
 
-// grid (h_s, B), block dv threads: joins the parts of one (sequence, head).
-__global__ void __launch_bounds__(256) gda_decode_fp4_combine_kernel(const Params p) {
-    __shared__ float red[8];
-    const int h = blockIdx.x, b = blockIdx.y, col = threadIdx.x, dv = blockDim.x;
-    __nv_bfloat16 *out = p.out + (static_cast<size_t>(b) * p.hs + h) * dv + col;
+// grid (h_s, B): joins the parts of one (sequence, head).  DV / 2 threads
+// hold the DV + DV columns of (O1, O2), four each; THREADS / (DV / 2) such
+// groups share the parts, so that a long sequence's several hundred are read
+// in few dependent steps.
+template <int DV, int THREADS>
+__global__ void __launch_bounds__(THREADS) gda_decode_fp4_combine_kernel(const Params p) {
+    constexpr int COLS = DV / 2, GROUPS = THREADS / COLS, WARPS = THREADS / 32;
+    __shared__ float4 sums[GROUPS][COLS];
+    __shared__ float red[WARPS][4];
+    // a programmatic dependent of the split kernel: this wait returns once that grid has completed and its writes are visible
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int h = blockIdx.x, b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __nv_bfloat16 *out = p.out + (static_cast<size_t>(b) * p.hs + h) * DV;
     if (length_of(p, b) == 0) {          // no position: the row is zero
-        *out = __float2bfloat16_rn(0.f);
+        if (threadIdx.x < DV / 2) reinterpret_cast<uint32_t *>(out)[threadIdx.x] = 0u;
         return;
     }
+    // ranges c0 .. c1 left a part in slots c + b (clamped so that a damaged workspace cannot send the reads astray)
     const int c0 = min(max(p.ws_seg[2 * b], 0), p.splits - 1);
     const int c1 = min(max(p.ws_seg[2 * b + 1], c0), p.splits - 1);
-    const float4 *ml = reinterpret_cast<const float4 *>(p.ws_ml);
+    const size_t at0 = (static_cast<size_t>(c0) + b) * p.hs + h;
+    const int parts = c1 - c0 + 1;
+    const float4 *ml = reinterpret_cast<const float4 *>(p.ws_ml) + at0;
+    const float4 *o = reinterpret_cast<const float4 *>(p.ws_o) + at0 * COLS;
+
+    // maxima over the parts, then the sums
     float M1 = -INFINITY, M2 = -INFINITY;
-    for (int c = c0; c <= c1; ++c) {
-        const float4 s = ml[(static_cast<size_t>(c) + b) * p.hs + h];
+    for (int c = threadIdx.x; c < parts; c += THREADS) {
+        const float4 s = ml[static_cast<size_t>(c) * p.hs];
         M1 = fmaxf(M1, s.x);
         M2 = fmaxf(M2, s.z);
     }
-    float L1 = 0.f, L2 = 0.f, O1 = 0.f, O2 = 0.f;
-    for (int c = c0; c <= c1; ++c) {
-        const size_t at = (static_cast<size_t>(c) + b) * p.hs + h;
-        const float4 s = ml[at];
-        const float f1 = exp2f(s.x - M1), f2 = exp2f(s.z - M2);
-        L1 = fmaf(s.y, f1, L1);
-        L2 = fmaf(s.w, f2, L2);
-        O1 = fmaf(p.ws_o[at * 2 * dv + col], f1, O1);
-        O2 = fmaf(p.ws_o[(at * 2 + 1) * dv + col], f2, O2);
-    }
-    const float o = O1 / L1 - p.lambda[h] * (O2 / L2);
-    float ss = o * o;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-    if ((col & 31) == 0) red[col >> 5] = ss;
+    for (int off = 16; off > 0; off >>= 1) {
+        M1 = fmaxf(M1, __shfl_xor_sync(0xffffffffu, M1, off));
+        M2 = fmaxf(M2, __shfl_xor_sync(0xffffffffu, M2, off));
+    }
+    if (lane == 0) red[warp][0] = M1, red[warp][1] = M2;
     __syncthreads();
-    float tot = 0.f;
-    for (int w = 0; w < dv / 32; ++w) tot += red[w];
-    *out = __float2bfloat16_rn((1.f - p.lambda_init) * o * rsqrtf(tot / static_cast<float>(dv) + p.eps));
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) M1 = fmaxf(M1, red[w][0]), M2 = fmaxf(M2, red[w][1]);
+    float L1 = 0.f, L2 = 0.f;
+    for (int c = threadIdx.x; c < parts; c += THREADS) {
+        const float4 s = ml[static_cast<size_t>(c) * p.hs];
+        L1 = fmaf(s.y, fast_exp2(s.x - M1), L1);
+        L2 = fmaf(s.w, fast_exp2(s.z - M2), L2);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        L1 += __shfl_xor_sync(0xffffffffu, L1, off);
+        L2 += __shfl_xor_sync(0xffffffffu, L2, off);
+    }
+    if (lane == 0) red[warp][2] = L1, red[warp][3] = L2;
+
+    const int col = threadIdx.x % COLS, group = threadIdx.x / COLS;
+    const bool second = col >= COLS / 2;
+    const float M = second ? M2 : M1;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int c = group; c < parts; c += GROUPS) {
+        const size_t at = static_cast<size_t>(c) * p.hs;
+        const float4 s = ml[at], v = o[at * COLS + col];
+        const float f = fast_exp2((second ? s.z : s.x) - M);
+        sum.x = fmaf(v.x, f, sum.x);
+        sum.y = fmaf(v.y, f, sum.y);
+        sum.z = fmaf(v.z, f, sum.z);
+        sum.w = fmaf(v.w, f, sum.w);
+    }
+    sums[group][col] = sum;
+    __syncthreads();
+    if (threadIdx.x >= COLS / 2) return;   // whole warps from here on, or one half warp (DV = 64)
+    L1 = L2 = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) L1 += red[w][2], L2 += red[w][3];
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), d = a;
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) {
+        const float4 x = sums[g][col], y = sums[g][col + COLS / 2];
+        a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
+        d.x += y.x, d.y += y.y, d.z += y.z, d.w += y.w;
+    }
+    const float i1 = 1.f / L1, i2 = p.lambda[h] / L2;
+    const float v[4] = {a.x * i1 - d.x * i2, a.y * i1 - d.y * i2, a.z * i1 - d.z * i2, a.w * i1 - d.w * i2};
+    float ss = v[0] * v[0] + v[1] * v[1] + v[2] * v[2] + v[3] * v[3];
+    constexpr unsigned mask = COLS / 2 >= 32 ? 0xffffffffu : 0xffffu;
+#pragma unroll
+    for (int off = (COLS / 2 >= 32 ? 32 : COLS / 2) / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(mask, ss, off);
+    if constexpr (COLS / 2 > 32) {         // DV = 256: two warps
+        __shared__ float both[2];
+        if (lane == 0) both[warp] = ss;
+        named_bar_sync(1, COLS / 2);
+        ss = both[0] + both[1];
+    }
+    const float y = (1.f - p.lambda_init) * rsqrtf(ss * (1.f / DV) + p.eps);
+    reinterpret_cast<uint2 *>(out)[col] = make_uint2(pack_bf16x2(v[0] * y, v[1] * y), pack_bf16x2(v[2] * y, v[3] * y));
+}
+
+template <int DV, int THREADS>
+cudaError_t launch_combine(const Params &p, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(p.hs, p.B);
+    cfg.blockDim = dim3(THREADS);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, gda_decode_fp4_combine_kernel<DV, THREADS>, p);
+    return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+// Few sequences have many parts each: 1024 threads a row then, else 256.
+template <int DV>
+cudaError_t launch_combine(const Params &p, cudaStream_t stream) {
+    return p.splits > 16 * p.B ? launch_combine<DV, 1024>(p, stream) : launch_combine<DV, 256>(p, stream);
 }
 
 template <int D, int DV, int RH>
@@ -658,8 +737,9 @@ int launch_decode_fp4(const DecodeFp4Args &a, cudaStream_t stream) {
         default: return GDA_ERR_UNSUPPORTED;
     }
     if (e != cudaSuccess) return record_cuda_error(e);
-    gda_decode_fp4_combine_kernel<<<dim3(a.hs, a.B), a.dv, 0, stream>>>(p);
-    e = cudaGetLastError();
+    e = a.dv == 64    ? launch_combine<64>(p, stream)
+        : a.dv == 128 ? launch_combine<128>(p, stream)
+                      : launch_combine<256>(p, stream);
     return e == cudaSuccess ? GDA_OK : record_cuda_error(e);
 }
 

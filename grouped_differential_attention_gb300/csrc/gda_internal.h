@@ -92,7 +92,7 @@ struct NormRopeArgs {
     bool interleaved, f32;
     float eps;
 };
-constexpr int kNormRopeBlocks = 608;   // blocks of the backward kernel at most (four for each of 152 SMs)
+constexpr int kNormRopeSms = 152;      // SMs that its launches and its workspace count on
 
 struct BlockTablesArgs {
     const int *cache_lens, *new_lens;
@@ -153,6 +153,7 @@ int launch_cache_append_fp4(const CacheFp4Args &a, cudaStream_t stream);
 int launch_cache_read_fp4(const CacheFp4Args &a, cudaStream_t stream);
 int launch_qk_norm_rope(const NormRopeArgs &a, cudaStream_t stream);
 int launch_qk_norm_rope_bwd(const NormRopeArgs &a, cudaStream_t stream);
+size_t qk_norm_rope_bwd_workspace_bytes(int T, int hs, int hn, int d);
 int launch_block_tables(const BlockTablesArgs &a, cudaStream_t stream);
 int launch_decode_fp4(const DecodeFp4Args &a, cudaStream_t stream);
 size_t decode_fp4_workspace_bytes(int B, int hs, int hn, int d, int dv);
