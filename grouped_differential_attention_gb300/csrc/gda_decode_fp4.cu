@@ -53,7 +53,7 @@ constexpr int kMinRange = 32;          // fewest positions of a range
 constexpr int kSms = 152;              // SMs that the plan counts on
 constexpr float kWeightBits = 7.f;     // weights carry a factor 2^7
 
-// Signal heads of a warp: a noise head's group in equal parts of at most
+// Signal heads of a warp: a noise head's group in parts of at most
 // three (two where the accumulators of three would not fit the registers).
 struct Heads {
     int parts, each;   // parts of a group; signal heads of the largest part
@@ -179,14 +179,13 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const uint8_t *src, boo
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n) : "memory");
 }
 
-// c += a * b: 16 x 16 (f16) times 16 x 8 (f16).
-__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                          uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// a * b + c: 16 x 16 (f16) times 16 x 8 (f16).
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1, const float (&c)[4]) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
 __device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b) {
@@ -242,9 +241,10 @@ struct Tile {
     static constexpr int warp_bytes = ring * bytes + queries;
 };
 
-// V codes: row order and 16-byte chunk order that keep the four rows a load
-// reads at once (positions 2t + const) in different banks.
-template <int DV>
+// V codes in shared memory: position pos is row v_row(pos), so that a lane's
+// four positions 2t, 2t + 8, 2t + 1, 2t + 9 are rows t, t + 4, t + 8, t + 12;
+// 16-byte chunks of a row change places by its low bits, so that the rows t =
+// 0 .. 3 that one load reads lie in different banks.
 __device__ __forceinline__ int v_row(int pos) { return (pos >> 1) | ((pos & 1) << 3); }
 template <int DV>
 __device__ __forceinline__ int v_chunk(int row, int chunk) {
@@ -254,79 +254,67 @@ __device__ __forceinline__ int v_chunk(int row, int chunk) {
 }
 
 // Starts the copies of a tile: positions whose cache rows are `row` of lanes
-// 0 .. 15 (and again 16 .. 31), the first n of them; nh signal heads from h0 on.
+// 0 .. 15 (and again 16 .. 31), the first n of them; RH signal heads from h0 on.
 template <int D, int DV, int RH>
-__device__ __forceinline__ void issue_tile(const Params &p, uint32_t tile, uint32_t row, int n, int h0, int nh, int g) {
+__device__ __forceinline__ void issue_tile(const Params &p, uint32_t tile, uint32_t row, int n, int h0, int g) {
     using T = Tile<D, DV, RH>;
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) {                   // K codes: D / 32 chunks a row
-        const int at = lane + 32 * i, pos = at / (D / 32), ch = at % (D / 32);
-        const size_t r = __shfl_sync(0xffffffffu, row, pos);
-        const uint8_t *s1 = p.k1c + (r * p.hs + h0) * T::KC + ch * 16;
+        const int pos = lane / (D / 32) + i * (1024 / D), ch = lane % (D / 32);
+        const uint32_t r = __shfl_sync(0xffffffffu, row, pos);
+        const uint8_t *s1 = p.k1c + static_cast<uint64_t>(r) * (p.hs * T::KC) + (h0 * T::KC + ch * 16);
+        const uint8_t *s2 = p.k2c + static_cast<uint64_t>(r) * (p.hn * T::KC) + (g * T::KC + ch * 16);
         const uint32_t dst = tile + T::k_codes + pos * T::KC + ch * 16;
+        const bool ok = pos < n;
 #pragma unroll
-        for (int j = 0; j < RH; ++j)
-            if (j < nh) copy_async<16>(dst + j * kTile * T::KC, s1 + j * T::KC, pos < n);
-        copy_async<16>(dst + RH * kTile * T::KC, p.k2c + (r * p.hn + g) * T::KC + ch * 16, pos < n);
+        for (int j = 0; j < RH; ++j) copy_async<16>(dst + j * kTile * T::KC, s1 + j * T::KC, ok);
+        copy_async<16>(dst + RH * kTile * T::KC, s2, ok);
     }
 #pragma unroll
     for (int i = 0; i < DV / 64; ++i) {                  // V codes: DV / 32 chunks a row
-        const int at = lane + 32 * i, pos = at / (DV / 32), ch = at % (DV / 32);
-        const size_t r = __shfl_sync(0xffffffffu, row, pos);
-        const uint8_t *s = p.vc + (r * p.hs + h0) * T::VC + ch * 16;
-        const int vr = v_row<DV>(pos);
+        const int pos = lane / (DV / 32) + i * (1024 / DV), ch = lane % (DV / 32);
+        const uint32_t r = __shfl_sync(0xffffffffu, row, pos);
+        const uint8_t *s = p.vc + static_cast<uint64_t>(r) * (p.hs * T::VC) + (h0 * T::VC + ch * 16);
+        const int vr = v_row(pos);
         const uint32_t dst = tile + T::v_codes + vr * T::VC + v_chunk<DV>(vr, ch) * 16;
+        const bool ok = pos < n;
 #pragma unroll
-        for (int j = 0; j < RH; ++j)
-            if (j < nh) copy_async<16>(dst + j * kTile * T::VC, s + j * T::VC, pos < n);
+        for (int j = 0; j < RH; ++j) copy_async<16>(dst + j * kTile * T::VC, s + j * T::VC, ok);
     }
-    const int pos = lane & 15, odd = lane >> 4;
-    const size_t r = row;
+    // scales: lanes 0 .. 15 take the first half of the heads, the others the rest
+    const int pos = lane & 15;
+    const bool ok = pos < n, upper = lane >= 16;
+    const uint8_t *k1 = p.k1b + static_cast<uint64_t>(row) * (p.hs * T::KS) + h0 * T::KS;
+    const uint8_t *k2 = p.k2b + static_cast<uint64_t>(row) * (p.hn * T::KS) + g * T::KS;
+    const uint8_t *v = p.vb + static_cast<uint64_t>(row) * (p.hs * T::VS) + h0 * T::VS;
+    const uint32_t kd = tile + T::k_scales + pos * T::KS, vd = tile + T::v_scales + pos * T::VS;
+    constexpr int KH = (T::NH + 1) / 2, VH = (RH + 1) / 2;
 #pragma unroll
-    for (int i = 0; i < (T::NH + 1) / 2; ++i) {          // scales: a lane takes a row of every other head
-        const int j = 2 * i + odd;
-        if (j < nh || j == RH) {
-            const uint8_t *s = j == RH ? p.k2b + (r * p.hn + g) * T::KS : p.k1b + (r * p.hs + h0 + j) * T::KS;
-            copy_async<T::KS>(tile + T::k_scales + (j * kTile + pos) * T::KS, s, pos < n);
-        }
-        if (j < nh)
-            copy_async<T::VS>(tile + T::v_scales + (j * kTile + pos) * T::VS, p.vb + (r * p.hs + h0 + j) * T::VS, pos < n);
+    for (int i = 0; i < KH; ++i) {
+        const int j = upper ? i + KH : i;
+        if (j < T::NH) copy_async<T::KS>(kd + j * kTile * T::KS, j == RH ? k2 : k1 + j * T::KS, ok);
+    }
+#pragma unroll
+    for (int i = 0; i < VH; ++i) {
+        const int j = upper ? i + VH : i;
+        if (j < RH) copy_async<T::VS>(vd + j * kTile * T::VS, v + j * T::VS, ok);
     }
 }
 
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
-    return v;
-}
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-    return v;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-    return v;
-}
-__device__ __forceinline__ uint32_t lds16(uint32_t a) {
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
-    return v;
-}
+template <typename V>
+__device__ __forceinline__ V at(const uint8_t *smem) { return *reinterpret_cast<const V *>(smem); }
 
 // The query rows of the warp's heads as f16 in shared memory, scaled by a
 // power of two that brings their largest element to [2^14, 2^15) (f16 then
 // holds all of bf16's digits down to 2^-31 of that).  Returns this lane's
 // factor from a score head to exp2 units: that of head lane % 4.
 template <int D, int RH>
-__device__ __forceinline__ float load_queries(const Params &p, uint32_t dst, int b, int h0, int nh, int g) {
+__device__ __forceinline__ float load_queries(const Params &p, uint8_t *dst, int b, int h0, int g) {
     const int lane = threadIdx.x & 31;
     float mine = 0.f;
 #pragma unroll
     for (int j = 0; j <= RH; ++j) {
-        if (j >= nh && j != RH) continue;
         const __nv_bfloat16 *q = j == RH ? p.q2 + (static_cast<size_t>(b) * p.hn + g) * D
                                          : p.q1 + (static_cast<size_t>(b) * p.hs + h0 + j) * D;
         uint32_t w[D / 64], most = 0;
@@ -340,8 +328,8 @@ __device__ __forceinline__ float load_queries(const Params &p, uint32_t dst, int
         const float f = __uint_as_float(static_cast<uint32_t>(up) << 23);
 #pragma unroll
         for (int i = 0; i < D / 64; ++i)
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + j * D * 2 + (lane + 32 * i) * 4),
-                         "r"(pack_half2(bf16_lo(w[i]) * f, bf16_hi(w[i]) * f)) : "memory");
+            reinterpret_cast<uint32_t *>(dst + j * D * 2)[lane + 32 * i] =
+                pack_half2(bf16_lo(w[i]) * f, bf16_hi(w[i]) * f);
         const float back = __uint_as_float(static_cast<uint32_t>(254 - up) << 23);
         const float k = j == RH ? p.k2_scale[g] : p.k1_scale[h0 + j];
         if ((lane & 3) == j) mine = p.scale_log2 * k * back;
@@ -356,14 +344,15 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32, (Tile<D, DV, RH>::blocks)
     constexpr int NH = T::NH, SLABS = DV / 64, S = T::ring;
     extern __shared__ __align__(128) uint8_t smem[];
     const int lane = threadIdx.x & 31, quad = lane >> 2, t = lane & 3;
-    const uint32_t ring = smem_u32(smem) + (threadIdx.x >> 5) * T::warp_bytes;
-    const uint32_t queries = ring + S * T::bytes, zeros = queries + NH * D * 2;
+    uint8_t *const ring = smem + (threadIdx.x >> 5) * T::warp_bytes;
+    uint8_t *const queries = ring + S * T::bytes, *const zeros = queries + NH * D * 2;
     const int units = p.hn * p.parts;
     const int u = blockIdx.x * kWarpsPerBlock + (threadIdx.x >> 5);
     const int split = u / units, g = (u % units) / p.parts, part = u % p.parts;
     if (split >= p.splits) return;
-    const int r = p.hs / p.hn;
-    const int first = part * r / p.parts, h0 = g * r + first, nh = (part + 1) * r / p.parts - first;
+    // every part is RH heads: the last begins early where they do not divide the group, and leaves what the parts
+    // before it have done unwritten
+    const int r = p.hs / p.hn, begin = min(part * RH, r - RH), done = part * RH - begin, h0 = g * r + begin;
     Range range;
     if (!range_of(p, split, range)) return;
 
@@ -384,12 +373,12 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32, (Tile<D, DV, RH>::blocks)
         if (get.pos < get.hi) return;
         if (get.left > 0) next_sequence(p, get); else more = false;
     };
-    if (lane < 8) asm volatile("st.shared.u32 [%0], %1;" ::"r"(zeros + lane * 4), "r"(0) : "memory");
+    if (lane < 8) reinterpret_cast<uint32_t *>(zeros)[lane] = 0u;
     find();
 #pragma unroll
     for (int s = 0; s < S - 1; ++s) {
         if (more) {
-            issue_tile<D, DV, RH>(p, ring + s * T::bytes, row, n, h0, nh, g);
+            issue_tile<D, DV, RH>(p, smem_u32(ring) + s * T::bytes, row, n, h0, g);
             step();
             if (more) find();
         }
@@ -399,7 +388,7 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32, (Tile<D, DV, RH>::blocks)
 
     float acc[RH][SLABS][4][4];
     float m = -INFINITY, l = 0.f;                        // of head t (both its lanes' positions; l of this lane's only)
-    float factor = load_queries<D, RH>(p, queries, use.b, h0, nh, g);
+    float factor = load_queries<D, RH>(p, queries, use.b, h0, g);
 #pragma unroll
     for (int j = 0; j < RH; ++j)
 #pragma unroll
@@ -413,44 +402,42 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32, (Tile<D, DV, RH>::blocks)
         asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
         __syncwarp();                                    // every lane's copies have landed; the oldest tile is free
         if (more) {
-            issue_tile<D, DV, RH>(p, ring + to * T::bytes, row, n, h0, nh, g);
+            issue_tile<D, DV, RH>(p, smem_u32(ring) + to * T::bytes, row, n, h0, g);
             step();
             if (more) find();
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
         to = to + 1 == S ? 0 : to + 1;
-        const uint32_t tile = ring + from * T::bytes;
+        const uint8_t *const tile = ring + from * T::bytes;
         from = from + 1 == S ? 0 : from + 1;
 
         // ---- scores: lane (quad, t) ends up with positions quad, quad + 8 of head t
         float x0[4] = {}, x1[4] = {};
 #pragma unroll
         for (int j = 0; j < NH; ++j) {
-            if (j >= nh && j != RH) continue;
             float c[4] = {0.f, 0.f, 0.f, 0.f};
-            const uint32_t q = queries + j * D * 2;
+            const uint8_t *q = queries + j * D * 2;
 #pragma unroll
             for (int half = 0; half < D / 64; ++half) {  // 16 dims of this lane: block `blk`
                 const int blk = D == 64 ? t : 2 * t + half;
-                const uint32_t qa = quad == blk ? q + blk * 32 : zeros;
-                const uint4 b0 = lds128(qa), b1 = lds128(qa + 16);
-                const uint32_t ka = tile + T::k_codes + (j * kTile + quad) * T::KC + blk * 8;
-                const uint2 lo = lds64(ka), hi = lds64(ka + 8 * T::KC);
+                const uint8_t *qa = quad == blk ? q + blk * 32 : zeros;
+                const uint4 b0 = at<uint4>(qa), b1 = at<uint4>(qa + 16);
+                const uint8_t *ka = tile + T::k_codes + (j * kTile + quad) * T::KC + blk * 8;
+                const uint2 lo = at<uint2>(ka), hi = at<uint2>(ka + 8 * T::KC);
                 uint32_t a0[4], a1[4];
                 e2m1x8_to_half2x4(a0, lo.x);
                 e2m1x8_to_half2x4(a1, hi.x);
-                mma_16816(c, a0[0], a1[0], a0[1], a1[1], b0.x, b0.y);
-                mma_16816(c, a0[2], a1[2], a0[3], a1[3], b0.z, b0.w);
+                mma_16816(c, a0[0], a1[0], a0[1], a1[1], b0.x, b0.y, c);
+                mma_16816(c, a0[2], a1[2], a0[3], a1[3], b0.z, b0.w, c);
                 e2m1x8_to_half2x4(a0, lo.y);
                 e2m1x8_to_half2x4(a1, hi.y);
-                mma_16816(c, a0[0], a1[0], a0[1], a1[1], b1.x, b1.y);
-                mma_16816(c, a0[2], a1[2], a0[3], a1[3], b1.z, b1.w);
+                mma_16816(c, a0[0], a1[0], a0[1], a1[1], b1.x, b1.y, c);
+                mma_16816(c, a0[2], a1[2], a0[3], a1[3], b1.z, b1.w, c);
             }
             if (D == 128 || t < 2) {                     // columns 2t, 2t + 1 are blocks
-                const uint32_t sa = tile + T::k_scales + (j * kTile + quad) * T::KS + 2 * t;
-                const float2 s0 = half2_bits_to_float2(e4m3x2_to_half2(lds16(sa)));
-                const float2 s1 = half2_bits_to_float2(e4m3x2_to_half2(lds16(sa + 8 * T::KS)));
-                // the noise head goes to place RH of the four
+                const uint8_t *sa = tile + T::k_scales + (j * kTile + quad) * T::KS + 2 * t;
+                const float2 s0 = half2_bits_to_float2(e4m3x2_to_half2(at<uint16_t>(sa)));
+                const float2 s1 = half2_bits_to_float2(e4m3x2_to_half2(at<uint16_t>(sa + 8 * T::KS)));
                 x0[j] = fmaf(c[1], s0.y, c[0] * s0.x);
                 x1[j] = fmaf(c[3], s1.y, c[2] * s1.x);
             }
@@ -492,21 +479,36 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32, (Tile<D, DV, RH>::blocks)
         const uint32_t pick = 0x40u + 0x11u * (quad >> 1);   // byte of block quad / 2 from either word
 #pragma unroll
         for (int j = 0; j < RH; ++j) {
-            if (j >= nh) continue;
             const int src = 8 * t + (quad & 1 ? RH : j);
             const uint32_t w0 = __shfl_sync(0xffffffffu, weights, src), w1 = __shfl_sync(0xffffffffu, weights, src + 4);
-            const uint32_t vs = tile + T::v_scales + (j * kTile + 2 * t) * T::VS;
-            const uint32_t vc = tile + T::v_codes + j * kTile * T::VC;
+            // scales of positions 2t, 2t + 1 and 2t + 8, 2t + 9: four blocks to a word
+            const uint8_t *vs = tile + T::v_scales + (j * kTile + 2 * t) * T::VS;
+            uint32_t e[4][SLABS];                        // [2t, 2t + 8, 2t + 1, 2t + 9][slab]
+            if constexpr (DV == 64) {
+                const uint2 u = at<uint2>(vs), v = at<uint2>(vs + 8 * T::VS);
+                e[0][0] = u.x, e[2][0] = u.y, e[1][0] = v.x, e[3][0] = v.y;
+            } else if constexpr (DV == 128) {
+                const uint4 u = at<uint4>(vs), v = at<uint4>(vs + 8 * T::VS);
+                e[0][0] = u.x, e[0][1] = u.y, e[2][0] = u.z, e[2][1] = u.w;
+                e[1][0] = v.x, e[1][1] = v.y, e[3][0] = v.z, e[3][1] = v.w;
+            } else {
+                const int at_pos[4] = {0, 8, 1, 9};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint4 u = at<uint4>(vs + at_pos[k] * T::VS);
+                    e[k][0] = u.x, e[k][1] = u.y, e[k][2] = u.z, e[k][3] = u.w;
+                }
+            }
+            // codes of 8 dims of slab 0 in row t of the tile; slab s has bits 5, 6 of the place turned over
+            const uint32_t lane_at = t * T::VC + (v_chunk<DV>(t, 0) + (quad >> 2)) * 16 + (quad & 3) * 4;
+            const uint8_t *vc = tile + T::v_codes + j * kTile * T::VC;
 #pragma unroll
             for (int s = 0; s < SLABS; ++s) {
-                // scales of positions 2t, 2t + 1 and 2t + 8, 2t + 9: four blocks to a word
-                const uint32_t e0 = prmt(lds32(vs + 4 * s), lds32(vs + 8 * T::VS + 4 * s), pick);
-                const uint32_t e1 = prmt(lds32(vs + T::VS + 4 * s), lds32(vs + 9 * T::VS + 4 * s), pick);
-                const uint32_t b0 = half2_mul(w0, e4m3x2_to_half2(e0)), b1 = half2_mul(w1, e4m3x2_to_half2(e1));
-                auto word = [&](int vr) {                // codes of 8 dims in row vr of the tile
-                    return lds32(vc + vr * T::VC + v_chunk<DV>(vr, 2 * s + (quad >> 2)) * 16 + (quad & 3) * 4);
-                };
-                const uint32_t p0w = word(t), p8w = word(t + 4), p1w = word(t + 8), p9w = word(t + 12);
+                const uint32_t b0 = half2_mul(w0, e4m3x2_to_half2(prmt(e[0][s], e[1][s], pick)));
+                const uint32_t b1 = half2_mul(w1, e4m3x2_to_half2(prmt(e[2][s], e[3][s], pick)));
+                const uint8_t *row = vc + (lane_at ^ (32 * s));
+                const uint32_t p0w = at<uint32_t>(row), p8w = at<uint32_t>(row + 4 * T::VC),
+                               p1w = at<uint32_t>(row + 8 * T::VC), p9w = at<uint32_t>(row + 12 * T::VC);
                 uint32_t a0[4], a1[4], a2[4], a3[4];
                 // two positions' codes of one dim side by side in a byte: even dims, odd dims
                 e2m1x8_to_half2x4(a0, (p0w & 0x0f0f0f0fu) | ((p8w << 4) & 0xf0f0f0f0u));
@@ -514,7 +516,7 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32, (Tile<D, DV, RH>::blocks)
                 e2m1x8_to_half2x4(a2, (p1w & 0x0f0f0f0fu) | ((p9w << 4) & 0xf0f0f0f0u));
                 e2m1x8_to_half2x4(a3, ((p1w >> 4) & 0x0f0f0f0fu) | (p9w & 0xf0f0f0f0u));
 #pragma unroll
-                for (int i = 0; i < 4; ++i) mma_16816(acc[j][s][i], a0[i], a1[i], a2[i], a3[i], b0, b1);
+                for (int i = 0; i < 4; ++i) mma_16816(acc[j][s][i], a0[i], a1[i], a2[i], a3[i], b0, b1, acc[j][s][i]);
             }
         }
 
@@ -528,13 +530,13 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32, (Tile<D, DV, RH>::blocks)
         const size_t slot = static_cast<size_t>(split) + use.b;
 #pragma unroll
         for (int j = 0; j < RH; ++j) {
-            if (j >= nh) continue;
+            if (j < done) continue;
             const float mj = __shfl_sync(0xffffffffu, m, j), lj = __shfl_sync(0xffffffffu, l, j);
-            const size_t at = slot * p.hs + h0 + j;
-            if (lane == 0) reinterpret_cast<float4 *>(p.ws_ml)[at] = make_float4(mj, lj, mn, ln);
+            const size_t place = slot * p.hs + h0 + j;
+            if (lane == 0) reinterpret_cast<float4 *>(p.ws_ml)[place] = make_float4(mj, lj, mn, ln);
             if (t == quad >> 1) {                        // the lanes whose columns are their own block
                 const float v = p.v_scale[h0 + j];
-                float4 *o1 = reinterpret_cast<float4 *>(p.ws_o + at * 2 * DV), *o2 = o1 + DV / 4;
+                float4 *o1 = reinterpret_cast<float4 *>(p.ws_o + place * 2 * DV), *o2 = o1 + DV / 4;
 #pragma unroll
                 for (int s = 0; s < SLABS; ++s)
 #pragma unroll
@@ -555,7 +557,7 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32, (Tile<D, DV, RH>::blocks)
         len = next_sequence(p, use);
         m = -INFINITY, l = 0.f;
         __syncwarp();                                    // the queries' last readers are done
-        factor = load_queries<D, RH>(p, queries, use.b, h0, nh, g);
+        factor = load_queries<D, RH>(p, queries, use.b, h0, g);
 #pragma unroll
         for (int j = 0; j < RH; ++j)
 #pragma unroll
