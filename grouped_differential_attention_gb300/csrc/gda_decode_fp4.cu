@@ -232,9 +232,9 @@ struct Tile {
     static constexpr int k_scales = v_codes + RH * kTile * VC;
     static constexpr int v_scales = k_scales + NH * kTile * KS;
     static constexpr int bytes = (v_scales + RH * kTile * VS + 15) / 16 * 16;
-    static constexpr int queries = NH * D * 2 + 32;      // f16, and 32 bytes of zeros
+    static constexpr int queries = NH * D * 2;           // f16; a block has as many bytes of zeros once more
     static constexpr int blocks = blocks_per_sm(RH, DV);
-    static constexpr int room = (227 * 1024 / blocks - 1024) / kWarpsPerBlock;
+    static constexpr int room = (227 * 1024 / blocks - 1024 - queries) / kWarpsPerBlock;
     static constexpr int fit = (room - queries) / bytes;
     static constexpr int ring = fit > 6 ? 6 : fit;       // tiles of the ring
     static_assert(ring >= 2, "a tile must be copied while another is used");
@@ -337,6 +337,23 @@ __device__ __forceinline__ float load_queries(const Params &p, uint8_t *dst, int
     return mine;
 }
 
+// Sum over the blocks of head t's score, on lane t of a quad: lane t holds x[j] = the share of blocks 2t, 2t + 1 in
+// head j's (D = 64: there are four blocks, and what lanes 2 and 3 hold is not used).
+template <int D>
+__device__ __forceinline__ float gather(const float (&x)[4], int t) {
+    const bool odd = t & 1;
+    if constexpr (D == 64) {
+        const float a = (odd ? x[1] : x[0]) + __shfl_xor_sync(0xffffffffu, odd ? x[0] : x[1], 1);
+        const float b = (odd ? x[3] : x[2]) + __shfl_xor_sync(0xffffffffu, odd ? x[2] : x[3], 1);
+        const float c = __shfl_xor_sync(0xffffffffu, b, 2);
+        return t < 2 ? a : c;
+    } else {
+        const float a = (t < 2 ? x[0] : x[2]) + __shfl_xor_sync(0xffffffffu, t < 2 ? x[2] : x[0], 2);
+        const float b = (t < 2 ? x[1] : x[3]) + __shfl_xor_sync(0xffffffffu, t < 2 ? x[3] : x[1], 2);
+        return (odd ? b : a) + __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+    }
+}
+
 // One warp: split u / units of the range, unit u % units = (noise head, part of its group).
 template <int D, int DV, int RH>
 __global__ void __launch_bounds__(kWarpsPerBlock * 32, (Tile<D, DV, RH>::blocks)) gda_decode_fp4_split_kernel(const Params p) {
@@ -345,7 +362,9 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32, (Tile<D, DV, RH>::blocks)
     extern __shared__ __align__(128) uint8_t smem[];
     const int lane = threadIdx.x & 31, quad = lane >> 2, t = lane & 3;
     uint8_t *const ring = smem + (threadIdx.x >> 5) * T::warp_bytes;
-    uint8_t *const queries = ring + S * T::bytes, *const zeros = queries + NH * D * 2;
+    uint8_t *const queries = ring + S * T::bytes, *const zeros = smem + kWarpsPerBlock * T::warp_bytes;
+    for (int i = threadIdx.x; i < NH * D / 2; i += kWarpsPerBlock * 32) reinterpret_cast<uint32_t *>(zeros)[i] = 0u;
+    __syncthreads();                                     // the only one: from here on every warp is on its own
     const int units = p.hn * p.parts;
     const int u = blockIdx.x * kWarpsPerBlock + (threadIdx.x >> 5);
     const int split = u / units, g = (u % units) / p.parts, part = u % p.parts;
@@ -373,7 +392,6 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32, (Tile<D, DV, RH>::blocks)
         if (get.pos < get.hi) return;
         if (get.left > 0) next_sequence(p, get); else more = false;
     };
-    if (lane < 8) reinterpret_cast<uint32_t *>(zeros)[lane] = 0u;
     find();
 #pragma unroll
     for (int s = 0; s < S - 1; ++s) {
@@ -385,6 +403,11 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32, (Tile<D, DV, RH>::blocks)
         asm volatile("cp.async.commit_group;" ::: "memory");
     }
     int to = S - 1, from = 0;
+    // lane parts of places in shared memory
+    const uint8_t *const qa0 = quad == (D == 64 ? t : 2 * t) ? queries + t * (D / 2) : zeros;
+    const uint8_t *const qa1 = quad == 2 * t + 1 ? queries + t * (D / 2) + 32 : zeros;   // D = 128: the second block
+    const int k_at = T::k_codes + quad * T::KC + t * (D / 8);
+    const int ks_at = T::k_scales + quad * T::KS + (D == 64 ? t & 1 : t) * 2;
 
     float acc[RH][SLABS][4][4];
     float m = -INFINITY, l = 0.f;                        // of head t (both its lanes' positions; l of this lane's only)
@@ -416,14 +439,12 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32, (Tile<D, DV, RH>::blocks)
 #pragma unroll
         for (int j = 0; j < NH; ++j) {
             float c[4] = {0.f, 0.f, 0.f, 0.f};
-            const uint8_t *q = queries + j * D * 2;
+            const uint8_t *ka = tile + k_at + j * kTile * T::KC, *sa = tile + ks_at + j * kTile * T::KS;
 #pragma unroll
-            for (int half = 0; half < D / 64; ++half) {  // 16 dims of this lane: block `blk`
-                const int blk = D == 64 ? t : 2 * t + half;
-                const uint8_t *qa = quad == blk ? q + blk * 32 : zeros;
+            for (int half = 0; half < D / 64; ++half) {  // 16 dims of this lane: a block
+                const uint8_t *qa = (half ? qa1 : qa0) + j * D * 2;
                 const uint4 b0 = at<uint4>(qa), b1 = at<uint4>(qa + 16);
-                const uint8_t *ka = tile + T::k_codes + (j * kTile + quad) * T::KC + blk * 8;
-                const uint2 lo = at<uint2>(ka), hi = at<uint2>(ka + 8 * T::KC);
+                const uint2 lo = at<uint2>(ka + half * 8), hi = at<uint2>(ka + 8 * T::KC + half * 8);
                 uint32_t a0[4], a1[4];
                 e2m1x8_to_half2x4(a0, lo.x);
                 e2m1x8_to_half2x4(a1, hi.x);
@@ -434,21 +455,14 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32, (Tile<D, DV, RH>::blocks)
                 mma_16816(c, a0[0], a1[0], a0[1], a1[1], b1.x, b1.y, c);
                 mma_16816(c, a0[2], a1[2], a0[3], a1[3], b1.z, b1.w, c);
             }
-            if (D == 128 || t < 2) {                     // columns 2t, 2t + 1 are blocks
-                const uint8_t *sa = tile + T::k_scales + (j * kTile + quad) * T::KS + 2 * t;
-                const float2 s0 = half2_bits_to_float2(e4m3x2_to_half2(at<uint16_t>(sa)));
-                const float2 s1 = half2_bits_to_float2(e4m3x2_to_half2(at<uint16_t>(sa + 8 * T::KS)));
-                x0[j] = fmaf(c[1], s0.y, c[0] * s0.x);
-                x1[j] = fmaf(c[3], s1.y, c[2] * s1.x);
-            }
+            // columns 2t, 2t + 1 are blocks 2t, 2t + 1 (at D = 64 there are four: lanes 2, 3 hold nothing of use)
+            const float2 s0 = half2_bits_to_float2(e4m3x2_to_half2(at<uint16_t>(sa)));
+            const float2 s1 = half2_bits_to_float2(e4m3x2_to_half2(at<uint16_t>(sa + 8 * T::KS)));
+            x0[j] = fmaf(c[1], s0.y, c[0] * s0.x);
+            x1[j] = fmaf(c[3], s1.y, c[2] * s1.x);
         }
-        auto gather = [&](const float (&x)[4]) {         // sum over the quad's lanes, head t to lane t
-            const float a = (t < 2 ? x[0] : x[2]) + __shfl_xor_sync(0xffffffffu, t < 2 ? x[2] : x[0], 2);
-            const float b = (t < 2 ? x[1] : x[3]) + __shfl_xor_sync(0xffffffffu, t < 2 ? x[3] : x[1], 2);
-            return (t & 1 ? b : a) + __shfl_xor_sync(0xffffffffu, t & 1 ? a : b, 1);
-        };
         const int have = use.hi - use.pos;               // positions of the tile, if below 16
-        float sc0 = gather(x0) * factor, sc1 = gather(x1) * factor;   // every lane takes part in the shuffles
+        float sc0 = gather<D>(x0, t) * factor, sc1 = gather<D>(x1, t) * factor;
         if (quad >= have) sc0 = -INFINITY;
         if (quad + 8 >= have) sc1 = -INFINITY;
         float mt = max3f(m, sc0, sc1);
@@ -691,7 +705,7 @@ template <int D, int DV, int RH>
 cudaError_t launch_split(const Params &p, cudaStream_t stream) {
     using T = Tile<D, DV, RH>;
     auto kern = gda_decode_fp4_split_kernel<D, DV, RH>;
-    const int smem = T::warp_bytes * kWarpsPerBlock;
+    const int smem = T::warp_bytes * kWarpsPerBlock + T::queries;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int warps = p.splits * p.hn * p.parts;
