@@ -169,14 +169,32 @@ __device__ __forceinline__ bool range_of(const Params &p, int split, Range &r) {
     return false;                         // not reached: start < total
 }
 
-// Copies into shared memory, asynchronous; zeros in place of what `ok` leaves out.
+// Notes the first and last range of every sequence that begins in range r of split `split`, for the combine kernel.
+__device__ __forceinline__ void note_sequences(const Params &p, const Range &r, int split) {
+    long long before = r.before;
+    for (int b = r.b; before < r.end; ++b) {
+        const int len = length_of(p, b);
+        if (len > 0 && before >= r.start && (threadIdx.x & 31) == 0) {
+            p.ws_seg[2 * b] = split;
+            p.ws_seg[2 * b + 1] = static_cast<int>((before + len - 1) / r.per);
+        }
+        before += len;
+    }
+}
+
+// BYTES into shared memory, asynchronous; zeros in their place if `ok` is false, nothing at all if `there` is,
+// (a predicate of the one instruction, not a branch around it).
 template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t dst, const uint8_t *src, bool ok) {
+__device__ __forceinline__ void copy_async(uint32_t dst, const uint8_t *src, bool ok, bool there = true) {
     const int n = ok ? BYTES : 0;
     if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\t"
+                     "@p cp.async.cg.shared.global [%0], [%1], 16, %2;\n\t}" ::"r"(dst),
+                     "l"(src), "r"(n), "r"(static_cast<int>(there)) : "memory");
     else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n) : "memory");
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "@p cp.async.ca.shared.global [%0], [%1], %2, %3;\n\t}" ::"r"(dst),
+                     "l"(src), "n"(BYTES), "r"(n), "r"(static_cast<int>(there)) : "memory");
 }
 
 // a * b + c: 16 x 16 (f16) times 16 x 8 (f16).
@@ -213,13 +231,12 @@ __device__ __forceinline__ void enter(const Params &p, Cursor &c, int pos, int l
     c.left -= n;
 }
 
-// To the next sequence with positions; there is one while left > 0.  Returns its length.
-__device__ __forceinline__ int next_sequence(const Params &p, Cursor &c) {
+// To the next sequence with positions; there is one while left > 0.
+__device__ __forceinline__ void next_sequence(const Params &p, Cursor &c) {
     int len = 0;
     do len = length_of(p, ++c.b);
     while (len == 0);
     enter(p, c, 0, len);
-    return len;
 }
 
 // Sizes of a warp's tile in shared memory, in bytes.
@@ -253,53 +270,59 @@ __device__ __forceinline__ int v_chunk(int row, int chunk) {
     return chunk;
 }
 
+// base + row * pitch, one multiply-add.
+__device__ __forceinline__ const uint8_t *row_at(const uint8_t *base, uint32_t row, uint32_t pitch) {
+    return base + static_cast<uint64_t>(row) * pitch;
+}
+
 // Starts the copies of a tile: positions whose cache rows are `row` of lanes
 // 0 .. 15 (and again 16 .. 31), the first n of them; RH signal heads from h0 on.
 template <int D, int DV, int RH>
-__device__ __forceinline__ void issue_tile(const Params &p, uint32_t tile, uint32_t row, int n, int h0, int g) {
+__device__ __forceinline__ void issue_tile(const Params &p, uint32_t tile, uint32_t row, int n, uint32_t h0, uint32_t g) {
     using T = Tile<D, DV, RH>;
-    const int lane = threadIdx.x & 31;
+    const uint32_t lane = threadIdx.x & 31, hs = p.hs, hn = p.hn;
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) {                   // K codes: D / 32 chunks a row
-        const int pos = lane / (D / 32) + i * (1024 / D), ch = lane % (D / 32);
+        const uint32_t pos = lane / (D / 32) + i * (1024 / D), ch = lane % (D / 32);
         const uint32_t r = __shfl_sync(0xffffffffu, row, pos);
-        const uint8_t *s1 = p.k1c + static_cast<uint64_t>(r) * (p.hs * T::KC) + (h0 * T::KC + ch * 16);
-        const uint8_t *s2 = p.k2c + static_cast<uint64_t>(r) * (p.hn * T::KC) + (g * T::KC + ch * 16);
+        const uint8_t *s1 = row_at(p.k1c, r, hs * T::KC) + (h0 * T::KC + ch * 16);
+        const uint8_t *s2 = row_at(p.k2c, r, hn * T::KC) + (g * T::KC + ch * 16);
         const uint32_t dst = tile + T::k_codes + pos * T::KC + ch * 16;
-        const bool ok = pos < n;
+        const bool ok = static_cast<int>(pos) < n;
 #pragma unroll
         for (int j = 0; j < RH; ++j) copy_async<16>(dst + j * kTile * T::KC, s1 + j * T::KC, ok);
         copy_async<16>(dst + RH * kTile * T::KC, s2, ok);
     }
 #pragma unroll
     for (int i = 0; i < DV / 64; ++i) {                  // V codes: DV / 32 chunks a row
-        const int pos = lane / (DV / 32) + i * (1024 / DV), ch = lane % (DV / 32);
+        const uint32_t pos = lane / (DV / 32) + i * (1024 / DV), ch = lane % (DV / 32);
         const uint32_t r = __shfl_sync(0xffffffffu, row, pos);
-        const uint8_t *s = p.vc + static_cast<uint64_t>(r) * (p.hs * T::VC) + (h0 * T::VC + ch * 16);
-        const int vr = v_row(pos);
-        const uint32_t dst = tile + T::v_codes + vr * T::VC + v_chunk<DV>(vr, ch) * 16;
-        const bool ok = pos < n;
+        const uint8_t *s = row_at(p.vc, r, hs * T::VC) + (h0 * T::VC + ch * 16);
+        const uint32_t vr = v_row(pos), dst = tile + T::v_codes + vr * T::VC + v_chunk<DV>(vr, ch) * 16;
+        const bool ok = static_cast<int>(pos) < n;
 #pragma unroll
         for (int j = 0; j < RH; ++j) copy_async<16>(dst + j * kTile * T::VC, s + j * T::VC, ok);
     }
     // scales: lanes 0 .. 15 take the first half of the heads, the others the rest
-    const int pos = lane & 15;
-    const bool ok = pos < n, upper = lane >= 16;
-    const uint8_t *k1 = p.k1b + static_cast<uint64_t>(row) * (p.hs * T::KS) + h0 * T::KS;
-    const uint8_t *k2 = p.k2b + static_cast<uint64_t>(row) * (p.hn * T::KS) + g * T::KS;
-    const uint8_t *v = p.vb + static_cast<uint64_t>(row) * (p.hs * T::VS) + h0 * T::VS;
-    const uint32_t kd = tile + T::k_scales + pos * T::KS, vd = tile + T::v_scales + pos * T::VS;
     constexpr int KH = (T::NH + 1) / 2, VH = (RH + 1) / 2;
+    const uint32_t pos = lane & 15, upper = lane >> 4;
+    const bool ok = static_cast<int>(pos) < n;
+    const uint8_t *k1 = row_at(p.k1b, row, hs * T::KS) + (h0 + upper * KH) * T::KS;
+    const uint8_t *k2 = row_at(p.k2b, row, hn * T::KS) + g * T::KS;
+    const uint8_t *v = row_at(p.vb, row, hs * T::VS) + (h0 + upper * VH) * T::VS;
+    const uint32_t kd = tile + T::k_scales + (upper * KH * kTile + pos) * T::KS;
+    const uint32_t vd = tile + T::v_scales + (upper * VH * kTile + pos) * T::VS;
 #pragma unroll
     for (int i = 0; i < KH; ++i) {
-        const int j = upper ? i + KH : i;
-        if (j < T::NH) copy_async<T::KS>(kd + j * kTile * T::KS, j == RH ? k2 : k1 + j * T::KS, ok);
+        // the upper lanes' last head is the noise head (or none, where NH is odd)
+        const bool noise = upper && i + KH == RH;
+        const bool some = i + KH <= RH || !upper;
+        if (i + KH == RH) copy_async<T::KS>(kd + i * kTile * T::KS, noise ? k2 : k1 + i * T::KS, ok);
+        else copy_async<T::KS>(kd + i * kTile * T::KS, k1 + i * T::KS, ok, some);
     }
 #pragma unroll
-    for (int i = 0; i < VH; ++i) {
-        const int j = upper ? i + VH : i;
-        if (j < RH) copy_async<T::VS>(vd + j * kTile * T::VS, v + j * T::VS, ok);
-    }
+    for (int i = 0; i < VH; ++i)
+        copy_async<T::VS>(vd + i * kTile * T::VS, v + i * T::VS, ok, i + VH < RH || !upper);
 }
 
 template <typename V>
@@ -375,9 +398,9 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32, (Tile<D, DV, RH>::blocks)
     Range range;
     if (!range_of(p, split, range)) return;
 
+    if (u % units == 0) note_sequences(p, range, split);
     Cursor use{range.b, 0, 0, static_cast<int>(range.end - range.start)};
-    int len = length_of(p, range.b);
-    enter(p, use, static_cast<int>(range.start - range.before), len);
+    enter(p, use, static_cast<int>(range.start - range.before), length_of(p, range.b));
     Cursor get = use;                                    // the copies' place, ahead of the arithmetic's
     bool more = true;
     uint32_t row = 0;
@@ -393,16 +416,7 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32, (Tile<D, DV, RH>::blocks)
         if (get.left > 0) next_sequence(p, get); else more = false;
     };
     find();
-#pragma unroll
-    for (int s = 0; s < S - 1; ++s) {
-        if (more) {
-            issue_tile<D, DV, RH>(p, smem_u32(ring) + s * T::bytes, row, n, h0, g);
-            step();
-            if (more) find();
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    }
-    int to = S - 1, from = 0;
+    int to = 0, from = 0, ahead = S - 1;                 // places of the ring; tiles to copy before the first is used
     // lane parts of places in shared memory
     const uint8_t *const qa0 = quad == (D == 64 ? t : 2 * t) ? queries + t * (D / 2) : zeros;
     const uint8_t *const qa1 = quad == 2 * t + 1 ? queries + t * (D / 2) + 32 : zeros;   // D = 128: the second block
@@ -422,8 +436,7 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32, (Tile<D, DV, RH>::blocks)
                 for (int k = 0; k < 4; ++k) acc[j][s][i][k] = 0.f;
 
     for (;;) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
-        __syncwarp();                                    // every lane's copies have landed; the oldest tile is free
+        __syncwarp();                                    // the readers of place `to` are done
         if (more) {
             issue_tile<D, DV, RH>(p, smem_u32(ring) + to * T::bytes, row, n, h0, g);
             step();
@@ -431,6 +444,12 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32, (Tile<D, DV, RH>::blocks)
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
         to = to + 1 == S ? 0 : to + 1;
+        if (ahead > 0) {
+            --ahead;
+            continue;
+        }
+        asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+        __syncwarp();                                    // every lane's copies of this tile have landed
         const uint8_t *const tile = ring + from * T::bytes;
         from = from + 1 == S ? 0 : from + 1;
 
@@ -561,14 +580,8 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32, (Tile<D, DV, RH>::blocks)
                     }
             }
         }
-        if (lane == 0 && h0 == 0 && range.before >= range.start) {
-            // the part begins with the sequence: the ranges that meet it
-            p.ws_seg[2 * use.b] = split;
-            p.ws_seg[2 * use.b + 1] = static_cast<int>((range.before + len - 1) / range.per);
-        }
         if (use.left == 0) return;
-        range.before += len;
-        len = next_sequence(p, use);
+        next_sequence(p, use);
         m = -INFINITY, l = 0.f;
         __syncwarp();                                    // the queries' last readers are done
         factor = load_queries<D, RH>(p, queries, use.b, h0, g);
