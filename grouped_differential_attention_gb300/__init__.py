@@ -649,12 +649,12 @@ def _workspace(workspace, need, device):
     return workspace
 
 
-def _expect_bytes(t, name, other, shape, device):
-    """_expect for a tensor of bytes: uint8, or the one-byte type `other`."""
-    if isinstance(t, torch.Tensor) and t.dtype is other:
-        _expect(t, name, other, shape, device)
-    else:
-        _expect(t, name, torch.uint8, shape, device)
+def _expect_all(device, *wanted):
+    """_expect for several (tensor, name, dtype, shape) at once: the checks without a call for each."""
+    for t, name, dtype, shape in wanted:
+        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
+                and t.is_contiguous()):
+            _expect(t, name, dtype, shape, device)
 
 
 def _token_stride(t, name, dtype, shape, device):
@@ -667,16 +667,16 @@ def _token_stride(t, name, dtype, shape, device):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    heads, dim = shape[-2:]
-    if t.is_contiguous():
-        return heads * dim
+    heads, dim = shape[-2], shape[-1]
     strides = t.stride()
-    if strides[-1] != 1 or (heads > 1 and strides[-2] != dim):
+    if strides[-1] != 1 or (strides[-2] != dim and heads > 1):
         raise ValueError(f"{name}: the heads of a token must be dense")
+    if len(strides) == 3:
+        return strides[0] if shape[0] > 1 else heads * dim
     step, expect = heads * dim, None
     for i in range(len(strides) - 3, -1, -1):
         size, stride = shape[i], strides[i]
@@ -701,12 +701,12 @@ def _norm_rope_sizes(q_sig, q_noise, weight, positions, inv_freq):
     *lead, hs, d = q_sig.shape
     lead = tuple(lead)
     hn = q_noise.shape[-2]
-    _expect(weight, "weight", torch.float32, (4, d), dev)
-    _expect(positions, "positions", torch.int32, lead, dev)
-    _expect(inv_freq, "inv_freq", torch.float32, (inv_freq.numel(),), dev)
+    half = inv_freq.numel()
+    _expect_all(dev, (weight, "weight", torch.float32, (4, d)), (positions, "positions", torch.int32, lead),
+                (inv_freq, "inv_freq", torch.float32, (half,)))
     sig, noise = lead + (hs, d), lead + (hn, d)
     shapes = (sig, sig, noise, noise)
-    return dev, q_sig.dtype, positions.numel(), hs, hn, d, 2 * inv_freq.numel(), shapes
+    return dev, q_sig.dtype, positions.numel(), hs, hn, d, 2 * half, shapes
 
 
 _PROJECTIONS = ("q_sig", "k_sig", "q_noise", "k_noise")
@@ -764,8 +764,9 @@ def gda_qk_norm_rope_bwd(q_sig, k_sig, q_noise, k_noise, weight, positions, inv_
     else:
         strides += [_token_stride(t, "grads " + n, dt, s, dev) for t, n, s in zip(grads, _PROJECTIONS, shapes)]
         _expect(grads[4], "dweight", torch.float32, (4, d), dev)
-    for t, n, s in zip(dy, _PROJECTIONS, shapes):
-        _expect(t, "d" + n, torch.float32, s, dev)
+    f32 = torch.float32
+    _expect_all(dev, (dq_sig, "dq_sig", f32, shapes[0]), (dk_sig, "dk_sig", f32, shapes[1]),
+                (dq_noise, "dq_noise", f32, shapes[2]), (dk_noise, "dk_noise", f32, shapes[3]))
     workspace = _workspace(workspace, gda_qk_norm_rope_bwd_workspace_size(T, hs, hn, d), dev)
     lib = _load()
     _enqueue(lib.gda_qk_norm_rope_bwd if dt is torch.bfloat16 else lib.gda_qk_norm_rope_bwd_f32,
@@ -796,11 +797,10 @@ def gda_block_tables(cache_lens, new_lens, block_table, free_pages, free_count, 
         raise ValueError("block_table must be [B, max_pages] and free_pages 1-D")
     i32 = torch.int32
     B, max_pages = block_table.shape
-    _expect(cache_lens, "cache_lens", i32, (B,), dev)
-    _expect(new_lens, "new_lens", i32, (B,), dev)
-    _expect(block_table, "block_table", i32, (B, max_pages), dev)
-    _expect(free_pages, "free_pages", i32, (free_pages.numel(),), dev)
-    _expect(free_count, "free_count", i32, (1,), dev)
+    free = free_pages.numel()
+    _expect_all(dev, (cache_lens, "cache_lens", i32, (B,)), (new_lens, "new_lens", i32, (B,)),
+                (block_table, "block_table", i32, (B, max_pages)), (free_pages, "free_pages", i32, (free,)),
+                (free_count, "free_count", i32, (1,)))
     shapes = ((max_rows,), (max_rows,), (B + 1,), (B,), (1,))
     if out is None:
         out = tuple([torch.empty(s, dtype=i32, device=dev) for s in shapes])
@@ -809,7 +809,7 @@ def gda_block_tables(cache_lens, new_lens, block_table, free_pages, free_count, 
             _expect(t, n, i32, s, dev)
     _enqueue(_load().gda_block_tables, "gda block tables", dev,
              *[t.data_ptr() for t in (cache_lens, new_lens, block_table, free_pages, free_count, *out)], B, max_pages,
-             page_size, num_pages, free_pages.numel(), max_rows)
+             page_size, num_pages, free, max_rows)
     return tuple(out)
 
 
@@ -819,15 +819,16 @@ _FP8 = torch.float8_e4m3fn
 
 def _fp4_cache(pools, blocks, scales, rows, hs, hn, d, dv, dev):
     """Checks the nine tensors of a 4-bit cache; returns their addresses in the order of the C entries."""
-    _expect_bytes(pools[0], "k_sig codes", _FP4, rows + (hs, d // 2), dev)
-    _expect_bytes(pools[1], "k_noise codes", _FP4, rows + (hn, d // 2), dev)
-    _expect_bytes(pools[2], "v codes", _FP4, rows + (hs, dv // 2), dev)
-    _expect_bytes(blocks[0], "k_sig_block_scale", _FP8, rows + (hs, d // 16), dev)
-    _expect_bytes(blocks[1], "k_noise_block_scale", _FP8, rows + (hn, d // 16), dev)
-    _expect_bytes(blocks[2], "v_block_scale", _FP8, rows + (hs, dv // 16), dev)
-    _expect(scales[0], "k_sig_scale", torch.float32, (hs,), dev)
-    _expect(scales[1], "k_noise_scale", torch.float32, (hn,), dev)
-    _expect(scales[2], "v_scale", torch.float32, (hs,), dev)
+    f32, sig, noise = torch.float32, rows + (hs, d // 2), rows + (hn, d // 2)
+    # one-byte tensors: uint8, or all of a kind in their own type
+    code = _FP4 if getattr(pools[0], "dtype", None) is _FP4 else torch.uint8
+    block = _FP8 if getattr(blocks[0], "dtype", None) is _FP8 else torch.uint8
+    _expect_all(dev, (pools[0], "k_sig codes", code, sig), (pools[1], "k_noise codes", code, noise),
+                (pools[2], "v codes", code, rows + (hs, dv // 2)),
+                (blocks[0], "k_sig_block_scale", block, rows + (hs, d // 16)),
+                (blocks[1], "k_noise_block_scale", block, rows + (hn, d // 16)),
+                (blocks[2], "v_block_scale", block, rows + (hs, dv // 16)), (scales[0], "k_sig_scale", f32, (hs,)),
+                (scales[1], "k_noise_scale", f32, (hn,)), (scales[2], "v_scale", f32, (hs,)))
     return [t.data_ptr() for t in (*pools, *blocks, *scales)]
 
 
@@ -906,11 +907,9 @@ def _decode_fp4(q_sig, q_noise, pools, blocks, scales, block_table, cache_lens, 
     hn, dv = q_noise.shape[1], 2 * pools[2].shape[3]
     rows = tuple(pools[0].shape[:2])
     bf = torch.bfloat16
-    _expect(q_sig, "q_sig", bf, (B, hs, d), dev)
-    _expect(q_noise, "q_noise", bf, (B, hn, d), dev)
+    _expect_all(dev, (q_sig, "q_sig", bf, (B, hs, d)), (q_noise, "q_noise", bf, (B, hn, d)),
+                (cache_lens, "cache_lens", torch.int32, (B,)), (lam, "lam", torch.float32, (hs,)))
     cache = _fp4_cache(pools, blocks, scales, rows, hs, hn, d, dv, dev)
-    _expect(cache_lens, "cache_lens", torch.int32, (B,), dev)
-    _expect(lam, "lam", torch.float32, (hs,), dev)
     if out is None:
         out = torch.empty((B, hs, dv), dtype=bf, device=dev)
     else:

@@ -166,7 +166,7 @@ int fill_cache_fp4(CacheFp4Args &a, int num_pages, int page_size, int hs, int hn
         if (a.ld[t] % 8 != 0 || !aligned16(a.rows[t]) || !aligned16(a.codes[t]) || !aligned16(a.blocks[t]) ||
             (reinterpret_cast<uintptr_t>(a.scale[t]) & 3u))
             return GDA_ERR_MISALIGNED;
-        a.dim[t] = dims[t];
+        a.shift[t] = dims[t] == 64 ? 2 : (dims[t] == 128 ? 3 : 4);
         a.nb[t] = static_cast<int>(row / 16);
     }
     a.slots = num_pages * page_size;

@@ -86,12 +86,18 @@ __global__ void __launch_bounds__(kThreads) gda_block_tables_kernel(const BlockT
         count = count < 0 ? 0 : a.free_capacity;
     }
 
+    // lengths and additions of the thread's sequences: read once (both at the same time), kept in shared memory
     long long mine = 0, rows = 0;
-    for (int b = b0; b < b1; ++b) mine += max(a.new_lens[b], 0);
+    for (int b = b0; b < b1; ++b) {
+        const int have = a.cache_lens[b], add = a.new_lens[b];
+        len[b] = have;
+        first[b] = add;
+        mine += max(add, 0);
+    }
     long long at = block_prefix(mine, scratch, &rows);
     mine = 0;
     for (int b = b0; b < b1; ++b) {
-        const int have = a.cache_lens[b], add = a.new_lens[b];
+        const int have = len[b], add = first[b];
         const long long n = max(add, 0);
         const bool ok = have >= 0 && add >= 0 && have + n <= cap && at + n <= a.max_rows;
         if (!ok) err |= GDA_DEVERR_BAD_LENGTH;
@@ -143,27 +149,42 @@ __global__ void __launch_bounds__(kThreads) gda_block_tables_kernel(const BlockT
         if (id < 0 || id >= a.num_pages) err |= GDA_DEVERR_BAD_PAGE;
         a.block_table[static_cast<size_t>(b) * a.max_pages + held + (q - first[b])] = id;
     }
-    // the rows
-    for (long long r64 = gt; r64 < a.max_rows; r64 += gn) {
-        const int r = static_cast<int>(r64);
-        int slot = -1, pos = 0;
-        if (r < rows) {
-            const int b = last_at_most(start, a.B, r);
-            if (len[b] >= 0) {
-                pos = len[b] + (r - start[b]);
-                const int j = pos / a.page_size, held = pages_of(len[b], a.page_size);
-                const int id = j < held ? a.block_table[static_cast<size_t>(b) * a.max_pages + j]
-                                        : a.free_pages[count - 1 - (first[b] + j - held)];
-                if (id >= 0 && id < a.num_pages) {
-                    slot = id * a.page_size + (pos - j * a.page_size);
-                } else {
-                    err |= GDA_DEVERR_BAD_PAGE;
-                    pos = 0;
+    // the rows, four in a row to a thread: one bisection for them, and a page looked up where it changes
+    const bool vector = ((reinterpret_cast<uintptr_t>(a.slot_map) | reinterpret_cast<uintptr_t>(a.positions)) & 15) == 0;
+    for (long long q = gt; 4 * q < a.max_rows; q += gn) {
+        const int r0 = static_cast<int>(4 * q), n = min(4, a.max_rows - r0);
+        int slot[4] = {-1, -1, -1, -1}, pos[4] = {0, 0, 0, 0};
+        if (r0 < rows) {
+            int b = last_at_most(start, a.B, r0), page = -1, base = -1;   // page: of the sequence; base: slot of its offset 0
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int r = r0 + k;
+                if (k >= n || r >= rows) break;
+                while (b + 1 < a.B && start[b + 1] <= r) ++b, page = -1;
+                if (len[b] < 0) continue;
+                const int at_pos = len[b] + (r - start[b]), j = at_pos / a.page_size;
+                if (j != page) {
+                    page = j;
+                    const int held = pages_of(len[b], a.page_size);
+                    const int id = j < held ? a.block_table[static_cast<size_t>(b) * a.max_pages + j]
+                                            : a.free_pages[count - 1 - (first[b] + j - held)];
+                    base = id >= 0 && id < a.num_pages ? id * a.page_size : -1;
+                    if (base < 0) err |= GDA_DEVERR_BAD_PAGE;
+                }
+                if (base >= 0) {
+                    slot[k] = base + (at_pos - j * a.page_size);
+                    pos[k] = at_pos;
                 }
             }
         }
-        a.slot_map[r] = slot;
-        a.positions[r] = pos;
+        if (n == 4 && vector) {
+            reinterpret_cast<int4 *>(a.slot_map)[q] = make_int4(slot[0], slot[1], slot[2], slot[3]);
+            reinterpret_cast<int4 *>(a.positions)[q] = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (k < n) a.slot_map[r0 + k] = slot[k], a.positions[r0 + k] = pos[k];
+        }
     }
     if (err) atomicOr(a.dev_err, err);
 }
@@ -172,7 +193,7 @@ __global__ void __launch_bounds__(kThreads) gda_block_tables_kernel(const BlockT
 
 int launch_block_tables(const BlockTablesArgs &a, cudaStream_t stream) {
     // one block for a decode step, up to eight (the portable cluster) for many rows
-    const int blocks = a.max_rows <= 2 * kThreads ? 1 : (a.max_rows <= 8 * kThreads ? 4 : 8);
+    const int blocks = a.max_rows <= 4 * kThreads ? 1 : (a.max_rows <= 16 * kThreads ? 4 : 8);
     const size_t smem = static_cast<size_t>(a.B) * 3 * sizeof(int);
     cudaError_t e = cudaFuncSetAttribute(gda_block_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(kBlockTablesMaxB * 3 * sizeof(int)));

@@ -50,12 +50,19 @@ __device__ __forceinline__ int slot_of(const CacheFp4Args &a, long long t) {
     return slot;
 }
 
-__global__ void __launch_bounds__(kThreads) gda_cache_append_fp4_kernel(const CacheFp4Args a) {
-    const int per_token = a.nb[0] + a.nb[1] + a.nb[2];
-    const long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
-    const long long tok = i / per_token;
-    if (tok >= a.T) return;
-    const Place pl = place_of(a, static_cast<int>(i - tok * per_token));
+// A thread's token and block within it: `tokens` tokens to a thread block (32-bit division, a 64-bit one costs as much
+// as the conversion).  False past the end.
+__device__ __forceinline__ bool place(const CacheFp4Args &a, unsigned tokens, unsigned i, long long *tok, Place *pl) {
+    const unsigned per_token = a.nb[0] + a.nb[1] + a.nb[2], t = i / per_token;
+    *tok = static_cast<long long>(blockIdx.x) * tokens + t;
+    *pl = place_of(a, static_cast<int>(i - t * per_token));
+    return t < tokens && *tok < a.T;
+}
+
+__global__ void __launch_bounds__(kThreads) gda_cache_append_fp4_kernel(const CacheFp4Args a, unsigned tokens) {
+    long long tok;
+    Place pl;
+    if (!place(a, tokens, blockIdx.y * kThreads + threadIdx.x, &tok, &pl)) return;
     const int slot = slot_of(a, tok);
     if (slot < 0) return;
     const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.rows[pl.t]) +
@@ -67,7 +74,7 @@ __global__ void __launch_bounds__(kThreads) gda_cache_append_fp4_kernel(const Ca
 #pragma unroll
     for (int j = 0; j < 8; ++j) most = __vmaxu2(most, w[j] & 0x7fff7fffu);
     most = max(most & 0xffffu, most >> 16);
-    const float g = a.scale[pl.t][pl.in_row * kFp4Block / a.dim[pl.t]];
+    const float g = a.scale[pl.t][pl.in_row >> a.shift[pl.t]];
     uint8_t s8 = 0x7f;
     float r = 0.f;
     if (most <= 0x7f80u) {
@@ -88,19 +95,17 @@ __global__ void __launch_bounds__(kThreads) gda_cache_append_fp4_kernel(const Ca
     a.blocks[pl.t][at] = s8;
 }
 
-__global__ void __launch_bounds__(kThreads) gda_cache_read_fp4_kernel(const CacheFp4Args a) {
-    const int per_token = a.nb[0] + a.nb[1] + a.nb[2];
-    const long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
-    const long long tok = i / per_token;
-    if (tok >= a.T) return;
-    const Place pl = place_of(a, static_cast<int>(i - tok * per_token));
+__global__ void __launch_bounds__(kThreads) gda_cache_read_fp4_kernel(const CacheFp4Args a, unsigned tokens) {
+    long long tok;
+    Place pl;
+    if (!place(a, tokens, blockIdx.y * kThreads + threadIdx.x, &tok, &pl)) return;
     const int slot = slot_of(a, tok);
     uint32_t o[8] = {};
     if (slot >= 0) {
         const size_t at = static_cast<size_t>(slot) * a.nb[pl.t] + pl.in_row;
         const uint2 codes = reinterpret_cast<const uint2 *>(a.codes[pl.t])[at];
         const float s = e4m3_to_float(a.blocks[pl.t][at]);
-        const float g = a.scale[pl.t][pl.in_row * kFp4Block / a.dim[pl.t]];
+        const float g = a.scale[pl.t][pl.in_row >> a.shift[pl.t]];
         uint32_t h[2][4];
         e2m1x8_to_half2x4(h[0], codes.x);
         e2m1x8_to_half2x4(h[1], codes.y);
@@ -116,30 +121,33 @@ __global__ void __launch_bounds__(kThreads) gda_cache_read_fp4_kernel(const Cach
     dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
-int grid_of(const CacheFp4Args &a, unsigned *grid) {
-    const long long n = a.T * (a.nb[0] + a.nb[1] + a.nb[2]);
-    const long long g = (n + kThreads - 1) / kThreads;
-    if (g > 0x7fffffffLL) return GDA_ERR_UNSUPPORTED;
-    *grid = static_cast<unsigned>(g);
-    return GDA_OK;
+// Thread blocks of kThreads blocks of 16 elements each: over groups of as many tokens as fill them best (x), and the
+// pieces of a group (y).
+dim3 grid_of(const CacheFp4Args &a, unsigned *tokens) {
+    const unsigned per_token = a.nb[0] + a.nb[1] + a.nb[2];
+    *tokens = 1;
+    unsigned waste = kThreads;                       // idle threads, relative to the group's work
+    for (unsigned t = 1; t <= 8; ++t) {
+        const unsigned idle = (kThreads - t * per_token % kThreads) % kThreads;
+        if (idle * *tokens < waste * t) *tokens = t, waste = idle;
+    }
+    return dim3(static_cast<unsigned>((a.T + *tokens - 1) / *tokens), (*tokens * per_token + kThreads - 1) / kThreads);
 }
 
 }  // namespace
 
 int launch_cache_append_fp4(const CacheFp4Args &a, cudaStream_t stream) {
-    unsigned grid = 0;
-    const int st = grid_of(a, &grid);
-    if (st != GDA_OK) return st;
-    gda_cache_append_fp4_kernel<<<grid, kThreads, 0, stream>>>(a);
+    unsigned tokens = 0;
+    const dim3 grid = grid_of(a, &tokens);
+    gda_cache_append_fp4_kernel<<<grid, kThreads, 0, stream>>>(a, tokens);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? GDA_OK : record_cuda_error(e);
 }
 
 int launch_cache_read_fp4(const CacheFp4Args &a, cudaStream_t stream) {
-    unsigned grid = 0;
-    const int st = grid_of(a, &grid);
-    if (st != GDA_OK) return st;
-    gda_cache_read_fp4_kernel<<<grid, kThreads, 0, stream>>>(a);
+    unsigned tokens = 0;
+    const dim3 grid = grid_of(a, &tokens);
+    gda_cache_read_fp4_kernel<<<grid, kThreads, 0, stream>>>(a, tokens);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? GDA_OK : record_cuda_error(e);
 }

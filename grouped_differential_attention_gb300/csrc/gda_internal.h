@@ -71,7 +71,7 @@ struct CacheFp4Args {
     const int *slot_map;            // [T], negative: leave the token out
     uint8_t *codes[3], *blocks[3];  // [slots, heads, dim / 2], [slots, heads, dim / 16]
     const float *scale[3];          // [heads]
-    int nb[3], dim[3];              // blocks of 16 elements in a token's row; elements of a head row
+    int nb[3], shift[3];            // blocks of 16 elements in a token's row; log2 of those in a head row
     long long T;
     int slots;
     unsigned *dev_err;
