@@ -45,7 +45,9 @@ namespace {
 
 constexpr int kMaxWarps = 8;        // of a block
 constexpr int kTokens = 16;         // tokens of a block's sine table
-constexpr int kForwardBlocks = 4, kBackwardBlocks = 3;   // of an SM
+// Blocks of an SM: enough copies in flight, and few fronts in memory (prompt of 32768 tokens, 24 + 8 heads: 93 us with
+// 3 and rings of 7 tokens, 101 with 4 and 5, 117 with 2 and 8; gradients, float32: 86 us with 2, 90 with 3).
+constexpr int kForwardBlocks = 3, kBackwardBlocks = 2;
 
 // A warp's head rows of one token in its ring: 256 elements, rows of 64 bf16
 // with a gap of 64 bytes, which puts the two rows that a load of half a warp
@@ -427,7 +429,7 @@ Shape shape_of(const NormRopeArgs &a, int most) {
 
 template <typename T, int D, bool INTER>
 cudaError_t forward(const NormRopeArgs &a, const Shape &s, cudaStream_t stream) {
-    constexpr int RING = sizeof(T) == 2 ? 8 : 5;
+    constexpr int RING = sizeof(T) == 2 ? 7 : 5;
     auto kern = gda_qk_norm_rope_kernel<T, D, INTER, RING>;
     const int warps = s.groups * s.subsets, one = RING * Stage<T, D>::bytes;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxWarps * one);
