@@ -138,6 +138,7 @@ struct Range {
 __device__ __forceinline__ bool range_of(const Params &p, int split, Range &r) {
     const int lane = threadIdx.x & 31;
     long long total = 0;
+#pragma unroll 4
     for (int b = lane; b < p.B; b += 32) total += length_of(p, b);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
@@ -335,17 +336,22 @@ __device__ __forceinline__ V at(const uint8_t *smem) { return *reinterpret_cast<
 template <int D, int RH>
 __device__ __forceinline__ float load_queries(const Params &p, uint8_t *dst, int b, int h0, int g) {
     const int lane = threadIdx.x & 31;
-    float mine = 0.f;
+    float mine = 0.f, scale[RH + 1];
+    uint32_t words[RH + 1][D / 64];                      // all on their way before the first is used
 #pragma unroll
     for (int j = 0; j <= RH; ++j) {
         const __nv_bfloat16 *q = j == RH ? p.q2 + (static_cast<size_t>(b) * p.hn + g) * D
                                          : p.q1 + (static_cast<size_t>(b) * p.hs + h0 + j) * D;
-        uint32_t w[D / 64], most = 0;
+        scale[j] = j == RH ? p.k2_scale[g] : p.k1_scale[h0 + j];
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
-            w[i] = reinterpret_cast<const uint32_t *>(q)[lane + 32 * i];
-            most = max(most, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
-        }
+        for (int i = 0; i < D / 64; ++i) words[j][i] = reinterpret_cast<const uint32_t *>(q)[lane + 32 * i];
+    }
+#pragma unroll
+    for (int j = 0; j <= RH; ++j) {
+        const uint32_t(&w)[D / 64] = words[j];
+        uint32_t most = 0;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) most = max(most, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
         most = __reduce_max_sync(0xffffffffu, most);
         const int up = min(268 - static_cast<int>(most >> 7), 254);       // biased exponent of the factor
         const float f = __uint_as_float(static_cast<uint32_t>(up) << 23);
@@ -354,8 +360,7 @@ __device__ __forceinline__ float load_queries(const Params &p, uint8_t *dst, int
             reinterpret_cast<uint32_t *>(dst + j * D * 2)[lane + 32 * i] =
                 pack_half2(bf16_lo(w[i]) * f, bf16_hi(w[i]) * f);
         const float back = __uint_as_float(static_cast<uint32_t>(254 - up) << 23);
-        const float k = j == RH ? p.k2_scale[g] : p.k1_scale[h0 + j];
-        if ((lane & 3) == j) mine = p.scale_log2 * k * back;
+        if ((lane & 3) == j) mine = p.scale_log2 * scale[j] * back;
     }
     return mine;
 }
@@ -597,96 +602,74 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32, (Tile<D, DV, RH>::blocks)
 }
 
 // grid (h_s, B): joins the parts of one (sequence, head).  DV / 2 threads
-// hold the DV + DV columns of (O1, O2), four each; THREADS / (DV / 2) such
-// groups share the parts, so that a long sequence's several hundred are read
-// in few dependent steps.
+// hold the DV + DV columns of (O1, O2), four each, with the maximum and sum of
+// their map; THREADS / (DV / 2) such groups share the parts, each joining its
+// own as it reads them (a part's statistics and values are fetched together),
+// and are joined with one another at the end.
 template <int DV, int THREADS>
 __global__ void __launch_bounds__(THREADS) gda_decode_fp4_combine_kernel(const Params p) {
-    constexpr int COLS = DV / 2, GROUPS = THREADS / COLS, WARPS = THREADS / 32;
+    constexpr int COLS = DV / 2, GROUPS = THREADS / COLS, HALF = COLS / 2;
     __shared__ float4 sums[GROUPS][COLS];
-    __shared__ float red[WARPS][4];
+    __shared__ float2 stats[GROUPS][2];
     // a programmatic dependent of the split kernel: this wait returns once that grid has completed and its writes are visible
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int h = blockIdx.x, b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int col = threadIdx.x % COLS, group = threadIdx.x / COLS;
+    const bool second = col >= HALF;
     __nv_bfloat16 *out = p.out + (static_cast<size_t>(b) * p.hs + h) * DV;
+    const int2 seg = reinterpret_cast<const int2 *>(p.ws_seg)[b];
     if (length_of(p, b) == 0) {          // no position: the row is zero
         if (threadIdx.x < DV / 2) reinterpret_cast<uint32_t *>(out)[threadIdx.x] = 0u;
         return;
     }
     // ranges c0 .. c1 left a part in slots c + b (clamped so that a damaged workspace cannot send the reads astray)
-    const int c0 = min(max(p.ws_seg[2 * b], 0), p.splits - 1);
-    const int c1 = min(max(p.ws_seg[2 * b + 1], c0), p.splits - 1);
+    const int c0 = min(max(seg.x, 0), p.splits - 1), c1 = min(max(seg.y, c0), p.splits - 1);
     const size_t at0 = (static_cast<size_t>(c0) + b) * p.hs + h;
     const int parts = c1 - c0 + 1;
-    const float4 *ml = reinterpret_cast<const float4 *>(p.ws_ml) + at0;
-    const float4 *o = reinterpret_cast<const float4 *>(p.ws_o) + at0 * COLS;
+    const float2 *ml = reinterpret_cast<const float2 *>(p.ws_ml) + at0 * 2 + second;
+    const float4 *o = reinterpret_cast<const float4 *>(p.ws_o) + at0 * COLS + col;
 
-    // maxima over the parts, then the sums
-    float M1 = -INFINITY, M2 = -INFINITY;
-    for (int c = threadIdx.x; c < parts; c += THREADS) {
-        const float4 s = ml[static_cast<size_t>(c) * p.hs];
-        M1 = fmaxf(M1, s.x);
-        M2 = fmaxf(M2, s.z);
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        M1 = fmaxf(M1, __shfl_xor_sync(0xffffffffu, M1, off));
-        M2 = fmaxf(M2, __shfl_xor_sync(0xffffffffu, M2, off));
-    }
-    if (lane == 0) red[warp][0] = M1, red[warp][1] = M2;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) M1 = fmaxf(M1, red[w][0]), M2 = fmaxf(M2, red[w][1]);
-    float L1 = 0.f, L2 = 0.f;
-    for (int c = threadIdx.x; c < parts; c += THREADS) {
-        const float4 s = ml[static_cast<size_t>(c) * p.hs];
-        L1 = fmaf(s.y, fast_exp2(s.x - M1), L1);
-        L2 = fmaf(s.w, fast_exp2(s.z - M2), L2);
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        L1 += __shfl_xor_sync(0xffffffffu, L1, off);
-        L2 += __shfl_xor_sync(0xffffffffu, L2, off);
-    }
-    if (lane == 0) red[warp][2] = L1, red[warp][3] = L2;
-
-    const int col = threadIdx.x % COLS, group = threadIdx.x / COLS;
-    const bool second = col >= COLS / 2;
-    const float M = second ? M2 : M1;
+    float m = -INFINITY, l = 0.f;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
+#pragma unroll 4
     for (int c = group; c < parts; c += GROUPS) {
         const size_t at = static_cast<size_t>(c) * p.hs;
-        const float4 s = ml[at], v = o[at * COLS + col];
-        const float f = fast_exp2((second ? s.z : s.x) - M);
-        sum.x = fmaf(v.x, f, sum.x);
-        sum.y = fmaf(v.y, f, sum.y);
-        sum.z = fmaf(v.z, f, sum.z);
-        sum.w = fmaf(v.w, f, sum.w);
+        const float2 s = ml[at * 2];
+        const float4 v = o[at * COLS];
+        const float top = fmaxf(m, s.x), f = fast_exp2(m - top), g = fast_exp2(s.x - top);
+        m = top;
+        l = fmaf(s.y, g, l * f);
+        sum.x = fmaf(v.x, g, sum.x * f);
+        sum.y = fmaf(v.y, g, sum.y * f);
+        sum.z = fmaf(v.z, g, sum.z * f);
+        sum.w = fmaf(v.w, g, sum.w * f);
     }
     sums[group][col] = sum;
+    if (col % HALF == 0) stats[group][second] = make_float2(m, l);
     __syncthreads();
-    if (threadIdx.x >= COLS / 2) return;   // whole warps from here on, or one half warp (DV = 64)
-    L1 = L2 = 0.f;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) L1 += red[w][2], L2 += red[w][3];
+    if (threadIdx.x >= HALF) return;       // whole warps from here on, or half a warp (DV = 64)
+    // groups beyond the parts hold (-inf, 0); the first one has at least one part
+    const int used = min(GROUPS, parts);
+    float M1 = -INFINITY, M2 = -INFINITY, L1 = 0.f, L2 = 0.f;
+    for (int g = 0; g < used; ++g) M1 = fmaxf(M1, stats[g][0].x), M2 = fmaxf(M2, stats[g][1].x);
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f), d = a;
-#pragma unroll
-    for (int g = 0; g < GROUPS; ++g) {
-        const float4 x = sums[g][col], y = sums[g][col + COLS / 2];
-        a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
-        d.x += y.x, d.y += y.y, d.z += y.z, d.w += y.w;
+    for (int g = 0; g < used; ++g) {
+        const float f1 = fast_exp2(stats[g][0].x - M1), f2 = fast_exp2(stats[g][1].x - M2);
+        const float4 x = sums[g][col], y = sums[g][col + HALF];
+        L1 = fmaf(stats[g][0].y, f1, L1), L2 = fmaf(stats[g][1].y, f2, L2);
+        a.x = fmaf(x.x, f1, a.x), a.y = fmaf(x.y, f1, a.y), a.z = fmaf(x.z, f1, a.z), a.w = fmaf(x.w, f1, a.w);
+        d.x = fmaf(y.x, f2, d.x), d.y = fmaf(y.y, f2, d.y), d.z = fmaf(y.z, f2, d.z), d.w = fmaf(y.w, f2, d.w);
     }
     const float i1 = 1.f / L1, i2 = p.lambda[h] / L2;
     const float v[4] = {a.x * i1 - d.x * i2, a.y * i1 - d.y * i2, a.z * i1 - d.z * i2, a.w * i1 - d.w * i2};
     float ss = v[0] * v[0] + v[1] * v[1] + v[2] * v[2] + v[3] * v[3];
-    constexpr unsigned mask = COLS / 2 >= 32 ? 0xffffffffu : 0xffffu;
+    constexpr unsigned mask = HALF >= 32 ? 0xffffffffu : 0xffffu;
 #pragma unroll
-    for (int off = (COLS / 2 >= 32 ? 32 : COLS / 2) / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(mask, ss, off);
-    if constexpr (COLS / 2 > 32) {         // DV = 256: two warps
+    for (int off = (HALF >= 32 ? 32 : HALF) / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(mask, ss, off);
+    if constexpr (HALF > 32) {             // DV = 256: two warps
         __shared__ float both[2];
         if (lane == 0) both[warp] = ss;
-        named_bar_sync(1, COLS / 2);
+        named_bar_sync(1, HALF);
         ss = both[0] + both[1];
     }
     const float y = (1.f - p.lambda_init) * rsqrtf(ss * (1.f / DV) + p.eps);
@@ -708,10 +691,15 @@ cudaError_t launch_combine(const Params &p, cudaStream_t stream) {
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
-// Few sequences have many parts each: 1024 threads a row then, else 256.
+// The fewer the rows, the more parts each has and the more threads an SM can
+// give it.  us with 256 / 512 / 1024 threads: 24 rows of 450 parts 31.7 / 18.3
+// / 9.9, of 12 parts 5.7 / 5.8 / 5.2; 256 rows 9.2 / 6.6 / 8.6; 768 rows 6.8 /
+// 8.8 / 14.4.  So 1024 up to a row an SM, 512 up to two, 256 beyond.
 template <int DV>
 cudaError_t launch_combine(const Params &p, cudaStream_t stream) {
-    return p.splits > 16 * p.B ? launch_combine<DV, 1024>(p, stream) : launch_combine<DV, 256>(p, stream);
+    const int rows = p.hs * p.B;
+    if (rows <= kSms) return launch_combine<DV, 1024>(p, stream);
+    return rows <= 2 * kSms ? launch_combine<DV, 512>(p, stream) : launch_combine<DV, 256>(p, stream);
 }
 
 template <int D, int DV, int RH>
