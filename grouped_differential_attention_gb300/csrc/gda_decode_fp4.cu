@@ -33,6 +33,14 @@
 // too, after a power of two; a weight times a scale is rounded to 11 bits.
 // The weights are 2^7 exp2(score - maximum) so that a small one times a small
 // scale stays clear of f16's end; numerator and denominator share the factor.
+//
+// Measured (both kernels; of the 6781 GB/s of a copy): 64 sequences of 4096 to
+// 8192, 12 + 4 heads of 64/128, 566 MB: 123 us (68 %); one of 131072, 24 + 8
+// heads, 378 MB: 97 us (57 %); 16 of up to 8191, 16 + 4 heads of 128/256,
+// 245 MB: 65 us (56 %).  Of the first one's 117 us in the split kernel the
+// copies alone take 98 and the arithmetic alone 92 (67.5 M warp instructions,
+// 12 warps an SM); they overlap but for the start (a cold first tile arrives
+// after 10 us) and the slowest warps, 10 % behind the mean.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <algorithm>
