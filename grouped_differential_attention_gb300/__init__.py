@@ -24,7 +24,6 @@ positions of a serving step), and a 4-bit cache (``gda_cache_append_fp4``,
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 import threading
 
@@ -642,6 +641,13 @@ def _enqueue(entry, what, device, *args):
         raise GDAError(rc, what)
 
 
+def _int32(**sizes):
+    """Refuses sizes that a C int does not hold (ctypes would pass their low 32 bits)."""
+    for name, value in sizes.items():
+        if not -0x80000000 <= value <= 0x7fffffff:
+            raise ValueError(f"{name} = {value} does not fit 32 bits")
+
+
 def _workspace(workspace, need, device):
     if workspace is None:
         return torch.empty((max(need, 16),), dtype=torch.uint8, device=device)
@@ -739,8 +745,8 @@ def gda_qk_norm_rope(q_sig, k_sig, q_noise, k_noise, weight, positions, inv_freq
     return tuple(out)
 
 
-@functools.lru_cache(maxsize=64)
 def gda_qk_norm_rope_bwd_workspace_size(T: int, h_s: int, h_n: int, d: int) -> int:
+    _int32(T=T, h_s=h_s, h_n=h_n, d=d)
     return int(_load().gda_qk_norm_rope_bwd_workspace_size(T, h_s, h_n, d))
 
 
@@ -798,6 +804,7 @@ def gda_block_tables(cache_lens, new_lens, block_table, free_pages, free_count, 
     i32 = torch.int32
     B, max_pages = block_table.shape
     free = free_pages.numel()
+    _int32(page_size=page_size, num_pages=num_pages, max_rows=max_rows, free_pages=free, max_pages=max_pages)
     _expect_all(dev, (cache_lens, "cache_lens", i32, (B,)), (new_lens, "new_lens", i32, (B,)),
                 (block_table, "block_table", i32, (B, max_pages)), (free_pages, "free_pages", i32, (free,)),
                 (free_count, "free_count", i32, (1,)))
@@ -892,8 +899,8 @@ def gda_cache_read_fp4(slot_map, k_sig_pool, k_noise_pool, v_pool, k_sig_block_s
     return tuple(out)
 
 
-@functools.lru_cache(maxsize=64)
 def gda_attn_decode_fp4_workspace_size(B: int, h_s: int, h_n: int, d: int, dv: int) -> int:
+    _int32(B=B, h_s=h_s, h_n=h_n, d=d, dv=dv)
     return int(_load().gda_attn_decode_fp4_workspace_size(B, h_s, h_n, d, dv))
 
 

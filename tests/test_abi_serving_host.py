@@ -125,6 +125,9 @@ def test_decode_refuses(lib, call):
         assert call(lib, **bad) == INVALID
     for bad in (dict(d=96), dict(dv=96), dict(hs=128, hn=1), dict(B=65536)):
         assert call(lib, **bad) == UNSUPPORTED
+    for bad in (dict(Lcap=0x7ffffff1), dict(Lcap=0x7fffffff), dict(Lcap=(1 << 30) + 16, B=32)):   # positions of 32 bits
+        args = dict(bad, ps=bad["Lcap"], Lcap=16) if call is paged else bad                       # one page each
+        assert call(lib, **args) == UNSUPPORTED
     assert call(lib, ws=None) == WORKSPACE and call(lib, ws=A + 8) == WORKSPACE
     need = lib.gda_attn_decode_fp4_workspace_size(4, 6, 2, 64, 128)
     assert need > 0 and call(lib, ws_bytes=need - 1) == WORKSPACE
@@ -135,6 +138,28 @@ def test_decode_refuses(lib, call):
 def test_paged_decode_refuses_tables(lib):
     assert paged(lib, table=None) == INVALID and paged(lib, table=A + 2) == MISALIGNED
     assert paged(lib, ps=0) == INVALID and paged(lib, pages=0) == INVALID and paged(lib, ps=1 << 30, Lcap=64) == INVALID
+
+
+def test_ranges_of_the_longest_batch_fit_32_bits(lib):
+    """The decode counts a range's positions in 32 bits: the fewest ranges of any supported shape against the most
+    positions.  The workspace has (ranges + B) slots of h_s (2 dv + 4) floats, so its size gives the ranges."""
+    fewest = 1 << 30
+    for dv in (64, 128, 256):
+        for hn in range(1, 65):
+            for hs in range(hn, 129 - hn, hn):
+                slots = lib.gda_attn_decode_fp4_workspace_size(1, hs, hn, 64, dv) / (4 * hs * (2 * dv + 4))
+                fewest = min(fewest, int(slots) - 1)
+    assert fewest >= 19 - 1 and (1 << 35) / 18 + 16 < 1 << 31
+
+
+def test_sizes_past_32_bits_are_refused_by_the_binding(lib):
+    import grouped_differential_attention_gb300 as gda
+    for big in (1 << 31, (1 << 32) + 4, -(1 << 32) + 4):
+        with pytest.raises(ValueError):
+            gda.gda_attn_decode_fp4_workspace_size(big, 6, 2, 64, 128)
+        with pytest.raises(ValueError):
+            gda.gda_qk_norm_rope_bwd_workspace_size(big, 6, 2, 64)
+    assert gda.gda_attn_decode_fp4_workspace_size(0, 6, 2, 64, 128) == 0
 
 
 def test_binding_refuses_host_tensors():

@@ -131,3 +131,6 @@ def test_binding_refuses():
         gda.gda_block_tables(*a, 0, 4, 8)
     with pytest.raises(gda.GDAError):
         gda.gda_block_tables(*a, 1 << 30, 4, 8)                       # slots pass 31 bits
+    for sizes in ((1 << 32) + 16, 4, 8), (16, (1 << 32) + 4, 8), (16, 4, (1 << 32) + 8):
+        with pytest.raises(ValueError):                               # not their low 32 bits
+            gda.gda_block_tables(*a, *sizes)
