@@ -35,12 +35,12 @@
 // scale stays clear of f16's end; numerator and denominator share the factor.
 //
 // Measured (both kernels; of the 6781 GB/s of a copy): 64 sequences of 4096 to
-// 8192, 12 + 4 heads of 64/128, 566 MB: 123 us (68 %); one of 131072, 24 + 8
-// heads, 378 MB: 97 us (57 %); 16 of up to 8191, 16 + 4 heads of 128/256,
-// 245 MB: 65 us (56 %).  Of the first one's 117 us in the split kernel the
-// copies alone take 98 and the arithmetic alone 92 (67.5 M warp instructions,
-// 12 warps an SM); they overlap but for the start (a cold first tile arrives
-// after 10 us) and the slowest warps, 10 % behind the mean.
+// 8192, 12 + 4 heads of 64/128, 566 MB: 119 us (70 %); one of 131072, 24 + 8
+// heads, 378 MB: 94 us (59 %); 16 of up to 8191, 16 + 4 heads of 128/256,
+// 245 MB: 65 us (56 %).  Of the first one's 114 us in the split kernel the
+// copies alone take 98 and the arithmetic alone 90 (67 M warp instructions);
+// they overlap but for the start (a cold first tile arrives after several us)
+// and the slowest warps, 10 % behind the mean.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <algorithm>
@@ -57,12 +57,16 @@ namespace {
 
 constexpr int kWarpsPerBlock = 4;
 constexpr int kTile = 16;              // positions of a tile
-constexpr int kMinRange = 32;          // fewest positions of a range
+// Fewest positions of a range: a tile.  4 sequences of 37 to 600, both kernels: 15 us, with 32 15.5, 64 17.2, 128 22.7.
+constexpr int kMinRange = 16;
 constexpr int kSms = 152;              // SMs that the plan counts on
 constexpr float kWeightBits = 7.f;     // weights carry a factor 2^7
 
-// Signal heads of a warp: a noise head's group in parts of at most
-// three (two where the accumulators of three would not fit the registers).
+// Signal heads of a warp: a noise head's group in parts of at most three (two
+// where the accumulators of three would not fit the registers).  Fewer read
+// the noise head again and repeat its arithmetic: groups of three at dv = 128,
+// split kernel, 114 us against 158 in parts of one or of two and one; groups
+// of four at dv = 256, 59 us against 69 in parts of one.
 struct Heads {
     int parts, each;   // parts of a group; signal heads of the largest part
 };
@@ -75,9 +79,13 @@ Heads heads_of(int hs, int hn, int dv) {
 }
 
 // Blocks that share an SM, by the accumulator registers of a thread (DV / 4
-// for each signal head): as many as leave room for those and about 70 more.
+// for each signal head).  us in the split kernel, this many / one more, 64
+// sequences of 4096 to 8192, 4 noise heads of 64/128: one signal head each
+// 57.7 / 60.5, two 83 / 87.6, three 114 / 117 (a warp more on each scheduler
+// costs ring depth; 9 or 10 warps an SM, unevenly spread, 140 to 160).
+// Fewer: two heads 90, one 58.5; 128/256, two heads, 82 against 59.
 __host__ __device__ constexpr int blocks_per_sm(int rh, int dv) {
-    return rh * dv / 4 <= 32 ? 5 : (rh * dv / 4 <= 64 ? 4 : (rh * dv / 4 <= 96 ? 3 : 2));
+    return rh * dv / 4 <= 32 ? 4 : (rh * dv / 4 <= 64 ? 3 : 2);
 }
 
 struct Fp4Plan {
