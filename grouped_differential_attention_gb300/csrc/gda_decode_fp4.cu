@@ -35,9 +35,9 @@
 // scale stays clear of f16's end; numerator and denominator share the factor.
 //
 // Measured (both kernels; of the 6781 GB/s of a copy): 64 sequences of 4096 to
-// 8192, 12 + 4 heads of 64/128, 566 MB: 119 us (70 %); one of 131072, 24 + 8
-// heads, 378 MB: 94 us (59 %); 16 of up to 8191, 16 + 4 heads of 128/256,
-// 245 MB: 65 us (56 %).  Of the first one's 114 us in the split kernel the
+// 8192, 12 + 4 heads of 64/128, 566 MB: 114 us (73 %); one of 131072, 24 + 8
+// heads, 378 MB: 89 us (62 %); 16 of up to 8191, 16 + 4 heads of 128/256,
+// 245 MB: 63 us (57 %).  Of the first one's 108 us in the split kernel the
 // copies alone take 98 and the arithmetic alone 90 (67 M warp instructions);
 // they overlap but for the start (a cold first tile arrives after several us)
 // and the slowest warps, 10 % behind the mean.
@@ -57,7 +57,8 @@ namespace {
 
 constexpr int kWarpsPerBlock = 4;
 constexpr int kTile = 16;              // positions of a tile
-// Fewest positions of a range: a tile.  4 sequences of 37 to 600, both kernels: 15 us, with 32 15.5, 64 17.2, 128 22.7.
+// Fewest positions of a range: a tile.  4 sequences of 37 to 600, us of both kernels: 15 with 16, 15.5 with 32, 17.2 with
+// 64, 22.7 with 128.
 constexpr int kMinRange = 16;
 constexpr int kSms = 152;              // SMs that the plan counts on
 constexpr float kWeightBits = 7.f;     // weights carry a factor 2^7
@@ -65,8 +66,8 @@ constexpr float kWeightBits = 7.f;     // weights carry a factor 2^7
 // Signal heads of a warp: a noise head's group in parts of at most three (two
 // where the accumulators of three would not fit the registers).  Fewer read
 // the noise head again and repeat its arithmetic: groups of three at dv = 128,
-// split kernel, 114 us against 158 in parts of one or of two and one; groups
-// of four at dv = 256, 59 us against 69 in parts of one.
+// split kernel, 108 us against 146 in parts of two and one; groups of four at
+// dv = 256, 58 us against 67 in parts of one.
 struct Heads {
     int parts, each;   // parts of a group; signal heads of the largest part
 };
@@ -81,9 +82,9 @@ Heads heads_of(int hs, int hn, int dv) {
 // Blocks that share an SM, by the accumulator registers of a thread (DV / 4
 // for each signal head).  us in the split kernel, this many / one more, 64
 // sequences of 4096 to 8192, 4 noise heads of 64/128: one signal head each
-// 57.7 / 60.5, two 83 / 87.6, three 114 / 117 (a warp more on each scheduler
-// costs ring depth; 9 or 10 warps an SM, unevenly spread, 140 to 160).
-// Fewer: two heads 90, one 58.5; 128/256, two heads, 82 against 59.
+// 55.5 / 58.5, two 80 / 87.5, three 108 / 117 (one more costs ring depth and
+// registers; one fewer: 56, 84.5; 9 or 10 warps an SM, unevenly spread over
+// its four schedulers, 140 to 160; 128/256, two heads, one block: 82 against 59).
 __host__ __device__ constexpr int blocks_per_sm(int rh, int dv) {
     return rh * dv / 4 <= 32 ? 4 : (rh * dv / 4 <= 64 ? 3 : 2);
 }
@@ -437,7 +438,7 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32, (Tile<D, DV, RH>::blocks)
         if (get.left > 0) next_sequence(p, get); else more = false;
     };
     find();
-    int to = 0, from = 0, ahead = S - 1;                 // places of the ring; tiles to copy before the first is used
+    int to = 0, from = 0, ahead = S - 2;                 // places of the ring; tiles to copy before the first is used
     // lane parts of places in shared memory
     const uint8_t *const qa0 = quad == (D == 64 ? t : 2 * t) ? queries + t * (D / 2) : zeros;
     const uint8_t *const qa1 = quad == 2 * t + 1 ? queries + t * (D / 2) + 32 : zeros;   // D = 128: the second block
@@ -456,25 +457,10 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32, (Tile<D, DV, RH>::blocks)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) acc[j][s][i][k] = 0.f;
 
-    for (;;) {
-        __syncwarp();                                    // the readers of place `to` are done
-        if (more) {
-            issue_tile<D, DV, RH>(p, smem_u32(ring) + to * T::bytes, row, n, h0, g);
-            step();
-            if (more) find();
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        to = to + 1 == S ? 0 : to + 1;
-        if (ahead > 0) {
-            --ahead;
-            continue;
-        }
-        asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
-        __syncwarp();                                    // every lane's copies of this tile have landed
-        const uint8_t *const tile = ring + from * T::bytes;
-        from = from + 1 == S ? 0 : from + 1;
-
-        // ---- scores: lane (quad, t) ends up with positions quad, quad + 8 of head t
+    uint32_t weights = 0;                                // of head t in the tile whose values are added next
+    float scale = 1.f;                                   // of what was added before them
+    auto scores_of = [&](const uint8_t *const tile, uint32_t &next) {
+        // lane (quad, t) ends up with positions quad, quad + 8 of head t
         float x0[4] = {}, x1[4] = {};
 #pragma unroll
         for (int j = 0; j < NH; ++j) {
@@ -508,11 +494,13 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32, (Tile<D, DV, RH>::blocks)
         float mt = max3f(m, sc0, sc1);
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
-        const float scale = fast_exp2(m - mt);           // m = -inf gives 0
+        scale = fast_exp2(m - mt);                       // m = -inf gives 0
         const float p0 = fast_exp2(sc0 - mt + kWeightBits), p1 = fast_exp2(sc1 - mt + kWeightBits);
         m = mt;
         l = fmaf(l, scale, p0 + p1);
-        const uint32_t weights = pack_half2(p0, p1);
+        next = pack_half2(p0, p1);
+    };
+    auto rescale = [&]() {
         if (__any_sync(0xffffffffu, scale != 1.f)) {
             const float sn = __shfl_sync(0xffffffffu, scale, RH);
 #pragma unroll
@@ -527,8 +515,9 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32, (Tile<D, DV, RH>::blocks)
                     }
             }
         }
-
-        // ---- values: k slots (2t, 2t + 1) are positions 2t, 2t + 8 and (2t + 8, 2t + 9) are 2t + 1, 2t + 9;
+    };
+    auto values_of = [&](const uint8_t *const tile) {
+        // k slots (2t, 2t + 1) are positions 2t, 2t + 8 and (2t + 8, 2t + 9) are 2t + 1, 2t + 9;
         // column 2 n + map, n the block within the slab; row `quad` of tile i is dim 8 quad + 2 i, row quad + 8 the next
         const uint32_t pick = 0x40u + 0x11u * (quad >> 1);   // byte of block quad / 2 from either word
 #pragma unroll
@@ -573,9 +562,43 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32, (Tile<D, DV, RH>::blocks)
                 for (int i = 0; i < 4; ++i) mma_16816(acc[j][s][i], a0[i], a1[i], a2[i], a3[i], b0, b1, acc[j][s][i]);
             }
         }
-
+    };
+    // The scores of a tile come with the values of the one before it, in one run of instructions without a branch: the
+    // chain from scores to weights then has other work beside it (64 sequences, split kernel: 114 -> 108 us).
+    const uint8_t *before = ring;                        // the tile whose values are still to be added
+    bool fresh = true;                                   // there is none: a part begins
+    for (;;) {
+        __syncwarp();                                    // the readers of place `to` are done
+        if (more) {
+            issue_tile<D, DV, RH>(p, smem_u32(ring) + to * T::bytes, row, n, h0, g);
+            step();
+            if (more) find();
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        to = to + 1 == S ? 0 : to + 1;
+        if (ahead > 0) {
+            --ahead;
+            continue;
+        }
+        asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+        __syncwarp();                                    // every lane's copies of this tile have landed
+        const uint8_t *const tile = ring + from * T::bytes;
+        from = from + 1 == S ? 0 : from + 1;
+        uint32_t next;
+        if (fresh) {
+            scores_of(tile, next);
+            fresh = false;
+        } else {                                         // twice, so that these two are not parted by the test
+            scores_of(tile, next);
+            values_of(before);
+            rescale();
+        }
+        weights = next;
+        before = tile;
         use.pos += kTile;
         if (use.pos < use.hi) continue;
+        values_of(before);
+        fresh = true;
 
         // ---- end of the part that lies in sequence use.b
 #pragma unroll
