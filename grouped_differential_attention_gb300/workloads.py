@@ -197,6 +197,18 @@ def make_decode_inputs_fp8(w: DecodeWorkload, **overrides):
     return q1, q2, k1q, k2q, vq, k1s, k2s, vs, lens, lam
 
 
+def empty_fp4_cache(pages: int, page_size: int, h_s: int, h_n: int, d: int, dv: int, device):
+    """A zeroed 4-bit cache with head scales of 1: the nine tensors in the order the entry points take them.
+
+    (k_sig, k_noise, v) codes [pages, page_size, heads, dim / 2], the three
+    block scales [.., dim / 16] and head scales [heads].
+    """
+    dims = ((h_s, d), (h_n, d), (h_s, dv))
+    codes = [torch.zeros(pages, page_size, h, n // 2, dtype=torch.uint8, device=device) for h, n in dims]
+    blocks = [torch.zeros(pages, page_size, h, n // 16, dtype=torch.uint8, device=device) for h, n in dims]
+    return (*codes, *blocks, *(torch.ones(h, dtype=torch.float32, device=device) for h, _ in dims))
+
+
 def page_caches(k1c, k2c, vc, page_size: int, seed: int = 0, spare_pages: int = 3):
     """Scatter contiguous caches [B, Lcap, heads, dim] into page pools.
 
