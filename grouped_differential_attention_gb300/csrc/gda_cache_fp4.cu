@@ -14,7 +14,7 @@
 // consecutive bf16 whatever the head layout.  Memory-bound: 2.5625 bytes an
 // element in each direction.  8192 tokens of 12 + 4 heads of 64/128, 53.7 MB:
 // 12.5 us to write the cache, 13.3 to read it (kernels alone, cold; 7.9 at
-// the copy rate of 6781 GB/s, the rest is the launch and the ramp at both
+// the copy rate of 6793 GB/s, the rest is the launch and the ramp at both
 // ends); 64 tokens 3.6 and 3.4.  Two or four blocks to a thread, or threads in
 // blocks of 128 or 512, are no faster (12.5 to 15.7, and 4 to 5.5 for 64).
 #include <cuda_bf16.h>

@@ -32,7 +32,7 @@
 // the copy rate half used.  The grid is as many blocks as the SMs hold at a
 // time, each with an equal run of tokens.
 //
-// Measured, of the 6781 GB/s of a copy: 32768 tokens, 24 + 8 heads of 64,
+// Measured, of the 6793 GB/s of a copy: 32768 tokens, 24 + 8 heads of 64,
 // bf16, 537 MB: 93 us (85 %); gradients of 8190 tokens, 16 + 4 heads of 128,
 // float32, 503 MB: 86 us (86 %); of 8192 tokens, 12 + 4 heads of 64, bf16, 134
 // MB: 24 us and 4 for the sum of dw (70 % together); 64 tokens: 4 us.
