@@ -731,9 +731,9 @@ cudaError_t launch_combine(const Params &p, cudaStream_t stream) {
 }
 
 // The fewer the rows, the more parts each has and the more threads an SM can
-// give it.  us with 256 / 512 / 1024 threads: 24 rows of 450 parts 31.7 / 18.3
-// / 9.9, of 12 parts 5.7 / 5.8 / 5.2; 256 rows 9.2 / 6.6 / 8.6; 768 rows 6.8 /
-// 8.8 / 14.4.  So 1024 up to a row an SM, 512 up to two, 256 beyond.
+// give it.  us with 256 / 512 / 1024 threads: 24 rows of 152 parts 22.6 / 15.0
+// / 8.1, of up to 38 8.3 / 6.8 / 5.8; 256 rows 9.2 / 6.7 / 8.5; 768 rows 5.8 /
+// 7.6 / 13.6.  So 1024 up to a row an SM, 512 up to two, 256 beyond.
 template <int DV>
 cudaError_t launch_combine(const Params &p, cudaStream_t stream) {
     const int rows = p.hs * p.B;
