@@ -96,6 +96,16 @@ def test_slots_past_the_pool_are_left_out_and_reported():
     assert all((t[3] == 0).all() and (t[4] != 0).any() for t in back)
 
 
+def test_a_slot_read_twice():
+    rows, slots, pools, blocks, scales = make(6, 3, 1, 64, 128, 4, seed=2)
+    cache = [t.cuda() for t in (*pools, *blocks, *scales)]
+    gda.gda_cache_append_fp4(*(t.cuda() for t in rows), slots.cuda(), *cache)
+    once = gda.gda_cache_read_fp4(slots.cuda(), *cache)
+    order = [3, 3, 0, 5, 3]
+    for a, b in zip(gda.gda_cache_read_fp4(slots[order].cuda(), *cache), once):
+        assert torch.equal(a, b[order])
+
+
 def test_rows_out_of_a_fused_projection_on_another_stream():
     hs, hn, d, dv, T = 6, 2, 64, 128, 50
     g = torch.Generator().manual_seed(2)

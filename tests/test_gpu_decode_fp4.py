@@ -217,6 +217,61 @@ def test_two_graphs_and_another_stream():
     check(graphs[0][1], c)
 
 
+@pytest.mark.parametrize("hs,hn,d,dv", [(120, 8, 64, 128), (96, 32, 128, 256), (64, 64, 64, 64), (127, 1, 64, 128),
+                                        (21, 3, 128, 64)])
+def test_many_heads(hs, hn, d, dv):
+    c = make(3, 130, hs, hn, d, dv, [130, 0, 77], seed=hs, page=32)
+    check(run(c), c)
+
+
+def test_a_batch_of_many_more_sequences_than_ranges():
+    c = make(3000, 20, 2, 1, 64, 64, [b % 21 for b in range(3000)], seed=15, page=10)
+    check(run(c), c)
+
+
+def test_sequences_that_share_pages():
+    c = make(3, 96, 6, 2, 64, 128, [96, 70, 33], seed=13, page=32)
+    c["table"][1, 0], c["table"][2] = c["table"][0, 0], c["table"][0]
+    check(run(c), c)
+    c["table"][0, 1:] = c["table"][0, 0]                               # one page three times in a sequence
+    check(run(c), c)
+
+
+def test_codes_and_scales_in_their_own_types():
+    c = make(2, 64, 3, 1, 64, 128, [64, 9], seed=14)
+    typed = dict(c, blocks=[t.view(torch.float8_e4m3fn) for t in c["blocks"]])
+    if hasattr(torch, "float4_e2m1fn_x2"):
+        typed["pools"] = [t.view(torch.float4_e2m1fn_x2) for t in c["pools"]]
+    assert torch.equal(run(typed), run(c))
+
+
+def test_a_nan_in_a_query_stays_with_its_heads():
+    c = make(3, 100, 6, 2, 64, 128, [100, 50, 7], seed=16)
+    ref = run(c)
+    c["q1"][1, 2, 5] = float("nan")
+    c["q2"][2, 1, 0] = float("inf")                                    # heads 3 .. 5 share it
+    out = run(c)
+    assert torch.isnan(out[1, 2]).all() and torch.isnan(out[2, 3:]).all()
+    same = torch.ones(3, 6, dtype=torch.bool, device="cuda")
+    same[1, 2], same[2, 3:] = False, False
+    assert torch.equal(out[same], ref[same])
+
+
+def test_calls_on_two_streams_at_once():
+    cs = [make(5, 900, 6, 2, 64, 128, [900, 20 * i, 1, 333, 512], seed=17 + i, page=16) for i in range(2)]
+    refs = [run(c) for c in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(20):
+        for c, s, o in zip(cs, streams, outs):
+            with torch.cuda.stream(s):
+                o.append(run(c))
+    torch.cuda.synchronize()
+    for ref, o in zip(refs, outs):
+        assert all(torch.equal(x, ref) for x in o)
+
+
 def test_the_serving_batch():
     c = make(64, 8192, 12, 4, 64, 128, [4096 + 65 * b for b in range(64)], seed=11)
     check(run(c), c)

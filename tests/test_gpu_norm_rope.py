@@ -63,6 +63,8 @@ CASES = [  # tokens, h_s, h_n, d, rot, dtype, far, interleaved, fused
     ((1, 777), 12, 4, 64, 16, "f32", (1 << 31) - 1, False, True),
     ((4, 1000), 2, 1, 64, 64, "f32", (1 << 24) + 9, True, False),
     ((5003,), 1, 1, 128, 64, "bf16", 0, False, False),
+    ((3,), 768, 256, 64, 64, "bf16", 0, False, True),       # as many heads as there may be
+    ((2, 5), 1000, 8, 128, 16, "f32", 0, True, False),
 ]
 
 
