@@ -63,19 +63,26 @@ constexpr int kMinRange = 16;
 constexpr int kSms = 152;              // SMs that the plan counts on
 constexpr float kWeightBits = 7.f;     // weights carry a factor 2^7
 
-// Signal heads of a warp: a noise head's group in parts of at most three (two
-// where the accumulators of three would not fit the registers).  Fewer read
-// the noise head again and repeat its arithmetic: groups of three at dv = 128,
-// split kernel, 108 us against 146 in parts of two and one; groups of four at
-// dv = 256, 58 us against 67 in parts of one.
+// Signal heads of a warp: a noise head's group in equal parts of at most three
+// (two at dv = 256, where the accumulators of three would not fit the
+// registers).  Every part reads and scores the noise head for itself, and where
+// the parts do not divide the group the last one does a head again, so a part
+// costs about its heads and one more; the fewest of those are taken, of as many
+// the smaller parts.  us in the split kernel, 64 sequences of 4096 to 8192, 4
+// noise heads of 64/128: groups of three as 3 108, as 2 + 1 146; of four as 2 +
+// 2 160, as ones 195; of five as 3 + 3 207, as 2 + 2 + 2 218; of seven as three
+// of 3 309, as four of 2 298.  16 sequences, 4 noise heads of 128/256: groups
+// of three as 2 + 2 55, as ones 52.5; of four as 2 + 2 58, as ones 67.
 struct Heads {
-    int parts, each;   // parts of a group; signal heads of the largest part
+    int parts, each;   // parts of a group; signal heads of a part
 };
 Heads heads_of(int hs, int hn, int dv) {
     const int r = hs / hn, most = dv == 256 ? 2 : 3;
-    Heads h;
-    h.parts = (r + most - 1) / most;
-    h.each = (r + h.parts - 1) / h.parts;
+    Heads h{r, 1};
+    for (int each = 2; each <= most && each <= r; ++each) {
+        const int parts = (r + each - 1) / each;
+        if (parts * (each + 1) < h.parts * (h.each + 1)) h = {parts, each};
+    }
     return h;
 }
 
@@ -272,7 +279,7 @@ struct Tile {
     static constexpr int room = (227 * 1024 / blocks - 1024 - queries) / kWarpsPerBlock;
     static constexpr int fit = (room - queries) / bytes;
     static constexpr int ring = fit > 6 ? 6 : fit;       // tiles of the ring
-    static_assert(ring >= 2, "a tile must be copied while another is used");
+    static_assert(ring >= 3, "a tile must be copied while two others are used");
     static constexpr int warp_bytes = ring * bytes + queries;
 };
 
