@@ -5,8 +5,8 @@
 // The batch's cache positions, concatenated sequence after sequence, are cut
 // into equal contiguous ranges.  A warp takes one range for one noise head
 // and up to RH signal heads that share it, on its own: it copies 16 positions
-// at a time into a ring of its own in shared memory (cp.async, RING - 1 tiles
-// ahead, so no thread of another warp is ever waited for), and keeps the
+// at a time into a ring of its own in shared memory (cp.async, one to four
+// tiles ahead, so no thread of another warp is ever waited for), and keeps the
 // online softmax of all its maps and the accumulators O1, O2 in registers.
 // Each part of a range that lies in one sequence leaves (m, l) of both maps
 // and (O1, O2) in workspace slot (range + sequence), which is unique because
@@ -92,8 +92,23 @@ Heads heads_of(int hs, int hn, int dv) {
 // 55.5 / 58.5, two 80 / 87.5, three 108 / 117 (one more costs ring depth and
 // registers; one fewer: 56, 84.5; 9 or 10 warps an SM, unevenly spread over
 // its four schedulers, 140 to 160; 128/256, two heads, one block: 82 against 59).
-__host__ __device__ constexpr int blocks_per_sm(int rh, int dv) {
-    return rh * dv / 4 <= 32 ? 4 : (rh * dv / 4 <= 64 ? 3 : 2);
+// And as few as leave each warp a ring of kMinRing tiles.
+constexpr int kMinRing = 3, kMaxRing = 6;
+
+// Bytes of shared memory of 16 positions: codes and block scales of rh + 1 rows of K and rh of V.
+__host__ __device__ constexpr int tile_bytes(int rh, int d, int dv) {
+    return kTile * ((rh + 1) * (d / 2 + d / 16) + rh * (dv / 2 + dv / 16));
+}
+// Tiles of a warp's ring; a block also has the f16 queries of its warps and as many zeros as those of one.
+__host__ __device__ constexpr int ring_of(int blocks, int rh, int d, int dv) {
+    const int queries = (rh + 1) * d * 2;
+    const int fit = ((227 * 1024 / blocks - 1024 - queries) / kWarpsPerBlock - queries) / tile_bytes(rh, d, dv);
+    return fit > kMaxRing ? kMaxRing : fit;
+}
+__host__ __device__ constexpr int blocks_per_sm(int rh, int d, int dv) {
+    int blocks = rh * dv / 4 <= 32 ? 4 : (rh * dv / 4 <= 64 ? 3 : 2);
+    while (blocks > 1 && ring_of(blocks, rh, d, dv) < kMinRing) --blocks;
+    return blocks;
 }
 
 struct Fp4Plan {
@@ -102,10 +117,10 @@ struct Fp4Plan {
     size_t ml_at, seg_at, bytes;
 };
 
-Fp4Plan plan_of(int B, int hs, int hn, int dv) {
+Fp4Plan plan_of(int B, int hs, int hn, int d, int dv) {
     Fp4Plan p;
     p.heads = heads_of(hs, hn, dv);
-    p.splits = std::max(1, kSms * blocks_per_sm(p.heads.each, dv) * kWarpsPerBlock / (hn * p.heads.parts));
+    p.splits = std::max(1, kSms * blocks_per_sm(p.heads.each, d, dv) * kWarpsPerBlock / (hn * p.heads.parts));
     const size_t slots = static_cast<size_t>(p.splits) + B;
     p.ml_at = (slots * hs * 2 * dv * sizeof(float) + 255) / 256 * 256;
     p.seg_at = p.ml_at + (slots * hs * 4 * sizeof(float) + 255) / 256 * 256;
@@ -273,12 +288,11 @@ struct Tile {
     static constexpr int v_codes = k_codes + NH * kTile * KC;
     static constexpr int k_scales = v_codes + RH * kTile * VC;
     static constexpr int v_scales = k_scales + NH * kTile * KS;
-    static constexpr int bytes = (v_scales + RH * kTile * VS + 15) / 16 * 16;
+    static constexpr int bytes = v_scales + RH * kTile * VS;
+    static_assert(bytes == tile_bytes(RH, D, DV) && bytes % 16 == 0, "tiles follow one another");
     static constexpr int queries = NH * D * 2;           // f16; a block has as many bytes of zeros once more
-    static constexpr int blocks = blocks_per_sm(RH, DV);
-    static constexpr int room = (227 * 1024 / blocks - 1024 - queries) / kWarpsPerBlock;
-    static constexpr int fit = (room - queries) / bytes;
-    static constexpr int ring = fit > 6 ? 6 : fit;       // tiles of the ring
+    static constexpr int blocks = blocks_per_sm(RH, D, DV);
+    static constexpr int ring = ring_of(blocks, RH, D, DV);   // tiles of the ring
     static_assert(ring >= 3, "a tile must be copied while two others are used");
     static constexpr int warp_bytes = ring * bytes + queries;
 };
@@ -771,12 +785,11 @@ cudaError_t launch_split(const Params &p, int rh, cudaStream_t stream) {
 }  // namespace
 
 size_t decode_fp4_workspace_bytes(int B, int hs, int hn, int d, int dv) {
-    (void)d;
-    return plan_of(B, hs, hn, dv).bytes;
+    return plan_of(B, hs, hn, d, dv).bytes;
 }
 
 int launch_decode_fp4(const DecodeFp4Args &a, cudaStream_t stream) {
-    const Fp4Plan pl = plan_of(a.B, a.hs, a.hn, a.dv);
+    const Fp4Plan pl = plan_of(a.B, a.hs, a.hn, a.d, a.dv);
     char *ws = static_cast<char *>(a.workspace);
     const Params p{static_cast<const __nv_bfloat16 *>(a.q1),
                    static_cast<const __nv_bfloat16 *>(a.q2),
