@@ -92,7 +92,9 @@ Heads heads_of(int hs, int hn, int dv) {
 // 55.5 / 58.5, two 80 / 87.5, three 108 / 117 (one more costs ring depth and
 // registers; one fewer: 56, 84.5; 9 or 10 warps an SM, unevenly spread over
 // its four schedulers, 140 to 160; 128/256, two heads, one block: 82 against 59).
-// And as few as leave each warp a ring of kMinRing tiles.
+// And as few as leave each warp a ring of three tiles, two of which are in use
+// at a time: with two, heads of 128/64, three signal heads 123 us against 111,
+// two 92 against 81; with four or more, 128/256, 78 against 58.
 constexpr int kMinRing = 3, kMaxRing = 6;
 
 // Bytes of shared memory of 16 positions: codes and block scales of rh + 1 rows of K and rh of V.
