@@ -641,11 +641,10 @@ def _enqueue(entry, what, device, *args):
         raise GDAError(rc, what)
 
 
-def _int32(**sizes):
+def _int32(*sizes):
     """Refuses sizes that a C int does not hold (ctypes would pass their low 32 bits)."""
-    for name, value in sizes.items():
-        if not -0x80000000 <= value <= 0x7fffffff:
-            raise ValueError(f"{name} = {value} does not fit 32 bits")
+    if min(sizes) < -0x80000000 or max(sizes) > 0x7fffffff:
+        raise ValueError(f"sizes {sizes} do not all fit 32 bits")
 
 
 def _workspace(workspace, need, device):
@@ -657,8 +656,9 @@ def _workspace(workspace, need, device):
 
 def _expect_all(device, *wanted):
     """_expect for several (tensor, name, dtype, shape) at once: the checks without a call for each."""
+    index = device.index
     for t, name, dtype, shape in wanted:
-        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
+        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index
                 and t.is_contiguous()):
             _expect(t, name, dtype, shape, device)
 
@@ -671,7 +671,7 @@ def _token_stride(t, name, dtype, shape, device):
     """
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != device:
+    if t.get_device() != device.index:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
@@ -746,7 +746,7 @@ def gda_qk_norm_rope(q_sig, k_sig, q_noise, k_noise, weight, positions, inv_freq
 
 
 def gda_qk_norm_rope_bwd_workspace_size(T: int, h_s: int, h_n: int, d: int) -> int:
-    _int32(T=T, h_s=h_s, h_n=h_n, d=d)
+    _int32(T, h_s, h_n, d)
     return int(_load().gda_qk_norm_rope_bwd_workspace_size(T, h_s, h_n, d))
 
 
@@ -773,8 +773,8 @@ def gda_qk_norm_rope_bwd(q_sig, k_sig, q_noise, k_noise, weight, positions, inv_
     f32 = torch.float32
     _expect_all(dev, (dq_sig, "dq_sig", f32, shapes[0]), (dk_sig, "dk_sig", f32, shapes[1]),
                 (dq_noise, "dq_noise", f32, shapes[2]), (dk_noise, "dk_noise", f32, shapes[3]))
-    workspace = _workspace(workspace, gda_qk_norm_rope_bwd_workspace_size(T, hs, hn, d), dev)
     lib = _load()
+    workspace = _workspace(workspace, lib.gda_qk_norm_rope_bwd_workspace_size(T, hs, hn, d), dev)
     _enqueue(lib.gda_qk_norm_rope_bwd if dt is torch.bfloat16 else lib.gda_qk_norm_rope_bwd_f32,
              "gda norm and rotation backward", dev,
              *[t.data_ptr() for t in (*x, weight, positions, inv_freq, *dy, *grads)], T, hs, hn, d, rot,
@@ -804,7 +804,7 @@ def gda_block_tables(cache_lens, new_lens, block_table, free_pages, free_count, 
     i32 = torch.int32
     B, max_pages = block_table.shape
     free = free_pages.numel()
-    _int32(page_size=page_size, num_pages=num_pages, max_rows=max_rows, free_pages=free, max_pages=max_pages)
+    _int32(page_size, num_pages, max_rows, free, max_pages)
     _expect_all(dev, (cache_lens, "cache_lens", i32, (B,)), (new_lens, "new_lens", i32, (B,)),
                 (block_table, "block_table", i32, (B, max_pages)), (free_pages, "free_pages", i32, (free,)),
                 (free_count, "free_count", i32, (1,)))
@@ -900,7 +900,7 @@ def gda_cache_read_fp4(slot_map, k_sig_pool, k_noise_pool, v_pool, k_sig_block_s
 
 
 def gda_attn_decode_fp4_workspace_size(B: int, h_s: int, h_n: int, d: int, dv: int) -> int:
-    _int32(B=B, h_s=h_s, h_n=h_n, d=d, dv=dv)
+    _int32(B, h_s, h_n, d, dv)
     return int(_load().gda_attn_decode_fp4_workspace_size(B, h_s, h_n, d, dv))
 
 
@@ -921,7 +921,7 @@ def _decode_fp4(q_sig, q_noise, pools, blocks, scales, block_table, cache_lens, 
         out = torch.empty((B, hs, dv), dtype=bf, device=dev)
     else:
         _expect(out, "out", bf, (B, hs, dv), dev)
-    workspace = _workspace(workspace, gda_attn_decode_fp4_workspace_size(B, hs, hn, d, dv), dev)
+    workspace = _workspace(workspace, _load().gda_attn_decode_fp4_workspace_size(B, hs, hn, d, dv), dev)
     head = (q_sig.data_ptr(), q_noise.data_ptr(), *cache)
     tail = (hs, hn, d, dv, float(eps), workspace.data_ptr(), workspace.numel())
     if block_table is None:
