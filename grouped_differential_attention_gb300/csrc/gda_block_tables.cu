@@ -14,7 +14,7 @@
 // (they fit its shared memory), the barrier of the cluster stands between
 // the reading of the lengths and their update in place, and rows and pages
 // are then written by all its threads, each finding its sequence by bisection.
-// 10 us for the 256 rows of a decode step, 18 for 131072 rows of chunks, of
+// 10 us for the 256 rows of a decode step, 17 for 131072 rows of chunks, of
 // which 9 are the launch, the prefix sums and the barrier (kernel alone, cold).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
@@ -151,32 +151,46 @@ __global__ void __launch_bounds__(kThreads) gda_block_tables_kernel(const BlockT
         if (id < 0 || id >= a.num_pages) err |= GDA_DEVERR_BAD_PAGE;
         a.block_table[static_cast<size_t>(b) * a.max_pages + held + (q - first[b])] = id;
     }
-    // the rows, four in a row to a thread: one bisection for them, and a page looked up where it changes
+    // the rows, four in a row to a thread: one bisection for them, a division where a sequence begins and a page looked
+    // up where it changes (the integer work of a row, not its 8 bytes, is what the blocks' SMs spend their time on)
     const bool vector = ((reinterpret_cast<uintptr_t>(a.slot_map) | reinterpret_cast<uintptr_t>(a.positions)) & 15) == 0;
     for (long long q = gt; 4 * q < a.max_rows; q += gn) {
         const int r0 = static_cast<int>(4 * q), n = min(4, a.max_rows - r0);
         int slot[4] = {-1, -1, -1, -1}, pos[4] = {0, 0, 0, 0};
         if (r0 < rows) {
-            int b = last_at_most(start, a.B, r0), page = -1, base = -1;   // page: of the sequence; base: slot of its offset 0
+            int b = last_at_most(start, a.B, r0);
+            int have = 0, page = 0, at = 0, off = a.page_size, base = -1;   // of the row before: page, position, place in the page
+            bool begin = true;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int r = r0 + k;
                 if (k >= n || r >= rows) break;
-                while (b + 1 < a.B && start[b + 1] <= r) ++b, page = -1;
-                if (len[b] < 0) continue;
-                const int at_pos = len[b] + (r - start[b]), j = at_pos / a.page_size;
-                if (j != page) {
-                    page = j;
-                    const int held = pages_of(len[b], a.page_size);
-                    const int id = j < held ? a.block_table[static_cast<size_t>(b) * a.max_pages + j]
-                                            : a.free_pages[count - 1 - (first[b] + j - held)];
+                while (b + 1 < a.B && start[b + 1] <= r) ++b, begin = true;
+                if (begin) {
+                    have = len[b];
+                    at = have + (r - start[b]);
+                    page = at / a.page_size;
+                    off = at - page * a.page_size;
+                } else {
+                    ++at, ++off;
+                    if (off == a.page_size) off = 0, ++page;
+                }
+                if (have < 0) {
+                    begin = true;
+                    continue;
+                }
+                if (begin || off == 0) {
+                    int id;
+                    if (static_cast<long long>(page) * a.page_size < have) {
+                        id = a.block_table[static_cast<size_t>(b) * a.max_pages + page];
+                    } else {
+                        id = a.free_pages[count - 1 - (first[b] + page - pages_of(have, a.page_size))];
+                    }
                     base = id >= 0 && id < a.num_pages ? id * a.page_size : -1;
                     if (base < 0) err |= GDA_DEVERR_BAD_PAGE;
                 }
-                if (base >= 0) {
-                    slot[k] = base + (at_pos - j * a.page_size);
-                    pos[k] = at_pos;
-                }
+                begin = false;
+                if (base >= 0) slot[k] = base + off, pos[k] = at;
             }
         }
         if (n == 4 && vector) {
@@ -195,7 +209,7 @@ __global__ void __launch_bounds__(kThreads) gda_block_tables_kernel(const BlockT
 
 int launch_block_tables(const BlockTablesArgs &a, cudaStream_t stream) {
     // One block for a decode step, up to eight (the portable cluster) for many rows.  us with 1 / 4 / 8 blocks: 4096 rows
-    // 10.3 / 10.0 / 10.0, 8192 12.5 / 9.5 / 9.5, 16384 18.5 / 9.6 / 9.8, 131072 90 / 28 / 18; 256 rows 10.5 with any.
+    // 10.3 / 10.0 / 10.0, 8192 12.5 / 9.5 / 9.5, 16384 18.5 / 9.6 / 9.8, 131072 90 / 28 / 17; 256 rows 10.5 with any.
     const int blocks = a.max_rows <= 4 * kThreads ? 1 : (a.max_rows <= 16 * kThreads ? 4 : 8);
     const size_t smem = static_cast<size_t>(a.B) * 3 * sizeof(int);
     cudaError_t e = cudaFuncSetAttribute(gda_block_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
