@@ -908,7 +908,7 @@ def _decode_fp4(q_sig, q_noise, pools, blocks, scales, block_table, cache_lens, 
     dev = q_sig.device
     if dev.type != "cuda":
         raise ValueError("inputs must be CUDA tensors")
-    if q_sig.dim() != 3 or q_noise.dim() != 3 or any(t.dim() != 4 for t in pools):
+    if q_sig.dim() != 3 or q_noise.dim() != 3 or pools[0].dim() != 4 or pools[2].dim() != 4:
         raise ValueError("bad ranks: q [B, heads, d], caches [.., .., heads, dim / 2]")
     B, hs, d = q_sig.shape
     hn, dv = q_noise.shape[1], 2 * pools[2].shape[3]

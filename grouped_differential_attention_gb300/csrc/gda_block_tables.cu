@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kThreads) gda_block_tables_kernel(const BlockT
 
 int launch_block_tables(const BlockTablesArgs &a, cudaStream_t stream) {
     // One block for a decode step, up to eight (the portable cluster) for many rows.  us with 1 / 4 / 8 blocks: 4096 rows
-    // 10.3 / 10.0 / 10.0, 8192 12.5 / 9.5 / 9.5, 16384 18.5 / 9.6 / 9.8, 131072 90 / 28 / 17; 256 rows 10.5 with any.
+    // 10.4 / 10.2 / 10.2, 8192 13.0 / 9.4 / 9.7, 16384 18.0 / 9.7 / 9.6, 131072 82 / 25.7 / 16.7; 256 rows 10.5 with any.
     const int blocks = a.max_rows <= 4 * kThreads ? 1 : (a.max_rows <= 16 * kThreads ? 4 : 8);
     const size_t smem = static_cast<size_t>(a.B) * 3 * sizeof(int);
     cudaError_t e = cudaFuncSetAttribute(gda_block_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
