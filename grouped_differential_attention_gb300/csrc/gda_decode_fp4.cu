@@ -35,7 +35,7 @@
 // scale stays clear of f16's end; numerator and denominator share the factor.
 //
 // Measured (both kernels; of the 6793 GB/s of a copy): 64 sequences of 4096 to
-// 8192, 12 + 4 heads of 64/128, 566 MB: 114 us (73 %); one of 131072, 24 + 8
+// 8192, 12 + 4 heads of 64/128, 566 MB: 115 us (73 %); one of 131072, 24 + 8
 // heads, 378 MB: 89 us (62 %); 16 of up to 8191, 16 + 4 heads of 128/256,
 // 245 MB: 63 us (57 %).  Of the first one's 108 us in the split kernel the
 // copies alone take 98 and the arithmetic alone 90 (67 M warp instructions);
