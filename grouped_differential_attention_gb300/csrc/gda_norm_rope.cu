@@ -312,7 +312,7 @@ gda_qk_norm_rope_bwd_kernel(const NormRopeArgs p, const Shape shape) {
     const long long ldx = p.ld[t], lddx = p.ldy[t], ldg = static_cast<long long>(t < 2 ? p.hs : p.hn) * D;
     const int half = p.rot / 2, ahead = ln.b - ln.a;
     const long long first = blockIdx.x * shape.per, last = min(p.T, first + shape.per);
-    float dwa[4] = {}, dwb[4] = {};
+    float dwa[4] = {}, dwb[4] = {}, suma[4] = {}, sumb[4] = {};   // of a table's tokens; of all before
     fill_rest(p, table, freq);
     const long long at = min(first + subset, p.T - 1);
     const int eighth = lane % LANES * 8;
@@ -380,22 +380,29 @@ gda_qk_norm_rope_bwd_kernel(const NormRopeArgs p, const Shape shape) {
             dx += shape.subsets * lddx;
             cs += shape.subsets * ln.step;
         }
+        // sums of sums: the error of one long float32 sum grows with its length (dw of 8190 tokens was off by 2.0e-7 of
+        // its size, this way by 1.5e-7; at no cost)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            suma[i] += dwa[i], sumb[i] += dwb[i];
+            dwa[i] = dwb[i] = 0.f;
+        }
     }
     const int mine = warp * ROWS + lane / LANES;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        part[mine][ln.a + i] = dwa[i];
-        part[mine][ln.b + i] = dwb[i];
+        part[mine][ln.a + i] = suma[i];
+        part[mine][ln.b + i] = sumb[i];
     }
     if (lane % LANES == 0) owner[mine] = ln.t;
     __syncthreads();
     const int rows = (blockDim.x >> 5) * ROWS;
     float *out = p.partial + static_cast<size_t>(blockIdx.y * gridDim.x + blockIdx.x) * 4 * D;
     for (int i = threadIdx.x; i < 4 * D; i += blockDim.x) {
-        float s = 0.f;
+        float s[4] = {};
         for (int k = 0; k < rows; ++k)
-            if (owner[k] == i / D) s += part[k][i % D];
-        out[i] = s;
+            if (owner[k] == i / D) s[k & 3] += part[k][i % D];
+        out[i] = (s[0] + s[1]) + (s[2] + s[3]);
     }
 }
 
