@@ -21,26 +21,28 @@
 // multiply (mma.sync m16n8k16, f16 in, float32 out; a tile of a decode has
 // one row of queries, so the 128-row tcgen05 forms would sit idle for 127),
 // and the work left per element is half a conversion.  An mma has eight
-// columns where a decode needs one or two, and the others take the block
-// scales out of the inner loop:
+// columns where a decode needs one or two; the others are put to use:
 //   - scores: A = codes of 16 positions, B column n = the query with all but
 //     its n-th block of 16 dims zeroed, so C holds the dot product of every
 //     block by itself, and a score is sum_n scale[n] * C[n];
-//   - values: A = codes of 16 dims x 16 positions, B column (n, map) =
-//     weight of the map * scale of block n, for the four blocks of a 64-dim
-//     slab and both maps; each dim is read from its own block's column.
+//   - values: A = code * scale of 16 dims x 16 positions, B = four columns of
+//     weights, the upper and the lower part of both maps', the other four
+//     zero, so that two tiles of dims share one set of accumulators.
 // e2m1 codes, e4m3 scales and their products are exact in f16; the query is
-// too, after a power of two; a weight times a scale is rounded to 11 bits.
-// The weights are 2^7 exp2(score - maximum) so that a small one times a small
-// scale stays clear of f16's end; numerator and denominator share the factor.
+// too, after a power of two.  A weight is two f16 numbers, its first 11 bits
+// and what they leave, so that it keeps 22 bits down to 2^-18 of its map's
+// largest and 2^-40 of that below (rounded to one f16, with the scale in B,
+// the 64 sequences below took 115 us and not 120, but outputs were off by
+// 2^-12 of their terms, and weights below 2^-32 were lost).  The weights are 2^15
+// exp2(score - maximum); numerator and denominator share the factor.
 //
 // Measured (both kernels; of the 6793 GB/s of a copy): 64 sequences of 4096 to
-// 8192, 12 + 4 heads of 64/128, 566 MB: 115 us (73 %); one of 131072, 24 + 8
-// heads, 378 MB: 89 us (62 %); 16 of up to 8191, 16 + 4 heads of 128/256,
-// 245 MB: 63 us (57 %).  Of the first one's 108 us in the split kernel the
-// copies alone take 98 and the arithmetic alone 90 (67 M warp instructions);
-// they overlap but for the start (a cold first tile arrives after several us)
-// and the slowest warps, 10 % behind the mean.
+// 8192, 12 + 4 heads of 64/128, 566 MB: 120 us (70 %); one of 131072, 24 + 8
+// heads, 378 MB: 93 us (60 %); 16 of up to 8191, 16 + 4 heads of 128/256,
+// 245 MB: 64 us (57 %).  The first one's split kernel takes 113 us; with the
+// weights rounded it took 108, of which the copies alone 98 and the arithmetic
+// alone 90: they overlap but for the start (a cold first tile arrives after
+// several us) and the slowest warps, 10 % behind the mean.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <algorithm>
@@ -61,18 +63,18 @@ constexpr int kTile = 16;              // positions of a tile
 // 64, 22.7 with 128.
 constexpr int kMinRange = 16;
 constexpr int kSms = 152;              // SMs that the plan counts on
-constexpr float kWeightBits = 7.f;     // weights carry a factor 2^7
+constexpr float kWeightBits = 15.f;    // weights carry a factor 2^15: the largest is within f16, the smallest far from its end
 
 // Signal heads of a warp: a noise head's group in equal parts of at most three
-// (two at dv = 256, where the accumulators of three would not fit the
-// registers).  Every part reads and scores the noise head for itself, and where
+// (two at dv = 256, where three tiles of three signal heads of 128 would leave an
+// SM one block).  Every part reads and scores the noise head for itself, and where
 // the parts do not divide the group the last one does a head again, so a part
 // costs about its heads and one more; the fewest of those are taken, of as many
 // the smaller parts.  us in the split kernel, 64 sequences of 4096 to 8192, 4
-// noise heads of 64/128: groups of three as 3 108, as 2 + 1 146; of four as 2 +
-// 2 160, as ones 195; of five as 3 + 3 207, as 2 + 2 + 2 218; of seven as three
-// of 3 309, as four of 2 298.  16 sequences, 4 noise heads of 128/256: groups
-// of three as 2 + 2 55, as ones 52.5; of four as 2 + 2 58, as ones 67.
+// noise heads of 64/128: groups of three as 3 113, as 2 + 2 153; of four as 2 +
+// 2 163, as ones 202; of five as 3 + 3 217, as 2 + 2 + 2 225; of seven as three
+// of 3 324, as four of 2 303.  16 sequences, 4 noise heads of 128/256: groups
+// of three as 2 + 2 56, as ones 52; of four as 2 + 2 59, as ones 67.
 struct Heads {
     int parts, each;   // parts of a group; signal heads of a part
 };
@@ -86,15 +88,16 @@ Heads heads_of(int hs, int hn, int dv) {
     return h;
 }
 
-// Blocks that share an SM, by the accumulator registers of a thread (DV / 4
-// for each signal head).  us in the split kernel, this many / one more, 64
-// sequences of 4096 to 8192, 4 noise heads of 64/128: one signal head each
-// 55.5 / 58.5, two 80 / 87.5, three 108 / 117 (one more costs ring depth and
-// registers; one fewer: 56, 84.5; 9 or 10 warps an SM, unevenly spread over
-// its four schedulers, 140 to 160; 128/256, two heads, one block: 82 against 59).
+// Blocks that share an SM, by the accumulator registers of a thread (DV / 8
+// for each signal head).  us in the split kernel, this many / one fewer, 4
+// noise heads, one signal head each: 64 sequences of 4096 to 8192 of 64/128
+// 57.5 / 58, of 64/64 46.5 / 48.5; 32 of 128/128 38.5 / 38.5; two: 82 / 89 of
+// 64/128, 53 / 57 of 128/128; three of 64/64 86 / 96.  One more makes no
+// difference (three signal heads of 64/128 113 / 113 with one fewer tile in the
+// ring, one of 131072 positions 94.4 / 94.5 with the joining of its parts).
 // And as few as leave each warp a ring of three tiles, two of which are in use
-// at a time: with two, heads of 128/64, three signal heads 123 us against 111,
-// two 92 against 81; with four or more, 128/256, 78 against 58.
+// at a time; with four or more, two signal heads of 128/256 take 75 against 59,
+// three of 128/128 92 against 73.
 constexpr int kMinRing = 3, kMaxRing = 6;
 
 // Bytes of shared memory of 16 positions: codes and block scales of rh + 1 rows of K and rh of V.
@@ -108,7 +111,7 @@ __host__ __device__ constexpr int ring_of(int blocks, int rh, int d, int dv) {
     return fit > kMaxRing ? kMaxRing : fit;
 }
 __host__ __device__ constexpr int blocks_per_sm(int rh, int d, int dv) {
-    int blocks = rh * dv / 4 <= 32 ? 4 : (rh * dv / 4 <= 64 ? 3 : 2);
+    int blocks = rh * dv / 8 <= 16 ? 4 : (rh * dv / 8 <= 32 ? 3 : 2);
     while (blocks > 1 && ring_of(blocks, rh, d, dv) < kMinRing) --blocks;
     return blocks;
 }
@@ -468,7 +471,7 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32, (Tile<D, DV, RH>::blocks)
     const int k_at = T::k_codes + quad * T::KC + t * (D / 8);
     const int ks_at = T::k_scales + quad * T::KS + (D == 64 ? t & 1 : t) * 2;
 
-    float acc[RH][SLABS][4][4];
+    float acc[RH][SLABS][2][4];                          // [u]: of tile 2 u + t / 2 and map t % 2, see values_of
     float m = -INFINITY, l = 0.f;                        // of head t (both its lanes' positions; l of this lane's only)
     float factor = load_queries<D, RH>(p, queries, use.b, h0, g);
 #pragma unroll
@@ -476,13 +479,15 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32, (Tile<D, DV, RH>::blocks)
 #pragma unroll
         for (int s = 0; s < SLABS; ++s)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) acc[j][s][i][k] = 0.f;
 
-    uint32_t weights = 0;                                // of head t in the tile whose values are added next
+    // of head t in the tile whose values are added next, as pairs of positions 8 apart: the upper parts of positions
+    // quad & 6 and the next on a lane of an even quad, the lower parts of the same two on a lane of an odd one
+    uint32_t weights[2] = {0u, 0u};
     float scale = 1.f;                                   // of what was added before them
-    auto scores_of = [&](const uint8_t *const tile, uint32_t &next) {
+    auto scores_of = [&](const uint8_t *const tile, uint32_t (&next)[2]) {
         // lane (quad, t) ends up with positions quad, quad + 8 of head t
         float x0[4] = {}, x1[4] = {};
 #pragma unroll
@@ -521,32 +526,37 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32, (Tile<D, DV, RH>::blocks)
         const float p0 = fast_exp2(sc0 - mt + kWeightBits), p1 = fast_exp2(sc1 - mt + kWeightBits);
         m = mt;
         l = fmaf(l, scale, p0 + p1);
-        next = pack_half2(p0, p1);
+        const uint32_t hi = pack_half2(p0, p1);
+        const float2 h = half2_bits_to_float2(hi);
+        const uint32_t lo = pack_half2(p0 - h.x, p1 - h.y), got = __shfl_xor_sync(0xffffffffu, quad & 1 ? hi : lo, 4);
+        next[0] = quad & 1 ? got : hi;
+        next[1] = quad & 1 ? lo : got;
     };
     auto rescale = [&]() {
         if (__any_sync(0xffffffffu, scale != 1.f)) {
-            const float sn = __shfl_sync(0xffffffffu, scale, RH);
 #pragma unroll
             for (int j = 0; j < RH; ++j) {
-                const float sj = __shfl_sync(0xffffffffu, scale, j);
+                const float sj = __shfl_sync(0xffffffffu, scale, t & 1 ? RH : j);
 #pragma unroll
                 for (int s = 0; s < SLABS; ++s)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        acc[j][s][i][0] *= sj, acc[j][s][i][2] *= sj;
-                        acc[j][s][i][1] *= sn, acc[j][s][i][3] *= sn;
-                    }
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) acc[j][s][i][k] *= sj;
             }
         }
     };
     auto values_of = [&](const uint8_t *const tile) {
         // k slots (2t, 2t + 1) are positions 2t, 2t + 8 and (2t + 8, 2t + 9) are 2t + 1, 2t + 9;
-        // column 2 n + map, n the block within the slab; row `quad` of tile i is dim 8 quad + 2 i, row quad + 8 the next
+        // row `quad` of tile i is dim 8 quad + 2 i, row quad + 8 the next; columns 4 (i % 2) + 2 map and the next take the
+        // upper and the lower part of that map's weights, the other four are zero, so that tiles 2 u and 2 u + 1 share
+        // their accumulators
         const uint32_t pick = 0x40u + 0x11u * (quad >> 1);   // byte of block quad / 2 from either word
 #pragma unroll
         for (int j = 0; j < RH; ++j) {
-            const int src = 8 * t + (quad & 1 ? RH : j);
-            const uint32_t w0 = __shfl_sync(0xffffffffu, weights, src), w1 = __shfl_sync(0xffffffffu, weights, src + 4);
+            const int src = 8 * t + 4 * (quad & 1) + (quad & 2 ? RH : j);
+            const uint32_t w0 = __shfl_sync(0xffffffffu, weights[0], src), w1 = __shfl_sync(0xffffffffu, weights[1], src);
+            const uint32_t b0[2] = {quad < 4 ? w0 : 0u, quad < 4 ? 0u : w0}, b1[2] = {quad < 4 ? w1 : 0u, quad < 4 ? 0u : w1};
             // scales of positions 2t, 2t + 1 and 2t + 8, 2t + 9: four blocks to a word
             const uint8_t *vs = tile + T::v_scales + (j * kTile + 2 * t) * T::VS;
             uint32_t e[4][SLABS];                        // [2t, 2t + 8, 2t + 1, 2t + 9][slab]
@@ -570,8 +580,8 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32, (Tile<D, DV, RH>::blocks)
             const uint8_t *vc = tile + T::v_codes + j * kTile * T::VC;
 #pragma unroll
             for (int s = 0; s < SLABS; ++s) {
-                const uint32_t b0 = half2_mul(w0, e4m3x2_to_half2(prmt(e[0][s], e[1][s], pick)));
-                const uint32_t b1 = half2_mul(w1, e4m3x2_to_half2(prmt(e[2][s], e[3][s], pick)));
+                const uint32_t e0 = e4m3x2_to_half2(prmt(e[0][s], e[1][s], pick));
+                const uint32_t e1 = e4m3x2_to_half2(prmt(e[2][s], e[3][s], pick));
                 const uint8_t *row = vc + (lane_at ^ (32 * s));
                 const uint32_t p0w = at<uint32_t>(row), p8w = at<uint32_t>(row + 4 * T::VC),
                                p1w = at<uint32_t>(row + 8 * T::VC), p9w = at<uint32_t>(row + 12 * T::VC);
@@ -582,12 +592,16 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32, (Tile<D, DV, RH>::blocks)
                 e2m1x8_to_half2x4(a2, (p1w & 0x0f0f0f0fu) | ((p9w << 4) & 0xf0f0f0f0u));
                 e2m1x8_to_half2x4(a3, ((p1w >> 4) & 0x0f0f0f0fu) | (p9w & 0xf0f0f0f0u));
 #pragma unroll
-                for (int i = 0; i < 4; ++i) mma_16816(acc[j][s][i], a0[i], a1[i], a2[i], a3[i], b0, b1, acc[j][s][i]);
+                for (int k = 0; k < 4; ++k) {            // tiles 0, 2, 1, 3: the two that share accumulators are apart
+                    const int i = 2 * (k & 1) + (k >> 1);
+                    mma_16816(acc[j][s][i / 2], half2_mul(a0[i], e0), half2_mul(a1[i], e0), half2_mul(a2[i], e1),
+                              half2_mul(a3[i], e1), b0[i % 2], b1[i % 2], acc[j][s][i / 2]);
+                }
             }
         }
     };
     // The scores of a tile come with the values of the one before it, in one run of instructions without a branch: the
-    // chain from scores to weights then has other work beside it (64 sequences, split kernel: 114 -> 108 us).
+    // chain from scores to weights then has other work beside it (64 sequences, split kernel, weights of one f16: 114 -> 108 us).
     const uint8_t *before = ring;                        // the tile whose values are still to be added
     bool fresh = true;                                   // there is none: a part begins
     for (;;) {
@@ -607,7 +621,7 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32, (Tile<D, DV, RH>::blocks)
         __syncwarp();                                    // every lane's copies of this tile have landed
         const uint8_t *const tile = ring + from * T::bytes;
         from = from + 1 == S ? 0 : from + 1;
-        uint32_t next;
+        uint32_t next[2];
         if (fresh) {
             scores_of(tile, next);
             fresh = false;
@@ -616,7 +630,7 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32, (Tile<D, DV, RH>::blocks)
             values_of(before);
             rescale();
         }
-        weights = next;
+        weights[0] = next[0], weights[1] = next[1];
         before = tile;
         use.pos += kTile;
         if (use.pos < use.hi) continue;
@@ -634,18 +648,15 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32, (Tile<D, DV, RH>::blocks)
             const float mj = __shfl_sync(0xffffffffu, m, j), lj = __shfl_sync(0xffffffffu, l, j);
             const size_t place = slot * p.hs + h0 + j;
             if (lane == 0) reinterpret_cast<float4 *>(p.ws_ml)[place] = make_float4(mj, lj, mn, ln);
-            if (t == quad >> 1) {                        // the lanes whose columns are their own block
-                const float v = p.v_scale[h0 + j];
-                float4 *o1 = reinterpret_cast<float4 *>(p.ws_o + place * 2 * DV), *o2 = o1 + DV / 4;
+            const float v = p.v_scale[h0 + j];
+            float2 *o = reinterpret_cast<float2 *>(p.ws_o + (place * 2 + (t & 1)) * DV) + 4 * quad + (t >> 1);
 #pragma unroll
-                for (int s = 0; s < SLABS; ++s)
+            for (int s = 0; s < SLABS; ++s)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float(&c)[4] = acc[j][s][2 * i], (&d)[4] = acc[j][s][2 * i + 1];
-                        o1[16 * s + 2 * quad + i] = make_float4(c[0] * v, c[2] * v, d[0] * v, d[2] * v);
-                        o2[16 * s + 2 * quad + i] = make_float4(c[1] * v, c[3] * v, d[1] * v, d[3] * v);
-                    }
-            }
+                for (int i = 0; i < 2; ++i) {
+                    const float(&c)[4] = acc[j][s][i];
+                    o[32 * s + 2 * i] = make_float2((c[0] + c[1]) * v, (c[2] + c[3]) * v);
+                }
         }
         if (use.left == 0) return;
         next_sequence(p, use);
@@ -657,7 +668,7 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32, (Tile<D, DV, RH>::blocks)
 #pragma unroll
             for (int s = 0; s < SLABS; ++s)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) acc[j][s][i][k] = 0.f;
     }
