@@ -624,6 +624,7 @@ int gda_lambda_reparam(const float *lambda_q1, const float *lambda_k1, const flo
 size_t gda_attn_decode_fp4_workspace_size(int B, int h_s, int h_n, int d, int dv) {
     if (B < 1 || h_s < 1 || h_n < 1 || d < 1 || dv < 1 || h_s % h_n != 0) return 0;
     if (B > 65535 || h_s + h_n > 128) return 0;
+    if (!(d == 64 || d == 128) || !(dv == 64 || dv == 128 || dv == 256)) return 0;   // the plan divides by a tile's bytes
     return decode_fp4_workspace_bytes(B, h_s, h_n, d, dv);
 }
 

@@ -1,0 +1,40 @@
+"""Sizes at the C entries of the operators around the attention (host only)."""
+import os
+import subprocess
+import sys
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from grouped_differential_attention_gb300 import build
+    build.build()
+    import grouped_differential_attention_gb300 as gda
+    return gda._load()
+
+
+UNSUPPORTED_DIMS = [(1, 1), (2, 2), (16, 16), (96, 128), (64, 96), (64, 4096), (4096, 64), (64, 512), (256, 256),
+                    (10 ** 9, 10 ** 9), (2 ** 31 - 1, 2 ** 31 - 1), (64, 2 ** 31 - 1)]
+
+
+def test_fp4_workspace_size_is_zero_for_head_dims_without_a_kernel(lib):
+    """In a child process: a size that ends the process fails this test alone."""
+    code = ("import grouped_differential_attention_gb300 as gda\n"
+            f"for d, dv in {UNSUPPORTED_DIMS}:\n"
+            "    for B, hs, hn in ((1, 1, 1), (1, 2, 1), (4, 6, 2), (65535, 127, 1)):\n"
+            "        n = gda.gda_attn_decode_fp4_workspace_size(B, hs, hn, d, dv)\n"
+            "        assert n == 0, (B, hs, hn, d, dv, n)\n")
+    res = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert res.returncode == 0, (res.returncode, res.stderr[-500:])
+
+
+def test_fp4_workspace_size_of_supported_head_dims(lib):
+    for d in (64, 128):
+        for dv in (64, 128, 256):
+            assert lib.gda_attn_decode_fp4_workspace_size(1, 1, 1, d, dv) > 0
+            assert lib.gda_attn_decode_fp4_workspace_size(65535, 127, 1, d, dv) > 0
+            assert lib.gda_attn_decode_fp4_workspace_size(65536, 1, 1, d, dv) == 0
+            assert lib.gda_attn_decode_fp4_workspace_size(1, 127, 2, d, dv) == 0
