@@ -124,6 +124,9 @@ namespace {
 
 const uint8_t *bytes_of(const void *p) { return static_cast<const uint8_t *>(p); }
 
+// Whether hs + hn (both positive) is above `most`; the sum itself may not fit an int.
+bool heads_above(int hs, int hn, int most) { return hs > most || hn > most - hs; }
+
 // Arguments that both decodes over a 4-bit cache check; `rows`: rows of the caches.
 int check_decode_fp4(const void *const (&ptrs)[9], const float *k1_scale, const float *k2_scale,
                      const float *v_scale, const int *lens, const float *lambda, float lambda_init, int B, int Lcap,
@@ -136,7 +139,7 @@ int check_decode_fp4(const void *const (&ptrs)[9], const float *k1_scale, const 
     if (!std::isfinite(eps) || eps < 0.f || !std::isfinite(lambda_init)) return GDA_ERR_INVALID_ARG;
     if (rows * hs * (d > dv ? d : dv) > 9.0e15) return GDA_ERR_INVALID_ARG;
     if (!(d == 64 || d == 128) || !(dv == 64 || dv == 128 || dv == 256)) return GDA_ERR_UNSUPPORTED;
-    if (hs + hn > 128 || B > 65535) return GDA_ERR_UNSUPPORTED;
+    if (heads_above(hs, hn, 128) || B > 65535) return GDA_ERR_UNSUPPORTED;
     // positions are 32 bits wide and stepped by 16; a range (a 19th of the batch's at most) is counted in 32 bits too
     if (Lcap > 0x7ffffff0 || static_cast<long long>(B) * Lcap > 1LL << 35) return GDA_ERR_UNSUPPORTED;
     for (const void *p : ptrs)
@@ -160,7 +163,7 @@ int fill_cache_fp4(CacheFp4Args &a, int num_pages, int page_size, int hs, int hn
         return GDA_ERR_INVALID_ARG;
     if (static_cast<long long>(num_pages) * page_size > 0x7fffffffLL) return GDA_ERR_INVALID_ARG;
     if (!(d == 64 || d == 128) || !(dv == 64 || dv == 128 || dv == 256)) return GDA_ERR_UNSUPPORTED;
-    if (hs + hn > 128) return GDA_ERR_UNSUPPORTED;
+    if (heads_above(hs, hn, 128)) return GDA_ERR_UNSUPPORTED;
     if (reinterpret_cast<uintptr_t>(a.slot_map) & 3u) return GDA_ERR_MISALIGNED;
     for (int t = 0; t < 3; ++t) {
         const long long row = static_cast<long long>(heads[t]) * dims[t];
@@ -193,7 +196,7 @@ int check_norm_rope(const Four &x, const FourOut &y, const float *weight, const 
     if (T < 1 || hs < 1 || hn < 1 || d < 1 || rot < 1 || hs % hn != 0) return GDA_ERR_INVALID_ARG;
     if (!std::isfinite(eps) || eps < 0.f) return GDA_ERR_INVALID_ARG;
     if (flags & ~GDA_FLAG_ROPE_INTERLEAVED) return GDA_ERR_INVALID_ARG;
-    if (!(d == 64 || d == 128) || rot > d || rot % 16 != 0 || hs + hn > 1024) return GDA_ERR_UNSUPPORTED;
+    if (!(d == 64 || d == 128) || rot > d || rot % 16 != 0 || heads_above(hs, hn, 1024)) return GDA_ERR_UNSUPPORTED;
     for (int t = 0; t < 4; ++t)
         if (!aligned16(x.p[t]) || !aligned16(y.p[t])) return GDA_ERR_MISALIGNED;
     if (!aligned16(weight) || ((reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(inv_freq)) & 3u))
@@ -623,7 +626,7 @@ int gda_lambda_reparam(const float *lambda_q1, const float *lambda_k1, const flo
 
 size_t gda_attn_decode_fp4_workspace_size(int B, int h_s, int h_n, int d, int dv) {
     if (B < 1 || h_s < 1 || h_n < 1 || d < 1 || dv < 1 || h_s % h_n != 0) return 0;
-    if (B > 65535 || h_s + h_n > 128) return 0;
+    if (B > 65535 || heads_above(h_s, h_n, 128)) return 0;
     if (!(d == 64 || d == 128) || !(dv == 64 || dv == 128 || dv == 256)) return 0;   // the plan divides by a tile's bytes
     return decode_fp4_workspace_bytes(B, h_s, h_n, d, dv);
 }
@@ -734,7 +737,7 @@ int gda_qk_norm_rope_f32(const float *q_sig, const float *k_sig, const float *q_
 }
 
 size_t gda_qk_norm_rope_bwd_workspace_size(int T, int h_s, int h_n, int d) {
-    if (T < 1 || h_s < 1 || h_n < 1 || h_s % h_n != 0 || h_s + h_n > 1024 || !(d == 64 || d == 128)) return 0;
+    if (T < 1 || h_s < 1 || h_n < 1 || h_s % h_n != 0 || heads_above(h_s, h_n, 1024) || !(d == 64 || d == 128)) return 0;
     return qk_norm_rope_bwd_workspace_bytes(T, h_s, h_n, d);
 }
 

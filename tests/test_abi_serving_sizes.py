@@ -38,3 +38,18 @@ def test_fp4_workspace_size_of_supported_head_dims(lib):
             assert lib.gda_attn_decode_fp4_workspace_size(65535, 127, 1, d, dv) > 0
             assert lib.gda_attn_decode_fp4_workspace_size(65536, 1, 1, d, dv) == 0
             assert lib.gda_attn_decode_fp4_workspace_size(1, 127, 2, d, dv) == 0
+
+
+def test_head_counts_whose_sum_wraps_are_refused(lib):
+    """h_s + h_n past 2^31: every entry refuses them before any device work."""
+    from test_abi_serving_host import UNSUPPORTED, append, decode, paged, read, rope, rope_bwd
+    big = 2 ** 31 - 1
+    for hs, hn in ((big, 1), (big, big), (2 ** 30, 2 ** 30), (big - 128, 1)):
+        assert lib.gda_attn_decode_fp4_workspace_size(1, hs, hn, 64, 128) == 0
+        assert lib.gda_qk_norm_rope_bwd_workspace_size(1, hs, hn, 64) == 0
+        for call in (rope, rope_bwd):
+            assert call(lib, hs=hs, hn=hn, T=1) == UNSUPPORTED
+        for call in (append, read):
+            assert call(lib, hs=hs, hn=hn) == UNSUPPORTED
+        for call in (decode, paged):
+            assert call(lib, hs=hs, hn=hn, ws_bytes=1 << 60) == UNSUPPORTED
