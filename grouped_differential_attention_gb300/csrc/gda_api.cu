@@ -140,6 +140,7 @@ int check_decode_fp4(const void *const (&ptrs)[9], const float *k1_scale, const 
     if (rows * hs * (d > dv ? d : dv) > 9.0e15) return GDA_ERR_INVALID_ARG;
     if (!(d == 64 || d == 128) || !(dv == 64 || dv == 128 || dv == 256)) return GDA_ERR_UNSUPPORTED;
     if (heads_above(hs, hn, 128) || B > 65535) return GDA_ERR_UNSUPPORTED;
+    if (rows > 4294967296.0) return GDA_ERR_UNSUPPORTED;   // rows of the caches are counted in 32 bits
     // positions are 32 bits wide and stepped by 16; a range (a 19th of the batch's at most) is counted in 32 bits too
     if (Lcap > 0x7ffffff0 || static_cast<long long>(B) * Lcap > 1LL << 35) return GDA_ERR_UNSUPPORTED;
     for (const void *p : ptrs)

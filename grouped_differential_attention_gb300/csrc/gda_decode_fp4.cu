@@ -160,7 +160,7 @@ __device__ __forceinline__ int length_of(const Params &p, int b) {
 }
 
 // Cache row of position pos of sequence b.  A page outside the pool is read
-// as page 0 and reported.  (2^32 rows of the smallest cache are 464 GB.)
+// as page 0 and reported.  (The caches have 2^32 rows at most.)
 __device__ __forceinline__ uint32_t row_of(const Params &p, int b, int pos) {
     if (p.block_table == nullptr) return static_cast<uint32_t>(b) * static_cast<uint32_t>(p.Lcap) + pos;
     const int pg = pos / p.page_size;

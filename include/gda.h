@@ -528,8 +528,9 @@ int gda_cache_read_fp4(const int *slot_map, const void *k_sig_pool, const void *
  *   aligned, owned by the caller; needs no initialisation.  Calls in flight
  *   at the same time need a workspace each.
  * Supported: d in {64, 128}; dv in {64, 128, 256}; h_s + h_n <= 128;
- * B <= 65535; page_size >= 1; Lcap (max_pages * page_size) at most 2^31 - 16
- * and B times that at most 2^35.
+ * B <= 65535; page_size >= 1; Lcap (max_pages * page_size) at most 2^31 - 16;
+ * at most 2^32 rows in the caches (B * Lcap, num_pages * page_size), and paged
+ * B times Lcap at most 2^35.
  */
 int gda_attn_decode_fp4(const void *q_sig, const void *q_noise, const void *k_sig_cache,
                         const void *k_noise_cache, const void *v_cache, const void *k_sig_block_scale,

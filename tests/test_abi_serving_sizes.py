@@ -53,3 +53,17 @@ def test_head_counts_whose_sum_wraps_are_refused(lib):
             assert call(lib, hs=hs, hn=hn) == UNSUPPORTED
         for call in (decode, paged):
             assert call(lib, hs=hs, hn=hn, ws_bytes=1 << 60) == UNSUPPORTED
+
+
+def test_decode_refuses_caches_of_more_than_32_bit_rows(lib):
+    """The decode counts cache rows in 32 bits: 2^32 rows are the most, one more would be read as a low one."""
+    from test_abi_serving_host import CUDA, UNSUPPORTED, decode, paged
+    import torch
+    assert decode(lib, B=33, Lcap=1 << 27) == UNSUPPORTED                    # 2^32 + 2^27 rows
+    assert decode(lib, B=1025, Lcap=1 << 22) == UNSUPPORTED
+    assert paged(lib, ps=16, pages=(1 << 28) + 1) == UNSUPPORTED
+    assert paged(lib, ps=3, pages=(1 << 32) // 3 + 1) == UNSUPPORTED
+    if not torch.cuda.is_available():
+        assert decode(lib, B=32, Lcap=1 << 27) == CUDA                       # 2^32 rows
+        assert paged(lib, ps=16, pages=1 << 28) == CUDA
+        assert paged(lib, B=256, Lcap=1 << 27, ps=16) == CUDA                # tables may name a page more than once
