@@ -14,8 +14,10 @@
 // where a float32 product has lost the phase.  inv_freq / (2 pi) is held as
 // two floats (48 bits); the product with the position is split exactly by a
 // fused multiply-add, whole turns drop out without rounding, and the rest
-// goes to sincospif.  Positions of 2^24 and beyond, which float32 does not
-// hold exactly, take the same steps in double.
+// goes to sincospif.  Those 48 bits leave an angle off by 2^-49 of itself, so
+// from 2^22 turns on (and at positions of 2^24 and beyond, which float32 does
+// not hold exactly) the same steps are taken in double, with 1 / (2 pi) as two
+// doubles.  Either way the angle is off by its one rounding to float32.
 //
 // Memory-bound: a head row is read and written once (and dy read, for the
 // gradients), so the arithmetic is kept below the copy.  d/8 lanes hold a
@@ -33,9 +35,10 @@
 // time, each with an equal run of tokens.
 //
 // Measured, of the 6793 GB/s of a copy: 32768 tokens, 24 + 8 heads of 64,
-// bf16, 537 MB: 93 us (85 %); gradients of 8190 tokens, 16 + 4 heads of 128,
-// float32, 503 MB: 86 us (86 %); of 8192 tokens, 12 + 4 heads of 64, bf16, 134
-// MB: 24 us and 4 for the sum of dw (70 % together); 64 tokens: 4 us.
+// bf16, 537 MB: 87.5 us (90 %), the kernel alone 81; 12 + 4 heads, float32,
+// 537 MB: 81 alone; gradients of 8190 tokens, 16 + 4 heads of 128, float32,
+// 503 MB: 84 us (88 %); of 8192 tokens, 12 + 4 heads of 64, bf16, 134 MB: 21.5
+// us and 4.4 for the sum of dw (76 % together); 64 tokens: 4 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <algorithm>
@@ -50,8 +53,8 @@ namespace {
 
 constexpr int kMaxWarps = 8;        // of a block
 constexpr int kTokens = 16;         // tokens of a block's sine table
-// Blocks of an SM: enough copies in flight, and few fronts in memory (prompt of 32768 tokens, 24 + 8 heads: 93 us with
-// 3 and rings of 7 tokens, 101 with 4 and 5, 117 with 2 and 8; gradients, float32: 86 us with 2, 90 with 3).
+// Blocks of an SM: enough copies in flight, and few fronts in memory (prompt of 32768 tokens, 24 + 8 heads: 87.5 us with
+// 3, 95 with 2, 99.5 with 4; gradients, float32: 84 us with 2, 92.5 with 1, 95 with 3).
 constexpr int kForwardBlocks = 3, kBackwardBlocks = 2;
 
 // A warp's head rows of one token in its ring: 256 elements, rows of 64 bf16
@@ -91,28 +94,29 @@ __device__ __forceinline__ void store4(float *p, const float (&f)[4]) {
     *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
 }
 
-// Frequency in turns as hi + lo.
+// Frequency in turns as hi + lo, and as given.
 struct Turns {
-    float hi, lo;
+    float hi, lo, radians;
 };
 
 __device__ __forceinline__ Turns turns_of(float inv_freq) {
     const double t = static_cast<double>(inv_freq) * 0.15915494309189533577;   // 1 / (2 pi)
     const float hi = static_cast<float>(t);
-    return {hi, static_cast<float>(t - static_cast<double>(hi))};
+    return {hi, static_cast<float>(t - static_cast<double>(hi)), inv_freq};
 }
 
 // (cos, sin) of position * frequency.
 __device__ __forceinline__ float2 angle(int pos, Turns f) {
+    const float p = static_cast<float>(pos), whole = p * f.hi;
     float turn;
-    if (pos > -(1 << 24) && pos < (1 << 24)) {
-        const float p = static_cast<float>(pos);
-        const float whole = p * f.hi;
+    if (pos > -(1 << 24) && pos < (1 << 24) && fabsf(whole) < 4194304.f) {
         const float rest = fmaf(p, f.hi, -whole);
         turn = (whole - rintf(whole)) + fmaf(p, f.lo, rest);
     } else {
-        const double t = static_cast<double>(pos) * (static_cast<double>(f.hi) + static_cast<double>(f.lo));
-        turn = static_cast<float>(t - rint(t));
+        constexpr double c = 0.15915494309189535, rest_of_c = -9.839338337591243e-18;   // 1 / (2 pi)
+        const double q = pos, r = f.radians, t = r * c, low = fma(r, rest_of_c, fma(r, c, -t));   // frequency: t + low
+        const double turns = q * t;
+        turn = static_cast<float>((turns - rint(turns)) + fma(q, low, fma(q, t, -turns)));
     }
     float s, c;
     sincospif(2.f * turn, &s, &c);
@@ -441,7 +445,7 @@ Shape shape_of(const NormRopeArgs &a, int most) {
 
 template <typename T, int D, bool INTER>
 cudaError_t forward(const NormRopeArgs &a, const Shape &s, cudaStream_t stream) {
-    constexpr int RING = sizeof(T) == 2 ? 7 : 5;
+    constexpr int RING = 5;                       // prompt of 32768 tokens: 87.5 us; 88.5 with 4, 94 with 6, 98.5 with 7
     auto kern = gda_qk_norm_rope_kernel<T, D, INTER, RING>;
     const int warps = s.groups * s.subsets, one = RING * Stage<T, D>::bytes;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxWarps * one);

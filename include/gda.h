@@ -398,8 +398,9 @@ int gda_lambda_reparam(const float *lambda_q1, const float *lambda_k1, const flo
  *   Outputs: dense [T, h, d] of the inputs' type; an output may be its own
  *   input when that is dense, and overlaps nothing else.
  * Float32 arithmetic, one rounding at the end; angles keep float32 accuracy
- * at any position.  Supported: d in {64, 128}; rot a multiple of 16, at most
- * d; h_s % h_n == 0, h_s + h_n <= 1024.  No workspace, no allocation.
+ * (2^-26 of a turn) at any position, up to 2^50 turns.  Supported: d in {64,
+ * 128}; rot a multiple of 16, at most d; h_s % h_n == 0, h_s + h_n <= 1024.
+ * No workspace, no allocation.
  */
 int gda_qk_norm_rope(const void *q_sig, const void *k_sig, const void *q_noise, const void *k_noise,
                      const float *weight, const int *positions, const float *inv_freq, void *q_sig_out,
