@@ -438,6 +438,14 @@ def gda_attn_fwd_2pass(q_sig, k_sig, q_noise, k_noise, v, lam, lambda_init: floa
                     eps, out, flags)
 
 
+def _given(tensors, count, what):
+    """The caller's output tensors as a tuple of exactly `count`: the C entries take a pointer for each."""
+    tensors = tuple(tensors)
+    if len(tensors) != count:
+        raise ValueError(f"{what} holds {len(tensors)} tensors, expected {count}")
+    return tensors
+
+
 def gda_attn_bwd_workspace_size(B: int, L: int, h_s: int, d: int, dv: int) -> int:
     return int(_load().gda_attn_bwd_workspace_size(B, L, h_s, d, dv))
 
@@ -466,6 +474,7 @@ def gda_attn_bwd(q_sig, k_sig, q_noise, k_noise, v, lam, lambda_init: float, dy,
     _expect(dy, "dy", f32, (B, L, hs, dv), dev)
     if grads is None:
         grads = tuple(torch.empty(s, dtype=f32, device=dev) for s in shapes)
+    grads = _given(grads, 6, "grads")
     for t, name, shape in zip(grads, ("dq_sig", "dk_sig", "dq_noise", "dk_noise", "dv", "dlambda"), shapes):
         _expect(t, name, f32, shape, dev)
     need = gda_attn_bwd_workspace_size(B, L, hs, d, dv)
@@ -505,6 +514,7 @@ def gda_attn_bwd_bf16(q_sig, k_sig, q_noise, k_noise, v, lam, lambda_init: float
     _expect(dy, "dy", bf, (B, L, hs, dv), dev)
     if grads is None:
         grads = tuple(torch.empty(s, dtype=f32, device=dev) for s in shapes)
+    grads = _given(grads, 6, "grads")
     for t, name, shape in zip(grads, ("dq_sig", "dk_sig", "dq_noise", "dk_noise", "dv", "dlambda"), shapes):
         _expect(t, name, f32, shape, dev)
     need = gda_attn_bwd_bf16_workspace_size(B, L, hs, hn, dv)
@@ -736,6 +746,7 @@ def gda_qk_norm_rope(q_sig, k_sig, q_noise, k_noise, weight, positions, inv_freq
     if out is None:
         out = tuple([torch.empty(s, dtype=dt, device=dev) for s in shapes])
     else:
+        out = _given(out, 4, "out")
         for t, n, s in zip(out, _PROJECTIONS, shapes):
             _expect(t, "out " + n, dt, s, dev)
     lib = _load()
@@ -768,6 +779,7 @@ def gda_qk_norm_rope_bwd(q_sig, k_sig, q_noise, k_noise, weight, positions, inv_
                  torch.empty((4, d), dtype=torch.float32, device=dev))
         strides += [hs * d, hs * d, hn * d, hn * d]
     else:
+        grads = _given(grads, 5, "grads")
         strides += [_token_stride(t, "grads " + n, dt, s, dev) for t, n, s in zip(grads, _PROJECTIONS, shapes)]
         _expect(grads[4], "dweight", torch.float32, (4, d), dev)
     f32 = torch.float32
@@ -812,6 +824,7 @@ def gda_block_tables(cache_lens, new_lens, block_table, free_pages, free_count, 
     if out is None:
         out = tuple([torch.empty(s, dtype=i32, device=dev) for s in shapes])
     else:
+        out = _given(out, 5, "out")
         for t, n, s in zip(out, ("slot_map", "positions", "row_starts", "lens", "free_left"), shapes):
             _expect(t, n, i32, s, dev)
     _enqueue(_load().gda_block_tables, "gda block tables", dev,
@@ -892,6 +905,7 @@ def gda_cache_read_fp4(slot_map, k_sig_pool, k_noise_pool, v_pool, k_sig_block_s
     if out is None:
         out = tuple([torch.empty(s, dtype=torch.bfloat16, device=dev) for s in shapes])
     else:
+        out = _given(out, 3, "out")
         for t, n, s in zip(out, ("k_sig", "k_noise", "v"), shapes):
             _expect(t, n, torch.bfloat16, s, dev)
     _enqueue(_load().gda_cache_read_fp4, "gda 4-bit cache read", dev, slot_map.data_ptr(), *cache,
