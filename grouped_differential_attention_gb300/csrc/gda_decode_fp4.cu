@@ -396,7 +396,7 @@ __device__ __forceinline__ float load_queries(const Params &p, uint8_t *dst, int
 #pragma unroll
         for (int i = 0; i < D / 64; ++i) most = max(most, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
         most = __reduce_max_sync(0xffffffffu, most);
-        const int up = min(268 - static_cast<int>(most >> 7), 254);       // biased exponent of the factor
+        const int up = min(268 - static_cast<int>(most >> 7), 253);       // biased exponent of the factor (254 has no inverse)
         const float f = __uint_as_float(static_cast<uint32_t>(up) << 23);
 #pragma unroll
         for (int i = 0; i < D / 64; ++i)

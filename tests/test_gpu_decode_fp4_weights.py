@@ -90,3 +90,13 @@ def test_one_position_far_above_the_others_with_no_value(hs, hn, d, dv, gap):
     slots = torch.tensor([at, n + at], dtype=torch.int32, device="cuda")
     gda.gda_cache_append_fp4(*(t.bfloat16() for t in rows), slots, *c["pools"], *c["blocks"], *c["scales"])
     check(run(c, eps=0.0), c, 0.0)
+
+
+def test_queries_and_scales_at_the_ends_of_their_ranges():
+    """Queries of 2^-118 over keys with a head scale of 2^118, and the reverse: the scores are ordinary ones."""
+    for up in (118, 125, -110):
+        c = make(3, 100, 6, 2, 64, 128, [100, 33, 7], seed=up + 200)
+        for q, s in (("q1", 0), ("q2", 1)):
+            c[q] = (c[q].double() * 2.0 ** -up).bfloat16()
+            c["scales"][s] = (c["scales"][s].double() * 2.0 ** up).float()
+        check(run(c), c, 1e-5)
