@@ -39,7 +39,7 @@
 // Measured (both kernels; of the 6793 GB/s of a copy): 64 sequences of 4096 to
 // 8192, 12 + 4 heads of 64/128, 566 MB: 120 us (70 %); one of 131072, 24 + 8
 // heads, 378 MB: 93 us (60 %); 16 of up to 8191, 16 + 4 heads of 128/256,
-// 245 MB: 64 us (57 %).  The first one's split kernel takes 113 us; with the
+// 245 MB: 64 us (57 %).  The first one's split kernel takes 114 us; with the
 // weights rounded it took 108, of which the copies alone 98 and the arithmetic
 // alone 90: they overlap but for the start (a cold first tile arrives after
 // several us) and the slowest warps, 10 % behind the mean.

@@ -524,6 +524,8 @@ int gda_cache_read_fp4(const int *slot_map, const void *k_sig_pool, const void *
  * A length outside [0, Lcap] is clamped and reported (GDA_DEVERR_BAD_LENGTH);
  * a block-table entry outside the pool is read as page 0 and reported
  * (GDA_DEVERR_BAD_PAGE).  Cache rows past a sequence's length are never used.
+ * Softmax weights keep 22 bits, down to 2^-18 of the largest of their map, and
+ * 2^-40 of that largest below; sums are float32.
  *   workspace: device memory of at least
  *   gda_attn_decode_fp4_workspace_size(B, h_s, h_n, d, dv) bytes, 16-byte
  *   aligned, owned by the caller; needs no initialisation.  Calls in flight
