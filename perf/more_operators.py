@@ -319,8 +319,8 @@ def _plain_select(s):
         b = _by_block(s, bounds)[:, :most].float()
         dot = (torch.where(q8 > 0, q8, 0.0) * b[..., 0, :] + torch.where(q8 < 0, q8, 0.0) * b[..., 1, :]).sum(-1)
         x = dot * _by_block(s, scale)[:, :most] * amax[:, None]                       # whole numbers below 2^24: exact
-        x = torch.where(ok[:, None], x, 0.0).masked_fill(~there[..., None], -math.inf)
-        x = x - x.amax(1, keepdim=True).clamp(min=-3e38)
+        x = x.masked_fill(~there[..., None], -math.inf)
+        x = (x - x.amax(1, keepdim=True).clamp(min=-3e38)).masked_fill(~ok[:, None], -math.inf)
         score = torch.maximum(score, x.view(B, most, hn, r).amax(-1).transpose(1, 2))
     at = torch.arange(most, device=DEV)[None]
     forced = there & ((at < s["first"]) | (at >= count[:, None] - s["last"]))
