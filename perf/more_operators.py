@@ -367,8 +367,8 @@ def run(state):
                                            k_noise_bounds=s["bounds"][1])
             return [*gda.gda_cache_read_fp8_block(s["read"], *cache), *s["scales"], *s["bounds"]]
         if s["op"] == "select":
-            return list(gda.gda_block_select(s["q1"], s["q2"], *s["bounds"], *s["scales"], s["lens"], s["keep"],
-                                             block_table=s["table"], first=s["first"], last=s["last"]))
+            return list(gda.gda_block_select(s["q1"], s["q2"], *s["bounds"], *s["scales"], s["lens"], s["block"],
+                                             s["keep"], block_table=s["table"], first=s["first"], last=s["last"]))
         if s["op"] == "sparse":
             return gda.gda_attn_decode_sparse_fp8_block(s["q1"], s["q2"], *s["pools"], *s["scales"], s["blocks"],
                                                         s["counts"], s["lens"], s["lam"], LAMBDA_INIT,
