@@ -8,7 +8,8 @@ Five operators, as a serving loop runs them:
 * ``decode``: one query token per sequence over all of that cache, contiguous or
   paged (``gda_attn_decode_fp8_block``, ``gda_attn_decode_paged_fp8_block``);
 * ``select``: the blocks of each sequence and noise head that a score over the
-  bounds keeps (``gda_block_select``);
+  bounds keeps: the largest share that the block has, by the bound on its
+  logits, in one of the group's heads (``gda_block_select``);
 * ``sparse``: one query token per sequence over listed blocks only
   (``gda_attn_decode_sparse_fp8_block``).
 
@@ -309,7 +310,8 @@ def _plain_select(s):
     most = -(-s["hi"] // bl)
     count = (s["lens"].long() + bl - 1) // bl
     there = torch.arange(most, device=DEV)[None] < count[:, None]                     # [B, most]
-    score = torch.full((B, hn, most), -math.inf, device=DEV)
+    score = torch.zeros(B, hn, most, device=DEV)
+    unit = 4 / 127 / math.log(2) / math.sqrt(s["d"])                                  # from bounds to powers of two
     for q, bounds, scale, r in ((s["q1"], s["bounds"][0], s["scales"][0], hs // hn),
                                 (s["q2"], s["bounds"][1], s["scales"][1], 1)):
         f = q.float()
@@ -320,11 +322,16 @@ def _plain_select(s):
         dot = (torch.where(q8 > 0, q8, 0.0) * b[..., 0, :] + torch.where(q8 < 0, q8, 0.0) * b[..., 1, :]).sum(-1)
         x = dot * _by_block(s, scale)[:, :most] * amax[:, None]                       # whole numbers below 2^24: exact
         x = x.masked_fill(~there[..., None], -math.inf)
-        x = (x - x.amax(1, keepdim=True).clamp(min=-3e38)).masked_fill(~ok[:, None], -math.inf)
-        score = torch.maximum(score, x.view(B, most, hn, r).amax(-1).transpose(1, 2))
+        t = ((x - x.amax(1, keepdim=True).clamp(min=-3e38)) * unit).clamp(min=-126.0)
+        e = t.floor()                                                                 # 2^t, a straight line from e to e + 1
+        w = (((e.int() + 127) << 23) + torch.round((t - e) * 2.0 ** 23).int()).view(torch.float32)
+        w = torch.where(there[..., None] & ok[:, None], w, 0.0)
+        total = (w * 2.0 ** 40).long().sum(1, keepdim=True).float() * 2.0 ** -40      # whole numbers: in any order
+        share = w * torch.where(total > 0, 1.0 / total, 0.0)
+        score = torch.maximum(score, share.view(B, most, hn, r).amax(-1).transpose(1, 2))
     at = torch.arange(most, device=DEV)[None]
     forced = there & ((at < s["first"]) | (at >= count[:, None] - s["last"]))
-    score = score.masked_fill(forced[:, None], math.inf).masked_fill(~there[:, None], -math.inf)
+    score = score.masked_fill(forced[:, None], math.inf).masked_fill(~there[:, None], -1.0)
     order = torch.sort(score, dim=-1, descending=True, stable=True).indices[..., :keep]
     if order.shape[-1] < keep:
         order = torch.nn.functional.pad(order, (0, keep - order.shape[-1]), value=most)
