@@ -20,6 +20,11 @@ Around the attention: ``gda_qk_norm_rope`` (per-head norm and rotation of the
 four projections, with gradients), ``gda_block_tables`` (block table, slots and
 positions of a serving step), and a 4-bit cache (``gda_cache_append_fp4``,
 ``gda_cache_read_fp4``, ``gda_attn_decode_fp4``, ``gda_attn_decode_paged_fp4``).
+An 8-bit cache with a scale for each block of tokens and head
+(``gda_cache_append_fp8_block``, ``gda_cache_read_fp8_block``), decodes over all
+of it (``gda_attn_decode_fp8_block``, ``gda_attn_decode_paged_fp8_block``), and
+over the blocks that a bound on their logits keeps (``gda_block_select``,
+``gda_attn_decode_sparse_fp8_block``).
 """
 from __future__ import annotations
 
@@ -40,6 +45,9 @@ __all__ = [
     "gda_qk_norm_rope", "gda_qk_norm_rope_bwd", "gda_qk_norm_rope_bwd_workspace_size", "gda_block_tables",
     "gda_cache_append_fp4", "gda_cache_read_fp4", "gda_attn_decode_fp4", "gda_attn_decode_paged_fp4",
     "gda_attn_decode_fp4_workspace_size", "GDA_FLAG_ROPE_INTERLEAVED",
+    "gda_cache_append_fp8_block", "gda_cache_append_fp8_block_workspace_size", "gda_cache_read_fp8_block",
+    "gda_block_select", "gda_block_select_workspace_size", "gda_attn_decode_fp8_block",
+    "gda_attn_decode_paged_fp8_block", "gda_attn_decode_sparse_fp8_block", "gda_attn_decode_fp8_block_workspace_size",
 ]
 
 GDA_OK = 0
@@ -153,6 +161,24 @@ def _load():
             lib.gda_attn_decode_paged_fp4.restype = I
             lib.gda_attn_decode_fp4_workspace_size.argtypes = [I] * 5
             lib.gda_attn_decode_fp4_workspace_size.restype = Z
+            lib.gda_cache_append_fp8_block.argtypes = [P] * 12 + [I] * 8 + [X] * 3 + [P, Z, P]
+            lib.gda_cache_append_fp8_block.restype = I
+            lib.gda_cache_append_fp8_block_workspace_size.argtypes = [I] * 2
+            lib.gda_cache_append_fp8_block_workspace_size.restype = Z
+            lib.gda_cache_read_fp8_block.argtypes = [P] * 10 + [I] * 8 + [P]
+            lib.gda_cache_read_fp8_block.restype = I
+            lib.gda_block_select.argtypes = [P] * 10 + [I] * 11 + [P, Z, P]
+            lib.gda_block_select.restype = I
+            lib.gda_block_select_workspace_size.argtypes = [I] * 4
+            lib.gda_block_select_workspace_size.restype = Z
+            lib.gda_attn_decode_fp8_block.argtypes = [P] * 10 + [F, P] + [I] * 7 + [F, P, Z, P]
+            lib.gda_attn_decode_fp8_block.restype = I
+            lib.gda_attn_decode_paged_fp8_block.argtypes = [P] * 11 + [F, P] + [I] * 9 + [F, P, Z, P]
+            lib.gda_attn_decode_paged_fp8_block.restype = I
+            lib.gda_attn_decode_sparse_fp8_block.argtypes = [P] * 13 + [F, P] + [I] * 10 + [F, P, Z, P]
+            lib.gda_attn_decode_sparse_fp8_block.restype = I
+            lib.gda_attn_decode_fp8_block_workspace_size.argtypes = [I] * 5
+            lib.gda_attn_decode_fp8_block_workspace_size.restype = Z
             lib.gda_device_error.argtypes = [I]
             lib.gda_last_cuda_error.argtypes = []
             lib.gda_last_cuda_error.restype = I
@@ -978,6 +1004,255 @@ def gda_attn_decode_paged_fp4(q_sig, q_noise, k_sig_pool, k_noise_pool, v_pool, 
     return _decode_fp4(q_sig, q_noise, (k_sig_pool, k_noise_pool, v_pool),
                        (k_sig_block_scale, k_noise_block_scale, v_block_scale), (k_sig_scale, k_noise_scale, v_scale),
                        block_table, cache_lens, lam, lambda_init, eps, out, workspace)
+
+
+def _fp8_block_cache(pools, scales, hs, hn, d, dv, dev):
+    """Checks the six tensors of an 8-bit cache with block scales; returns their addresses, the rows of a page, the
+    number of pages and the tokens of a block."""
+    f32 = torch.float32
+    code = _FP8 if getattr(pools[0], "dtype", None) is _FP8 else torch.uint8
+    if not isinstance(scales[0], torch.Tensor) or scales[0].dim() != 3:
+        raise ValueError("scales must be [num_pages, page_size / block, heads]")
+    pages, size = pools[0].shape[:2]
+    per = scales[0].shape[1]
+    if per < 1 or size % per != 0:
+        raise ValueError(f"pages of {size} rows do not hold {per} blocks of equal size")
+    _int32(pages, size)
+    _expect_all(dev, (pools[0], "k_sig codes", code, (pages, size, hs, d)),
+                (pools[1], "k_noise codes", code, (pages, size, hn, d)),
+                (pools[2], "v codes", code, (pages, size, hs, dv)), (scales[0], "k_sig_scale", f32, (pages, per, hs)),
+                (scales[1], "k_noise_scale", f32, (pages, per, hn)), (scales[2], "v_scale", f32, (pages, per, hs)))
+    return [t.data_ptr() for t in (*pools, *scales)], size, pages, size // per
+
+
+def gda_cache_append_fp8_block_workspace_size(num_pages: int, page_size: int) -> int:
+    _int32(num_pages, page_size)
+    return int(_load().gda_cache_append_fp8_block_workspace_size(num_pages, page_size))
+
+
+def gda_cache_append_fp8_block(k_sig, k_noise, v, slot_map, k_sig_pool, k_noise_pool, v_pool, k_sig_scale,
+                               k_noise_scale, v_scale, *, k_sig_bounds=None, k_noise_bounds=None, workspace=None):
+    """Writes tokens' K and V rows (bf16 [T, heads, dim]) into an 8-bit cache with block scales, in place.
+
+    slot_map [T] int32 as for ``gda_cache_append_fp4``.  Pools [num_pages,
+    page_size, heads, dim] float8_e4m3fn (or uint8); scales [num_pages,
+    page_size / block, heads] float32, one for ``block`` (16, 32, 64 or 128)
+    consecutive rows of a page: a contiguous cache [B, Lcap, ...] is B pages of
+    Lcap.  A call that writes the first row of a block starts it anew, others
+    may raise its scale, and then the codes that are there follow.
+    k_sig_bounds, k_noise_bounds [num_pages, page_size / block, heads, 2, d]
+    int8 (both or neither) are kept for ``gda_block_select``.  The rows may be
+    slices of a fused projection.  See include/gda.h.
+    """
+    dev = k_sig.device
+    if dev.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    if k_sig.dim() != 3 or k_noise.dim() != 3 or v.dim() != 3 or k_sig_pool.dim() != 4:
+        raise ValueError("rows must be [T, heads, dim] and pools [num_pages, page_size, heads, dim]")
+    T, hs, d = k_sig.shape
+    hn, dv = k_noise.shape[1], v.shape[2]
+    bf = torch.bfloat16
+    strides = [_token_stride(t, n, bf, (T, h, dim), dev)
+               for t, n, h, dim in ((k_sig, "k_sig", hs, d), (k_noise, "k_noise", hn, d), (v, "v", hs, dv))]
+    cache, size, pages, block = _fp8_block_cache((k_sig_pool, k_noise_pool, v_pool), (k_sig_scale, k_noise_scale, v_scale),
+                                                 hs, hn, d, dv, dev)
+    _expect_all(dev, (slot_map, "slot_map", torch.int32, (T,)))
+    if (k_sig_bounds is None) != (k_noise_bounds is None):
+        raise ValueError("k_sig_bounds and k_noise_bounds are given both or not at all")
+    bounds = (None, None)
+    if k_sig_bounds is not None:
+        i8 = torch.int8
+        _expect_all(dev, (k_sig_bounds, "k_sig_bounds", i8, (pages, size // block, hs, 2, d)),
+                    (k_noise_bounds, "k_noise_bounds", i8, (pages, size // block, hn, 2, d)))
+        bounds = (k_sig_bounds.data_ptr(), k_noise_bounds.data_ptr())
+    lib = _load()
+    workspace = _workspace(workspace, lib.gda_cache_append_fp8_block_workspace_size(pages, size), dev)
+    _enqueue(lib.gda_cache_append_fp8_block, "gda 8-bit block cache append", dev, k_sig.data_ptr(), k_noise.data_ptr(),
+             v.data_ptr(), slot_map.data_ptr(), *cache, *bounds, T, pages, size, block, hs, hn, d, dv, *strides,
+             workspace.data_ptr(), workspace.numel())
+
+
+def gda_cache_read_fp8_block(slot_map, k_sig_pool, k_noise_pool, v_pool, k_sig_scale, k_noise_scale, v_scale, *,
+                             out=None):
+    """The rows of an 8-bit cache with block scales at slot_map [T] as bf16: (k_sig, k_noise, v), each [T, heads, dim].
+
+    Zero rows for negative slots.  ``out`` may hold the three tensors.  The
+    cache is as in ``gda_cache_append_fp8_block``; the rows of a sequence's
+    slots, in order, are the keys and values of a prefix for
+    ``gda_attn_fwd_chunk``.
+    """
+    dev = slot_map.device
+    if dev.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    if slot_map.dim() != 1 or k_sig_pool.dim() != 4 or k_noise_pool.dim() != 4 or v_pool.dim() != 4:
+        raise ValueError("slot_map must be 1-D and pools [num_pages, page_size, heads, dim]")
+    T = slot_map.numel()
+    hs, d = k_sig_pool.shape[2:]
+    hn, dv = k_noise_pool.shape[2], v_pool.shape[3]
+    cache, size, pages, block = _fp8_block_cache((k_sig_pool, k_noise_pool, v_pool), (k_sig_scale, k_noise_scale, v_scale),
+                                                 hs, hn, d, dv, dev)
+    _expect_all(dev, (slot_map, "slot_map", torch.int32, (T,)))
+    bf = torch.bfloat16
+    shapes = ((T, hs, d), (T, hn, d), (T, hs, dv))
+    if out is None:
+        out = tuple([torch.empty(s, dtype=bf, device=dev) for s in shapes])
+    else:
+        out = _given(out, 3, "out")
+        for t, n, s in zip(out, ("k_sig", "k_noise", "v"), shapes):
+            _expect(t, n, bf, s, dev)
+    _enqueue(_load().gda_cache_read_fp8_block, "gda 8-bit block cache read", dev, slot_map.data_ptr(), *cache,
+             *[t.data_ptr() for t in out], T, pages, size, block, hs, hn, d, dv)
+    return tuple(out)
+
+
+def _pages_of_sequences(block_table, pages, B, dev):
+    """Address of the block table and its pages a sequence; contiguous caches are a page for each sequence."""
+    if block_table is None:
+        if pages != B:
+            raise ValueError(f"caches hold {pages} sequences, expected {B}")
+        return None, 1
+    if not isinstance(block_table, torch.Tensor):
+        raise TypeError("block_table must be a torch.Tensor")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    max_pages = block_table.shape[1]
+    _expect_all(dev, (block_table, "block_table", torch.int32, (B, max_pages)))
+    _int32(max_pages)
+    return block_table.data_ptr(), max_pages
+
+
+def gda_block_select_workspace_size(B: int, max_blocks: int, h_s: int, h_n: int) -> int:
+    _int32(B, max_blocks, h_s, h_n)
+    return int(_load().gda_block_select_workspace_size(B, max_blocks, h_s, h_n))
+
+
+def gda_block_select(q_sig, q_noise, k_sig_bounds, k_noise_bounds, k_sig_scale, k_noise_scale, cache_lens, block: int,
+                     keep: int, *, block_table=None, first: int = 1, last: int = 1, out=None, workspace=None):
+    """The ``keep`` blocks of each sequence that its queries are to attend, by a bound on their logits.
+
+    q_sig [B, h_s, d], q_noise [B, h_n, d] bf16 (as the decode takes them);
+    bounds and key scales as ``gda_cache_append_fp8_block`` keeps them for
+    blocks of ``block`` tokens; cache_lens [B] int32; block_table [B, max_pages]
+    int32, or None for contiguous caches.  Returns (block_list [B, h_n, keep]
+    int32, ascending and then -1, block_count [B] int32) for
+    ``gda_attn_decode_sparse_fp8_block``: all blocks of a sequence that has no
+    more, else its first ``first`` and last ``last`` ones and those of the
+    highest score (include/gda.h).  ``out`` may hold the two.
+    """
+    dev = q_sig.device
+    if dev.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    if q_sig.dim() != 3 or q_noise.dim() != 3:
+        raise ValueError("queries must be [B, heads, d]")
+    if not isinstance(k_sig_bounds, torch.Tensor) or k_sig_bounds.dim() != 5:
+        raise ValueError("bounds must be [num_pages, page_size / block, heads, 2, d]")
+    B, hs, d = q_sig.shape
+    hn = q_noise.shape[1]
+    pages, per = k_sig_bounds.shape[:2]
+    bf, i8, i32, f32 = torch.bfloat16, torch.int8, torch.int32, torch.float32
+    _int32(pages, per * block, keep, first, last)
+    _expect_all(dev, (q_sig, "q_sig", bf, (B, hs, d)), (q_noise, "q_noise", bf, (B, hn, d)),
+                (k_sig_bounds, "k_sig_bounds", i8, (pages, per, hs, 2, d)),
+                (k_noise_bounds, "k_noise_bounds", i8, (pages, per, hn, 2, d)),
+                (k_sig_scale, "k_sig_scale", f32, (pages, per, hs)),
+                (k_noise_scale, "k_noise_scale", f32, (pages, per, hn)), (cache_lens, "cache_lens", i32, (B,)))
+    table, max_pages = _pages_of_sequences(block_table, pages, B, dev)
+    shapes = ((B, hn, keep), (B,))
+    if out is None:
+        out = tuple([torch.empty(s, dtype=i32, device=dev) for s in shapes])
+    else:
+        out = _given(out, 2, "out")
+        _expect_all(dev, (out[0], "block_list", i32, shapes[0]), (out[1], "block_count", i32, shapes[1]))
+    lib = _load()
+    _int32(max_pages * per)
+    workspace = _workspace(workspace, lib.gda_block_select_workspace_size(B, max_pages * per, hs, hn), dev)
+    _enqueue(lib.gda_block_select, "gda block selection", dev, q_sig.data_ptr(), q_noise.data_ptr(),
+             k_sig_bounds.data_ptr(), k_noise_bounds.data_ptr(), k_sig_scale.data_ptr(), k_noise_scale.data_ptr(), table,
+             cache_lens.data_ptr(), *[t.data_ptr() for t in out], B, max_pages, per * block, pages, block, keep, first,
+             last, hs, hn, d, workspace.data_ptr(), workspace.numel())
+    return tuple(out)
+
+
+def gda_attn_decode_fp8_block_workspace_size(B: int, h_s: int, h_n: int, d: int, dv: int) -> int:
+    _int32(B, h_s, h_n, d, dv)
+    return int(_load().gda_attn_decode_fp8_block_workspace_size(B, h_s, h_n, d, dv))
+
+
+def _decode_fp8_block(q_sig, q_noise, pools, scales, block_table, lists, cache_lens, lam, lambda_init, eps, out,
+                      workspace):
+    dev = q_sig.device
+    if dev.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    if q_sig.dim() != 3 or q_noise.dim() != 3 or pools[0].dim() != 4 or pools[2].dim() != 4:
+        raise ValueError("bad ranks: q [B, heads, d], caches [.., .., heads, dim]")
+    B, hs, d = q_sig.shape
+    hn, dv = q_noise.shape[1], pools[2].shape[3]
+    bf, i32 = torch.bfloat16, torch.int32
+    _expect_all(dev, (q_sig, "q_sig", bf, (B, hs, d)), (q_noise, "q_noise", bf, (B, hn, d)),
+                (cache_lens, "cache_lens", i32, (B,)), (lam, "lam", torch.float32, (hs,)))
+    cache, size, pages, block = _fp8_block_cache(pools, scales, hs, hn, d, dv, dev)
+    table, max_pages = _pages_of_sequences(block_table, pages, B, dev)
+    if out is None:
+        out = torch.empty((B, hs, dv), dtype=bf, device=dev)
+    else:
+        _expect(out, "out", bf, (B, hs, dv), dev)
+    lib = _load()
+    workspace = _workspace(workspace, lib.gda_attn_decode_fp8_block_workspace_size(B, hs, hn, d, dv), dev)
+    head = (q_sig.data_ptr(), q_noise.data_ptr(), *cache)
+    body = (cache_lens.data_ptr(), lam.data_ptr(), float(lambda_init), out.data_ptr(), B)
+    tail = (hs, hn, d, dv, float(eps), workspace.data_ptr(), workspace.numel())
+    what = "gda decode (8-bit block cache)"
+    if lists is not None:
+        block_list, block_count = lists
+        if not isinstance(block_list, torch.Tensor) or block_list.dim() != 3:
+            raise ValueError("block_list must be [B, h_n, keep]")
+        keep = block_list.shape[2]
+        _int32(keep)
+        _expect_all(dev, (block_list, "block_list", i32, (B, hn, keep)), (block_count, "block_count", i32, (B,)))
+        _enqueue(lib.gda_attn_decode_sparse_fp8_block, what, dev, *head, table, block_list.data_ptr(),
+                 block_count.data_ptr(), *body, max_pages, size, pages, block, keep, *tail)
+    elif table is None:
+        _enqueue(lib.gda_attn_decode_fp8_block, what, dev, *head, *body, size, block, *tail)
+    else:
+        _enqueue(lib.gda_attn_decode_paged_fp8_block, what, dev, *head, table, *body, max_pages, size, pages, block, *tail)
+    return out
+
+
+def gda_attn_decode_fp8_block(q_sig, q_noise, k_sig_cache, k_noise_cache, v_cache, k_sig_scale, k_noise_scale, v_scale,
+                              cache_lens, lam, lambda_init: float, *, eps: float = 1e-5, out=None, workspace=None):
+    """bf16 decode over 8-bit caches with a scale for each block of tokens and head: cached value = code * scale.
+
+    Caches [B, Lcap, heads, dim] float8_e4m3fn (or uint8), scales [B, Lcap /
+    block, heads] float32, as ``gda_cache_append_fp8_block`` writes them.  A
+    cache length of 0 gives a zero row.
+    """
+    return _decode_fp8_block(q_sig, q_noise, (k_sig_cache, k_noise_cache, v_cache), (k_sig_scale, k_noise_scale, v_scale),
+                             None, None, cache_lens, lam, lambda_init, eps, out, workspace)
+
+
+def gda_attn_decode_paged_fp8_block(q_sig, q_noise, k_sig_pool, k_noise_pool, v_pool, k_sig_scale, k_noise_scale,
+                                    v_scale, block_table, cache_lens, lam, lambda_init: float, *, eps: float = 1e-5,
+                                    out=None, workspace=None):
+    """``gda_attn_decode_fp8_block`` over page pools [num_pages, page_size, heads, dim], scales [num_pages, page_size /
+    block, heads] and a block table [B, max_pages] int32 (position j of sequence b is row j % page_size of page
+    block_table[b, j // page_size])."""
+    if not isinstance(block_table, torch.Tensor):
+        raise TypeError("block_table must be a torch.Tensor")
+    return _decode_fp8_block(q_sig, q_noise, (k_sig_pool, k_noise_pool, v_pool), (k_sig_scale, k_noise_scale, v_scale),
+                             block_table, None, cache_lens, lam, lambda_init, eps, out, workspace)
+
+
+def gda_attn_decode_sparse_fp8_block(q_sig, q_noise, k_sig_pool, k_noise_pool, v_pool, k_sig_scale, k_noise_scale,
+                                     v_scale, block_list, block_count, cache_lens, lam, lambda_init: float, *,
+                                     block_table=None, eps: float = 1e-5, out=None, workspace=None):
+    """The decode over listed blocks only: block_list [B, h_n, keep] and block_count [B] int32 as ``gda_block_select``
+    gives them (a block counts as often as it is listed, negative entries are passed over).
+
+    Page pools and ``block_table`` as in ``gda_attn_decode_paged_fp8_block``, or contiguous caches without one.  Both
+    softmax maps are normalised over the listed positions; a row without any is zero.
+    """
+    return _decode_fp8_block(q_sig, q_noise, (k_sig_pool, k_noise_pool, v_pool), (k_sig_scale, k_noise_scale, v_scale),
+                             block_table, (block_list, block_count), cache_lens, lam, lambda_init, eps, out, workspace)
 
 
 def gda_device_error(clear: bool = True) -> int:

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 #include <mutex>
 
 #include "gda.h"
@@ -177,6 +178,77 @@ int fill_cache_fp4(CacheFp4Args &a, int num_pages, int page_size, int hs, int hn
     }
     a.slots = num_pages * page_size;
     return current_device(&a.dev_err);
+}
+
+// What the calls over an 8-bit cache with a scale for each block of tokens ask of its geometry.
+bool block_fits(int block) { return block == 16 || block == 32 || block == 64 || block == 128; }
+
+int check_pages(int num_pages, int page_size, int block) {
+    if (num_pages < 1 || page_size < 1 || block < 1 || page_size % block != 0) return GDA_ERR_INVALID_ARG;
+    return block_fits(block) ? GDA_OK : GDA_ERR_UNSUPPORTED;
+}
+
+bool aligned4(std::initializer_list<const void *> ptrs) {
+    uintptr_t any = 0;
+    for (const void *p : ptrs) any |= reinterpret_cast<uintptr_t>(p);
+    return (any & 3u) == 0;
+}
+
+// Checks the arguments of gda_cache_append_fp8_block and gda_cache_read_fp8_block and fills what follows from them.
+int fill_cache_fp8_block(CacheFp8BlockArgs &a, int num_pages, int page_size, int hs, int hn, int d, int dv) {
+    if (!a.slot_map) return GDA_ERR_INVALID_ARG;
+    for (int t = 0; t < 3; ++t)
+        if (!a.rows[t] || !a.codes[t] || !a.scale[t]) return GDA_ERR_INVALID_ARG;
+    if (!a.bounds[0] != !a.bounds[1]) return GDA_ERR_INVALID_ARG;
+    if (a.T < 1 || hs < 1 || hn < 1 || d < 1 || dv < 1 || hs % hn != 0) return GDA_ERR_INVALID_ARG;
+    const int st = check_pages(num_pages, page_size, a.block);
+    if (st != GDA_OK) return st;
+    if (static_cast<long long>(num_pages) * page_size > 0x7fffffffLL) return GDA_ERR_INVALID_ARG;
+    if (!(d == 64 || d == 128) || !(dv == 64 || dv == 128 || dv == 256)) return GDA_ERR_UNSUPPORTED;
+    if (heads_above(hs, hn, 128)) return GDA_ERR_UNSUPPORTED;
+    if (!aligned4({a.slot_map, a.scale[0], a.scale[1], a.scale[2]})) return GDA_ERR_MISALIGNED;
+    a.heads[0] = a.heads[2] = hs, a.heads[1] = hn, a.dims[0] = a.dims[1] = d, a.dims[2] = dv;
+    for (int t = 0; t < 3; ++t) {
+        if (a.ld[t] < static_cast<long long>(a.heads[t]) * a.dims[t] || a.ld[t] > (1LL << 40)) return GDA_ERR_INVALID_ARG;
+        if (a.ld[t] % 8 != 0 || !aligned16(a.rows[t]) || !aligned16(a.codes[t])) return GDA_ERR_MISALIGNED;
+    }
+    if (!aligned16(a.bounds[0]) || !aligned16(a.bounds[1])) return GDA_ERR_MISALIGNED;
+    a.slots = num_pages * page_size;
+    return GDA_OK;
+}
+
+// Checks what the three decodes over that cache have in common, and launches.
+int decode_fp8_block(DecodeFp8BlockArgs &a, size_t workspace_bytes, gda_stream_t stream) {
+    const void *ptrs[] = {a.q1, a.q2, a.k1c, a.k2c, a.vc, a.out};
+    for (const void *p : ptrs)
+        if (!p) return GDA_ERR_INVALID_ARG;
+    if (!a.k1s || !a.k2s || !a.vs || !a.lens || !a.lambda) return GDA_ERR_INVALID_ARG;
+    if (a.B < 1 || a.max_pages < 1 || a.hs < 1 || a.hn < 1 || a.d < 1 || a.dv < 1 || a.hs % a.hn != 0)
+        return GDA_ERR_INVALID_ARG;
+    int st = check_pages(a.num_pages, a.page_size, a.block);
+    if (st == GDA_ERR_INVALID_ARG) return st;
+    if (!std::isfinite(a.eps) || a.eps < 0.f || !std::isfinite(a.lambda_init)) return GDA_ERR_INVALID_ARG;
+    const long long Lcap = static_cast<long long>(a.max_pages) * a.page_size;
+    const double rows = static_cast<double>(a.num_pages) * a.page_size;
+    if (Lcap > 0x7fffffffLL || rows * a.hs * (a.d > a.dv ? a.d : a.dv) > 9.0e15) return GDA_ERR_INVALID_ARG;
+    if (a.list && a.keep < 1) return GDA_ERR_INVALID_ARG;
+    if (st != GDA_OK) return st;
+    if (!(a.d == 64 || a.d == 128) || !(a.dv == 64 || a.dv == 128 || a.dv == 256)) return GDA_ERR_UNSUPPORTED;
+    if (heads_above(a.hs, a.hn, 128) || a.B > 65535) return GDA_ERR_UNSUPPORTED;
+    if (rows > 4294967296.0) return GDA_ERR_UNSUPPORTED;   // rows of the caches are counted in 32 bits
+    // positions are 32 bits wide and stepped by 16; a range (a 19th of the batch's at most) is counted in 32 bits too
+    const long long reach = a.list ? static_cast<long long>(a.keep) * a.block : Lcap;
+    if (Lcap > 0x7ffffff0 || reach > 0x7ffffff0 || a.B * reach > 1LL << 35) return GDA_ERR_UNSUPPORTED;
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return GDA_ERR_MISALIGNED;
+    if (!aligned16(a.lens) || !aligned16(a.lambda)) return GDA_ERR_MISALIGNED;
+    if (!aligned4({a.k1s, a.k2s, a.vs, a.block_table, a.list, a.count})) return GDA_ERR_MISALIGNED;
+    if (!a.workspace || !aligned16(a.workspace) ||
+        workspace_bytes < decode_fp8_block_workspace_bytes(a.B, a.hs, a.hn, a.d, a.dv))
+        return GDA_ERR_WORKSPACE;
+    a.Lcap = static_cast<int>(Lcap);
+    if ((st = device_state(&a.dev_err)) != GDA_OK) return st;
+    return launch_decode_fp8_block(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 struct Four {
@@ -787,6 +859,136 @@ int gda_block_tables(const int *cache_lens, const int *new_lens, int *block_tabl
     const int st = current_device(&a.dev_err);
     if (st != GDA_OK) return st;
     return launch_block_tables(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int gda_cache_append_fp8_block(const void *k_sig, const void *k_noise, const void *v, const int *slot_map,
+                               void *k_sig_pool, void *k_noise_pool, void *v_pool, float *k_sig_scale,
+                               float *k_noise_scale, float *v_scale, int8_t *k_sig_bounds, int8_t *k_noise_bounds, int T,
+                               int num_pages, int page_size, int block, int h_s, int h_n, int d, int dv,
+                               long long k_sig_stride, long long k_noise_stride, long long v_stride, void *workspace,
+                               size_t workspace_bytes, gda_stream_t stream) {
+    CacheFp8BlockArgs a{{k_sig, k_noise, v}, {k_sig_stride, k_noise_stride, v_stride}, slot_map,
+                        {static_cast<uint8_t *>(k_sig_pool), static_cast<uint8_t *>(k_noise_pool),
+                         static_cast<uint8_t *>(v_pool)},
+                        {k_sig_scale, k_noise_scale, v_scale}, {k_sig_bounds, k_noise_bounds}, {}, {}, T, 0, block,
+                        static_cast<int *>(workspace), nullptr};
+    int st = fill_cache_fp8_block(a, num_pages, page_size, h_s, h_n, d, dv);
+    if (st != GDA_OK) return st;
+    if (!workspace || !aligned16(workspace) ||
+        workspace_bytes < gda_cache_append_fp8_block_workspace_size(num_pages, page_size))
+        return GDA_ERR_WORKSPACE;
+    if ((st = current_device(&a.dev_err)) != GDA_OK) return st;
+    return launch_cache_append_fp8_block(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t gda_cache_append_fp8_block_workspace_size(int num_pages, int page_size) {
+    if (num_pages < 1 || page_size < 1 || static_cast<long long>(num_pages) * page_size > 0x7fffffffLL) return 0;
+    return static_cast<size_t>(num_pages) * page_size * sizeof(int);
+}
+
+int gda_cache_read_fp8_block(const int *slot_map, const void *k_sig_pool, const void *k_noise_pool, const void *v_pool,
+                             const float *k_sig_scale, const float *k_noise_scale, const float *v_scale,
+                             void *k_sig_out, void *k_noise_out, void *v_out, int T, int num_pages, int page_size,
+                             int block, int h_s, int h_n, int d, int dv, gda_stream_t stream) {
+    auto pool = [](const void *x) { return const_cast<uint8_t *>(bytes_of(x)); };
+    auto scale = [](const float *x) { return const_cast<float *>(x); };
+    CacheFp8BlockArgs a{{k_sig_out, k_noise_out, v_out},
+                        {static_cast<long long>(h_s) * d, static_cast<long long>(h_n) * d, static_cast<long long>(h_s) * dv},
+                        slot_map, {pool(k_sig_pool), pool(k_noise_pool), pool(v_pool)},
+                        {scale(k_sig_scale), scale(k_noise_scale), scale(v_scale)}, {}, {}, {}, T, 0, block, nullptr, nullptr};
+    int st = fill_cache_fp8_block(a, num_pages, page_size, h_s, h_n, d, dv);
+    if (st != GDA_OK) return st;
+    if ((st = current_device(&a.dev_err)) != GDA_OK) return st;
+    return launch_cache_read_fp8_block(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t gda_block_select_workspace_size(int B, int max_blocks, int h_s, int h_n) {
+    if (B < 1 || max_blocks < 1 || h_s < 1 || h_n < 1 || h_s % h_n != 0) return 0;
+    if (B > 65535 || max_blocks > kBlockSelectMaxBlocks || heads_above(h_s, h_n, 128)) return 0;
+    return static_cast<size_t>(B) * max_blocks * (h_s + h_n) * sizeof(float);
+}
+
+int gda_block_select(const void *q_sig, const void *q_noise, const int8_t *k_sig_bounds, const int8_t *k_noise_bounds,
+                     const float *k_sig_scale, const float *k_noise_scale, const int *block_table, const int *cache_lens,
+                     int *block_list, int *block_count, int B, int max_pages, int page_size, int num_pages, int block,
+                     int keep, int first, int last, int h_s, int h_n, int d, void *workspace, size_t workspace_bytes,
+                     gda_stream_t stream) {
+    if (!q_sig || !q_noise || !k_sig_bounds || !k_noise_bounds || !k_sig_scale || !k_noise_scale || !cache_lens ||
+        !block_list || !block_count)
+        return GDA_ERR_INVALID_ARG;
+    if (B < 1 || max_pages < 1 || h_s < 1 || h_n < 1 || d < 1 || h_s % h_n != 0) return GDA_ERR_INVALID_ARG;
+    if (keep < 1 || first < 0 || last < 0 || first > keep || last > keep - first) return GDA_ERR_INVALID_ARG;
+    if (!block_table && (max_pages != 1 || num_pages != B)) return GDA_ERR_INVALID_ARG;
+    int st = check_pages(num_pages, page_size, block);
+    if (st != GDA_OK) return st;
+    if (static_cast<long long>(max_pages) * page_size > 0x7fffffffLL) return GDA_ERR_INVALID_ARG;
+    if (!(d == 64 || d == 128) || heads_above(h_s, h_n, 128) || B > 65535) return GDA_ERR_UNSUPPORTED;
+    const long long most = static_cast<long long>(max_pages) * (page_size / block);
+    if (most > kBlockSelectMaxBlocks || static_cast<double>(num_pages) * page_size > 4294967296.0)
+        return GDA_ERR_UNSUPPORTED;
+    if (!aligned16(q_sig) || !aligned16(q_noise) || !aligned16(k_sig_bounds) || !aligned16(k_noise_bounds))
+        return GDA_ERR_MISALIGNED;
+    if (!aligned4({k_sig_scale, k_noise_scale, block_table, cache_lens, block_list, block_count}))
+        return GDA_ERR_MISALIGNED;
+    if (!workspace || !aligned16(workspace) ||
+        workspace_bytes < gda_block_select_workspace_size(B, static_cast<int>(most), h_s, h_n))
+        return GDA_ERR_WORKSPACE;
+    BlockSelectArgs a{q_sig, q_noise, k_sig_bounds, k_noise_bounds, k_sig_scale, k_noise_scale, block_table, cache_lens,
+                      block_list, block_count, B, max_pages, page_size, num_pages, block, keep, first, last, h_s, h_n, d,
+                      static_cast<float>(4.0 / 127.0 / std::log(2.0) / std::sqrt(static_cast<double>(d))),
+                      static_cast<float *>(workspace), nullptr};
+    if ((st = current_device(&a.dev_err)) != GDA_OK) return st;
+    return launch_block_select(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t gda_attn_decode_fp8_block_workspace_size(int B, int h_s, int h_n, int d, int dv) {
+    if (B < 1 || h_s < 1 || h_n < 1 || d < 1 || dv < 1 || h_s % h_n != 0) return 0;
+    if (B > 65535 || heads_above(h_s, h_n, 128)) return 0;
+    if (!(d == 64 || d == 128) || !(dv == 64 || dv == 128 || dv == 256)) return 0;
+    return decode_fp8_block_workspace_bytes(B, h_s, h_n, d, dv);
+}
+
+int gda_attn_decode_fp8_block(const void *q_sig, const void *q_noise, const void *k_sig_cache, const void *k_noise_cache,
+                              const void *v_cache, const float *k_sig_scale, const float *k_noise_scale,
+                              const float *v_scale, const int *cache_lens, const float *lambda, float lambda_init,
+                              void *out, int B, int Lcap, int block, int h_s, int h_n, int d, int dv, float eps,
+                              void *workspace, size_t workspace_bytes, gda_stream_t stream) {
+    DecodeFp8BlockArgs a{q_sig, q_noise, bytes_of(k_sig_cache), bytes_of(k_noise_cache), bytes_of(v_cache), k_sig_scale,
+                         k_noise_scale, v_scale, cache_lens, lambda, lambda_init, out, B, 0, block, h_s, h_n, d, dv, eps,
+                         workspace, nullptr};
+    a.page_size = Lcap, a.max_pages = 1, a.num_pages = B;
+    return decode_fp8_block(a, workspace_bytes, stream);
+}
+
+int gda_attn_decode_paged_fp8_block(const void *q_sig, const void *q_noise, const void *k_sig_pool,
+                                    const void *k_noise_pool, const void *v_pool, const float *k_sig_scale,
+                                    const float *k_noise_scale, const float *v_scale, const int *block_table,
+                                    const int *cache_lens, const float *lambda, float lambda_init, void *out, int B,
+                                    int max_pages, int page_size, int num_pages, int block, int h_s, int h_n, int d,
+                                    int dv, float eps, void *workspace, size_t workspace_bytes, gda_stream_t stream) {
+    if (!block_table) return GDA_ERR_INVALID_ARG;
+    DecodeFp8BlockArgs a{q_sig, q_noise, bytes_of(k_sig_pool), bytes_of(k_noise_pool), bytes_of(v_pool), k_sig_scale,
+                         k_noise_scale, v_scale, cache_lens, lambda, lambda_init, out, B, 0, block, h_s, h_n, d, dv, eps,
+                         workspace, nullptr};
+    a.block_table = block_table, a.page_size = page_size, a.max_pages = max_pages, a.num_pages = num_pages;
+    return decode_fp8_block(a, workspace_bytes, stream);
+}
+
+int gda_attn_decode_sparse_fp8_block(const void *q_sig, const void *q_noise, const void *k_sig_pool,
+                                     const void *k_noise_pool, const void *v_pool, const float *k_sig_scale,
+                                     const float *k_noise_scale, const float *v_scale, const int *block_table,
+                                     const int *block_list, const int *block_count, const int *cache_lens,
+                                     const float *lambda, float lambda_init, void *out, int B, int max_pages,
+                                     int page_size, int num_pages, int block, int keep, int h_s, int h_n, int d, int dv,
+                                     float eps, void *workspace, size_t workspace_bytes, gda_stream_t stream) {
+    if (!block_list || !block_count) return GDA_ERR_INVALID_ARG;
+    if (!block_table && (max_pages != 1 || num_pages != B)) return GDA_ERR_INVALID_ARG;
+    DecodeFp8BlockArgs a{q_sig, q_noise, bytes_of(k_sig_pool), bytes_of(k_noise_pool), bytes_of(v_pool), k_sig_scale,
+                         k_noise_scale, v_scale, cache_lens, lambda, lambda_init, out, B, 0, block, h_s, h_n, d, dv, eps,
+                         workspace, nullptr};
+    a.block_table = block_table, a.page_size = page_size, a.max_pages = max_pages, a.num_pages = num_pages;
+    a.list = block_list, a.count = block_count, a.keep = keep;
+    return decode_fp8_block(a, workspace_bytes, stream);
 }
 
 const char *gda_status_string(int status) {

@@ -121,6 +121,53 @@ struct DecodeFp4Args {
     int page_size = 0, max_pages = 0, num_pages = 0;
 };
 
+// Rows of the three cached tensors and the 8-bit pools with a scale for each block of tokens that they go to or come from.
+struct CacheFp8BlockArgs {
+    const void *rows[3];            // bf16 [T, heads, dim]
+    long long ld[3];                // elements between tokens
+    const int *slot_map;            // [T], negative: leave the token out
+    uint8_t *codes[3];              // e4m3 [slots, heads, dim]
+    float *scale[3];                // [slots / block, heads]
+    int8_t *bounds[2];              // [slots / block, heads, 2, d] of the keys, or nullptr
+    int heads[3], dims[3];
+    long long T;
+    int slots, block;               // block: a power of two
+    int *index;                     // [slots]: workspace
+    unsigned *dev_err;
+};
+
+struct BlockSelectArgs {
+    const void *q1, *q2;                                   // bf16 [B, heads, d]
+    const int8_t *k1b, *k2b;                               // [pages, page_size / block, heads, 2, d]
+    const float *k1s, *k2s;                                // [pages, page_size / block, heads]
+    const int *block_table;                                // nullptr: page b is sequence b
+    const int *lens;
+    int *list, *count;                                     // [B, hn, keep], [B]
+    int B, max_pages, page_size, num_pages, block, keep, first, last, hs, hn, d;
+    float unit;                                            // 4 / (127 ln 2 sqrt(d)): from x to powers of two
+    float *scores;                                         // workspace: [B, hs + hn, blocks]
+    unsigned *dev_err;
+};
+constexpr int kBlockSelectMaxBlocks = 32768;
+
+struct DecodeFp8BlockArgs {
+    const void *q1, *q2;                                   // bf16 [B, heads, d]
+    const uint8_t *k1c, *k2c, *vc;                         // e4m3 codes [pages, page_size, heads, dim]
+    const float *k1s, *k2s, *vs;                           // [pages, page_size / block, heads]
+    const int *lens;
+    const float *lambda;
+    float lambda_init;
+    void *out;
+    int B, Lcap, block, hs, hn, d, dv;                     // block: a power of two
+    float eps;
+    void *workspace;
+    unsigned *dev_err;
+    const int *block_table = nullptr;                      // nullptr: contiguous caches [B, Lcap, heads, dim]
+    int page_size = 0, max_pages = 0, num_pages = 0;       // contiguous: Lcap, 1, B
+    const int *list = nullptr, *count = nullptr;           // [B, hn, keep], [B]: only these blocks
+    int keep = 0;
+};
+
 // Remembers `e` as this thread's last CUDA error (see gda_last_cuda_error),
 // clears the runtime's sticky-free error state and returns GDA_ERR_CUDA.
 int record_cuda_error(cudaError_t e);
@@ -157,6 +204,12 @@ size_t qk_norm_rope_bwd_workspace_bytes(int T, int hs, int hn, int d);
 int launch_block_tables(const BlockTablesArgs &a, cudaStream_t stream);
 int launch_decode_fp4(const DecodeFp4Args &a, cudaStream_t stream);
 size_t decode_fp4_workspace_bytes(int B, int hs, int hn, int d, int dv);
+
+int launch_cache_append_fp8_block(const CacheFp8BlockArgs &a, cudaStream_t stream);
+int launch_cache_read_fp8_block(const CacheFp8BlockArgs &a, cudaStream_t stream);
+int launch_block_select(const BlockSelectArgs &a, cudaStream_t stream);
+int launch_decode_fp8_block(const DecodeFp8BlockArgs &a, cudaStream_t stream);
+size_t decode_fp8_block_workspace_bytes(int B, int hs, int hn, int d, int dv);
 
 // Split plan of the decode kernel (positions per split and split count).
 struct DecodePlan {

@@ -552,6 +552,151 @@ int gda_attn_decode_paged_fp4(const void *q_sig, const void *q_noise, const void
 /* Bytes of workspace gda_attn_decode_fp4 and gda_attn_decode_paged_fp4 need (0 for invalid sizes). */
 size_t gda_attn_decode_fp4_workspace_size(int B, int h_s, int h_n, int d, int dv);
 
+/*
+ * 8-bit cache with a scale for each block of tokens and head, and keys'
+ * bounds for choosing blocks.  A cached tensor (K_sig [slots, h_s, d], K_noise
+ * [slots, h_n, d], V [slots, h_s, dv]; slots = num_pages * page_size, or B *
+ * Lcap of a contiguous cache) is held as
+ *   codes [slots, heads, dim]           e4m3
+ *   scale [slots / block, heads]        float32, of `block` consecutive slots
+ * and stands for code * scale.  block: 16, 32, 64 or 128; page_size (Lcap) is
+ * a multiple of it.  Any finite scales >= 0 may be read; those that are
+ * written here are powers of two.
+ *   bounds [slots / block, heads, 2, d] int8, of K_sig and K_noise: the
+ *     greatest of ceil(code / 4) and the least of floor(code / 4) over the
+ *     rows written to the block, for every channel (-128 and 127: none).
+ *
+ * gda_cache_append_fp8_block writes T tokens' rows (bf16, `*_stride` elements
+ * between tokens, a multiple of 8) to the slots slot_map[T] (int32; negative:
+ * the token is left out; past the pool: left out and reported through
+ * gda_device_error as GDA_DEVERR_BAD_PAGE), in any order.  For a block and a
+ * head, with x the rows that this call writes there: s is the least power of
+ * two >= 2^-126 with |x| <= 448 s; the scale becomes max(scale, s), and codes
+ * that are there are multiplied by (old scale / new) and rounded again (exact
+ * down to e4m3's subnormals); code = e4m3(x * (1 / scale)), to the nearest,
+ * ties to even (|x| at most 1.875 * 2^127: the next code would stand for
+ * 2^128).  NaN and infinities become NaN codes and count neither for s nor for
+ * the bounds.  A call that writes a block's first slot starts the
+ * block anew: scale and bounds are those of its rows alone, and slots of the
+ * block that it does not write hold nothing of meaning.  Nothing outside the
+ * blocks of slot_map's slots is touched.  The slots of a call differ (of two
+ * rows with one slot, one whole row is written).  Scales, codes and bounds of
+ * a block that no call has started are not read.
+ *   k_sig_bounds, k_noise_bounds: both, or both NULL (then not kept).
+ *   workspace: device memory of at least
+ *   gda_cache_append_fp8_block_workspace_size(num_pages, page_size) bytes (4 a
+ *   slot), 16-byte aligned, owned by the caller; needs no initialisation.
+ *   Calls in flight at the same time need a workspace each.
+ *
+ * gda_cache_read_fp8_block is the reverse: rows of the slots as dense bf16
+ * [T, heads, dim], rounded once (exact for scales that are powers of two; zero
+ * rows for slots that append leaves out): the keys and values of a cached
+ * prefix for gda_attn_fwd_chunk.
+ *
+ * Supported: d in {64, 128}; dv in {64, 128, 256}; h_s + h_n <= 128; fewer
+ * than 2^31 slots.  Pointers 16-byte aligned, slot_map and scales 4-byte.
+ * GDA_ERR_INVALID_ARG also for a page_size that block does not divide.
+ */
+int gda_cache_append_fp8_block(const void *k_sig, const void *k_noise, const void *v, const int *slot_map,
+                               void *k_sig_pool, void *k_noise_pool, void *v_pool, float *k_sig_scale,
+                               float *k_noise_scale, float *v_scale, int8_t *k_sig_bounds, int8_t *k_noise_bounds, int T,
+                               int num_pages, int page_size, int block, int h_s, int h_n, int d, int dv,
+                               long long k_sig_stride, long long k_noise_stride, long long v_stride, void *workspace,
+                               size_t workspace_bytes, gda_stream_t stream);
+int gda_cache_read_fp8_block(const int *slot_map, const void *k_sig_pool, const void *k_noise_pool, const void *v_pool,
+                             const float *k_sig_scale, const float *k_noise_scale, const float *v_scale,
+                             void *k_sig_out, void *k_noise_out, void *v_out, int T, int num_pages, int page_size,
+                             int block, int h_s, int h_n, int d, int dv, gda_stream_t stream);
+
+/* Bytes of workspace gda_cache_append_fp8_block needs (0 for invalid sizes). */
+size_t gda_cache_append_fp8_block_workspace_size(int num_pages, int page_size);
+
+/*
+ * The blocks that a decode step is to attend, chosen by a bound on their
+ * logits, for gda_attn_decode_sparse_fp8_block.  For every head h, with
+ * q8 = rint(q * (127 / amax)), amax = max |q| (float32):
+ *   x_h(block) = (sum over channels of max(q8 * greatest, q8 * least)) * scale_h(block) * amax
+ * from the block's bounds and key scale, a bound on its logits up to a factor;
+ * with t = (x_h(block) - max over the sequence's blocks of x_h) * 4 / (127 ln 2
+ * sqrt(d)) and w_h = 2^floor(t) (1 + t - floor(t)), about 2^t, the block's share
+ * of head h is w_h / (sum of w_h over the blocks), and its score the largest
+ * share among the heads of a noise head's group (its signal heads and itself).
+ * A head whose amax is below 2^-100 or not finite takes no part.  A sequence
+ * of n = ceil(cache_lens[b] / block) blocks keeps all of them if n <= keep,
+ * else its first `first` and last `last` ones and the highest scores up to
+ * keep, of equal scores the lower block.
+ *   k_sig_bounds, k_noise_bounds, k_sig_scale, k_noise_scale: as
+ *   gda_cache_append_fp8_block keeps them.
+ *   block_table [B, max_pages] int32 and page pools, or NULL for contiguous
+ *   caches (then max_pages = 1, page_size = Lcap, num_pages = B).
+ *   block_list [B, h_n, keep] int32: the blocks of the sequence (position /
+ *   block) that each noise head keeps, ascending, then -1.
+ *   block_count [B] int32: min(n, keep).
+ *   workspace: gda_block_select_workspace_size(B, max_pages * page_size /
+ *   block, h_s, h_n) bytes, 16-byte aligned, owned by the caller, needs no
+ *   initialisation; calls in flight at the same time need a workspace each.
+ * A length outside [0, max_pages * page_size] is clamped and reported
+ * (GDA_DEVERR_BAD_LENGTH), a page outside the pool is read as page 0 and
+ * reported (GDA_DEVERR_BAD_PAGE).  The result does not depend on the order of
+ * any sum.  Supported: d in {64, 128}; h_s + h_n <= 128; B <= 65535; block 16,
+ * 32, 64 or 128; at most 32768 blocks a sequence; at most 2^32 rows in the
+ * caches; first + last <= keep.
+ */
+int gda_block_select(const void *q_sig, const void *q_noise, const int8_t *k_sig_bounds, const int8_t *k_noise_bounds,
+                     const float *k_sig_scale, const float *k_noise_scale, const int *block_table, const int *cache_lens,
+                     int *block_list, int *block_count, int B, int max_pages, int page_size, int num_pages, int block,
+                     int keep, int first, int last, int h_s, int h_n, int d, void *workspace, size_t workspace_bytes,
+                     gda_stream_t stream);
+
+/* Bytes of workspace gda_block_select needs (0 for invalid sizes). */
+size_t gda_block_select_workspace_size(int B, int max_blocks, int h_s, int h_n);
+
+/*
+ * Decode over that 8-bit cache: the operation of gda_attn_decode on the values
+ * the format stands for.  Contiguous (codes [B, Lcap, heads, dim], scales [B,
+ * Lcap / block, heads]), paged (page pools and a block table as in
+ * gda_attn_decode_paged), or sparse: over the listed blocks of each sequence
+ * and noise head only, both softmax maps normalised over those.
+ *   Queries, lambda, out, cache_lens, their clamping and the errors of block
+ *   tables as in gda_attn_decode_fp4: a length of 0 gives a zero row.
+ *   block_list [B, h_n, keep], block_count [B] (sparse), as gda_block_select
+ *   gives them: the first block_count[b] entries of a list are attended;
+ *   negative ones are passed over, positions from cache_lens[b] on do not
+ *   exist, a block listed twice counts twice, and a row for which no position
+ *   is left is zero.  A count outside [0, keep] is clamped and reported
+ *   (GDA_DEVERR_BAD_LENGTH).  block_table may be NULL: contiguous caches
+ *   (max_pages = 1, page_size = Lcap, num_pages = B).
+ *   workspace: at least gda_attn_decode_fp8_block_workspace_size(B, h_s, h_n,
+ *   d, dv) bytes, 16-byte aligned, owned by the caller, needs no
+ *   initialisation; calls in flight at the same time need a workspace each.
+ * Supported: d in {64, 128}; dv in {64, 128, 256}; h_s + h_n <= 128;
+ * B <= 65535; block 16, 32, 64 or 128, dividing page_size (Lcap); Lcap
+ * (max_pages * page_size) at most 2^31 - 16; at most 2^32 rows in the caches;
+ * B times Lcap (sparse: times keep * block, itself at most 2^31 - 16) at most
+ * 2^35.
+ */
+int gda_attn_decode_fp8_block(const void *q_sig, const void *q_noise, const void *k_sig_cache, const void *k_noise_cache,
+                              const void *v_cache, const float *k_sig_scale, const float *k_noise_scale,
+                              const float *v_scale, const int *cache_lens, const float *lambda, float lambda_init,
+                              void *out, int B, int Lcap, int block, int h_s, int h_n, int d, int dv, float eps,
+                              void *workspace, size_t workspace_bytes, gda_stream_t stream);
+int gda_attn_decode_paged_fp8_block(const void *q_sig, const void *q_noise, const void *k_sig_pool,
+                                    const void *k_noise_pool, const void *v_pool, const float *k_sig_scale,
+                                    const float *k_noise_scale, const float *v_scale, const int *block_table,
+                                    const int *cache_lens, const float *lambda, float lambda_init, void *out, int B,
+                                    int max_pages, int page_size, int num_pages, int block, int h_s, int h_n, int d,
+                                    int dv, float eps, void *workspace, size_t workspace_bytes, gda_stream_t stream);
+int gda_attn_decode_sparse_fp8_block(const void *q_sig, const void *q_noise, const void *k_sig_pool,
+                                     const void *k_noise_pool, const void *v_pool, const float *k_sig_scale,
+                                     const float *k_noise_scale, const float *v_scale, const int *block_table,
+                                     const int *block_list, const int *block_count, const int *cache_lens,
+                                     const float *lambda, float lambda_init, void *out, int B, int max_pages,
+                                     int page_size, int num_pages, int block, int keep, int h_s, int h_n, int d, int dv,
+                                     float eps, void *workspace, size_t workspace_bytes, gda_stream_t stream);
+
+/* Bytes of workspace the three decodes above need (0 for invalid sizes). */
+size_t gda_attn_decode_fp8_block_workspace_size(int B, int h_s, int h_n, int d, int dv);
+
 /* Static English description of a gda_status value. */
 const char *gda_status_string(int status);
 

@@ -137,3 +137,109 @@ def unpack(packed):
     out = np.empty(packed.shape[:-1] + (2 * packed.shape[-1],), dtype=np.uint8)
     out[..., 0::2], out[..., 1::2] = packed & 15, packed >> 4
     return out
+
+
+# ---- 8-bit cache with a scale for each block of tokens and head ----
+
+def round_e4m3(x):
+    """float64 x to the nearest e4m3 value, ties to even, at most 448 in magnitude; NaN stays."""
+    x = np.asarray(x, dtype=np.float64)
+    with np.errstate(all="ignore"):
+        step = np.exp2(np.floor(np.log2(np.maximum(np.abs(x), 2.0 ** -6))) - 3)
+        y = np.round(x / step) * step                       # np.round: ties to even
+    return np.clip(y, -448.0, 448.0)
+
+
+def e4m3_byte(values):
+    """Bytes of float64 e4m3 values (exact)."""
+    return torch.from_numpy(np.asarray(values, dtype=np.float32)).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+
+
+def append_fp8_block(x, slots, codes, scale, bounds=None):
+    """Rows x [T, heads, n] (bf16 torch) into codes [slots, heads, n] uint8, scale [slots / block, heads] float32 and
+    bounds [slots / block, heads, 2, n] int8 (numpy, in place), one block of tokens after the other."""
+    x = x.double().numpy()
+    slots = np.asarray(slots)
+    block = codes.shape[0] // scale.shape[0]
+    f32 = np.float32
+    rows_of = {}
+    for t, s in enumerate(slots):
+        if 0 <= s < codes.shape[0]:
+            rows_of.setdefault(s // block, []).append(t)
+    for blk, rows in rows_of.items():
+        first = blk * block
+        fresh = first in slots[rows]
+        for h in range(x.shape[1]):
+            v = x[rows, h]
+            amax = float(np.abs(v[np.isfinite(v)]).max(initial=0.0))
+            need = 2.0 ** -126
+            while amax > 448 * need:
+                need *= 2
+            old = f32(0) if fresh else scale[blk, h]
+            new = max(f32(need), old)
+            scale[blk, h] = new
+            with np.errstate(all="ignore"):
+                shift = f32(1) if fresh else old / new
+                if shift != 1:
+                    was = e4m3_value(codes[first:first + block, h]).astype(f32)
+                    codes[first:first + block, h] = e4m3_byte(round_e4m3((was * shift).astype(f32)))
+                y = (v.astype(f32) * (f32(1) / new)).astype(f32)
+                limit = min(f32(448), f32(1.875 * 2.0 ** 127) / new)     # the next code would stand for 2^128
+                y = np.clip(y, -limit, limit)
+            y = round_e4m3(np.where(np.isfinite(v), y, np.nan))
+            codes[slots[rows], h] = e4m3_byte(y)
+            if bounds is None:
+                continue
+            top, low = bounds[blk, h].astype(np.float64)
+            if fresh:
+                top, low = np.full_like(top, -128), np.full_like(low, 127)
+            else:
+                top, low = np.ceil(top * shift), np.floor(low * shift)
+            known = np.isfinite(y)
+            top = np.maximum(top, np.where(known, np.ceil(y / 4), -128).max(0))
+            low = np.minimum(low, np.where(known, np.floor(y / 4), 127).min(0))
+            bounds[blk, h] = np.stack((top, low)).astype(np.int8)
+
+
+def block_select(q1, q2, bounds, scales, table, lens, block, keep, first, last):
+    """(lists [B][hn], counts [B]) in whole numbers and float32, one sequence and noise head at a time.
+
+    bounds, scales: numpy pairs [pages, blocks of a page, heads, ..]; table [B, max_pages] or None."""
+    f32 = np.float32
+    q = [t.float().numpy() for t in (q1, q2)]
+    B, hs, hn = len(lens), q[0].shape[1], q[1].shape[1]
+    per = bounds[0].shape[1]
+    lists, counts = [], []
+    for b in range(B):
+        n = -(-int(lens[b]) // block)
+        counts.append(min(n, keep))
+        at = [(int(table[b, j // per]) if table is not None else b, j % per) for j in range(n)]
+        lists.append([])
+        for g in range(hn):
+            if n <= keep:
+                lists[-1].append(list(range(n)))
+                continue
+            score = np.zeros(n, dtype=f32)
+            r = hs // hn
+            for i, h in [(0, h) for h in range(g * r, g * r + r)] + [(1, g)]:
+                x = q[i][b, h]
+                amax = f32(np.abs(x).max())
+                if not (np.isfinite(x).all() and amax >= 2.0 ** -100):
+                    continue
+                q8 = np.rint((x * (f32(127) / amax)).astype(f32)).astype(np.int64)
+                v = np.empty(n, dtype=f32)
+                for j, place in enumerate(at):
+                    hi, lo = bounds[i][place][h].astype(np.int64)
+                    ub = int((np.maximum(q8, 0) * hi + np.minimum(q8, 0) * lo).sum())
+                    v[j] = f32(f32(ub) * scales[i][place][h]) * amax
+                unit = f32(4 / 127 / np.log(2) / np.sqrt(x.size))
+                t = np.maximum(((v - v.max()).astype(f32) * unit).astype(f32), f32(-126))
+                e = np.floor(t)
+                line = 2.0 ** 23 + np.rint((t - e).astype(f32) * 2.0 ** 23).astype(np.float64)
+                w = line * 2.0 ** (e.astype(np.float64) - 23)
+                total = f32(sum(int(k) for k in np.floor(w * 2.0 ** 40))) * f32(2.0 ** -40)
+                score = np.maximum(score, (w.astype(f32) * (f32(1) / total)).astype(f32))
+            forced = [j for j in range(n) if j < first or j >= n - last]
+            rest = sorted((j for j in range(n) if j not in forced), key=lambda j: (-score[j], j))
+            lists[-1].append(sorted(forced + rest[:keep - len(forced)]))
+    return lists, counts
