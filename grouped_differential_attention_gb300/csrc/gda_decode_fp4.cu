@@ -50,6 +50,7 @@
 #include <cstdint>
 
 #include "gda.h"
+#include "gda_decode_join.cuh"
 #include "gda_device.cuh"
 #include "gda_fp4.cuh"
 #include "gda_internal.h"
@@ -62,7 +63,6 @@ constexpr int kTile = 16;              // positions of a tile
 // Fewest positions of a range: a tile.  4 sequences of 37 to 600, us of both kernels: 15 with 16, 15.5 with 32, 17.2 with
 // 64, 22.7 with 128.
 constexpr int kMinRange = 16;
-constexpr int kSms = 152;              // SMs that the plan counts on
 constexpr float kWeightBits = 15.f;    // weights carry a factor 2^15: the largest is within f16, the smallest far from its end
 
 // Signal heads of a warp: a noise head's group in equal parts of at most three
@@ -158,6 +158,8 @@ __device__ __forceinline__ int length_of(const Params &p, int b) {
     atomicOr(p.err, GDA_DEVERR_BAD_LENGTH);
     return len < 0 ? 0 : p.Lcap;
 }
+
+__device__ __forceinline__ int positions_of(const Params &p, int b) { return length_of(p, b); }
 
 // Cache row of position pos of sequence b.  A page outside the pool is read
 // as page 0 and reported.  (The caches have 2^32 rows at most.)
@@ -674,107 +676,6 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32, (Tile<D, DV, RH>::blocks)
     }
 }
 
-// grid (h_s, B): joins the parts of one (sequence, head).  DV / 2 threads
-// hold the DV + DV columns of (O1, O2), four each, with the maximum and sum of
-// their map; THREADS / (DV / 2) such groups share the parts, each joining its
-// own as it reads them (a part's statistics and values are fetched together),
-// and are joined with one another at the end.
-template <int DV, int THREADS>
-__global__ void __launch_bounds__(THREADS) gda_decode_fp4_combine_kernel(const Params p) {
-    constexpr int COLS = DV / 2, GROUPS = THREADS / COLS, HALF = COLS / 2;
-    __shared__ float4 sums[GROUPS][COLS];
-    __shared__ float2 stats[GROUPS][2];
-    // a programmatic dependent of the split kernel: this wait returns once that grid has completed and its writes are visible
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int h = blockIdx.x, b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int col = threadIdx.x % COLS, group = threadIdx.x / COLS;
-    const bool second = col >= HALF;
-    __nv_bfloat16 *out = p.out + (static_cast<size_t>(b) * p.hs + h) * DV;
-    const int2 seg = reinterpret_cast<const int2 *>(p.ws_seg)[b];
-    if (length_of(p, b) == 0) {          // no position: the row is zero
-        if (threadIdx.x < DV / 2) reinterpret_cast<uint32_t *>(out)[threadIdx.x] = 0u;
-        return;
-    }
-    // ranges c0 .. c1 left a part in slots c + b (clamped so that a damaged workspace cannot send the reads astray)
-    const int c0 = min(max(seg.x, 0), p.splits - 1), c1 = min(max(seg.y, c0), p.splits - 1);
-    const size_t at0 = (static_cast<size_t>(c0) + b) * p.hs + h;
-    const int parts = c1 - c0 + 1;
-    const float2 *ml = reinterpret_cast<const float2 *>(p.ws_ml) + at0 * 2 + second;
-    const float4 *o = reinterpret_cast<const float4 *>(p.ws_o) + at0 * COLS + col;
-
-    float m = -INFINITY, l = 0.f;
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int c = group; c < parts; c += GROUPS) {
-        const size_t at = static_cast<size_t>(c) * p.hs;
-        const float2 s = ml[at * 2];
-        const float4 v = o[at * COLS];
-        const float top = fmaxf(m, s.x), f = fast_exp2(m - top), g = fast_exp2(s.x - top);
-        m = top;
-        l = fmaf(s.y, g, l * f);
-        sum.x = fmaf(v.x, g, sum.x * f);
-        sum.y = fmaf(v.y, g, sum.y * f);
-        sum.z = fmaf(v.z, g, sum.z * f);
-        sum.w = fmaf(v.w, g, sum.w * f);
-    }
-    sums[group][col] = sum;
-    if (col % HALF == 0) stats[group][second] = make_float2(m, l);
-    __syncthreads();
-    if (threadIdx.x >= HALF) return;       // whole warps from here on, or half a warp (DV = 64)
-    // groups beyond the parts hold (-inf, 0); the first one has at least one part
-    const int used = min(GROUPS, parts);
-    float M1 = -INFINITY, M2 = -INFINITY, L1 = 0.f, L2 = 0.f;
-    for (int g = 0; g < used; ++g) M1 = fmaxf(M1, stats[g][0].x), M2 = fmaxf(M2, stats[g][1].x);
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), d = a;
-    for (int g = 0; g < used; ++g) {
-        const float f1 = fast_exp2(stats[g][0].x - M1), f2 = fast_exp2(stats[g][1].x - M2);
-        const float4 x = sums[g][col], y = sums[g][col + HALF];
-        L1 = fmaf(stats[g][0].y, f1, L1), L2 = fmaf(stats[g][1].y, f2, L2);
-        a.x = fmaf(x.x, f1, a.x), a.y = fmaf(x.y, f1, a.y), a.z = fmaf(x.z, f1, a.z), a.w = fmaf(x.w, f1, a.w);
-        d.x = fmaf(y.x, f2, d.x), d.y = fmaf(y.y, f2, d.y), d.z = fmaf(y.z, f2, d.z), d.w = fmaf(y.w, f2, d.w);
-    }
-    const float i1 = 1.f / L1, i2 = p.lambda[h] / L2;
-    const float v[4] = {a.x * i1 - d.x * i2, a.y * i1 - d.y * i2, a.z * i1 - d.z * i2, a.w * i1 - d.w * i2};
-    float ss = v[0] * v[0] + v[1] * v[1] + v[2] * v[2] + v[3] * v[3];
-    constexpr unsigned mask = HALF >= 32 ? 0xffffffffu : 0xffffu;
-#pragma unroll
-    for (int off = (HALF >= 32 ? 32 : HALF) / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(mask, ss, off);
-    if constexpr (HALF > 32) {             // DV = 256: two warps
-        __shared__ float both[2];
-        if (lane == 0) both[warp] = ss;
-        named_bar_sync(1, HALF);
-        ss = both[0] + both[1];
-    }
-    const float y = (1.f - p.lambda_init) * rsqrtf(ss * (1.f / DV) + p.eps);
-    reinterpret_cast<uint2 *>(out)[col] = make_uint2(pack_bf16x2(v[0] * y, v[1] * y), pack_bf16x2(v[2] * y, v[3] * y));
-}
-
-template <int DV, int THREADS>
-cudaError_t launch_combine(const Params &p, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(p.hs, p.B);
-    cfg.blockDim = dim3(THREADS);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, gda_decode_fp4_combine_kernel<DV, THREADS>, p);
-    return e == cudaSuccess ? cudaGetLastError() : e;
-}
-
-// The fewer the rows, the more parts each has and the more threads an SM can
-// give it.  us with 256 / 512 / 1024 threads: 24 rows of 152 parts 22.6 / 15.0
-// / 8.1, of up to 38 8.3 / 6.8 / 5.8; 256 rows 9.2 / 6.7 / 8.5; 768 rows 5.8 /
-// 7.6 / 13.6.  So 1024 up to a row an SM, 512 up to two, 256 beyond.
-template <int DV>
-cudaError_t launch_combine(const Params &p, cudaStream_t stream) {
-    const int rows = p.hs * p.B;
-    if (rows <= kSms) return launch_combine<DV, 1024>(p, stream);
-    return rows <= 2 * kSms ? launch_combine<DV, 512>(p, stream) : launch_combine<DV, 256>(p, stream);
-}
-
 template <int D, int DV, int RH>
 cudaError_t launch_split(const Params &p, cudaStream_t stream) {
     using T = Tile<D, DV, RH>;
@@ -826,9 +727,9 @@ int launch_decode_fp4(const DecodeFp4Args &a, cudaStream_t stream) {
         default: return GDA_ERR_UNSUPPORTED;
     }
     if (e != cudaSuccess) return record_cuda_error(e);
-    e = a.dv == 64    ? launch_combine<64>(p, stream)
-        : a.dv == 128 ? launch_combine<128>(p, stream)
-                      : launch_combine<256>(p, stream);
+    e = a.dv == 64    ? launch_join<64>(p, stream)
+        : a.dv == 128 ? launch_join<128>(p, stream)
+                      : launch_join<256>(p, stream);
     return e == cudaSuccess ? GDA_OK : record_cuda_error(e);
 }
 

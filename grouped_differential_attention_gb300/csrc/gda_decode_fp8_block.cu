@@ -1,13 +1,47 @@
 // Grouped differential attention decode over an 8-bit KV cache with a scale
 // for each block of tokens and head (one new query token per sequence; format
 // in gda_fp8_block.cuh), contiguous or paged, over all positions of a sequence
-// or over the blocks that a list names.
+// or over the blocks that a list names; split over the cache length, plus a
+// pass that joins the parts.
+//
+// The batch's positions, sequence after sequence, each rounded up to whole
+// tiles of 16 (of a list: count * block), are cut into equal contiguous
+// ranges.  A warp, which is a block of threads of its own, takes one range for
+// one noise head and up to RH signal heads that share it: it copies a tile at a
+// time into a ring in shared memory (cp.async) and keeps the online softmax of
+// all its maps and the accumulators O1, O2 in registers.  A tile lies in one
+// block of tokens, so its rows follow one another in the cache and every head
+// has one scale.  Each part of a range that lies in one sequence leaves (m, l)
+// of both maps and (O1, O2) in workspace slot (range + sequence), which is
+// unique because along the position axis neither index falls and one grows
+// from part to part.
+//
+// The tensor cores multiply (mma.sync m16n8k16, f16 in, float32 out; a decode
+// has one query row for a head, so the 128-row tcgen05 forms would sit idle for
+// 127), because on the CUDA cores an element costs a widening and one (K) or
+// two (V) multiply-adds, more than they can do at the copy rate.  e4m3 codes
+// are exact in f16, and so is the query after a power of two.
+//   - scores: A = codes of 16 positions x 16 dims, B = the query in every
+//     column; the block's scale is a factor of the score.
+//   - values: A = codes of 16 dims x 16 positions, B = four columns of weights,
+//     the upper and the lower part of both maps', the other four zero, so that
+//     two tiles of dims share one set of accumulators.  A weight is two f16
+//     numbers, so that it keeps 22 bits down to 2^-18 of its map's largest and
+//     2^-40 of that below.  The block's scale of V is in the weights, relative
+//     to the largest such scale so far: a larger one shrinks the accumulators,
+//     as a larger score does.
+// Step g of the loop copies K of tile g + A and V of the tile before that one,
+// scores tile g and adds the values of tile g - 1 in one run of instructions:
+// the chain from scores to weights has the values' work beside it, and no more
+// than a tile is held while it is used.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
 #include "gda.h"
+#include "gda_decode_join.cuh"
 #include "gda_device.cuh"
 #include "gda_fp8_block.cuh"
 #include "gda_internal.h"
@@ -15,157 +49,620 @@
 namespace gda {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kTile = 16;              // positions of a tile
+constexpr int kMinRange = 16;          // fewest positions of a range
+constexpr float kWeightBits = 15.f;    // weights carry a factor 2^15: the largest is within f16, the smallest far from its end
+constexpr float kLowest = -3.0e38f;    // a maximum over no position
+
+// Signal heads of a warp: a noise head's group in equal parts of at most three
+// (two at dv = 256).  Every part reads and scores the noise head for itself, and
+// where the parts do not divide the group the last one does a head again, so a
+// part costs about its heads and one more; the fewest of those are taken, of as
+// many the smaller parts.
+struct Heads {
+    int parts, each;   // parts of a group; signal heads of a part
+};
+Heads heads_of(int hs, int hn, int dv) {
+    const int r = hs / hn, most = dv == 256 ? 2 : 3;
+    Heads h{r, 1};
+    for (int each = 2; each <= most && each <= r; ++each) {
+        const int parts = (r + each - 1) / each;
+        if (parts * (each + 1) < h.parts * (h.each + 1)) h = {parts, each};
+    }
+    return h;
+}
+
+// Shared memory of a warp, in bytes: tiles (codes of rh + 1 rows of K and rh of
+// V for 16 positions, and their scales), then queries and weights.
+__host__ __device__ constexpr int tile_bytes(int rh, int d, int dv) { return kTile * ((rh + 1) * d + rh * dv) + 32; }
+__host__ __device__ constexpr int other_bytes(int rh, int d) { return (rh + 1) * d * 2 + 2 * rh * 128; }
+
+constexpr int kMaxStages = 6;
+// Warps that share an SM.
+__host__ __device__ constexpr int warps_per_sm(int rh, int d, int dv) {
+    int warps = 8;
+    while (warps > 1 && (227 * 1024 / warps - 1024 - other_bytes(rh, d)) / tile_bytes(rh, d, dv) < 3) --warps;
+    return warps;
+}
+__host__ __device__ constexpr int stages_of(int rh, int d, int dv) {
+    const int fit = (227 * 1024 / warps_per_sm(rh, d, dv) - 1024 - other_bytes(rh, d)) / tile_bytes(rh, d, dv);
+    return fit > kMaxStages ? kMaxStages : fit;
+}
+
+struct Plan {
+    Heads heads;
+    int splits;        // ranges at most
+    size_t ml_at, seg_at, bytes;
+};
+
+Plan plan_of(int B, int hs, int hn, int d, int dv) {
+    Plan p;
+    p.heads = heads_of(hs, hn, dv);
+    p.splits = std::max(1, kSms * warps_per_sm(p.heads.each, d, dv) / (hn * p.heads.parts));
+    const size_t slots = static_cast<size_t>(p.splits) + B;
+    p.ml_at = (slots * hs * 2 * dv * sizeof(float) + 255) / 256 * 256;
+    p.seg_at = p.ml_at + (slots * hs * 4 * sizeof(float) + 255) / 256 * 256;
+    p.bytes = p.seg_at + static_cast<size_t>(B) * 2 * sizeof(int);
+    return p;
+}
+
+struct Params {
+    const __nv_bfloat16 *q1, *q2;
+    const uint8_t *k1c, *k2c, *vc;
+    const float *k1s, *k2s, *vs;
+    const int *lens;
+    const float *lambda;
+    __nv_bfloat16 *out;
+    float *ws_o;       // [slots][hs][2][dv]
+    float *ws_ml;      // [slots][hs][4]: m1, l1, m2, l2
+    int *ws_seg;       // [B][2]: first and last range of a sequence
+    unsigned *err;
+    float lambda_init, eps, scale_log2;
+    int B, Lcap, hs, hn;
+    int splits, parts;                       // ranges; parts of a noise head's group
+    const int *block_table;
+    int page_size, max_pages, num_pages;
+    int shift;                               // log2 of a block's tokens
+    const int *list, *count;                 // [B][hn][keep], [B], or nullptr: all blocks
+    int keep;
+};
 
 // Length of sequence b; one outside [0, Lcap] is clamped and reported.
-__device__ __forceinline__ int length_of(const DecodeFp8BlockArgs &p, int b) {
+__device__ __forceinline__ int length_of(const Params &p, int b) {
     const int len = p.lens[b];
     if (len >= 0 && len <= p.Lcap) return len;
-    atomicOr(p.dev_err, GDA_DEVERR_BAD_LENGTH);
+    atomicOr(p.err, GDA_DEVERR_BAD_LENGTH);
     return len < 0 ? 0 : p.Lcap;
 }
 
-// Cache row of position pos of sequence b.  A page outside the pool is read as page 0 and reported.
-__device__ __forceinline__ uint32_t row_of(const DecodeFp8BlockArgs &p, int b, int pos) {
-    const int pg = pos / p.page_size;
+// Positions of sequence b along the axis that is cut into ranges: a multiple of 16.
+__device__ __forceinline__ int positions_of(const Params &p, int b) {
+    const int len = length_of(p, b);
+    if (p.list == nullptr) return (len + kTile - 1) / kTile * kTile;
+    int count = p.count[b];
+    if (count < 0 || count > p.keep) {
+        atomicOr(p.err, GDA_DEVERR_BAD_LENGTH);
+        count = count < 0 ? 0 : p.keep;
+    }
+    return len == 0 ? 0 : count << p.shift;
+}
+
+// The range [start, end) of a split in the concatenated positions, and where it begins.
+struct Range {
+    long long start, end, per, before;   // before: positions of the sequences ahead of b
+    int b;
+};
+
+// Computed by a whole warp; false if the split has nothing to do.
+__device__ __forceinline__ bool range_of(const Params &p, int split, Range &r) {
+    const int lane = threadIdx.x & 31;
+    long long total = 0;
+#pragma unroll 4
+    for (int b = lane; b < p.B; b += 32) total += positions_of(p, b);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    r.per = max(static_cast<long long>(kMinRange), (total + p.splits - 1) / p.splits);
+    r.per = (r.per + kTile - 1) / kTile * kTile;
+    r.start = split * r.per;
+    r.end = min(total, r.start + r.per);
+    if (r.start >= total) return false;
+    long long carry = 0;
+    for (int base = 0; base < p.B; base += 32) {
+        const int b = base + lane;
+        const long long len = b < p.B ? positions_of(p, b) : 0;
+        long long incl = len;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        const long long before = carry + incl - len;
+        const unsigned hit = __ballot_sync(0xffffffffu, before <= r.start && r.start < before + len);
+        if (hit) {
+            const int src = __ffs(hit) - 1;
+            r.b = base + src;
+            r.before = __shfl_sync(0xffffffffu, before, src);
+            return true;
+        }
+        carry += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return false;                         // not reached: start < total
+}
+
+// Notes the first and last range of every sequence that begins in range r of split `split`, for the joining kernel.
+__device__ __forceinline__ void note_sequences(const Params &p, const Range &r, int split) {
+    long long before = r.before;
+    for (int b = r.b; before < r.end; ++b) {
+        const int len = positions_of(p, b);
+        if (len > 0 && before >= r.start && (threadIdx.x & 31) == 0) {
+            p.ws_seg[2 * b] = split;
+            p.ws_seg[2 * b + 1] = static_cast<int>((before + len - 1) / r.per);
+        }
+        before += len;
+    }
+}
+
+// BYTES into shared memory, asynchronous; zeros in their place if `ok` is false.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, bool ok) {
+    const int n = ok ? BYTES : 0;
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n) : "memory");
+}
+
+// a * b + c: 16 x 16 (f16) times 16 x 8 (f16).
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// A place in a warp's range: sequence b, positions [pos, hi) of it, and the positions of the range after those.
+struct Cursor {
+    int b, pos, hi, left;
+};
+
+__device__ __forceinline__ void enter(Cursor &c, int pos, int len) {
+    const int n = min(len - pos, c.left);
+    c.pos = pos;
+    c.hi = pos + n;
+    c.left -= n;
+}
+
+// To the next sequence with positions; there is one while left > 0.
+__device__ __forceinline__ void next_sequence(const Params &p, Cursor &c) {
+    int len = 0;
+    do len = positions_of(p, ++c.b);
+    while (len == 0);
+    enter(c, 0, len);
+}
+
+// A tile in the cache: its first row, and how many of its 16 positions exist.
+struct Place {
+    uint32_t row;
+    int n;
+};
+
+// The tile at position pos (along the axis of ranges) of sequence b, whose length is len.  A page outside the pool is
+// read as page 0 and reported.  (The caches have 2^32 rows at most.)
+__device__ __forceinline__ Place place_of(const Params &p, int b, int g, int pos, int len) {
+    long long at = pos;
+    if (p.list != nullptr) {
+        const int id = p.list[(static_cast<size_t>(b) * p.hn + g) * p.keep + (pos >> p.shift)];
+        at = (static_cast<long long>(id) << p.shift) + (pos & ((1 << p.shift) - 1));
+        if (id < 0 || at >= len) return {0u, 0};
+    }
+    const int i = static_cast<int>(at), pg = i / p.page_size;
     int phys = b;
     if (p.block_table != nullptr) {
         phys = p.block_table[static_cast<size_t>(b) * p.max_pages + pg];
         if (phys < 0 || phys >= p.num_pages) {
-            atomicOr(p.dev_err, GDA_DEVERR_BAD_PAGE);
+            atomicOr(p.err, GDA_DEVERR_BAD_PAGE);
             phys = 0;
         }
     }
-    return static_cast<uint32_t>(phys) * p.page_size + (pos - pg * p.page_size);
+    return {static_cast<uint32_t>(phys) * p.page_size + (i - pg * p.page_size), min(kTile, len - i)};
 }
 
-template <int N>
-__device__ __forceinline__ void load_codes(float (&v)[N], const uint8_t *src, float scale) {
-#pragma unroll
-    for (int i = 0; i < N; i += 2) {
-        const float2 f = half2_bits_to_float2(e4m3x2_to_half2(*reinterpret_cast<const uint16_t *>(src + i)));
-        v[i] = f.x * scale, v[i + 1] = f.y * scale;
-    }
-}
-
-// One map's running softmax over the positions of a warp.
-template <int N>
-struct State {
-    float m = -INFINITY, l = 0.f, o[N] = {};
-    __device__ void add(float x, const float (&v)[N]) {
-        const float top = fmaxf(m, x), f = fast_exp2(m - top), w = fast_exp2(x - top);
-        m = top;
-        l = fmaf(l, f, w);
-#pragma unroll
-        for (int i = 0; i < N; ++i) o[i] = fmaf(o[i], f, w * v[i]);
-    }
+// Places of a stage of the ring, in bytes: K of one tile, its scales, V of the tile before it.
+template <int D, int DV, int RH>
+struct Stage {
+    static constexpr int NH = RH + 1;                    // heads with scores; the noise head is the last
+    static constexpr int k = 0, v = NH * kTile * D, scales = v + RH * kTile * DV, bytes = tile_bytes(RH, D, DV);
+    static_assert(bytes == scales + 32 && NH <= 4, "four scales of K, three of V, the number of positions");
+    static constexpr int count = stages_of(RH, D, DV);
+    static_assert(count >= 2, "a tile must be copied while another is used");
+    static constexpr int queries = count * bytes, weights = queries + NH * D * 2, total = weights + 2 * RH * 128;
+    static constexpr int warps = warps_per_sm(RH, D, DV);
 };
 
-// grid (hs, B): one signal head of one sequence; a warp takes every kWarps-th position, a lane D / 32 and DV / 32 dims.
-template <int D, int DV>
-__global__ void __launch_bounds__(kWarps * 32) gda_decode_fp8_block_kernel(const DecodeFp8BlockArgs p, float scale_log2) {
-    constexpr int ND = D / 32, NV = DV / 32;
-    __shared__ float2 stats[2][kWarps];
-    __shared__ float sums[2][kWarps][DV];
-    __shared__ float squares[kWarps];
-    const int h = blockIdx.x, b = blockIdx.y, g = h / (p.hs / p.hn);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + (static_cast<size_t>(b) * p.hs + h) * DV;
-    const int len = length_of(p, b);
-    long long n = len;
-    if (p.list != nullptr) {
-        int count = p.count[b];
-        if (count < 0 || count > p.keep) {
-            if (threadIdx.x == 0) atomicOr(p.dev_err, GDA_DEVERR_BAD_LENGTH);
-            count = count < 0 ? 0 : p.keep;
+// K codes in shared memory: 16-byte chunks of odd rows of 128 bytes change places, so that the two rows that eight lanes
+// read lie in different banks.
+template <int D>
+__device__ __forceinline__ uint32_t k_chunk(uint32_t row, uint32_t chunk) { return D == 128 ? chunk ^ ((row & 1) << 2) : chunk; }
+
+// V codes: position pos is row v_row(pos), so that a lane's four positions 2t,
+// 2t + 8, 2t + 1, 2t + 9 are rows t, t + 4, t + 8, t + 12; chunks of a row change
+// places by its low bits, so that the rows t = 0 .. 3 that one load reads lie in
+// different banks.
+__device__ __forceinline__ uint32_t v_row(uint32_t pos) { return (pos >> 1) | ((pos & 1) << 3); }
+template <int DV>
+__device__ __forceinline__ uint32_t v_chunk(uint32_t row, uint32_t chunk) {
+    return DV == 64 ? chunk ^ (((row >> 1) & 1) << 1) : chunk ^ ((row & 3) << 1);
+}
+
+// base + row * pitch, one multiply-add.
+__device__ __forceinline__ const uint8_t *row_at(const uint8_t *base, uint32_t row, uint32_t pitch) {
+    return base + static_cast<uint64_t>(row) * pitch;
+}
+
+// Starts the copies of K, and of all scales, of a tile.
+template <int D, int DV, int RH>
+__device__ __forceinline__ void issue_k(const Params &p, uint32_t stage, const Place &at, uint32_t h0, uint32_t g) {
+    using S = Stage<D, DV, RH>;
+    const uint32_t lane = threadIdx.x & 31, hs = p.hs, hn = p.hn;
+    const uint32_t pos = lane / (D / 16), ch = lane % (D / 16);
+    constexpr uint32_t STEP = 512 / D;                   // rows that 32 chunks cover
+    const uint8_t *s1 = row_at(p.k1c, at.row + pos, hs * D) + (h0 * D + ch * 16);
+    const uint8_t *s2 = row_at(p.k2c, at.row + pos, hn * D) + (g * D + ch * 16);
+#pragma unroll
+    for (uint32_t i = 0; i < kTile / STEP; ++i) {
+        const bool ok = static_cast<int>(pos + i * STEP) < at.n;
+        const uint32_t dst = stage + S::k + (pos + i * STEP) * D + k_chunk<D>(pos + i * STEP, ch) * 16;
+#pragma unroll
+        for (int j = 0; j < RH; ++j) copy_async<16>(dst + j * kTile * D, s1 + j * D, ok);
+        copy_async<16>(dst + RH * kTile * D, s2, ok);
+        s1 += static_cast<size_t>(STEP) * hs * D;
+        s2 += static_cast<size_t>(STEP) * hn * D;
+    }
+    // scales: lanes 0 .. RH of K, 4 .. RH + 3 of V; the eighth word is the number of positions
+    const uint32_t blk = at.row >> p.shift, j = lane & 3;
+    const float *src = lane < 4 ? (j < RH ? p.k1s + static_cast<size_t>(blk) * hs + h0 + j : p.k2s + static_cast<size_t>(blk) * hn + g)
+                                : p.vs + static_cast<size_t>(blk) * hs + h0 + min(j, RH - 1u);
+    if (lane < 7) copy_async<4>(stage + S::scales + lane * 4, src, at.n > 0);
+    if (lane == 7) asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage + S::scales + 28), "r"(at.n) : "memory");
+}
+
+// Starts the copies of V of a tile.
+template <int D, int DV, int RH>
+__device__ __forceinline__ void issue_v(const Params &p, uint32_t stage, const Place &at, uint32_t h0) {
+    using S = Stage<D, DV, RH>;
+    const uint32_t lane = threadIdx.x & 31, hs = p.hs;
+    const uint32_t pos = lane / (DV / 16), ch = lane % (DV / 16);
+    constexpr uint32_t STEP = 512 / DV;
+    const uint8_t *s = row_at(p.vc, at.row + pos, hs * DV) + (h0 * DV + ch * 16);
+#pragma unroll
+    for (uint32_t i = 0; i < kTile / STEP; ++i) {
+        const uint32_t row = v_row(pos + i * STEP), dst = stage + S::v + row * DV + v_chunk<DV>(row, ch) * 16;
+        const bool ok = static_cast<int>(pos + i * STEP) < at.n;
+#pragma unroll
+        for (int j = 0; j < RH; ++j) copy_async<16>(dst + j * kTile * DV, s + j * DV, ok);
+        s += static_cast<size_t>(STEP) * hs * DV;
+    }
+}
+
+template <typename V>
+__device__ __forceinline__ V at(const uint8_t *smem) { return *reinterpret_cast<const V *>(smem); }
+
+// The query rows of the warp's heads as f16 in shared memory, scaled by a
+// power of two that brings their largest element to [2^14, 2^15) (f16 then
+// holds all of bf16's digits down to 2^-31 of that).  Returns this lane's
+// factor from a product of codes to exp2 units: that of head lane % 4.
+template <int D, int RH>
+__device__ __forceinline__ float load_queries(const Params &p, uint8_t *dst, int b, int h0, int g) {
+    const int lane = threadIdx.x & 31;
+    float mine = 0.f;
+    uint32_t words[RH + 1][D / 64];                      // all on their way before the first is used
+#pragma unroll
+    for (int j = 0; j <= RH; ++j) {
+        const __nv_bfloat16 *q = j == RH ? p.q2 + (static_cast<size_t>(b) * p.hn + g) * D
+                                         : p.q1 + (static_cast<size_t>(b) * p.hs + h0 + j) * D;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) words[j][i] = reinterpret_cast<const uint32_t *>(q)[lane + 32 * i];
+    }
+#pragma unroll
+    for (int j = 0; j <= RH; ++j) {
+        const uint32_t(&w)[D / 64] = words[j];
+        uint32_t most = 0;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) most = max(most, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+        most = __reduce_max_sync(0xffffffffu, most);
+        const int up = min(268 - static_cast<int>(most >> 7), 253);       // biased exponent of the factor (254 has no inverse)
+        const float f = __uint_as_float(static_cast<uint32_t>(up) << 23);
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i)
+            reinterpret_cast<uint32_t *>(dst + j * D * 2)[lane + 32 * i] =
+                pack_half2(bf16_lo(w[i]) * f, bf16_hi(w[i]) * f);
+        const float back = __uint_as_float(static_cast<uint32_t>(254 - up) << 23);
+        if ((lane & 3) == j) mine = p.scale_log2 * back;
+    }
+    return mine;
+}
+
+// One warp: split u / units of the range, unit u % units = (noise head, part of its group).
+template <int D, int DV, int RH>
+__global__ void __launch_bounds__(32, (Stage<D, DV, RH>::warps)) gda_decode_fp8_block_split_kernel(const Params p) {
+    using S = Stage<D, DV, RH>;
+    constexpr int NH = S::NH, SLABS = DV < 128 ? 1 : DV / 128, WORDS = DV < 128 ? 2 : 4, A = S::count - 1;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int lane = threadIdx.x, quad = lane >> 2, t = lane & 3;
+    const uint32_t ring = smem_u32(smem);
+    const int units = p.hn * p.parts, u = blockIdx.x;
+    const int split = u / units, g = (u % units) / p.parts, part = u % p.parts;
+    // every part is RH heads: the last begins early where they do not divide the group, and leaves what the parts
+    // before it have done unwritten
+    const int r = p.hs / p.hn, begin = min(part * RH, r - RH), done = part * RH - begin, h0 = g * r + begin;
+    Range range;
+    if (!range_of(p, split, range)) return;
+    if (u % units == 0) note_sequences(p, range, split);
+
+    Cursor use{range.b, 0, 0, static_cast<int>(range.end - range.start)};
+    enter(use, static_cast<int>(range.start - range.before), positions_of(p, range.b));
+    Cursor get = use;                                    // the copies' place, ahead of the arithmetic's
+    int get_len = length_of(p, get.b);
+    Place next = place_of(p, get.b, g, get.pos, get_len), last{0u, 0};
+    bool more = true, pending = false;                   // K of `next`, V of `last` are still to be copied
+    int to = 0;
+    auto copy = [&]() {
+        __syncwarp();                                    // the readers of stage `to` are done
+        const uint32_t stage = ring + to * S::bytes;
+        if (pending) issue_v<D, DV, RH>(p, stage, last, h0);
+        if (more) issue_k<D, DV, RH>(p, stage, next, h0, g);
+        pending = more;
+        last = next;
+        if (more) {
+            get.pos += kTile;
+            if (get.pos >= get.hi) {
+                if (get.left > 0) {
+                    next_sequence(p, get);
+                    get_len = length_of(p, get.b);
+                } else {
+                    more = false;
+                }
+            }
+            if (more) next = place_of(p, get.b, g, get.pos, get_len);
         }
-        n = static_cast<long long>(count) * p.block;
-    }
-    float q1[ND], q2[ND];
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        to = to == A ? 0 : to + 1;
+    };
+    for (int i = 0; i < A; ++i) copy();
+
+    uint8_t *const queries = smem + S::queries, *const weights = smem + S::weights;
+    float factor = load_queries<D, RH>(p, queries, use.b, h0, g);
+    float acc[RH][SLABS * WORDS][4];                     // [w]: of tiles 2 w + t / 2 and map t % 2, see values_of
+    float m = kLowest, l = 0.f;                          // of head t (both its lanes' positions; l of this lane's only)
+    float v_most = 0.f, v_inverse = 0.f;                 // of head t: the largest scale of V so far, and 1 over it
+    float shrink = 1.f, v_shrink = 1.f;                  // of what was added before the last tile scored
+    auto clear = [&]() {
 #pragma unroll
-    for (int i = 0; i < ND; ++i) {
-        q1[i] = __bfloat162float(static_cast<const __nv_bfloat16 *>(p.q1)[(static_cast<size_t>(b) * p.hs + h) * D + lane * ND + i]);
-        q2[i] = __bfloat162float(static_cast<const __nv_bfloat16 *>(p.q2)[(static_cast<size_t>(b) * p.hn + g) * D + lane * ND + i]);
-    }
-    State<NV> s1, s2;
-    for (long long i = warp; i < n; i += kWarps) {
-        long long pos = i;
-        if (p.list != nullptr) {
-            const int id = p.list[(static_cast<size_t>(b) * p.hn + g) * p.keep + i / p.block];
-            if (id < 0) continue;
-            pos = static_cast<long long>(id) * p.block + i % p.block;
-            if (pos >= len) continue;
+        for (int j = 0; j < RH; ++j)
+#pragma unroll
+            for (int i = 0; i < SLABS * WORDS; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[j][i][k] = 0.f;
+    };
+    clear();
+    const uint32_t k_at = S::k + quad * D + k_chunk<D>(quad, t) * 16;
+    auto scores_of = [&](const uint8_t *const stage, uint8_t *const out) {
+        // lane (quad, t) ends up with positions quad, quad + 8 of head t
+        float sc0 = 0.f, sc1 = 0.f;
+#pragma unroll
+        for (int j = 0; j < NH; ++j) {
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int half = 0; half < D / 64; ++half) {  // 16 dims of this lane
+                const uint8_t *ka = stage + (k_at ^ (64 * half)) + j * kTile * D;
+                const uint8_t *qa = queries + j * D * 2 + half * 128 + t * 32;
+                const uint4 lo = at<uint4>(ka), hi = at<uint4>(ka + 8 * D), b0 = at<uint4>(qa), b1 = at<uint4>(qa + 16);
+                const uint32_t a[4] = {lo.x, lo.y, lo.z, lo.w}, e[4] = {hi.x, hi.y, hi.z, hi.w};
+                const uint32_t b[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint2 x = e4m3x4_to_half2x2(a[i]), y = e4m3x4_to_half2x2(e[i]);
+                    mma_16816(c, x.x, y.x, x.y, y.y, b[2 * i], b[2 * i + 1]);
+                }
+            }
+            if (t == j) sc0 = c[0], sc1 = c[2];
         }
-        const size_t row = row_of(p, b, static_cast<int>(pos)), blk = row / p.block;
-        float k[ND], v[NV], x1 = 0.f, x2 = 0.f;
-        load_codes<ND>(k, p.k1c + (row * p.hs + h) * D + lane * ND, p.k1s[blk * p.hs + h]);
+        const float ks = at<float>(stage + S::scales + 4 * t), vs = at<float>(stage + S::scales + 16 + 4 * t);
+        const int have = at<int>(stage + S::scales + 28);
+        sc0 = sc0 * factor * ks, sc1 = sc1 * factor * ks;
+        if (quad >= have) sc0 = -INFINITY;
+        if (quad + 8 >= have) sc1 = -INFINITY;
+        float mt = max3f(m, sc0, sc1);
 #pragma unroll
-        for (int j = 0; j < ND; ++j) x1 = fmaf(q1[j], k[j], x1);
-        load_codes<ND>(k, p.k2c + (row * p.hn + g) * D + lane * ND, p.k2s[blk * p.hn + g]);
-#pragma unroll
-        for (int j = 0; j < ND; ++j) x2 = fmaf(q2[j], k[j], x2);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            x1 += __shfl_xor_sync(0xffffffffu, x1, o);
-            x2 += __shfl_xor_sync(0xffffffffu, x2, o);
+        for (int o = 4; o < 32; o <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+        shrink = fast_exp2(m - mt);
+        const float p0 = fast_exp2(sc0 - mt + kWeightBits), p1 = fast_exp2(sc1 - mt + kWeightBits);
+        m = mt;
+        l = fmaf(l, shrink, p0 + p1);
+        v_shrink = 1.f;
+        if (vs > v_most) {
+            v_shrink = __fdiv_rn(v_most, vs);
+            v_most = vs;
+            v_inverse = __frcp_rn(vs);
         }
-        load_codes<NV>(v, p.vc + (row * p.hs + h) * DV + lane * NV, p.vs[blk * p.hs + h]);
-        s1.add(x1 * scale_log2, v);
-        s2.add(x2 * scale_log2, v);
-    }
-    if (lane == 0) stats[0][warp] = make_float2(s1.m, s1.l), stats[1][warp] = make_float2(s2.m, s2.l);
+        const float ratio = vs * v_inverse;
+        const float n0 = __shfl_sync(0xffffffffu, p0, (lane & ~3) | RH) * ratio, n1 = __shfl_sync(0xffffffffu, p1, (lane & ~3) | RH) * ratio;
+        const float s0 = p0 * ratio, s1 = p1 * ratio;
+        const uint32_t sh = pack_half2(s0, s1), nh = pack_half2(n0, n1);
+        const float2 sf = half2_bits_to_float2(sh), nf = half2_bits_to_float2(nh);
+        if (t < RH)
+            *reinterpret_cast<uint4 *>(out + t * 128 + quad * 16) =
+                make_uint4(sh, pack_half2(s0 - sf.x, s1 - sf.y), nh, pack_half2(n0 - nf.x, n1 - nf.y));
+    };
+
+    auto values_of = [&](const uint8_t *const stage, const uint8_t *const in) {
+        // k slots (2t, 2t + 1) are positions 2t, 2t + 8 and (2t + 8, 2t + 9) are 2t + 1, 2t + 9.  A lane has 4 WORDS dims
+        // from 4 WORDS quad on (and 128 further, at DV = 256); tile 2 w has the first two of word w in its rows quad and
+        // quad + 8, tile 2 w + 1 the others.  Columns 0 .. 3 are upper and lower parts of the signal map's weights and of
+        // the noise map's for even tiles, 4 .. 7 for odd ones.
+        constexpr int LOAD = 4 * WORDS;
+        const uint32_t place = t * DV + (DV == 64 ? v_chunk<DV>(t, quad >> 1) * 16 + (quad & 1) * 8 : v_chunk<DV>(t, quad) * 16);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) sums[0][warp][lane * NV + j] = s1.o[j], sums[1][warp][lane * NV + j] = s2.o[j];
-    __syncthreads();
-    float M[2], L[2] = {0.f, 0.f}, o = 0.f;
-    for (int i = 0; i < 2; ++i) {
-        M[i] = -INFINITY;
-        for (int w = 0; w < kWarps; ++w) M[i] = fmaxf(M[i], stats[i][w].x);
-        for (int w = 0; w < kWarps; ++w)
-            if (stats[i][w].y != 0.f) L[i] += stats[i][w].y * fast_exp2(stats[i][w].x - M[i]);
-    }
-    const bool none = L[0] == 0.f;                           // no position: the row is zero
-    if (threadIdx.x < DV && !none) {
-        for (int i = 0; i < 2; ++i) {
-            float a = 0.f;
-            for (int w = 0; w < kWarps; ++w)
-                if (stats[i][w].y != 0.f) a += sums[i][w][threadIdx.x] * fast_exp2(stats[i][w].x - M[i]);
-            o += (i == 0 ? 1.f : -p.lambda[h]) * a / L[i];
+        for (int j = 0; j < RH; ++j) {
+            const uint8_t *wa = in + j * 128 + t * 32 + (quad & 3) * 4;
+            const uint32_t w0 = at<uint32_t>(wa), w1 = at<uint32_t>(wa + 16);
+            const uint32_t even0 = quad < 4 ? w0 : 0u, even1 = quad < 4 ? w1 : 0u;
+            const uint32_t odd0 = quad < 4 ? 0u : w0, odd1 = quad < 4 ? 0u : w1;
+            const uint8_t *va = stage + S::v + j * kTile * DV + place;
+#pragma unroll
+            for (int s = 0; s < SLABS; ++s) {
+                uint32_t x[4][WORDS];                    // [2t, 2t + 8, 2t + 1, 2t + 9]
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint8_t *row = va + k * 4 * DV + s * 128;
+                    if constexpr (LOAD == 8) {
+                        const uint2 v = at<uint2>(row);
+                        x[k][0] = v.x, x[k][1] = v.y;
+                    } else {
+                        const uint4 v = at<uint4>(row);
+                        x[k][0] = v.x, x[k][1] = v.y, x[k][2] = v.z, x[k][3] = v.w;
+                    }
+                }
+#pragma unroll
+                for (int w = 0; w < WORDS; ++w) {
+                    // bytes of two positions side by side: two dims, one in each half
+                    const uint2 a = e4m3x4_to_half2x2(__byte_perm(x[0][w], x[1][w], 0x5140));
+                    const uint2 c = e4m3x4_to_half2x2(__byte_perm(x[2][w], x[3][w], 0x5140));
+                    mma_16816(acc[j][s * WORDS + w], a.x, a.y, c.x, c.y, even0, even1);
+                    const uint2 e = e4m3x4_to_half2x2(__byte_perm(x[0][w], x[1][w], 0x7362));
+                    const uint2 f = e4m3x4_to_half2x2(__byte_perm(x[2][w], x[3][w], 0x7362));
+                    mma_16816(acc[j][s * WORDS + w], e.x, e.y, f.x, f.y, odd0, odd1);
+                }
+            }
         }
-    }
-    float ss = o * o;
+    };
+    auto rescale = [&]() {
+        if (__any_sync(0xffffffffu, shrink != 1.f || v_shrink != 1.f)) {
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-    if (lane == 0) squares[warp] = ss;
-    __syncthreads();
-    ss = 0.f;
-    for (int w = 0; w < kWarps; ++w) ss += squares[w];
-    if (threadIdx.x < DV)
-        out[threadIdx.x] = __float2bfloat16((1.f - p.lambda_init) * o * rsqrtf(ss * (1.f / DV) + p.eps));
+            for (int j = 0; j < RH; ++j) {
+                const float f = __shfl_sync(0xffffffffu, shrink, t & 1 ? RH : j) * __shfl_sync(0xffffffffu, v_shrink, j);
+#pragma unroll
+                for (int i = 0; i < SLABS * WORDS; ++i)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) acc[j][i][k] *= f;
+            }
+        }
+    };
+    // Leaves what the part that lies in sequence use.b has come to.
+    auto leave = [&]() {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        l *= 0x1p-15f;
+        const float mn = __shfl_sync(0xffffffffu, m, RH), ln = __shfl_sync(0xffffffffu, l, RH);
+        const size_t slot = static_cast<size_t>(split) + use.b;
+#pragma unroll
+        for (int j = 0; j < RH; ++j) {
+            const float mj = __shfl_sync(0xffffffffu, m, j), lj = __shfl_sync(0xffffffffu, l, j);
+            const float v = __shfl_sync(0xffffffffu, v_most, j) * 0x1p-15f;
+            if (j < done) continue;
+            const size_t place = slot * p.hs + h0 + j;
+            if (lane == 0) reinterpret_cast<float4 *>(p.ws_ml)[place] = make_float4(mj, lj, mn, ln);
+            float *o = p.ws_o + (place * 2 + (t & 1)) * DV + 4 * WORDS * quad + 2 * (t >> 1);
+#pragma unroll
+            for (int i = 0; i < SLABS * WORDS; ++i) {
+                const float(&c)[4] = acc[j][i];
+                *reinterpret_cast<float2 *>(o + i / WORDS * 128 + i % WORDS * 4) = make_float2((c[0] + c[1]) * v, (c[2] + c[3]) * v);
+            }
+        }
+    };
+
+    int from = 0, buffer = 0;
+    bool fresh = true, ending = false;                   // no tile of this part has been scored; the last one was its last
+    for (;;) {
+        copy();
+        asm volatile("cp.async.wait_group %0;" ::"n"(A) : "memory");
+        __syncwarp();                                    // every lane's copies of this stage have landed
+        const uint8_t *const stage = smem + from * S::bytes;
+        uint8_t *const mine = weights + buffer * RH * 128, *const before = weights + (buffer ^ 1) * RH * 128;
+        from = from == A ? 0 : from + 1;
+        if (ending) {
+            values_of(stage, before);
+            leave();
+            if (use.left == 0) return;
+            next_sequence(p, use);
+            factor = load_queries<D, RH>(p, queries, use.b, h0, g);
+            __syncwarp();
+            clear();
+            m = kLowest, l = 0.f, v_most = 0.f, v_inverse = 0.f;
+            fresh = true;
+        }
+        if (fresh) {
+            scores_of(stage, mine);
+            fresh = false;
+        } else {                                         // twice, so that these are not parted by the test
+            scores_of(stage, mine);
+            values_of(stage, before);
+            rescale();
+        }
+        buffer ^= 1;
+        use.pos += kTile;
+        ending = use.pos >= use.hi;
+    }
+}
+
+template <int D, int DV, int RH>
+cudaError_t launch_split(const Params &p, cudaStream_t stream) {
+    using S = Stage<D, DV, RH>;
+    auto kern = gda_decode_fp8_block_split_kernel<D, DV, RH>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::total);
+    if (e != cudaSuccess) return e;
+    kern<<<p.splits * p.hn * p.parts, 32, S::total, stream>>>(p);
+    return cudaGetLastError();
 }
 
 template <int D, int DV>
-cudaError_t launch(const DecodeFp8BlockArgs &a, cudaStream_t stream) {
-    const float scale = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(D)));
-    gda_decode_fp8_block_kernel<D, DV><<<dim3(a.hs, a.B), kWarps * 32, 0, stream>>>(a, scale);
-    return cudaGetLastError();
+cudaError_t launch_split(const Params &p, int rh, cudaStream_t stream) {
+    if (rh == 1) return launch_split<D, DV, 1>(p, stream);
+    if constexpr (DV < 256)
+        if (rh == 3) return launch_split<D, DV, 3>(p, stream);
+    return launch_split<D, DV, 2>(p, stream);
 }
 
 }  // namespace
 
-size_t decode_fp8_block_workspace_bytes(int B, int hs, int hn, int d, int dv) { return 16; }
+size_t decode_fp8_block_workspace_bytes(int B, int hs, int hn, int d, int dv) { return plan_of(B, hs, hn, d, dv).bytes; }
 
 int launch_decode_fp8_block(const DecodeFp8BlockArgs &a, cudaStream_t stream) {
+    const Plan pl = plan_of(a.B, a.hs, a.hn, a.d, a.dv);
+    char *ws = static_cast<char *>(a.workspace);
+    int shift = 4;
+    while (1 << shift < a.block) ++shift;
+    const Params p{static_cast<const __nv_bfloat16 *>(a.q1),
+                   static_cast<const __nv_bfloat16 *>(a.q2),
+                   a.k1c, a.k2c, a.vc, a.k1s, a.k2s, a.vs, a.lens, a.lambda,
+                   static_cast<__nv_bfloat16 *>(a.out),
+                   reinterpret_cast<float *>(ws),
+                   reinterpret_cast<float *>(ws + pl.ml_at),
+                   reinterpret_cast<int *>(ws + pl.seg_at),
+                   a.dev_err, a.lambda_init, a.eps,
+                   static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(a.d))),
+                   a.B, a.Lcap, a.hs, a.hn, pl.splits, pl.heads.parts, a.block_table, a.page_size, a.max_pages,
+                   a.num_pages, shift, a.list, a.count, a.keep};
     cudaError_t e = cudaErrorInvalidValue;
     switch (a.d * 1000 + a.dv) {
-        case 64064: e = launch<64, 64>(a, stream); break;
-        case 64128: e = launch<64, 128>(a, stream); break;
-        case 64256: e = launch<64, 256>(a, stream); break;
-        case 128064: e = launch<128, 64>(a, stream); break;
-        case 128128: e = launch<128, 128>(a, stream); break;
-        case 128256: e = launch<128, 256>(a, stream); break;
+        case 64064: e = launch_split<64, 64>(p, pl.heads.each, stream); break;
+        case 64128: e = launch_split<64, 128>(p, pl.heads.each, stream); break;
+        case 64256: e = launch_split<64, 256>(p, pl.heads.each, stream); break;
+        case 128064: e = launch_split<128, 64>(p, pl.heads.each, stream); break;
+        case 128128: e = launch_split<128, 128>(p, pl.heads.each, stream); break;
+        case 128256: e = launch_split<128, 256>(p, pl.heads.each, stream); break;
         default: return GDA_ERR_UNSUPPORTED;
     }
+    if (e != cudaSuccess) return record_cuda_error(e);
+    e = a.dv == 64    ? launch_join<64>(p, stream)
+        : a.dv == 128 ? launch_join<128>(p, stream)
+                      : launch_join<256>(p, stream);
     return e == cudaSuccess ? GDA_OK : record_cuda_error(e);
 }
 

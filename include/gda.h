@@ -673,7 +673,7 @@ size_t gda_block_select_workspace_size(int B, int max_blocks, int h_s, int h_n);
  * B <= 65535; block 16, 32, 64 or 128, dividing page_size (Lcap); Lcap
  * (max_pages * page_size) at most 2^31 - 16; at most 2^32 rows in the caches;
  * B times Lcap (sparse: times keep * block, itself at most 2^31 - 16) at most
- * 2^35.
+ * 2^34.
  */
 int gda_attn_decode_fp8_block(const void *q_sig, const void *q_noise, const void *k_sig_cache, const void *k_noise_cache,
                               const void *v_cache, const float *k_sig_scale, const float *k_noise_scale,
