@@ -37,11 +37,11 @@
 namespace gda {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxBlock = 128;
 constexpr int kScanRows = 1024;        // a call of at most so many rows needs no index
-constexpr int kHeadsPerBlock = 8;      // heads that a thread block writes: one for each warp
 constexpr int kMaxRows = 32;           // rows of the call that a thread block looks at
+constexpr int kKeep = 16;              // pieces of 8 elements that a lane holds
 
 __global__ void __launch_bounds__(kThreads) gda_cache_index_kernel(const CacheFp8BlockArgs a) {
     const long long t = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
@@ -65,90 +65,117 @@ __device__ __forceinline__ uint32_t finite_abs(uint32_t bits) {
     return bits < 0x7f800000u ? bits : 0u;
 }
 
-// The rows of a call that go into one block of tokens: what[k] = the row's place in the block, rows[k] = the row.
-struct Members {
-    int rows[kMaxBlock];
-    short what[kMaxBlock];
-    int place[kMaxBlock];              // the row of each place, or -1
-    int count;
+// Warps that share a head row of n elements: a lane's kKeep pieces of 8 then hold the whole block of tokens.
+__host__ __device__ constexpr int warps_of(int block, int n) {
+    return block * n <= kKeep * 8 * 32 ? 1 : block * n / (kKeep * 8 * 32);
+}
+__host__ __device__ constexpr int groups_of(int heads, int block, int n) {   // thread blocks for the heads of a tensor
+    return (heads * warps_of(block, n) + kWarps - 1) / kWarps;
+}
+
+struct Shared {
+    int place[kMaxBlock];              // the call's row of each place of the block of tokens, or -1
+    int slots[kMaxRows];
+    unsigned some;
+    uint32_t most[kWarps];
+    uint32_t top[kWarps][64], low[kWarps][64];   // pairs of a key's channels
 };
+constexpr int kPieces = kKeep * 512;   // bytes of a warp's pieces
 
-// One warp, one (block, head): N / 8 lanes to a row, KEEP rows of a lane held between the two passes over them.
-template <int N>
-__device__ void write_head(const CacheFp8BlockArgs &a, int tensor, int head, int blk, const Members &in, bool fresh) {
-    constexpr int LANES = N / 8, STEP = 32 / LANES, KEEP = 8;
-    const int lane = threadIdx.x & 31, sub = lane / LANES, ch = lane % LANES * 8, count = in.count;
-    const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(a.rows[tensor]) + head * N + ch;
-    const long long ld = a.ld[tensor];
-    const size_t pitch = static_cast<size_t>(a.heads[tensor]) * N;
-    uint8_t *codes = a.codes[tensor] + static_cast<size_t>(blk) * a.block * pitch + head * N + ch;
-    float *const where = a.scale[tensor] + static_cast<size_t>(blk) * a.heads[tensor] + head;
-    const float old = fresh ? 0.f : *where;
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async8(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_landed() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-    uint4 w[KEEP];
-    auto load = [&](int base) {                              // rows base + sub + STEP * 0 .. KEEP - 1
-#pragma unroll
-        for (int i = 0; i < KEEP; ++i) {
-            const int k = base + sub + i * STEP;
-            w[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (k < count) w[i] = *reinterpret_cast<const uint4 *>(x + in.rows[k] * ld);
-        }
-    };
-    constexpr int BATCH = KEEP * STEP;
+// One block of tokens, the heads of this thread block: `share` warps to a head, n / 8 lanes to a row.  A lane's pieces
+// go through shared memory, where no other thread reads them: that many loads are in flight without as many registers,
+// in loops that need not be unrolled (a call of few rows runs once through cold instructions: unrolled over registers 64
+// rows took 18 us and 8192 rows 50).
+__device__ __forceinline__ void write_heads(const CacheFp8BlockArgs &a, int tensor, int group, int blk, Shared &sh,
+                                            uint8_t *pieces, bool fresh) {
+    const int n = a.dims[tensor], log = n == 64 ? 3 : (n == 128 ? 4 : 5), lanes = 1 << log, step = 32 >> log;
+    const int share = warps_of(a.block, n), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int head = (group * kWarps + warp) / share, member = warp % share;
+    const bool here = head < a.heads[tensor];
+    const int ch = (lane & (lanes - 1)) * 8, row0 = member * step + (lane >> log), stride = share * step;   // this lane's places
+    const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(a.rows[tensor]) + head * n + ch;
+    const size_t pitch = static_cast<size_t>(a.heads[tensor]) * n, place = static_cast<size_t>(blk) * a.heads[tensor] + head;
+    uint8_t *codes = a.codes[tensor] + static_cast<size_t>(blk) * a.block * pitch + head * n + ch;
+    const bool bounds_too = tensor < 2 && a.bounds[0] != nullptr;
+    int8_t *const bounds = bounds_too ? a.bounds[tensor] + place * 2 * n + ch : nullptr;
+
+    uint8_t *const mine = pieces + warp * kPieces + lane * 16;
+    const uint32_t at_mine = smem_u32(mine);
+    const int count = here ? (a.block - row0 + stride - 1) / stride : 0;
+    unsigned have = 0;                                       // the pieces that are rows of this call
+    for (int i = 0; i < count; ++i) {
+        const int t = sh.place[row0 + i * stride];
+        if (t < 0) continue;
+        have |= 1u << i;
+        copy_async16(at_mine + i * 512, x + t * a.ld[tensor]);
+    }
+    const float old = fresh || !here ? 0.f : a.scale[tensor][place];
+    uint2 old_top = {}, old_low = {};
+    if (bounds_too && here && !fresh && member == 0 && lane < lanes) {
+        old_top = *reinterpret_cast<const uint2 *>(bounds);
+        old_low = *reinterpret_cast<const uint2 *>(bounds + n);
+    }
+    copies_landed();
     uint32_t most = 0;
-    int base = 0;
-    for (;; base += BATCH) {
-        load(base);
+    for (unsigned rest = have; rest != 0; rest &= rest - 1) {
+        const uint4 w = *reinterpret_cast<const uint4 *>(mine + (__ffs(rest) - 1) * 512);
+        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int i = 0; i < KEEP; ++i) {
-            const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) most = max(most, max(finite_abs(v[k] << 16), finite_abs(v[k] & 0xffff0000u)));
-        }
-        if (base + BATCH >= count) break;
+        for (int k = 0; k < 4; ++k) most = max(most, max(finite_abs(v[k] << 16), finite_abs(v[k] & 0xffff0000u)));
     }
     most = __reduce_max_sync(0xffffffffu, most);
+    if (share > 1) {
+        if (lane == 0) sh.most[warp] = most;
+        __syncthreads();
+        for (int i = 0; i < share; ++i) most = max(most, sh.most[warp - member + i]);
+    }
     const float scale = fmaxf(old, fp8_scale_of(most));
     const float r = __frcp_rn(scale), shift = fresh ? 1.f : __fdiv_rn(old, scale);
     const float most_code = fminf(448.f, __fdiv_rn(0x1.ep127f, scale));
-    __syncwarp();
-    if (lane == 0) *where = scale;
+    if (here && member == 0 && lane == 0) a.scale[tensor][place] = scale;   // all have read it: they share `most`
 
-    const bool bounds_too = tensor < 2 && a.bounds[0] != nullptr;
-    const uint32_t none_max = 0xfc00fc00u, none_min = 0x7c007c00u;   // -inf, inf
+    const uint32_t none_max = 0xfc00fc00u, none_min = 0x7c007c00u;          // -inf, inf
     uint32_t top[4] = {none_max, none_max, none_max, none_max}, low[4] = {none_min, none_min, none_min, none_min};
-    for (;; base -= BATCH) {                                 // the batch that is still here first
+    for (unsigned rest = have; rest != 0; rest &= rest - 1) {
+        const int i = __ffs(rest) - 1;
+        const uint4 w = *reinterpret_cast<const uint4 *>(mine + i * 512);
+        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+        uint32_t c[4];
 #pragma unroll
-        for (int i = 0; i < KEEP; ++i) {
-            const int row = base + sub + i * STEP;
-            if (row >= count) continue;
-            const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-            uint32_t c[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float lo = bf16_lo(v[k]), hi = bf16_hi(v[k]);
-                c[k] = float2_to_e4m3x2(fmaxf(-most_code, fminf(most_code, __fmul_rn(lo, r))),
-                                        fmaxf(-most_code, fminf(most_code, __fmul_rn(hi, r))));
-                // the limits have made a number of what is none
-                if ((v[k] & 0x7fffu) >= 0x7f80u) c[k] |= 0x7fu;
-                if ((v[k] & 0x7fff0000u) >= 0x7f800000u) c[k] |= 0x7f00u;
-                if (bounds_too) {
-                    const uint32_t h = e4m3x2_to_half2(c[k]);    // a NaN is passed over by max and min
-                    top[k] = hmax2(top[k], h);
-                    low[k] = hmin2(low[k], h);
-                }
+        for (int k = 0; k < 4; ++k) {
+            const float lo = bf16_lo(v[k]), hi = bf16_hi(v[k]);
+            c[k] = float2_to_e4m3x2(fmaxf(-most_code, fminf(most_code, __fmul_rn(lo, r))),
+                                    fmaxf(-most_code, fminf(most_code, __fmul_rn(hi, r))));
+            // the limits have made a number of what is none
+            if ((v[k] & 0x7fffu) >= 0x7f80u) c[k] |= 0x7fu;
+            if ((v[k] & 0x7fff0000u) >= 0x7f800000u) c[k] |= 0x7f00u;
+            if (bounds_too) {
+                const uint32_t h = e4m3x2_to_half2(c[k]);    // a NaN is passed over by max and min
+                top[k] = hmax2(top[k], h);
+                low[k] = hmin2(low[k], h);
             }
-            *reinterpret_cast<uint2 *>(codes + in.what[row] * pitch) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
         }
-        if (base == 0) break;
-        load(base - BATCH);
+        *reinterpret_cast<uint2 *>(codes + (row0 + i * stride) * pitch) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
     }
     if (shift != 1.f) {                                      // the rows that are there already
-        for (int i = sub; i < a.block; i += STEP) {
-            if (in.place[i] >= 0) continue;
-            uint2 *const dst = reinterpret_cast<uint2 *>(codes + i * pitch);
-            const uint2 c = *dst;
-            const uint32_t v[2] = {c.x, c.y};
+        const unsigned others = ~have & (count < 32 ? (1u << count) - 1 : ~0u);
+        for (unsigned rest = others; rest != 0; rest &= rest - 1) {
+            const int i = __ffs(rest) - 1;
+            copy_async8(at_mine + i * 512, codes + (row0 + i * stride) * pitch);
+        }
+        copies_landed();
+        for (unsigned rest = others; rest != 0; rest &= rest - 1) {
+            const int i = __ffs(rest) - 1;
+            const uint2 w = *reinterpret_cast<const uint2 *>(mine + i * 512);
+            const uint32_t v[2] = {w.x, w.y};
             uint32_t o[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
@@ -156,21 +183,30 @@ __device__ void write_head(const CacheFp8BlockArgs &a, int tensor, int head, int
                 const float2 p = half2_bits_to_float2(h.x), q = half2_bits_to_float2(h.y);
                 o[k] = float2_to_e4m3x2(p.x * shift, p.y * shift) | float2_to_e4m3x2(q.x * shift, q.y * shift) << 16;
             }
-            *dst = make_uint2(o[0], o[1]);
+            *reinterpret_cast<uint2 *>(codes + (row0 + i * stride) * pitch) = make_uint2(o[0], o[1]);
         }
     }
     if (!bounds_too) return;
+    for (int o = lanes; o < 32; o <<= 1)
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-#pragma unroll
-        for (int o = LANES; o < 32; o <<= 1) {
+        for (int k = 0; k < 4; ++k) {
             top[k] = hmax2(top[k], __shfl_xor_sync(0xffffffffu, top[k], o));
             low[k] = hmin2(low[k], __shfl_xor_sync(0xffffffffu, low[k], o));
         }
-    if (sub != 0) return;
-    int8_t *const bounds = a.bounds[tensor] + (static_cast<size_t>(blk) * a.heads[tensor] + head) * 2 * N + ch;
-    uint2 *const at_top = reinterpret_cast<uint2 *>(bounds), *const at_low = reinterpret_cast<uint2 *>(bounds + N);
-    const uint2 old_top = *at_top, old_low = *at_low;
+    if (share > 1) {
+        if (lane < lanes)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) sh.top[warp][4 * lane + k] = top[k], sh.low[warp][4 * lane + k] = low[k];
+        __syncthreads();
+        if (member == 0 && lane < lanes)
+            for (int i = 1; i < share; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    top[k] = hmax2(top[k], sh.top[warp + i][4 * lane + k]);
+                    low[k] = hmin2(low[k], sh.low[warp + i][4 * lane + k]);
+                }
+    }
+    if (!here || member != 0 || lane >= lanes) return;
     uint32_t nt[2] = {0u, 0u}, nl[2] = {0u, 0u};
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -186,19 +222,17 @@ __device__ void write_head(const CacheFp8BlockArgs &a, int tensor, int head, int
         nt[k / 4] |= (static_cast<uint32_t>(static_cast<int>(t)) & 0xffu) << 8 * (k & 3);
         nl[k / 4] |= (static_cast<uint32_t>(static_cast<int>(l)) & 0xffu) << 8 * (k & 3);
     }
-    *at_top = make_uint2(nt[0], nt[1]);
-    *at_low = make_uint2(nl[0], nl[1]);
+    *reinterpret_cast<uint2 *>(bounds) = make_uint2(nt[0], nt[1]);
+    *reinterpret_cast<uint2 *>(bounds + n) = make_uint2(nl[0], nl[1]);
 }
 
-// grid (groups of `per` rows of the call, groups of kHeadsPerBlock heads).  SCAN: members are looked for in the slot map.
+// grid (groups of `per` rows of the call, groups of heads).  SCAN: members are looked for in the slot map.
 template <bool SCAN>
 __global__ void __launch_bounds__(kThreads) gda_cache_append_fp8_block_kernel(const CacheFp8BlockArgs a, int per) {
-    __shared__ Members in;
-    __shared__ int slots[kMaxRows];
-    __shared__ unsigned some;
+    __shared__ Shared sh;
+    extern __shared__ __align__(16) uint8_t pieces[];        // [kWarps][kKeep][32][16]
     const long long t0 = static_cast<long long>(blockIdx.x) * per;
-    const int warp = threadIdx.x >> 5, heads = a.heads[0] + a.heads[1] + a.heads[2];
-    if (warp == 0) {                                         // the rows that may have the lowest slot of a block
+    if (threadIdx.x < 32) {                                  // the rows that may have the lowest slot of a block
         const long long t = t0 + threadIdx.x;
         const bool mine = static_cast<int>(threadIdx.x) < per && t < a.T;
         const int slot = mine ? a.slot_map[t] : -1;
@@ -206,48 +240,43 @@ __global__ void __launch_bounds__(kThreads) gda_cache_append_fp8_block_kernel(co
         if (slot >= a.slots && blockIdx.y == 0) atomicOr(a.dev_err, GDA_DEVERR_BAD_PAGE);
         // most rows of a prompt have the slot after that of the row before
         if (may && (slot & (a.block - 1)) != 0 && t > 0 && a.slot_map[t - 1] == slot - 1) may = false;
-        slots[threadIdx.x] = slot;
+        sh.slots[threadIdx.x] = slot;
         const unsigned mask = __ballot_sync(0xffffffffu, may);
-        if (threadIdx.x == 0) some = mask;
+        if (threadIdx.x == 0) sh.some = mask;
     }
     __syncthreads();
+    const unsigned some = sh.some;
     for (unsigned rest = some; rest != 0; rest &= rest - 1) {    // a step is the same for the whole thread block
-        const int step = __ffs(rest) - 1, slot = slots[step];
+        const int step = __ffs(rest) - 1, slot = sh.slots[step];
         const long long t = t0 + step;
         const int in_block = slot & (a.block - 1), first = slot - in_block, blk = slot / a.block;
-        if (rest != some) __syncthreads();                   // the readers of `in` are done
-        if (threadIdx.x < kMaxBlock) in.place[threadIdx.x] = -1;
-        if (threadIdx.x == 0) in.count = 0;
-        __syncthreads();
+        if (rest != some) __syncthreads();                   // the readers of `sh` are done
         if constexpr (SCAN) {
+            if (threadIdx.x < kMaxBlock) sh.place[threadIdx.x] = -1;
+            __syncthreads();
             for (int i = threadIdx.x; i < a.T; i += kThreads) {
                 const unsigned other = static_cast<unsigned>(a.slot_map[i]) - static_cast<unsigned>(first);
-                if (other < static_cast<unsigned>(a.block)) atomicMax(&in.place[other], i);
+                if (other < static_cast<unsigned>(a.block)) atomicMax(&sh.place[other], i);
             }
         } else if (threadIdx.x < a.block) {
             const int i = a.index[first + threadIdx.x];
-            if (i >= 0 && i < a.T && a.slot_map[i] == first + static_cast<int>(threadIdx.x)) in.place[threadIdx.x] = i;
+            sh.place[threadIdx.x] = i >= 0 && i < a.T && a.slot_map[i] == first + static_cast<int>(threadIdx.x) ? i : -1;
         }
         __syncthreads();
         bool lower = false;
-        if (threadIdx.x < a.block) {
-            const int i = in.place[threadIdx.x];
-            lower = threadIdx.x < in_block ? i >= 0 : threadIdx.x == in_block && i != t;   // two rows, one slot: one is written
-            if (i >= 0) {
-                const int k = atomicAdd(&in.count, 1);
-                in.rows[k] = i, in.what[k] = static_cast<short>(threadIdx.x);
-            }
+        if (threadIdx.x <= in_block) {                       // two rows with one slot: one of them is written
+            const int i = sh.place[threadIdx.x];
+            lower = threadIdx.x < in_block ? i >= 0 : i != t;
         }
         if (__syncthreads_or(lower)) continue;
-        const bool fresh = in.place[0] >= 0;
-        const int i = blockIdx.y * kHeadsPerBlock + warp;
-        if (i >= heads) continue;
-        const int tensor = i < a.heads[0] ? 0 : (i < a.heads[0] + a.heads[1] ? 1 : 2);
-        const int head = i - (tensor > 0 ? a.heads[0] : 0) - (tensor > 1 ? a.heads[1] : 0);
-        const int n = a.dims[tensor];
-        if (n == 64) write_head<64>(a, tensor, head, blk, in, fresh);
-        else if (n == 128) write_head<128>(a, tensor, head, blk, in, fresh);
-        else write_head<256>(a, tensor, head, blk, in, fresh);
+        const bool fresh = sh.place[0] >= 0;
+        int group = blockIdx.y, tensor = 0;
+        for (; tensor < 2; ++tensor) {
+            const int of = groups_of(a.heads[tensor], a.block, a.dims[tensor]);
+            if (group < of) break;
+            group -= of;
+        }
+        write_heads(a, tensor, group, blk, sh, pieces, fresh);
     }
 }
 
@@ -303,20 +332,21 @@ dim3 read_grid(const CacheFp8BlockArgs &a, unsigned *tokens) {
 }  // namespace
 
 int launch_cache_append_fp8_block(const CacheFp8BlockArgs &a, cudaStream_t stream) {
-    const unsigned heads = (a.heads[0] + a.heads[1] + a.heads[2] + kHeadsPerBlock - 1) / kHeadsPerBlock;
+    unsigned groups = 0;
+    for (int t = 0; t < 3; ++t) groups += groups_of(a.heads[t], a.block, a.dims[t]);
     const bool scan = a.T <= kScanRows;
     // rows of a thread block: the rows of a prompt but one in a block are passed over at once
     const int per = static_cast<int>(std::min<long long>(kMaxRows, std::max<long long>(1, a.T / 256)));
-    const dim3 grid(static_cast<unsigned>((a.T + per - 1) / per), heads);
-    if (scan) {
-        gda_cache_append_fp8_block_kernel<true><<<grid, kThreads, 0, stream>>>(a, per);
-    } else {
+    const dim3 grid(static_cast<unsigned>((a.T + per - 1) / per), groups);
+    const auto kern = scan ? gda_cache_append_fp8_block_kernel<true> : gda_cache_append_fp8_block_kernel<false>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kWarps * kPieces);
+    if (e != cudaSuccess) return record_cuda_error(e);
+    if (!scan) {
         gda_cache_index_kernel<<<static_cast<unsigned>((a.T + kThreads - 1) / kThreads), kThreads, 0, stream>>>(a);
-        const cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess) return record_cuda_error(e);
-        gda_cache_append_fp8_block_kernel<false><<<grid, kThreads, 0, stream>>>(a, per);
+        if ((e = cudaGetLastError()) != cudaSuccess) return record_cuda_error(e);
     }
-    const cudaError_t e = cudaGetLastError();
+    kern<<<grid, kThreads, kWarps * kPieces, stream>>>(a, per);
+    e = cudaGetLastError();
     return e == cudaSuccess ? GDA_OK : record_cuda_error(e);
 }
 
