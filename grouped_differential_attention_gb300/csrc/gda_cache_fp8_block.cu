@@ -24,7 +24,6 @@
 // index[slot] which row has that slot.  An entry counts only if that row's slot
 // is this slot, so what else the workspace holds does no harm.
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <algorithm>
 #include <cstdint>
@@ -50,19 +49,26 @@ __global__ void __launch_bounds__(kThreads) gda_cache_index_kernel(const CacheFp
     if (slot >= 0 && slot < a.slots) a.index[slot] = static_cast<int>(t);
 }
 
-__device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b) {
-    const __half2 r = __hmax2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
-    return *reinterpret_cast<const uint32_t *>(&r);
+// The greater and the lesser of two pairs of bf16; a NaN is passed over.
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
-__device__ __forceinline__ uint32_t hmin2(uint32_t a, uint32_t b) {
-    const __half2 r = __hmin2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
-    return *reinterpret_cast<const uint32_t *>(&r);
+__device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 
-// Bits of |x| where x is finite, 0 where not.
-__device__ __forceinline__ uint32_t finite_abs(uint32_t bits) {
-    bits &= 0x7fffffffu;
-    return bits < 0x7f800000u ? bits : 0u;
+// 0xffff in the halves of a pair of bf16 that are infinite or NaN.
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+    return ((w & 0x7fffu) >= 0x7f80u ? 0xffffu : 0u) | ((w & 0x7fff0000u) >= 0x7f800000u ? 0xffff0000u : 0u);
+}
+
+// The code of x: at most `most` in magnitude.
+__device__ __forceinline__ uint32_t codes_of(float lo, float hi, float r, float most) {
+    return float2_to_e4m3x2(fmaxf(-most, fminf(most, __fmul_rn(lo, r))), fmaxf(-most, fminf(most, __fmul_rn(hi, r))));
 }
 
 // Warps that share a head row of n elements: a lane's kKeep pieces of 8 then hold the whole block of tokens.
@@ -124,46 +130,70 @@ __device__ __forceinline__ void write_heads(const CacheFp8BlockArgs &a, int tens
         old_low = *reinterpret_cast<const uint2 *>(bounds + n);
     }
     copies_landed();
-    uint32_t most = 0;
+    // magnitudes of bf16 order like their bits; what is not finite is above all others, and then looked at once more
+    const uint32_t lowest = 0xff80ff80u, highest = 0x7f807f80u;             // -inf, inf
+    uint32_t top[4] = {lowest, lowest, lowest, lowest}, low[4] = {highest, highest, highest, highest};
+    uint32_t both = 0;
     for (unsigned rest = have; rest != 0; rest &= rest - 1) {
         const uint4 w = *reinterpret_cast<const uint4 *>(mine + (__ffs(rest) - 1) * 512);
         const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) most = max(most, max(finite_abs(v[k] << 16), finite_abs(v[k] & 0xffff0000u)));
+        for (int k = 0; k < 4; ++k) both = __vmaxu2(both, v[k] & 0x7fff7fffu);
+        if (bounds_too) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) top[k] = max_bf16x2(top[k], v[k]), low[k] = min_bf16x2(low[k], v[k]);
+        }
     }
-    most = __reduce_max_sync(0xffffffffu, most);
+    uint32_t most = __reduce_max_sync(0xffffffffu, max(both & 0xffffu, both >> 16));
+    bool odd = most >= 0x7f80u;                              // some of the warp's elements are not finite
+    if (odd) {
+        both = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) top[k] = lowest, low[k] = highest;
+        for (unsigned rest = have; rest != 0; rest &= rest - 1) {
+            const uint4 w = *reinterpret_cast<const uint4 *>(mine + (__ffs(rest) - 1) * 512);
+            const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t no = not_finite(v[k]);
+                both = __vmaxu2(both, v[k] & 0x7fff7fffu & ~no);
+                top[k] = max_bf16x2(top[k], (v[k] & ~no) | (lowest & no));
+                low[k] = min_bf16x2(low[k], (v[k] & ~no) | (highest & no));
+            }
+        }
+        most = __reduce_max_sync(0xffffffffu, max(both & 0xffffu, both >> 16));
+    }
     if (share > 1) {
-        if (lane == 0) sh.most[warp] = most;
+        if (lane == 0) sh.most[warp] = most | (odd ? 0x80000000u : 0u);
         __syncthreads();
-        for (int i = 0; i < share; ++i) most = max(most, sh.most[warp - member + i]);
+        for (int i = 0; i < share; ++i) {
+            const uint32_t other = sh.most[warp - member + i];
+            most = max(most, other & 0xffffu), odd |= other >> 31;
+        }
     }
-    const float scale = fmaxf(old, fp8_scale_of(most));
+    const float scale = fmaxf(old, fp8_scale_of(most << 16));
     const float r = __frcp_rn(scale), shift = fresh ? 1.f : __fdiv_rn(old, scale);
     const float most_code = fminf(448.f, __fdiv_rn(0x1.ep127f, scale));
     if (here && member == 0 && lane == 0) a.scale[tensor][place] = scale;   // all have read it: they share `most`
 
-    const uint32_t none_max = 0xfc00fc00u, none_min = 0x7c007c00u;          // -inf, inf
-    uint32_t top[4] = {none_max, none_max, none_max, none_max}, low[4] = {none_min, none_min, none_min, none_min};
+    odd |= most_code < 448.f;
     for (unsigned rest = have; rest != 0; rest &= rest - 1) {
         const int i = __ffs(rest) - 1;
         const uint4 w = *reinterpret_cast<const uint4 *>(mine + i * 512);
         const uint32_t v[4] = {w.x, w.y, w.z, w.w};
         uint32_t c[4];
+        if (odd) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float lo = bf16_lo(v[k]), hi = bf16_hi(v[k]);
-            c[k] = float2_to_e4m3x2(fmaxf(-most_code, fminf(most_code, __fmul_rn(lo, r))),
-                                    fmaxf(-most_code, fminf(most_code, __fmul_rn(hi, r))));
-            // the limits have made a number of what is none
-            if ((v[k] & 0x7fffu) >= 0x7f80u) c[k] |= 0x7fu;
-            if ((v[k] & 0x7fff0000u) >= 0x7f800000u) c[k] |= 0x7f00u;
-            if (bounds_too) {
-                const uint32_t h = e4m3x2_to_half2(c[k]);    // a NaN is passed over by max and min
-                top[k] = hmax2(top[k], h);
-                low[k] = hmin2(low[k], h);
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t no = not_finite(v[k]);        // the limits make numbers of those
+                c[k] = codes_of(bf16_lo(v[k]), bf16_hi(v[k]), r, most_code) | (no & 0x7fu) | (no >> 16 & 0x7f00u);
             }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) c[k] = float2_to_e4m3x2(__fmul_rn(bf16_lo(v[k]), r), __fmul_rn(bf16_hi(v[k]), r));
         }
-        *reinterpret_cast<uint2 *>(codes + (row0 + i * stride) * pitch) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+        *reinterpret_cast<uint2 *>(codes + (row0 + i * stride) * pitch) =
+            make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
     }
     if (shift != 1.f) {                                      // the rows that are there already
         const unsigned others = ~have & (count < 32 ? (1u << count) - 1 : ~0u);
@@ -190,8 +220,8 @@ __device__ __forceinline__ void write_heads(const CacheFp8BlockArgs &a, int tens
     for (int o = lanes; o < 32; o <<= 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            top[k] = hmax2(top[k], __shfl_xor_sync(0xffffffffu, top[k], o));
-            low[k] = hmin2(low[k], __shfl_xor_sync(0xffffffffu, low[k], o));
+            top[k] = max_bf16x2(top[k], __shfl_xor_sync(0xffffffffu, top[k], o));
+            low[k] = min_bf16x2(low[k], __shfl_xor_sync(0xffffffffu, low[k], o));
         }
     if (share > 1) {
         if (lane < lanes)
@@ -202,17 +232,19 @@ __device__ __forceinline__ void write_heads(const CacheFp8BlockArgs &a, int tens
             for (int i = 1; i < share; ++i)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    top[k] = hmax2(top[k], sh.top[warp + i][4 * lane + k]);
-                    low[k] = hmin2(low[k], sh.low[warp + i][4 * lane + k]);
+                    top[k] = max_bf16x2(top[k], sh.top[warp + i][4 * lane + k]);
+                    low[k] = min_bf16x2(low[k], sh.low[warp + i][4 * lane + k]);
                 }
     }
     if (!here || member != 0 || lane >= lanes) return;
     uint32_t nt[2] = {0u, 0u}, nl[2] = {0u, 0u};
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-        const float2 t2 = half2_bits_to_float2(top[k / 2]), l2 = half2_bits_to_float2(low[k / 2]);
-        float t = ceilf((k & 1 ? t2.y : t2.x) * 0.25f), l = floorf((k & 1 ? l2.y : l2.x) * 0.25f);
-        t = fmaxf(t, -128.f), l = fminf(l, 127.f);           // no finite value: -128 and 127
+        // the code of the greatest is the greatest code
+        const float tx = k & 1 ? bf16_hi(top[k / 2]) : bf16_lo(top[k / 2]), lx = k & 1 ? bf16_hi(low[k / 2]) : bf16_lo(low[k / 2]);
+        const float2 tl = half2_bits_to_float2(e4m3x2_to_half2(codes_of(tx, lx, r, most_code)));
+        const bool none = tx < lx;                           // no finite value
+        float t = none ? -128.f : ceilf(tl.x * 0.25f), l = none ? 127.f : floorf(tl.y * 0.25f);
         if (!fresh) {
             const uint32_t ot = (k < 4 ? old_top.x : old_top.y) >> 8 * (k & 3);
             const uint32_t ol = (k < 4 ? old_low.x : old_low.y) >> 8 * (k & 3);
