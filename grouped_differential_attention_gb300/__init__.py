@@ -29,6 +29,7 @@ over the blocks that a bound on their logits keeps (``gda_block_select``,
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -163,7 +164,7 @@ def _load():
             lib.gda_attn_decode_fp4_workspace_size.restype = Z
             lib.gda_cache_append_fp8_block.argtypes = [P] * 12 + [I] * 8 + [X] * 3 + [P, Z, P]
             lib.gda_cache_append_fp8_block.restype = I
-            lib.gda_cache_append_fp8_block_workspace_size.argtypes = [I] * 2
+            lib.gda_cache_append_fp8_block_workspace_size.argtypes = [I] * 3
             lib.gda_cache_append_fp8_block_workspace_size.restype = Z
             lib.gda_cache_read_fp8_block.argtypes = [P] * 10 + [I] * 8 + [P]
             lib.gda_cache_read_fp8_block.restype = I
@@ -1006,28 +1007,64 @@ def gda_attn_decode_paged_fp4(q_sig, q_noise, k_sig_pool, k_noise_pool, v_pool, 
                        block_table, cache_lens, lam, lambda_init, eps, out, workspace)
 
 
-def _fp8_block_cache(pools, scales, hs, hn, d, dv, dev):
-    """Checks the six tensors of an 8-bit cache with block scales; returns their addresses, the rows of a page, the
-    number of pages and the tokens of a block."""
-    f32 = torch.float32
-    code = _FP8 if getattr(pools[0], "dtype", None) is _FP8 else torch.uint8
-    if not isinstance(scales[0], torch.Tensor) or scales[0].dim() != 3:
+def _addresses(index, device, *wanted):
+    """Checks (tensor, name, dtype, shape) as ``_expect`` does, and returns the tensors' addresses: one pass, as the checks
+    of a small call take as long as its kernels."""
+    out = []
+    try:
+        for t, _, dtype, shape in wanted:
+            if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+                break
+            out.append(t.data_ptr())
+        else:
+            return out
+    except AttributeError:
+        pass
+    for t, name, dtype, shape in wanted:
+        _expect(t, name, dtype, shape, device)
+    return [t.data_ptr() for t, _, _, _ in wanted]
+
+
+def _cuda_index(t):
+    """The device index of the tensor that the others are to share their device with."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("inputs must be torch.Tensors")
+    index = t.get_device()
+    if index < 0:
+        raise ValueError("inputs must be CUDA tensors")
+    return index
+
+
+@functools.lru_cache(maxsize=256)
+def _bytes_of(name, *sizes):
+    """A workspace size of the library, which depends on its arguments alone."""
+    _int32(*sizes)
+    return int(getattr(_load(), name)(*sizes))
+
+
+def _fp8_block_cache(pools, scales, hs, hn, d, dv):
+    """What ``_addresses`` is to check of an 8-bit cache with block scales, the rows of a page, the number of pages and
+    the tokens of a block."""
+    k1, k2, v = pools
+    s1, s2, s3 = scales
+    pages, size, _, _ = k1.shape
+    shape = getattr(s1, "shape", ())
+    if len(shape) != 3:
         raise ValueError("scales must be [num_pages, page_size / block, heads]")
-    pages, size = pools[0].shape[:2]
-    per = scales[0].shape[1]
+    per = shape[1]
     if per < 1 or size % per != 0:
         raise ValueError(f"pages of {size} rows do not hold {per} blocks of equal size")
-    _int32(pages, size)
-    _expect_all(dev, (pools[0], "k_sig codes", code, (pages, size, hs, d)),
-                (pools[1], "k_noise codes", code, (pages, size, hn, d)),
-                (pools[2], "v codes", code, (pages, size, hs, dv)), (scales[0], "k_sig_scale", f32, (pages, per, hs)),
-                (scales[1], "k_noise_scale", f32, (pages, per, hn)), (scales[2], "v_scale", f32, (pages, per, hs)))
-    return [t.data_ptr() for t in (*pools, *scales)], size, pages, size // per
+    if pages > 0x7fffffff or size > 0x7fffffff:
+        _int32(pages, size)
+    code = _FP8 if k1.dtype is _FP8 else torch.uint8
+    f32, sig, noise = torch.float32, (pages, per, hs), (pages, per, hn)
+    return ((k1, "k_sig codes", code, (pages, size, hs, d)), (k2, "k_noise codes", code, (pages, size, hn, d)),
+            (v, "v codes", code, (pages, size, hs, dv)), (s1, "k_sig_scale", f32, sig),
+            (s2, "k_noise_scale", f32, noise), (s3, "v_scale", f32, sig)), size, pages, size // per
 
 
-def gda_cache_append_fp8_block_workspace_size(num_pages: int, page_size: int) -> int:
-    _int32(num_pages, page_size)
-    return int(_load().gda_cache_append_fp8_block_workspace_size(num_pages, page_size))
+def gda_cache_append_fp8_block_workspace_size(T: int, num_pages: int, page_size: int) -> int:
+    return _bytes_of("gda_cache_append_fp8_block_workspace_size", T, num_pages, page_size)
 
 
 def gda_cache_append_fp8_block(k_sig, k_noise, v, slot_map, k_sig_pool, k_noise_pool, v_pool, k_sig_scale,
@@ -1044,9 +1081,8 @@ def gda_cache_append_fp8_block(k_sig, k_noise, v, slot_map, k_sig_pool, k_noise_
     int8 (both or neither) are kept for ``gda_block_select``.  The rows may be
     slices of a fused projection.  See include/gda.h.
     """
+    index = _cuda_index(k_sig)
     dev = k_sig.device
-    if dev.type != "cuda":
-        raise ValueError("inputs must be CUDA tensors")
     if k_sig.dim() != 3 or k_noise.dim() != 3 or v.dim() != 3 or k_sig_pool.dim() != 4:
         raise ValueError("rows must be [T, heads, dim] and pools [num_pages, page_size, heads, dim]")
     T, hs, d = k_sig.shape
@@ -1055,21 +1091,25 @@ def gda_cache_append_fp8_block(k_sig, k_noise, v, slot_map, k_sig_pool, k_noise_
     strides = [_token_stride(t, n, bf, (T, h, dim), dev)
                for t, n, h, dim in ((k_sig, "k_sig", hs, d), (k_noise, "k_noise", hn, d), (v, "v", hs, dv))]
     cache, size, pages, block = _fp8_block_cache((k_sig_pool, k_noise_pool, v_pool), (k_sig_scale, k_noise_scale, v_scale),
-                                                 hs, hn, d, dv, dev)
-    _expect_all(dev, (slot_map, "slot_map", torch.int32, (T,)))
-    if (k_sig_bounds is None) != (k_noise_bounds is None):
+                                                 hs, hn, d, dv)
+    bounds = ()
+    if k_sig_bounds is not None and k_noise_bounds is not None:
+        i8, per = torch.int8, size // block
+        bounds = ((k_sig_bounds, "k_sig_bounds", i8, (pages, per, hs, 2, d)),
+                  (k_noise_bounds, "k_noise_bounds", i8, (pages, per, hn, 2, d)))
+    elif k_sig_bounds is not None or k_noise_bounds is not None:
         raise ValueError("k_sig_bounds and k_noise_bounds are given both or not at all")
-    bounds = (None, None)
-    if k_sig_bounds is not None:
-        i8 = torch.int8
-        _expect_all(dev, (k_sig_bounds, "k_sig_bounds", i8, (pages, size // block, hs, 2, d)),
-                    (k_noise_bounds, "k_noise_bounds", i8, (pages, size // block, hn, 2, d)))
-        bounds = (k_sig_bounds.data_ptr(), k_noise_bounds.data_ptr())
-    lib = _load()
-    workspace = _workspace(workspace, lib.gda_cache_append_fp8_block_workspace_size(pages, size), dev)
-    _enqueue(lib.gda_cache_append_fp8_block, "gda 8-bit block cache append", dev, k_sig.data_ptr(), k_noise.data_ptr(),
-             v.data_ptr(), slot_map.data_ptr(), *cache, *bounds, T, pages, size, block, hs, hn, d, dv, *strides,
-             workspace.data_ptr(), workspace.numel())
+    at = _addresses(index, dev, (slot_map, "slot_map", torch.int32, (T,)), *cache, *bounds)
+    if not bounds:
+        at += (None, None)
+    need = _bytes_of("gda_cache_append_fp8_block_workspace_size", T, pages, size)
+    if workspace is not None or need:
+        workspace = _workspace(workspace, need, dev)
+        space = (workspace.data_ptr(), workspace.numel())
+    else:
+        space = (None, 0)
+    _enqueue(_load().gda_cache_append_fp8_block, "gda 8-bit block cache append", dev, k_sig.data_ptr(), k_noise.data_ptr(),
+             v.data_ptr(), *at, T, pages, size, block, hs, hn, d, dv, *strides, *space)
 
 
 def gda_cache_read_fp8_block(slot_map, k_sig_pool, k_noise_pool, v_pool, k_sig_scale, k_noise_scale, v_scale, *,
@@ -1081,49 +1121,48 @@ def gda_cache_read_fp8_block(slot_map, k_sig_pool, k_noise_pool, v_pool, k_sig_s
     slots, in order, are the keys and values of a prefix for
     ``gda_attn_fwd_chunk``.
     """
+    index = _cuda_index(slot_map)
     dev = slot_map.device
-    if dev.type != "cuda":
-        raise ValueError("inputs must be CUDA tensors")
     if slot_map.dim() != 1 or k_sig_pool.dim() != 4 or k_noise_pool.dim() != 4 or v_pool.dim() != 4:
         raise ValueError("slot_map must be 1-D and pools [num_pages, page_size, heads, dim]")
     T = slot_map.numel()
-    hs, d = k_sig_pool.shape[2:]
+    _, _, hs, d = k_sig_pool.shape
     hn, dv = k_noise_pool.shape[2], v_pool.shape[3]
     cache, size, pages, block = _fp8_block_cache((k_sig_pool, k_noise_pool, v_pool), (k_sig_scale, k_noise_scale, v_scale),
-                                                 hs, hn, d, dv, dev)
-    _expect_all(dev, (slot_map, "slot_map", torch.int32, (T,)))
+                                                 hs, hn, d, dv)
     bf = torch.bfloat16
-    shapes = ((T, hs, d), (T, hn, d), (T, hs, dv))
+    k1, k2, v = (T, hs, d), (T, hn, d), (T, hs, dv)
     if out is None:
-        out = tuple([torch.empty(s, dtype=bf, device=dev) for s in shapes])
+        out = (torch.empty(k1, dtype=bf, device=dev), torch.empty(k2, dtype=bf, device=dev),
+               torch.empty(v, dtype=bf, device=dev))
     else:
         out = _given(out, 3, "out")
-        for t, n, s in zip(out, ("k_sig", "k_noise", "v"), shapes):
-            _expect(t, n, bf, s, dev)
-    _enqueue(_load().gda_cache_read_fp8_block, "gda 8-bit block cache read", dev, slot_map.data_ptr(), *cache,
-             *[t.data_ptr() for t in out], T, pages, size, block, hs, hn, d, dv)
+    at = _addresses(index, dev, (slot_map, "slot_map", torch.int32, (T,)), *cache, (out[0], "out k_sig", bf, k1),
+                    (out[1], "out k_noise", bf, k2), (out[2], "out v", bf, v))
+    _enqueue(_load().gda_cache_read_fp8_block, "gda 8-bit block cache read", dev, *at, T, pages, size, block, hs, hn, d, dv)
     return tuple(out)
 
 
-def _pages_of_sequences(block_table, pages, B, dev):
-    """Address of the block table and its pages a sequence; contiguous caches are a page for each sequence."""
+def _pages_of_sequences(block_table, pages, B):
+    """What ``_addresses`` is to check of a block table, and its pages a sequence; contiguous caches are a page for each
+    sequence."""
     if block_table is None:
         if pages != B:
             raise ValueError(f"caches hold {pages} sequences, expected {B}")
-        return None, 1
-    if not isinstance(block_table, torch.Tensor):
+        return (), 1
+    shape = getattr(block_table, "shape", None)
+    if shape is None:
         raise TypeError("block_table must be a torch.Tensor")
-    if block_table.dim() != 2:
+    if len(shape) != 2:
         raise ValueError("block_table must be [B, max_pages]")
-    max_pages = block_table.shape[1]
-    _expect_all(dev, (block_table, "block_table", torch.int32, (B, max_pages)))
-    _int32(max_pages)
-    return block_table.data_ptr(), max_pages
+    max_pages = shape[1]
+    if max_pages > 0x7fffffff:
+        _int32(max_pages)
+    return ((block_table, "block_table", torch.int32, (B, max_pages)),), max_pages
 
 
 def gda_block_select_workspace_size(B: int, max_blocks: int, h_s: int, h_n: int) -> int:
-    _int32(B, max_blocks, h_s, h_n)
-    return int(_load().gda_block_select_workspace_size(B, max_blocks, h_s, h_n))
+    return _bytes_of("gda_block_select_workspace_size", B, max_blocks, h_s, h_n)
 
 
 def gda_block_select(q_sig, q_noise, k_sig_bounds, k_noise_bounds, k_sig_scale, k_noise_scale, cache_lens, block: int,
@@ -1139,82 +1178,78 @@ def gda_block_select(q_sig, q_noise, k_sig_bounds, k_noise_bounds, k_sig_scale, 
     more, else its first ``first`` and last ``last`` ones and those of the
     highest score (include/gda.h).  ``out`` may hold the two.
     """
+    index = _cuda_index(q_sig)
     dev = q_sig.device
-    if dev.type != "cuda":
-        raise ValueError("inputs must be CUDA tensors")
     if q_sig.dim() != 3 or q_noise.dim() != 3:
         raise ValueError("queries must be [B, heads, d]")
-    if not isinstance(k_sig_bounds, torch.Tensor) or k_sig_bounds.dim() != 5:
+    if k_sig_bounds.dim() != 5:
         raise ValueError("bounds must be [num_pages, page_size / block, heads, 2, d]")
     B, hs, d = q_sig.shape
     hn = q_noise.shape[1]
-    pages, per = k_sig_bounds.shape[:2]
+    pages, per, _, _, _ = k_sig_bounds.shape
     bf, i8, i32, f32 = torch.bfloat16, torch.int8, torch.int32, torch.float32
-    _int32(pages, per * block, keep, first, last)
-    _expect_all(dev, (q_sig, "q_sig", bf, (B, hs, d)), (q_noise, "q_noise", bf, (B, hn, d)),
-                (k_sig_bounds, "k_sig_bounds", i8, (pages, per, hs, 2, d)),
-                (k_noise_bounds, "k_noise_bounds", i8, (pages, per, hn, 2, d)),
-                (k_sig_scale, "k_sig_scale", f32, (pages, per, hs)),
-                (k_noise_scale, "k_noise_scale", f32, (pages, per, hn)), (cache_lens, "cache_lens", i32, (B,)))
-    table, max_pages = _pages_of_sequences(block_table, pages, B, dev)
-    shapes = ((B, hn, keep), (B,))
+    table, max_pages = _pages_of_sequences(block_table, pages, B)
+    _int32(pages, per * block, keep, first, last, max_pages * per)
     if out is None:
-        out = tuple([torch.empty(s, dtype=i32, device=dev) for s in shapes])
+        out = (torch.empty((B, hn, keep), dtype=i32, device=dev), torch.empty((B,), dtype=i32, device=dev))
     else:
         out = _given(out, 2, "out")
-        _expect_all(dev, (out[0], "block_list", i32, shapes[0]), (out[1], "block_count", i32, shapes[1]))
-    lib = _load()
-    _int32(max_pages * per)
-    workspace = _workspace(workspace, lib.gda_block_select_workspace_size(B, max_pages * per, hs, hn), dev)
-    _enqueue(lib.gda_block_select, "gda block selection", dev, q_sig.data_ptr(), q_noise.data_ptr(),
-             k_sig_bounds.data_ptr(), k_noise_bounds.data_ptr(), k_sig_scale.data_ptr(), k_noise_scale.data_ptr(), table,
-             cache_lens.data_ptr(), *[t.data_ptr() for t in out], B, max_pages, per * block, pages, block, keep, first,
-             last, hs, hn, d, workspace.data_ptr(), workspace.numel())
+    at = _addresses(index, dev, (q_sig, "q_sig", bf, (B, hs, d)), (q_noise, "q_noise", bf, (B, hn, d)),
+                    (k_sig_bounds, "k_sig_bounds", i8, (pages, per, hs, 2, d)),
+                    (k_noise_bounds, "k_noise_bounds", i8, (pages, per, hn, 2, d)),
+                    (k_sig_scale, "k_sig_scale", f32, (pages, per, hs)),
+                    (k_noise_scale, "k_noise_scale", f32, (pages, per, hn)), *table,
+                    (cache_lens, "cache_lens", i32, (B,)), (out[0], "block_list", i32, (B, hn, keep)),
+                    (out[1], "block_count", i32, (B,)))
+    if not table:
+        at.insert(6, None)
+    workspace = _workspace(workspace, _bytes_of("gda_block_select_workspace_size", B, max_pages * per, hs, hn), dev)
+    _enqueue(_load().gda_block_select, "gda block selection", dev, *at, B, max_pages, per * block, pages, block, keep,
+             first, last, hs, hn, d, workspace.data_ptr(), workspace.numel())
     return tuple(out)
 
 
 def gda_attn_decode_fp8_block_workspace_size(B: int, h_s: int, h_n: int, d: int, dv: int) -> int:
-    _int32(B, h_s, h_n, d, dv)
-    return int(_load().gda_attn_decode_fp8_block_workspace_size(B, h_s, h_n, d, dv))
+    return _bytes_of("gda_attn_decode_fp8_block_workspace_size", B, h_s, h_n, d, dv)
 
 
 def _decode_fp8_block(q_sig, q_noise, pools, scales, block_table, lists, cache_lens, lam, lambda_init, eps, out,
                       workspace):
+    index = _cuda_index(q_sig)
     dev = q_sig.device
-    if dev.type != "cuda":
-        raise ValueError("inputs must be CUDA tensors")
     if q_sig.dim() != 3 or q_noise.dim() != 3 or pools[0].dim() != 4 or pools[2].dim() != 4:
         raise ValueError("bad ranks: q [B, heads, d], caches [.., .., heads, dim]")
     B, hs, d = q_sig.shape
     hn, dv = q_noise.shape[1], pools[2].shape[3]
     bf, i32 = torch.bfloat16, torch.int32
-    _expect_all(dev, (q_sig, "q_sig", bf, (B, hs, d)), (q_noise, "q_noise", bf, (B, hn, d)),
-                (cache_lens, "cache_lens", i32, (B,)), (lam, "lam", torch.float32, (hs,)))
-    cache, size, pages, block = _fp8_block_cache(pools, scales, hs, hn, d, dv, dev)
-    table, max_pages = _pages_of_sequences(block_table, pages, B, dev)
+    cache, size, pages, block = _fp8_block_cache(pools, scales, hs, hn, d, dv)
+    table, max_pages = _pages_of_sequences(block_table, pages, B)
     if out is None:
         out = torch.empty((B, hs, dv), dtype=bf, device=dev)
-    else:
-        _expect(out, "out", bf, (B, hs, dv), dev)
-    lib = _load()
-    workspace = _workspace(workspace, lib.gda_attn_decode_fp8_block_workspace_size(B, hs, hn, d, dv), dev)
-    head = (q_sig.data_ptr(), q_noise.data_ptr(), *cache)
-    body = (cache_lens.data_ptr(), lam.data_ptr(), float(lambda_init), out.data_ptr(), B)
+    keep = 0
+    if lists is not None:
+        shape = getattr(lists[0], "shape", ())
+        if len(shape) != 3:
+            raise ValueError("block_list must be [B, h_n, keep]")
+        keep = shape[2]
+        _int32(keep)
+        lists = ((lists[0], "block_list", i32, (B, hn, keep)), (lists[1], "block_count", i32, (B,)))
+    at = _addresses(index, dev, (q_sig, "q_sig", bf, (B, hs, d)), (q_noise, "q_noise", bf, (B, hn, d)), *cache, *table,
+                    *(lists or ()), (cache_lens, "cache_lens", i32, (B,)), (lam, "lam", torch.float32, (hs,)),
+                    (out, "out", bf, (B, hs, dv)))
+    workspace = _workspace(workspace, _bytes_of("gda_attn_decode_fp8_block_workspace_size", B, hs, hn, d, dv), dev)
+    at.insert(-1, float(lambda_init))
     tail = (hs, hn, d, dv, float(eps), workspace.data_ptr(), workspace.numel())
     what = "gda decode (8-bit block cache)"
+    lib = _load()
     if lists is not None:
-        block_list, block_count = lists
-        if not isinstance(block_list, torch.Tensor) or block_list.dim() != 3:
-            raise ValueError("block_list must be [B, h_n, keep]")
-        keep = block_list.shape[2]
-        _int32(keep)
-        _expect_all(dev, (block_list, "block_list", i32, (B, hn, keep)), (block_count, "block_count", i32, (B,)))
-        _enqueue(lib.gda_attn_decode_sparse_fp8_block, what, dev, *head, table, block_list.data_ptr(),
-                 block_count.data_ptr(), *body, max_pages, size, pages, block, keep, *tail)
-    elif table is None:
-        _enqueue(lib.gda_attn_decode_fp8_block, what, dev, *head, *body, size, block, *tail)
+        if not table:
+            at.insert(8, None)
+        _enqueue(lib.gda_attn_decode_sparse_fp8_block, what, dev, *at, B, max_pages, size, pages, block, keep, *tail)
+    elif not table:
+        _enqueue(lib.gda_attn_decode_fp8_block, what, dev, *at, B, size, block, *tail)
     else:
-        _enqueue(lib.gda_attn_decode_paged_fp8_block, what, dev, *head, table, *body, max_pages, size, pages, block, *tail)
+        _enqueue(lib.gda_attn_decode_paged_fp8_block, what, dev, *at, B, max_pages, size, pages, block, *tail)
     return out
 
 

@@ -874,15 +874,15 @@ int gda_cache_append_fp8_block(const void *k_sig, const void *k_noise, const voi
                         static_cast<int *>(workspace), nullptr};
     int st = fill_cache_fp8_block(a, num_pages, page_size, h_s, h_n, d, dv);
     if (st != GDA_OK) return st;
-    if (!workspace || !aligned16(workspace) ||
-        workspace_bytes < gda_cache_append_fp8_block_workspace_size(num_pages, page_size))
-        return GDA_ERR_WORKSPACE;
+    const size_t need = gda_cache_append_fp8_block_workspace_size(T, num_pages, page_size);
+    if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return GDA_ERR_WORKSPACE;
     if ((st = current_device(&a.dev_err)) != GDA_OK) return st;
     return launch_cache_append_fp8_block(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
-size_t gda_cache_append_fp8_block_workspace_size(int num_pages, int page_size) {
+size_t gda_cache_append_fp8_block_workspace_size(int T, int num_pages, int page_size) {
     if (num_pages < 1 || page_size < 1 || static_cast<long long>(num_pages) * page_size > 0x7fffffffLL) return 0;
+    if (T <= kCacheScanRows) return 0;
     return static_cast<size_t>(num_pages) * page_size * sizeof(int);
 }
 

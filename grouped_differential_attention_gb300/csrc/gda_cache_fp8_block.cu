@@ -38,8 +38,7 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxBlock = 128;
-constexpr int kScanRows = 1024;        // a call of at most so many rows needs no index
-constexpr int kMaxRows = 32;           // rows of the call that a thread block looks at
+constexpr int kMaxRows = 64;           // rows of the call that a thread block looks at
 constexpr int kKeep = 16;              // pieces of 8 elements that a lane holds
 
 __global__ void __launch_bounds__(kThreads) gda_cache_index_kernel(const CacheFp8BlockArgs a) {
@@ -82,7 +81,7 @@ __host__ __device__ constexpr int groups_of(int heads, int block, int n) {   // 
 struct Shared {
     int place[kMaxBlock];              // the call's row of each place of the block of tokens, or -1
     int slots[kMaxRows];
-    unsigned some;
+    unsigned some[kMaxRows / 32];
     uint32_t most[kWarps];
     uint32_t top[kWarps][64], low[kWarps][64];   // pairs of a key's channels
 };
@@ -264,7 +263,8 @@ __global__ void __launch_bounds__(kThreads) gda_cache_append_fp8_block_kernel(co
     __shared__ Shared sh;
     extern __shared__ __align__(16) uint8_t pieces[];        // [kWarps][kKeep][32][16]
     const long long t0 = static_cast<long long>(blockIdx.x) * per;
-    if (threadIdx.x < 32) {                                  // the rows that may have the lowest slot of a block
+    if constexpr (!SCAN) asm volatile("griddepcontrol.wait;" ::: "memory");   // the index is written
+    if (threadIdx.x < kMaxRows) {                            // the rows that may have the lowest slot of a block
         const long long t = t0 + threadIdx.x;
         const bool mine = static_cast<int>(threadIdx.x) < per && t < a.T;
         const int slot = mine ? a.slot_map[t] : -1;
@@ -274,12 +274,12 @@ __global__ void __launch_bounds__(kThreads) gda_cache_append_fp8_block_kernel(co
         if (may && (slot & (a.block - 1)) != 0 && t > 0 && a.slot_map[t - 1] == slot - 1) may = false;
         sh.slots[threadIdx.x] = slot;
         const unsigned mask = __ballot_sync(0xffffffffu, may);
-        if (threadIdx.x == 0) sh.some = mask;
+        if (threadIdx.x % 32 == 0) sh.some[threadIdx.x / 32] = mask;
     }
     __syncthreads();
-    const unsigned some = sh.some;
-    for (unsigned rest = some; rest != 0; rest &= rest - 1) {    // a step is the same for the whole thread block
-        const int step = __ffs(rest) - 1, slot = sh.slots[step];
+    const uint64_t some = sh.some[0] | static_cast<uint64_t>(sh.some[1]) << 32;
+    for (uint64_t rest = some; rest != 0; rest &= rest - 1) {    // a step is the same for the whole thread block
+        const int step = __ffsll(static_cast<long long>(rest)) - 1, slot = sh.slots[step];
         const long long t = t0 + step;
         const int in_block = slot & (a.block - 1), first = slot - in_block, blk = slot / a.block;
         if (rest != some) __syncthreads();                   // the readers of `sh` are done
@@ -366,7 +366,7 @@ dim3 read_grid(const CacheFp8BlockArgs &a, unsigned *tokens) {
 int launch_cache_append_fp8_block(const CacheFp8BlockArgs &a, cudaStream_t stream) {
     unsigned groups = 0;
     for (int t = 0; t < 3; ++t) groups += groups_of(a.heads[t], a.block, a.dims[t]);
-    const bool scan = a.T <= kScanRows;
+    const bool scan = a.T <= kCacheScanRows;
     // rows of a thread block: the rows of a prompt but one in a block are passed over at once
     const int per = static_cast<int>(std::min<long long>(kMaxRows, std::max<long long>(1, a.T / 256)));
     const dim3 grid(static_cast<unsigned>((a.T + per - 1) / per), groups);
@@ -377,8 +377,17 @@ int launch_cache_append_fp8_block(const CacheFp8BlockArgs &a, cudaStream_t strea
         gda_cache_index_kernel<<<static_cast<unsigned>((a.T + kThreads - 1) / kThreads), kThreads, 0, stream>>>(a);
         if ((e = cudaGetLastError()) != cudaSuccess) return record_cuda_error(e);
     }
-    kern<<<grid, kThreads, kWarps * kPieces, stream>>>(a, per);
-    e = cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kWarps * kPieces;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = scan ? 0 : 1;                             // after the index kernel only: others may write what is read here
+    e = cudaLaunchKernelEx(&cfg, kern, a, per);
     return e == cudaSuccess ? GDA_OK : record_cuda_error(e);
 }
 

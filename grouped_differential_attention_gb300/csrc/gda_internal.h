@@ -132,9 +132,11 @@ struct CacheFp8BlockArgs {
     int heads[3], dims[3];
     long long T;
     int slots, block;               // block: a power of two
-    int *index;                     // [slots]: workspace
+    int *index;                     // [slots]: workspace, of calls of more than kCacheScanRows rows
     unsigned *dev_err;
 };
+
+constexpr int kCacheScanRows = 1024;   // a call of at most so many rows needs no index
 
 struct BlockSelectArgs {
     const void *q1, *q2;                                   // bf16 [B, heads, d]

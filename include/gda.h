@@ -584,9 +584,10 @@ size_t gda_attn_decode_fp4_workspace_size(int B, int h_s, int h_n, int d, int dv
  * a block that no call has started are not read.
  *   k_sig_bounds, k_noise_bounds: both, or both NULL (then not kept).
  *   workspace: device memory of at least
- *   gda_cache_append_fp8_block_workspace_size(num_pages, page_size) bytes (4 a
- *   slot), 16-byte aligned, owned by the caller; needs no initialisation.
- *   Calls in flight at the same time need a workspace each.
+ *   gda_cache_append_fp8_block_workspace_size(T, num_pages, page_size) bytes (4
+ *   a slot; 0, and then it may be NULL, for at most 1024 rows), 16-byte aligned,
+ *   owned by the caller; needs no initialisation.  Calls in flight at the same
+ *   time need a workspace each.
  *
  * gda_cache_read_fp8_block is the reverse: rows of the slots as dense bf16
  * [T, heads, dim], rounded once (exact for scales that are powers of two; zero
@@ -608,8 +609,8 @@ int gda_cache_read_fp8_block(const int *slot_map, const void *k_sig_pool, const 
                              void *k_sig_out, void *k_noise_out, void *v_out, int T, int num_pages, int page_size,
                              int block, int h_s, int h_n, int d, int dv, gda_stream_t stream);
 
-/* Bytes of workspace gda_cache_append_fp8_block needs (0 for invalid sizes). */
-size_t gda_cache_append_fp8_block_workspace_size(int num_pages, int page_size);
+/* Bytes of workspace gda_cache_append_fp8_block needs (0 for invalid sizes, and for few rows). */
+size_t gda_cache_append_fp8_block_workspace_size(int T, int num_pages, int page_size);
 
 /*
  * The blocks that a decode step is to attend, chosen by a bound on their

@@ -27,7 +27,7 @@ def ptrs(n, **change):
 
 def append(lib, p=None, T=5, pages=4, ps=64, block=32, hs=6, hn=2, d=64, dv=128, s=None, ws=A, ws_bytes=None):
     s = s or [hs * d, hn * d, hs * dv]
-    need = lib.gda_cache_append_fp8_block_workspace_size(pages, ps)
+    need = lib.gda_cache_append_fp8_block_workspace_size(T, pages, ps)
     return lib.gda_cache_append_fp8_block(*(p or ptrs(12)), T, pages, ps, block, hs, hn, d, dv, *s, ws,
                                           need if ws_bytes is None else ws_bytes, None)
 
@@ -57,11 +57,14 @@ def test_cache_rows_refuse(lib, call, n):
 def test_append_strides_and_workspace(lib):
     assert append(lib, s=[383, 128, 768]) == INVALID and append(lib, s=[384, 132, 768]) == MISALIGNED
     assert append(lib, s=[384, 128, (1 << 40) + 8]) == INVALID
-    assert append(lib, ws=None) == WORKSPACE and append(lib, ws=A + 8) == WORKSPACE
-    assert append(lib, ws_bytes=4 * 64 * 4 - 1) == WORKSPACE
+    assert append(lib, T=1025, ws=None) == WORKSPACE and append(lib, T=1025, ws=A + 8) == WORKSPACE
+    assert append(lib, T=1025, ws_bytes=4 * 64 * 4 - 1) == WORKSPACE
     size = lib.gda_cache_append_fp8_block_workspace_size
-    assert size(4, 64) == 1024 and size(0, 64) == 0 and size(4, 0) == 0 and size(1 << 20, 1 << 11) == 0
-    assert size(1, 2 ** 31 - 1) == 4 * (2 ** 31 - 1)
+    assert size(1025, 4, 64) == 1024 and size(1024, 4, 64) == 0 and size(0, 4, 64) == 0
+    assert size(9999, 0, 64) == 0 and size(9999, 4, 0) == 0 and size(9999, 1 << 20, 1 << 11) == 0
+    assert size(2 ** 31 - 1, 1, 2 ** 31 - 1) == 4 * (2 ** 31 - 1)
+    if not torch.cuda.is_available():
+        assert append(lib, ws=None) == CUDA                             # few rows: none is needed
 
 
 def select(lib, p=None, B=3, mp=4, ps=64, pages=9, block=32, keep=5, first=1, last=1, hs=6, hn=2, d=64, ws=A,
@@ -175,7 +178,7 @@ def test_sizes_past_32_bits_are_refused_by_the_binding(lib):
         with pytest.raises(ValueError):
             gda.gda_block_select_workspace_size(1, big, 6, 2)
         with pytest.raises(ValueError):
-            gda.gda_cache_append_fp8_block_workspace_size(big, 16)
+            gda.gda_cache_append_fp8_block_workspace_size(2000, big, 16)
 
 
 def test_binding_refuses_host_tensors():

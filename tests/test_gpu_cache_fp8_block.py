@@ -59,7 +59,8 @@ class Cache:
 CASES = [  # T, pages, page size, block, h_s, h_n, d, dv
     (1, 1, 16, 16, 1, 1, 64, 64), (5, 2, 32, 16, 3, 1, 64, 128), (64, 4, 64, 64, 12, 4, 64, 128),
     (77, 3, 96, 32, 16, 4, 128, 256), (300, 2, 256, 128, 6, 2, 128, 64), (1000, 11, 112, 16, 2, 2, 64, 256),
-    (333, 3, 128, 128, 5, 1, 64, 128),
+    (333, 3, 128, 128, 5, 1, 64, 128), (1500, 20, 112, 16, 3, 1, 64, 128), (2500, 20, 128, 128, 5, 1, 128, 256),
+    (1100, 10, 128, 64, 6, 2, 64, 64), (2049, 70, 32, 32, 9, 3, 128, 128),
 ]
 
 
@@ -170,16 +171,17 @@ def test_slots_past_the_pool_and_the_same_slot_twice():
 
 
 def test_fused_projection_other_stream_and_any_workspace():
-    hs, hn, d, dv, T = 6, 2, 64, 128, 50
+    hs, hn, d, dv, T = 6, 2, 64, 128, 1050
     g = torch.Generator().manual_seed(2)
     proj = torch.randn(T, hs * (d + dv) + hn * d + 24, generator=g).bfloat16()
     cuts = (0, hs * d, (hs + hn) * d, (hs + hn) * d + hs * dv)
     split = lambda p: [p[:, a:b].unflatten(-1, (-1, n)) for a, b, n in zip(cuts, cuts[1:], (d, d, dv))]
-    c = Cache(2, 48, 16, hs, hn, d, dv)
+    c = Cache(25, 48, 16, hs, hn, d, dv)
     slots = torch.arange(40, 40 + T, dtype=torch.int32)
     slots[10] = 0
     s = torch.cuda.Stream()
-    need = gda.gda_cache_append_fp8_block_workspace_size(2, 48)
+    need = gda.gda_cache_append_fp8_block_workspace_size(T, 25, 48)
+    assert need == 4 * 25 * 48
     with torch.cuda.stream(s):
         for fill in (0, 0xFF, 0x01):                                  # 0x01: rows that do not have the slot
             ws = torch.full((need,), fill, dtype=torch.uint8, device="cuda")
@@ -213,7 +215,7 @@ def test_captured_and_replayed():
     g = torch.Generator().manual_seed(6)
     c.append(c.rows(2, g), torch.tensor([0, 64], dtype=torch.int32))
     rows, slots = [t.cuda() for t in c.rows(2, g)], torch.zeros(2, dtype=torch.int32, device="cuda")
-    ws = torch.empty(gda.gda_cache_append_fp8_block_workspace_size(2, 64), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(16, dtype=torch.uint8, device="cuda")            # few rows: its size does not matter
     graph = torch.cuda.CUDAGraph()
     slots.fill_(-1)
     with torch.cuda.graph(graph):
@@ -249,5 +251,6 @@ def test_binding_refuses():
     with pytest.raises((TypeError, ValueError)):
         gda.gda_cache_append_fp8_block(*good, k_sig_bounds=c.dev[2][1], k_noise_bounds=c.dev[2][0])
     small = torch.empty(16, dtype=torch.uint8, device="cuda")
+    many = [t[:1].expand(1025, *t.shape[1:]).contiguous() for t in good[:4]]
     with pytest.raises(gda.GDAError):
-        gda.gda_cache_append_fp8_block(*good, workspace=small)
+        gda.gda_cache_append_fp8_block(*many, *good[4:], workspace=small)
