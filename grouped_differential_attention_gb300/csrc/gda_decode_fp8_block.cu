@@ -81,7 +81,7 @@ constexpr int kMaxStages = 6;
 // Warps that share an SM.
 __host__ __device__ constexpr int warps_per_sm(int rh, int d, int dv) {
     int warps = 8;
-    while (warps > 1 && (227 * 1024 / warps - 1024 - other_bytes(rh, d)) / tile_bytes(rh, d, dv) < 3) --warps;
+    while (warps > 1 && (227 * 1024 / warps - 1024 - other_bytes(rh, d)) / tile_bytes(rh, d, dv) < 2) --warps;
     return warps;
 }
 __host__ __device__ constexpr int stages_of(int rh, int d, int dv) {
@@ -246,31 +246,34 @@ __device__ __forceinline__ void next_sequence(const Params &p, Cursor &c) {
     enter(c, 0, len);
 }
 
-// A tile in the cache: its first row, and how many of its 16 positions exist.
+// A tile in the cache: its page, its first row there, and how many of its 16 positions exist.
 struct Place {
-    uint32_t row;
-    int n;
+    int page, offset, n;
 };
 
 // The tile at position pos (along the axis of ranges) of sequence b, whose length is len.  A page outside the pool is
 // read as page 0 and reported.  (The caches have 2^32 rows at most.)
 __device__ __forceinline__ Place place_of(const Params &p, int b, int g, int pos, int len) {
+    // no branch on what is loaded: the loads are waited for when the tile's copies are started, a step later
     long long at = pos;
     if (p.list != nullptr) {
         const int id = p.list[(static_cast<size_t>(b) * p.hn + g) * p.keep + (pos >> p.shift)];
         at = (static_cast<long long>(id) << p.shift) + (pos & ((1 << p.shift) - 1));
-        if (id < 0 || at >= len) return {0u, 0};
     }
-    const int i = static_cast<int>(at), pg = i / p.page_size;
-    int phys = b;
-    if (p.block_table != nullptr) {
-        phys = p.block_table[static_cast<size_t>(b) * p.max_pages + pg];
-        if (phys < 0 || phys >= p.num_pages) {
-            atomicOr(p.err, GDA_DEVERR_BAD_PAGE);
-            phys = 0;
-        }
+    const bool exists = at >= 0 && at < len;
+    const int i = exists ? static_cast<int>(at) : 0, pg = i / p.page_size;
+    const int phys = p.block_table != nullptr ? p.block_table[static_cast<size_t>(b) * p.max_pages + pg] : b;
+    return {phys, i - pg * p.page_size, exists ? min(kTile, len - i) : 0};
+}
+
+// Cache row that a tile begins at.
+__device__ __forceinline__ uint32_t row_of(const Params &p, const Place &at) {
+    int phys = at.page;
+    if (phys < 0 || phys >= p.num_pages) {
+        if (at.n > 0) atomicOr(p.err, GDA_DEVERR_BAD_PAGE);
+        phys = 0;
     }
-    return {static_cast<uint32_t>(phys) * p.page_size + (i - pg * p.page_size), min(kTile, len - i)};
+    return static_cast<uint32_t>(phys) * p.page_size + at.offset;
 }
 
 // Places of a stage of the ring, in bytes: K of one tile, its scales, V of the tile before it.
@@ -307,16 +310,16 @@ __device__ __forceinline__ const uint8_t *row_at(const uint8_t *base, uint32_t r
 
 // Starts the copies of K, and of all scales, of a tile.
 template <int D, int DV, int RH>
-__device__ __forceinline__ void issue_k(const Params &p, uint32_t stage, const Place &at, uint32_t h0, uint32_t g) {
+__device__ __forceinline__ void issue_k(const Params &p, uint32_t stage, uint32_t row, int n, uint32_t h0, uint32_t g) {
     using S = Stage<D, DV, RH>;
     const uint32_t lane = threadIdx.x & 31, hs = p.hs, hn = p.hn;
     const uint32_t pos = lane / (D / 16), ch = lane % (D / 16);
     constexpr uint32_t STEP = 512 / D;                   // rows that 32 chunks cover
-    const uint8_t *s1 = row_at(p.k1c, at.row + pos, hs * D) + (h0 * D + ch * 16);
-    const uint8_t *s2 = row_at(p.k2c, at.row + pos, hn * D) + (g * D + ch * 16);
+    const uint8_t *s1 = row_at(p.k1c, row + pos, hs * D) + (h0 * D + ch * 16);
+    const uint8_t *s2 = row_at(p.k2c, row + pos, hn * D) + (g * D + ch * 16);
 #pragma unroll
     for (uint32_t i = 0; i < kTile / STEP; ++i) {
-        const bool ok = static_cast<int>(pos + i * STEP) < at.n;
+        const bool ok = static_cast<int>(pos + i * STEP) < n;
         const uint32_t dst = stage + S::k + (pos + i * STEP) * D + k_chunk<D>(pos + i * STEP, ch) * 16;
 #pragma unroll
         for (int j = 0; j < RH; ++j) copy_async<16>(dst + j * kTile * D, s1 + j * D, ok);
@@ -325,25 +328,25 @@ __device__ __forceinline__ void issue_k(const Params &p, uint32_t stage, const P
         s2 += static_cast<size_t>(STEP) * hn * D;
     }
     // scales: lanes 0 .. RH of K, 4 .. RH + 3 of V; the eighth word is the number of positions
-    const uint32_t blk = at.row >> p.shift, j = lane & 3;
+    const uint32_t blk = row >> p.shift, j = lane & 3;
     const float *src = lane < 4 ? (j < RH ? p.k1s + static_cast<size_t>(blk) * hs + h0 + j : p.k2s + static_cast<size_t>(blk) * hn + g)
                                 : p.vs + static_cast<size_t>(blk) * hs + h0 + min(j, RH - 1u);
-    if (lane < 7) copy_async<4>(stage + S::scales + lane * 4, src, at.n > 0);
-    if (lane == 7) asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage + S::scales + 28), "r"(at.n) : "memory");
+    if (lane < 7) copy_async<4>(stage + S::scales + lane * 4, src, n > 0);
+    if (lane == 7) asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage + S::scales + 28), "r"(n) : "memory");
 }
 
 // Starts the copies of V of a tile.
 template <int D, int DV, int RH>
-__device__ __forceinline__ void issue_v(const Params &p, uint32_t stage, const Place &at, uint32_t h0) {
+__device__ __forceinline__ void issue_v(const Params &p, uint32_t stage, uint32_t first, int n, uint32_t h0) {
     using S = Stage<D, DV, RH>;
     const uint32_t lane = threadIdx.x & 31, hs = p.hs;
     const uint32_t pos = lane / (DV / 16), ch = lane % (DV / 16);
     constexpr uint32_t STEP = 512 / DV;
-    const uint8_t *s = row_at(p.vc, at.row + pos, hs * DV) + (h0 * DV + ch * 16);
+    const uint8_t *s = row_at(p.vc, first + pos, hs * DV) + (h0 * DV + ch * 16);
 #pragma unroll
     for (uint32_t i = 0; i < kTile / STEP; ++i) {
         const uint32_t row = v_row(pos + i * STEP), dst = stage + S::v + row * DV + v_chunk<DV>(row, ch) * 16;
-        const bool ok = static_cast<int>(pos + i * STEP) < at.n;
+        const bool ok = static_cast<int>(pos + i * STEP) < n;
 #pragma unroll
         for (int j = 0; j < RH; ++j) copy_async<16>(dst + j * kTile * DV, s + j * DV, ok);
         s += static_cast<size_t>(STEP) * hs * DV;
@@ -409,17 +412,18 @@ __global__ void __launch_bounds__(32, (Stage<D, DV, RH>::warps)) gda_decode_fp8_
     enter(use, static_cast<int>(range.start - range.before), positions_of(p, range.b));
     Cursor get = use;                                    // the copies' place, ahead of the arithmetic's
     int get_len = length_of(p, get.b);
-    Place next = place_of(p, get.b, g, get.pos, get_len), last{0u, 0};
-    bool more = true, pending = false;                   // K of `next`, V of `last` are still to be copied
-    int to = 0;
+    Place next = place_of(p, get.b, g, get.pos, get_len);
+    uint32_t last = 0;
+    int last_n = 0, to = 0;
+    bool more = true, pending = false;                   // K of `next`, V of the tile at row `last` are still to be copied
     auto copy = [&]() {
         __syncwarp();                                    // the readers of stage `to` are done
         const uint32_t stage = ring + to * S::bytes;
-        if (pending) issue_v<D, DV, RH>(p, stage, last, h0);
-        if (more) issue_k<D, DV, RH>(p, stage, next, h0, g);
+        if (pending) issue_v<D, DV, RH>(p, stage, last, last_n, h0);
         pending = more;
-        last = next;
         if (more) {
+            last = row_of(p, next), last_n = next.n;
+            issue_k<D, DV, RH>(p, stage, last, last_n, h0, g);
             get.pos += kTile;
             if (get.pos >= get.hi) {
                 if (get.left > 0) {
