@@ -173,14 +173,14 @@ __global__ void __launch_bounds__(THREADS) gda_block_select_kernel(const BlockSe
     __shared__ unsigned long long part_sum[WARPS];
     __shared__ uint32_t hist[WARPS][256];
     __shared__ uint2 sums[WARPS];
+    // a programmatic dependent of the scoring kernel: this wait, of every block, returns once its writes are visible
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int g = blockIdx.x, b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int n = (length_of(a, b) + a.block - 1) / a.block, kept = min(n, a.keep), r = a.hs / a.hn;
     int *list = a.list + (static_cast<size_t>(b) * a.hn + g) * a.keep;
     if (g == 0 && threadIdx.x == 0) a.count[b] = kept;
     for (int i = threadIdx.x + (n <= a.keep ? 0 : kept); i < a.keep; i += THREADS) list[i] = i < kept ? i : -1;
     if (n <= a.keep) return;
-    // a programmatic dependent of the scoring kernel: this wait returns once its writes are visible
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const float *x = a.scores + static_cast<size_t>(b) * (a.hs + a.hn) * most;
     auto row_of = [&](int i) { return x + static_cast<size_t>(i == r ? a.hs + g : g * r + i) * most; };
 

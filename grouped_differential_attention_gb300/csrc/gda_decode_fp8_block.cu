@@ -404,6 +404,8 @@ __global__ void __launch_bounds__(32, (Stage<D, DV, RH>::warps)) gda_decode_fp8_
     // every part is RH heads: the last begins early where they do not divide the group, and leaves what the parts
     // before it have done unwritten
     const int r = p.hs / p.hn, begin = min(part * RH, r - RH), done = part * RH - begin, h0 = g * r + begin;
+    // a programmatic dependent of whatever is ahead in the stream: nothing is read or written before that has completed
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     Range range;
     if (!range_of(p, split, range)) return;
     if (u % units == 0) note_sequences(p, range, split);
@@ -621,8 +623,17 @@ cudaError_t launch_split(const Params &p, cudaStream_t stream) {
     auto kern = gda_decode_fp8_block_split_kernel<D, DV, RH>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::total);
     if (e != cudaSuccess) return e;
-    kern<<<p.splits * p.hn * p.parts, 32, S::total, stream>>>(p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(p.splits * p.hn * p.parts);
+    cfg.blockDim = dim3(32);
+    cfg.dynamicSmemBytes = S::total;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 template <int D, int DV>
