@@ -203,10 +203,16 @@ __device__ __forceinline__ void note_sequences(const Params &p, const Range &r, 
 }
 
 // BYTES into shared memory, asynchronous; zeros in their place if `ok` is false.
-template <int BYTES>
+// Where noise heads list blocks of their own, no other warp reads what lies
+// beside a head's 64 bytes of a row, so L2 is to fetch no more than that (64
+// sequences, 16 blocks of 64 each: 191 MB and 43 us without the hint, 40 with
+// it; over all positions, where others do, 165 us without and 169 with it).
+template <int BYTES, bool LISTED>
 __device__ __forceinline__ void copy_async(uint32_t dst, const void *src, bool ok) {
     const int n = ok ? BYTES : 0;
-    if constexpr (BYTES == 16)
+    if constexpr (BYTES == 16 && LISTED)
+        asm volatile("cp.async.cg.shared.global.L2::64B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    else if constexpr (BYTES == 16)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
     else
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n) : "memory");
@@ -253,10 +259,11 @@ struct Place {
 
 // The tile at position pos (along the axis of ranges) of sequence b, whose length is len.  A page outside the pool is
 // read as page 0 and reported.  (The caches have 2^32 rows at most.)
+template <bool LISTED>
 __device__ __forceinline__ Place place_of(const Params &p, int b, int g, int pos, int len) {
     // no branch on what is loaded: the loads are waited for when the tile's copies are started, a step later
     long long at = pos;
-    if (p.list != nullptr) {
+    if constexpr (LISTED) {
         const int id = p.list[(static_cast<size_t>(b) * p.hn + g) * p.keep + (pos >> p.shift)];
         at = (static_cast<long long>(id) << p.shift) + (pos & ((1 << p.shift) - 1));
     }
@@ -309,7 +316,7 @@ __device__ __forceinline__ const uint8_t *row_at(const uint8_t *base, uint32_t r
 }
 
 // Starts the copies of K, and of all scales, of a tile.
-template <int D, int DV, int RH>
+template <int D, int DV, int RH, bool LISTED>
 __device__ __forceinline__ void issue_k(const Params &p, uint32_t stage, uint32_t row, int n, uint32_t h0, uint32_t g) {
     using S = Stage<D, DV, RH>;
     const uint32_t lane = threadIdx.x & 31, hs = p.hs, hn = p.hn;
@@ -322,8 +329,8 @@ __device__ __forceinline__ void issue_k(const Params &p, uint32_t stage, uint32_
         const bool ok = static_cast<int>(pos + i * STEP) < n;
         const uint32_t dst = stage + S::k + (pos + i * STEP) * D + k_chunk<D>(pos + i * STEP, ch) * 16;
 #pragma unroll
-        for (int j = 0; j < RH; ++j) copy_async<16>(dst + j * kTile * D, s1 + j * D, ok);
-        copy_async<16>(dst + RH * kTile * D, s2, ok);
+        for (int j = 0; j < RH; ++j) copy_async<16, LISTED>(dst + j * kTile * D, s1 + j * D, ok);
+        copy_async<16, LISTED>(dst + RH * kTile * D, s2, ok);
         s1 += static_cast<size_t>(STEP) * hs * D;
         s2 += static_cast<size_t>(STEP) * hn * D;
     }
@@ -331,12 +338,12 @@ __device__ __forceinline__ void issue_k(const Params &p, uint32_t stage, uint32_
     const uint32_t blk = row >> p.shift, j = lane & 3;
     const float *src = lane < 4 ? (j < RH ? p.k1s + static_cast<size_t>(blk) * hs + h0 + j : p.k2s + static_cast<size_t>(blk) * hn + g)
                                 : p.vs + static_cast<size_t>(blk) * hs + h0 + min(j, RH - 1u);
-    if (lane < 7) copy_async<4>(stage + S::scales + lane * 4, src, n > 0);
+    if (lane < 7) copy_async<4, LISTED>(stage + S::scales + lane * 4, src, n > 0);
     if (lane == 7) asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage + S::scales + 28), "r"(n) : "memory");
 }
 
 // Starts the copies of V of a tile.
-template <int D, int DV, int RH>
+template <int D, int DV, int RH, bool LISTED>
 __device__ __forceinline__ void issue_v(const Params &p, uint32_t stage, uint32_t first, int n, uint32_t h0) {
     using S = Stage<D, DV, RH>;
     const uint32_t lane = threadIdx.x & 31, hs = p.hs;
@@ -348,7 +355,7 @@ __device__ __forceinline__ void issue_v(const Params &p, uint32_t stage, uint32_
         const uint32_t row = v_row(pos + i * STEP), dst = stage + S::v + row * DV + v_chunk<DV>(row, ch) * 16;
         const bool ok = static_cast<int>(pos + i * STEP) < n;
 #pragma unroll
-        for (int j = 0; j < RH; ++j) copy_async<16>(dst + j * kTile * DV, s + j * DV, ok);
+        for (int j = 0; j < RH; ++j) copy_async<16, LISTED>(dst + j * kTile * DV, s + j * DV, ok);
         s += static_cast<size_t>(STEP) * hs * DV;
     }
 }
@@ -392,7 +399,7 @@ __device__ __forceinline__ float load_queries(const Params &p, uint8_t *dst, int
 }
 
 // One warp: split u / units of the range, unit u % units = (noise head, part of its group).
-template <int D, int DV, int RH>
+template <int D, int DV, int RH, bool LISTED>
 __global__ void __launch_bounds__(32, (Stage<D, DV, RH>::warps)) gda_decode_fp8_block_split_kernel(const Params p) {
     using S = Stage<D, DV, RH>;
     constexpr int NH = S::NH, SLABS = DV < 128 ? 1 : DV / 128, WORDS = DV < 128 ? 2 : 4, A = S::count - 1;
@@ -414,18 +421,18 @@ __global__ void __launch_bounds__(32, (Stage<D, DV, RH>::warps)) gda_decode_fp8_
     enter(use, static_cast<int>(range.start - range.before), positions_of(p, range.b));
     Cursor get = use;                                    // the copies' place, ahead of the arithmetic's
     int get_len = length_of(p, get.b);
-    Place next = place_of(p, get.b, g, get.pos, get_len);
+    Place next = place_of<LISTED>(p, get.b, g, get.pos, get_len);
     uint32_t last = 0;
     int last_n = 0, to = 0;
     bool more = true, pending = false;                   // K of `next`, V of the tile at row `last` are still to be copied
     auto copy = [&]() {
         __syncwarp();                                    // the readers of stage `to` are done
         const uint32_t stage = ring + to * S::bytes;
-        if (pending) issue_v<D, DV, RH>(p, stage, last, last_n, h0);
+        if (pending) issue_v<D, DV, RH, LISTED>(p, stage, last, last_n, h0);
         pending = more;
         if (more) {
             last = row_of(p, next), last_n = next.n;
-            issue_k<D, DV, RH>(p, stage, last, last_n, h0, g);
+            issue_k<D, DV, RH, LISTED>(p, stage, last, last_n, h0, g);
             get.pos += kTile;
             if (get.pos >= get.hi) {
                 if (get.left > 0) {
@@ -435,7 +442,7 @@ __global__ void __launch_bounds__(32, (Stage<D, DV, RH>::warps)) gda_decode_fp8_
                     more = false;
                 }
             }
-            if (more) next = place_of(p, get.b, g, get.pos, get_len);
+            if (more) next = place_of<LISTED>(p, get.b, g, get.pos, get_len);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
         to = to == A ? 0 : to + 1;
@@ -620,7 +627,8 @@ __global__ void __launch_bounds__(32, (Stage<D, DV, RH>::warps)) gda_decode_fp8_
 template <int D, int DV, int RH>
 cudaError_t launch_split(const Params &p, cudaStream_t stream) {
     using S = Stage<D, DV, RH>;
-    auto kern = gda_decode_fp8_block_split_kernel<D, DV, RH>;
+    const auto kern = p.list != nullptr ? gda_decode_fp8_block_split_kernel<D, DV, RH, true>
+                                       : gda_decode_fp8_block_split_kernel<D, DV, RH, false>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::total);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
