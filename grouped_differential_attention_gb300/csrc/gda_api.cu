@@ -97,8 +97,10 @@ int record_cuda_error(cudaError_t e) {
     return GDA_ERR_CUDA;
 }
 
-bool encode_tmap_4d_bf16(CUtensorMap *map, const void *base, const uint64_t dims[4],
-                         const uint64_t strides_bytes[3], const uint32_t box[4]) {
+namespace {
+
+// The driver's tensor map encoder, or nullptr.
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
     std::call_once(g_encode_once, []() {
         void *fn = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -109,15 +111,39 @@ bool encode_tmap_4d_bf16(CUtensorMap *map, const void *base, const uint64_t dims
         else
             cudaGetLastError();
     });
-    if (!g_encode) return false;
+    return g_encode;
+}
+
+}  // namespace
+
+bool encode_tmap_4d_bf16(CUtensorMap *map, const void *base, const uint64_t dims[4],
+                         const uint64_t strides_bytes[3], const uint32_t box[4]) {
+    const auto encode = encoder();
+    if (!encode) return false;
     cuuint64_t gdim[4] = {dims[0], dims[1], dims[2], dims[3]};
     cuuint64_t gstr[3] = {strides_bytes[0], strides_bytes[1], strides_bytes[2]};
     cuuint32_t bdim[4] = {box[0], box[1], box[2], box[3]};
     cuuint32_t estr[4] = {1, 1, 1, 1};
-    const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), gdim,
-                                gstr, bdim, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), gdim,
+                              gstr, bdim, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
+bool encode_tmap_3d_u8(CUtensorMap *map, const void *base, const uint64_t dims[3], const uint64_t strides_bytes[2],
+                       const uint32_t box[3], int swizzle, bool narrow) {
+    const auto encode = encoder();
+    if (!encode) return false;
+    const cuuint64_t gdim[3] = {dims[0], dims[1], dims[2]}, gstr[2] = {strides_bytes[0], strides_bytes[1]};
+    const cuuint32_t bdim[3] = {box[0], box[1], box[2]}, estr[3] = {1, 1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), gdim, gstr, bdim, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              swizzle == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                              : swizzle == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                              : CU_TENSOR_MAP_SWIZZLE_NONE,
+                              narrow ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }
 
@@ -235,7 +261,7 @@ int decode_fp8_block(DecodeFp8BlockArgs &a, size_t workspace_bytes, gda_stream_t
     if (st != GDA_OK) return st;
     if (!(a.d == 64 || a.d == 128) || !(a.dv == 64 || a.dv == 128 || a.dv == 256)) return GDA_ERR_UNSUPPORTED;
     if (heads_above(a.hs, a.hn, 128) || a.B > 65535) return GDA_ERR_UNSUPPORTED;
-    if (rows > 4294967296.0) return GDA_ERR_UNSUPPORTED;   // rows of the caches are counted in 32 bits
+    if (rows > 2147483647.0) return GDA_ERR_UNSUPPORTED;   // a row is a coordinate of the copies
     // positions are 32 bits wide and stepped by 16; a range (an 11th of the batch's at most) is counted in 32 bits too
     const long long reach = a.list ? static_cast<long long>(a.keep) * a.block : Lcap;
     if (Lcap > 0x7ffffff0 || reach > 0x7ffffff0 || a.B * reach > 1LL << 34) return GDA_ERR_UNSUPPORTED;

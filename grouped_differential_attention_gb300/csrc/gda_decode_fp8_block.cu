@@ -73,21 +73,22 @@ Heads heads_of(int hs, int hn, int dv) {
 }
 
 // Shared memory of a warp, in bytes: tiles (codes of rh + 1 rows of K and rh of
-// V for 16 positions, and their scales), then queries and weights.
-__host__ __device__ constexpr int tile_bytes(int rh, int d, int dv) { return kTile * ((rh + 1) * d + rh * dv) + 32; }
-__host__ __device__ constexpr int other_bytes(int rh, int d) { return (rh + 1) * d * 2 + 2 * rh * 128; }
-
-constexpr int kMaxStages = 6;
-// Warps that share an SM.
-__host__ __device__ constexpr int warps_per_sm(int rh, int d, int dv) {
-    int warps = 8;
-    while (warps > 1 && (227 * 1024 / warps - 1024 - other_bytes(rh, d)) / tile_bytes(rh, d, dv) < 2) --warps;
-    return warps;
-}
-__host__ __device__ constexpr int stages_of(int rh, int d, int dv) {
-    const int fit = (227 * 1024 / warps_per_sm(rh, d, dv) - 1024 - other_bytes(rh, d)) / tile_bytes(rh, d, dv);
+// V for 16 positions), the first at a multiple of 1024, then queries, weights,
+// and for each stage the tile's scales and a barrier.
+constexpr int kMaxStages = 4;
+__host__ __device__ constexpr int tile_bytes(int rh, int d, int dv) { return kTile * ((rh + 1) * d + rh * dv); }
+__host__ __device__ constexpr int other_bytes(int rh, int d) { return (rh + 1) * d * 2 + rh * 128 + kMaxStages * 40; }
+__host__ __device__ constexpr int stages_with(int warps, int rh, int d, int dv) {
+    const int fit = (227 * 1024 / warps - 2048 - other_bytes(rh, d)) / tile_bytes(rh, d, dv);
     return fit > kMaxStages ? kMaxStages : fit;
 }
+// Warps that share an SM: eight, or as many as leave each two stages.
+__host__ __device__ constexpr int warps_per_sm(int rh, int d, int dv) {
+    int warps = 8;
+    while (warps > 1 && stages_with(warps, rh, d, dv) < 2) --warps;
+    return warps;
+}
+__host__ __device__ constexpr int stages_of(int rh, int d, int dv) { return stages_with(warps_per_sm(rh, d, dv), rh, d, dv); }
 
 struct Plan {
     Heads heads;
@@ -202,20 +203,25 @@ __device__ __forceinline__ void note_sequences(const Params &p, const Range &r, 
     }
 }
 
-// BYTES into shared memory, asynchronous; zeros in their place if `ok` is false.
-// Where noise heads list blocks of their own, no other warp reads what lies
-// beside a head's 64 bytes of a row, so L2 is to fetch no more than that (64
-// sequences, 16 blocks of 64 each: 191 MB and 43 us without the hint, 40 with
-// it; over all positions, where others do, 165 us without and 169 with it).
-template <int BYTES, bool LISTED>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, bool ok) {
-    const int n = ok ? BYTES : 0;
-    if constexpr (BYTES == 16 && LISTED)
-        asm volatile("cp.async.cg.shared.global.L2::64B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-    else if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n) : "memory");
+// Four bytes into shared memory, asynchronous; zeros in their place if `ok` is false.
+__device__ __forceinline__ void copy_async4(uint32_t dst, const void *src, bool ok) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(ok ? 4 : 0) : "memory");
+}
+
+// A box of the tensor `map` into shared memory; its bytes count on the barrier `bar`.
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap &map, uint32_t bar, int row, int head) {
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(&map)), "r"(0), "r"(row),
+                 "r"(head), "r"(bar) : "memory");
+}
+
+// Waits, for a second at most, until the barrier's phase of this parity has completed.
+__device__ __forceinline__ bool landed(uint32_t bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(bar, parity))
+        if (global_timer_ns() - t0 > kWaitTimeoutNs) return false;
+    return true;
 }
 
 // a * b + c: 16 x 16 (f16) times 16 x 8 (f16).
@@ -283,81 +289,33 @@ __device__ __forceinline__ uint32_t row_of(const Params &p, const Place &at) {
     return static_cast<uint32_t>(phys) * p.page_size + at.offset;
 }
 
-// Places of a stage of the ring, in bytes: K of one tile, its scales, V of the tile before it.
+// Places in a warp's shared memory, in bytes; a stage holds K of one tile and V of the tile before it.
 template <int D, int DV, int RH>
 struct Stage {
     static constexpr int NH = RH + 1;                    // heads with scores; the noise head is the last
-    static constexpr int k = 0, v = NH * kTile * D, scales = v + RH * kTile * DV, bytes = tile_bytes(RH, D, DV);
-    static_assert(bytes == scales + 32 && NH <= 4, "four scales of K, three of V, the number of positions");
+    static constexpr int k = 0, v = NH * kTile * D, bytes = tile_bytes(RH, D, DV);
+    static constexpr int k_bytes = v, v_bytes = bytes - v;
+    static_assert(bytes % 1024 == 0 && v % 1024 == 0, "boxes change places by the bits of their addresses");
     static constexpr int count = stages_of(RH, D, DV);
-    static_assert(count >= 2, "a tile must be copied while another is used");
-    static constexpr int queries = count * bytes, weights = queries + NH * D * 2, total = weights + 2 * RH * 128;
+    static_assert(count >= 2 && NH <= 4, "a tile is copied while another is used; four scales of K, three of V");
+    static constexpr int queries = count * bytes, weights = queries + NH * D * 2, scales = weights + RH * 128;
+    static constexpr int bars = scales + kMaxStages * 32, total = bars + kMaxStages * 8 + 1024;
     static constexpr int warps = warps_per_sm(RH, D, DV);
 };
 
-// K codes in shared memory: 16-byte chunks of odd rows of 128 bytes change places, so that the two rows that eight lanes
-// read lie in different banks.
-template <int D>
-__device__ __forceinline__ uint32_t k_chunk(uint32_t row, uint32_t chunk) { return D == 128 ? chunk ^ ((row & 1) << 2) : chunk; }
+// The tensors of the caches, rows of heads: boxes of a head row (128 bytes of it at most) x 16 cache rows x heads.
+struct Maps {
+    CUtensorMap k1, k2, v;
+};
 
-// V codes: position pos is row v_row(pos), so that a lane's four positions 2t,
-// 2t + 8, 2t + 1, 2t + 9 are rows t, t + 4, t + 8, t + 12; chunks of a row change
-// places by its low bits, so that the rows t = 0 .. 3 that one load reads lie in
-// different banks.
-__device__ __forceinline__ uint32_t v_row(uint32_t pos) { return (pos >> 1) | ((pos & 1) << 3); }
-template <int DV>
-__device__ __forceinline__ uint32_t v_chunk(uint32_t row, uint32_t chunk) {
-    return DV == 64 ? chunk ^ (((row >> 1) & 1) << 1) : chunk ^ ((row & 3) << 1);
-}
-
-// base + row * pitch, one multiply-add.
-__device__ __forceinline__ const uint8_t *row_at(const uint8_t *base, uint32_t row, uint32_t pitch) {
-    return base + static_cast<uint64_t>(row) * pitch;
-}
-
-// Starts the copies of K, and of all scales, of a tile.
-template <int D, int DV, int RH, bool LISTED>
-__device__ __forceinline__ void issue_k(const Params &p, uint32_t stage, uint32_t row, int n, uint32_t h0, uint32_t g) {
-    using S = Stage<D, DV, RH>;
-    const uint32_t lane = threadIdx.x & 31, hs = p.hs, hn = p.hn;
-    const uint32_t pos = lane / (D / 16), ch = lane % (D / 16);
-    constexpr uint32_t STEP = 512 / D;                   // rows that 32 chunks cover
-    const uint8_t *s1 = row_at(p.k1c, row + pos, hs * D) + (h0 * D + ch * 16);
-    const uint8_t *s2 = row_at(p.k2c, row + pos, hn * D) + (g * D + ch * 16);
-#pragma unroll
-    for (uint32_t i = 0; i < kTile / STEP; ++i) {
-        const bool ok = static_cast<int>(pos + i * STEP) < n;
-        const uint32_t dst = stage + S::k + (pos + i * STEP) * D + k_chunk<D>(pos + i * STEP, ch) * 16;
-#pragma unroll
-        for (int j = 0; j < RH; ++j) copy_async<16, LISTED>(dst + j * kTile * D, s1 + j * D, ok);
-        copy_async<16, LISTED>(dst + RH * kTile * D, s2, ok);
-        s1 += static_cast<size_t>(STEP) * hs * D;
-        s2 += static_cast<size_t>(STEP) * hn * D;
-    }
-    // scales: lanes 0 .. RH of K, 4 .. RH + 3 of V; the eighth word is the number of positions
-    const uint32_t blk = row >> p.shift, j = lane & 3;
+// Starts the loads of the scales of a tile: lanes 0 .. RH of K, 4 .. RH + 3 of V; the eighth word is the number of positions.
+template <int RH>
+__device__ __forceinline__ void issue_scales(const Params &p, uint32_t dst, uint32_t row, int n, uint32_t h0, uint32_t g) {
+    const uint32_t lane = threadIdx.x & 31, hs = p.hs, hn = p.hn, blk = row >> p.shift, j = lane & 3;
     const float *src = lane < 4 ? (j < RH ? p.k1s + static_cast<size_t>(blk) * hs + h0 + j : p.k2s + static_cast<size_t>(blk) * hn + g)
                                 : p.vs + static_cast<size_t>(blk) * hs + h0 + min(j, RH - 1u);
-    if (lane < 7) copy_async<4, LISTED>(stage + S::scales + lane * 4, src, n > 0);
-    if (lane == 7) asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage + S::scales + 28), "r"(n) : "memory");
-}
-
-// Starts the copies of V of a tile.
-template <int D, int DV, int RH, bool LISTED>
-__device__ __forceinline__ void issue_v(const Params &p, uint32_t stage, uint32_t first, int n, uint32_t h0) {
-    using S = Stage<D, DV, RH>;
-    const uint32_t lane = threadIdx.x & 31, hs = p.hs;
-    const uint32_t pos = lane / (DV / 16), ch = lane % (DV / 16);
-    constexpr uint32_t STEP = 512 / DV;
-    const uint8_t *s = row_at(p.vc, first + pos, hs * DV) + (h0 * DV + ch * 16);
-#pragma unroll
-    for (uint32_t i = 0; i < kTile / STEP; ++i) {
-        const uint32_t row = v_row(pos + i * STEP), dst = stage + S::v + row * DV + v_chunk<DV>(row, ch) * 16;
-        const bool ok = static_cast<int>(pos + i * STEP) < n;
-#pragma unroll
-        for (int j = 0; j < RH; ++j) copy_async<16, LISTED>(dst + j * kTile * DV, s + j * DV, ok);
-        s += static_cast<size_t>(STEP) * hs * DV;
-    }
+    if (lane < 7) copy_async4(dst + lane * 4, src, n > 0);
+    if (lane == 7) asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + 28), "r"(n) : "memory");
 }
 
 template <typename V>
@@ -400,10 +358,12 @@ __device__ __forceinline__ float load_queries(const Params &p, uint8_t *dst, int
 
 // One warp: split u / units of the range, unit u % units = (noise head, part of its group).
 template <int D, int DV, int RH, bool LISTED>
-__global__ void __launch_bounds__(32, (Stage<D, DV, RH>::warps)) gda_decode_fp8_block_split_kernel(const Params p) {
+__global__ void __launch_bounds__(32, (Stage<D, DV, RH>::warps)) gda_decode_fp8_block_split_kernel(
+    const Params p, const __grid_constant__ Maps maps) {
     using S = Stage<D, DV, RH>;
     constexpr int NH = S::NH, SLABS = DV < 128 ? 1 : DV / 128, WORDS = DV < 128 ? 2 : 4, A = S::count - 1;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ __align__(1024) uint8_t raw[];
+    uint8_t *const smem = raw + (-smem_u32(raw) & 1023u);
     const int lane = threadIdx.x, quad = lane >> 2, t = lane & 3;
     const uint32_t ring = smem_u32(smem);
     const int units = p.hn * p.parts, u = blockIdx.x;
@@ -412,6 +372,9 @@ __global__ void __launch_bounds__(32, (Stage<D, DV, RH>::warps)) gda_decode_fp8_
     // before it have done unwritten
     const int r = p.hs / p.hn, begin = min(part * RH, r - RH), done = part * RH - begin, h0 = g * r + begin;
     // a programmatic dependent of whatever is ahead in the stream: nothing is read or written before that has completed
+    if (lane < S::count) mbar_init(reinterpret_cast<uint64_t *>(smem + S::bars) + lane, 1);
+    fence_mbar_init();
+    __syncwarp();
     asm volatile("griddepcontrol.wait;" ::: "memory");
     Range range;
     if (!range_of(p, split, range)) return;
@@ -421,18 +384,24 @@ __global__ void __launch_bounds__(32, (Stage<D, DV, RH>::warps)) gda_decode_fp8_
     enter(use, static_cast<int>(range.start - range.before), positions_of(p, range.b));
     Cursor get = use;                                    // the copies' place, ahead of the arithmetic's
     int get_len = length_of(p, get.b);
-    Place next = place_of<LISTED>(p, get.b, g, get.pos, get_len);
+    Place next{0, 0, 0};
     uint32_t last = 0;
-    int last_n = 0, to = 0;
-    bool more = true, pending = false;                   // K of `next`, V of the tile at row `last` are still to be copied
+    int to = 0;
+    bool more = true, ready = false, pending = false;    // positions are left; K of `next`, V of the tile at row `last` are to be copied
     auto copy = [&]() {
-        __syncwarp();                                    // the readers of stage `to` are done
-        const uint32_t stage = ring + to * S::bytes;
-        if (pending) issue_v<D, DV, RH, LISTED>(p, stage, last, last_n, h0);
-        pending = more;
-        if (more) {
-            last = row_of(p, next), last_n = next.n;
-            issue_k<D, DV, RH, LISTED>(p, stage, last, last_n, h0, g);
+        const uint32_t stage = ring + to * S::bytes, bar = ring + S::bars + to * 8;
+        if (lane == 0 && (ready || pending))
+            mbar_arrive_expect_tx(reinterpret_cast<uint64_t *>(smem + S::bars) + to,
+                                  (ready ? S::k_bytes : 0) + (pending ? S::v_bytes : 0));
+        if (pending && lane == 0) load_box(stage + S::v, maps.v, bar, static_cast<int>(last), h0 * (DV < 128 ? 1 : DV / 128));
+        pending = ready;
+        if (ready) {
+            last = row_of(p, next);
+            if (lane == 0) {
+                load_box(stage + S::k, maps.k1, bar, static_cast<int>(last), h0);
+                load_box(stage + S::k + RH * kTile * D, maps.k2, bar, static_cast<int>(last), g);
+            }
+            issue_scales<RH>(p, ring + S::scales + to * 32, last, next.n, h0, g);
             get.pos += kTile;
             if (get.pos >= get.hi) {
                 if (get.left > 0) {
@@ -442,15 +411,15 @@ __global__ void __launch_bounds__(32, (Stage<D, DV, RH>::warps)) gda_decode_fp8_
                     more = false;
                 }
             }
-            if (more) next = place_of<LISTED>(p, get.b, g, get.pos, get_len);
         }
+        ready = more;
+        if (more) next = place_of<LISTED>(p, get.b, g, get.pos, get_len);
         asm volatile("cp.async.commit_group;" ::: "memory");
         to = to == A ? 0 : to + 1;
     };
-    for (int i = 0; i < A; ++i) copy();
 
     uint8_t *const queries = smem + S::queries, *const weights = smem + S::weights;
-    float factor = load_queries<D, RH>(p, queries, use.b, h0, g);
+    float factor = 0.f;
     float acc[RH][SLABS * WORDS][4];                     // [w]: of tiles 2 w + t / 2 and map t % 2, see values_of
     float m = kLowest, l = 0.f;                          // of head t (both its lanes' positions; l of this lane's only)
     float v_most = 0.f, v_inverse = 0.f;                 // of head t: the largest scale of V so far, and 1 over it
@@ -463,9 +432,8 @@ __global__ void __launch_bounds__(32, (Stage<D, DV, RH>::warps)) gda_decode_fp8_
 #pragma unroll
                 for (int k = 0; k < 4; ++k) acc[j][i][k] = 0.f;
     };
-    clear();
-    const uint32_t k_at = S::k + quad * D + k_chunk<D>(quad, t) * 16;
-    auto scores_of = [&](const uint8_t *const stage, uint8_t *const out) {
+    int have = kTile;                                    // positions of the tile scored last
+    auto scores_of = [&](const uint8_t *const stage, const uint8_t *const scales) {
         // lane (quad, t) ends up with positions quad, quad + 8 of head t
         float sc0 = 0.f, sc1 = 0.f;
 #pragma unroll
@@ -473,8 +441,11 @@ __global__ void __launch_bounds__(32, (Stage<D, DV, RH>::warps)) gda_decode_fp8_
             float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int half = 0; half < D / 64; ++half) {  // 16 dims of this lane
-                const uint8_t *ka = stage + (k_at ^ (64 * half)) + j * kTile * D;
-                const uint8_t *qa = queries + j * D * 2 + half * 128 + t * 32;
+                // 16-byte chunks of rows of 128 bytes are exchanged by the row's low bits: two rows that eight lanes read
+                // lie in different banks
+                const int chunk = D == 64 ? t : 2 * t + half;
+                const uint8_t *ka = stage + S::k + (j * kTile + quad) * D + (D == 64 ? chunk : chunk ^ quad) * 16;
+                const uint8_t *qa = queries + j * D * 2 + chunk * 32;
                 const uint4 lo = at<uint4>(ka), hi = at<uint4>(ka + 8 * D), b0 = at<uint4>(qa), b1 = at<uint4>(qa + 16);
                 const uint32_t a[4] = {lo.x, lo.y, lo.z, lo.w}, e[4] = {hi.x, hi.y, hi.z, hi.w};
                 const uint32_t b[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
@@ -486,8 +457,8 @@ __global__ void __launch_bounds__(32, (Stage<D, DV, RH>::warps)) gda_decode_fp8_
             }
             if (t == j) sc0 = c[0], sc1 = c[2];
         }
-        const float ks = at<float>(stage + S::scales + 4 * t), vs = at<float>(stage + S::scales + 16 + 4 * t);
-        const int have = at<int>(stage + S::scales + 28);
+        const float ks = at<float>(scales + 4 * t), vs = at<float>(scales + 16 + 4 * t);
+        have = at<int>(scales + 28);
         sc0 = sc0 * factor * ks, sc1 = sc1 * factor * ks;
         if (quad >= have) sc0 = -INFINITY;
         if (quad + 8 >= have) sc1 = -INFINITY;
@@ -510,30 +481,36 @@ __global__ void __launch_bounds__(32, (Stage<D, DV, RH>::warps)) gda_decode_fp8_
         const uint32_t sh = pack_half2(s0, s1), nh = pack_half2(n0, n1);
         const float2 sf = half2_bits_to_float2(sh), nf = half2_bits_to_float2(nh);
         if (t < RH)
-            *reinterpret_cast<uint4 *>(out + t * 128 + quad * 16) =
+            *reinterpret_cast<uint4 *>(weights + t * 128 + quad * 16) =
                 make_uint4(sh, pack_half2(s0 - sf.x, s1 - sf.y), nh, pack_half2(n0 - nf.x, n1 - nf.y));
     };
 
-    auto values_of = [&](const uint8_t *const stage, const uint8_t *const in) {
+    auto values_of = [&](const uint8_t *const stage) {
         // k slots (2t, 2t + 1) are positions 2t, 2t + 8 and (2t + 8, 2t + 9) are 2t + 1, 2t + 9.  A lane has 4 WORDS dims
         // from 4 WORDS quad on (and 128 further, at DV = 256); tile 2 w has the first two of word w in its rows quad and
         // quad + 8, tile 2 w + 1 the others.  Columns 0 .. 3 are upper and lower parts of the signal map's weights and of
         // the noise map's for even tiles, 4 .. 7 for odd ones.
-        constexpr int LOAD = 4 * WORDS;
-        const uint32_t place = t * DV + (DV == 64 ? v_chunk<DV>(t, quad >> 1) * 16 + (quad & 1) * 8 : v_chunk<DV>(t, quad) * 16);
+        constexpr int LOAD = 4 * WORDS, ROW = DV < 128 ? 64 : 128;
+        // rows of 128 bytes: 16-byte chunks exchanged by the row's three low bits; of 64: by its bits 1 and 2
+        uint32_t place[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t row = 2 * t + 8 * (k & 1) + (k >> 1);
+            place[k] = row * ROW + (DV == 64 ? ((quad >> 1) ^ (row >> 1 & 3)) * 16 + (quad & 1) * 8 : (quad ^ (row & 7)) * 16);
+        }
 #pragma unroll
         for (int j = 0; j < RH; ++j) {
-            const uint8_t *wa = in + j * 128 + t * 32 + (quad & 3) * 4;
+            const uint8_t *wa = weights + j * 128 + t * 32 + (quad & 3) * 4;
             const uint32_t w0 = at<uint32_t>(wa), w1 = at<uint32_t>(wa + 16);
             const uint32_t even0 = quad < 4 ? w0 : 0u, even1 = quad < 4 ? w1 : 0u;
             const uint32_t odd0 = quad < 4 ? 0u : w0, odd1 = quad < 4 ? 0u : w1;
-            const uint8_t *va = stage + S::v + j * kTile * DV + place;
+            const uint8_t *va = stage + S::v + j * kTile * DV;
 #pragma unroll
             for (int s = 0; s < SLABS; ++s) {
                 uint32_t x[4][WORDS];                    // [2t, 2t + 8, 2t + 1, 2t + 9]
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const uint8_t *row = va + k * 4 * DV + s * 128;
+                    const uint8_t *row = va + s * kTile * 128 + place[k];
                     if constexpr (LOAD == 8) {
                         const uint2 v = at<uint2>(row);
                         x[k][0] = v.x, x[k][1] = v.y;
@@ -554,6 +531,15 @@ __global__ void __launch_bounds__(32, (Stage<D, DV, RH>::warps)) gda_decode_fp8_
                 }
             }
         }
+    };
+    // Rows of V behind the last position of a tile are whatever the cache holds there, NaN codes too, which no weight of 0
+    // takes away: they become zeros.
+    auto drop_rows = [&](uint8_t *const stage) {
+        constexpr int ROW = DV < 128 ? 64 : 128, ROWS = RH * kTile * DV / ROW;
+        for (int i = lane; i < ROWS * ROW / 16; i += 32)
+            if (i / (ROW / 16) % kTile >= have) *reinterpret_cast<uint4 *>(stage + S::v + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+        __syncwarp();
     };
     auto rescale = [&]() {
         if (__any_sync(0xffffffffu, shrink != 1.f || v_shrink != 1.f)) {
@@ -590,45 +576,78 @@ __global__ void __launch_bounds__(32, (Stage<D, DV, RH>::warps)) gda_decode_fp8_
         }
     };
 
-    int from = 0, buffer = 0;
-    bool fresh = true, ending = false;                   // no tile of this part has been scored; the last one was its last
+    // Step g: the values of tile g - 1, what ends with it and begins with tile g, and the scores of tile g.  Every piece
+    // of the work stands in one place: a kernel starts with cold instructions, and what a first and a last step had of
+    // their own cost more than the order of the pieces gains.
+    int from = 1, ahead = A + 1;                         // the first step copies nothing; steps until the first tile is there
+    uint32_t parity = 0;                                 // of each stage's barrier
+    bool first = true, ending = true;                    // no tile has been scored; the last one scored was its part's last
     for (;;) {
+        __syncwarp();                                    // the readers of the stage to be written are done
         copy();
+        if (ahead > 0) {
+            --ahead;
+            continue;
+        }
         asm volatile("cp.async.wait_group %0;" ::"n"(A) : "memory");
+        if (!landed(ring + S::bars + from * 8, parity >> from & 1u)) {
+            // it gives up; the copies of the other stages are waited for, as long again
+            atomicOr(p.err, GDA_DEVERR_DECODE_TIMEOUT);
+            for (int i = 0; i < S::count; ++i) landed(ring + S::bars + i * 8, parity >> i & 1u);
+            return;
+        }
+        parity ^= 1u << from;
         __syncwarp();                                    // every lane's copies of this stage have landed
-        const uint8_t *const stage = smem + from * S::bytes;
-        uint8_t *const mine = weights + buffer * RH * 128, *const before = weights + (buffer ^ 1) * RH * 128;
+        uint8_t *const stage = smem + from * S::bytes;
+        const uint8_t *const scales = smem + S::scales + from * 32;
         from = from == A ? 0 : from + 1;
+        if (!first) {
+            if (have < kTile) drop_rows(stage);
+            values_of(stage);
+        }
         if (ending) {
-            values_of(stage, before);
-            leave();
-            if (use.left == 0) return;
-            next_sequence(p, use);
+            if (!first) {
+                leave();
+                if (use.left == 0) return;
+                next_sequence(p, use);
+            }
             factor = load_queries<D, RH>(p, queries, use.b, h0, g);
-            __syncwarp();
             clear();
             m = kLowest, l = 0.f, v_most = 0.f, v_inverse = 0.f;
-            fresh = true;
+            first = false;
         }
-        if (fresh) {
-            scores_of(stage, mine);
-            fresh = false;
-        } else {                                         // twice, so that these are not parted by the test
-            scores_of(stage, mine);
-            values_of(stage, before);
-            rescale();
-        }
-        buffer ^= 1;
+        __syncwarp();                                    // the weights have been read, the queries are there
+        scores_of(stage, scales);
+        rescale();
         use.pos += kTile;
         ending = use.pos >= use.hi;
     }
+}
+
+// Rows of `heads` heads of n bytes each, in boxes of (at most 128 bytes) x 16 cache rows x `box` of those.
+// Where noise heads list blocks of their own, no other warp reads what lies beside a head's part of a row, so L2 is to
+// fetch no more than that.
+bool encode(CUtensorMap *map, const uint8_t *base, int n, int heads, long long rows, int box, int swizzle, bool listed) {
+    const int piece = n < 128 ? n : 128;
+    const uint64_t dims[3] = {static_cast<uint64_t>(piece), static_cast<uint64_t>(rows),
+                              static_cast<uint64_t>(heads) * (n / piece)};
+    const uint64_t strides[2] = {static_cast<uint64_t>(heads) * n, static_cast<uint64_t>(piece)};
+    const uint32_t shape[3] = {static_cast<uint32_t>(piece), kTile, static_cast<uint32_t>(box * (n / piece))};
+    return encode_tmap_3d_u8(map, base, dims, strides, shape, swizzle, listed);
 }
 
 template <int D, int DV, int RH>
 cudaError_t launch_split(const Params &p, cudaStream_t stream) {
     using S = Stage<D, DV, RH>;
     const auto kern = p.list != nullptr ? gda_decode_fp8_block_split_kernel<D, DV, RH, true>
-                                       : gda_decode_fp8_block_split_kernel<D, DV, RH, false>;
+                                        : gda_decode_fp8_block_split_kernel<D, DV, RH, false>;
+    Maps maps;
+    const long long rows = static_cast<long long>(p.num_pages) * p.page_size;
+    const bool listed = p.list != nullptr;
+    constexpr int KS = D == 64 ? 0 : 128, VS = DV == 64 ? 64 : 128;
+    if (!encode(&maps.k1, p.k1c, D, p.hs, rows, RH, KS, listed) || !encode(&maps.k2, p.k2c, D, p.hn, rows, 1, KS, listed) ||
+        !encode(&maps.v, p.vc, DV, p.hs, rows, RH, VS, listed))
+        return cudaErrorInvalidValue;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::total);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
@@ -641,7 +660,7 @@ cudaError_t launch_split(const Params &p, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, p);
+    return cudaLaunchKernelEx(&cfg, kern, p, maps);
 }
 
 template <int D, int DV>

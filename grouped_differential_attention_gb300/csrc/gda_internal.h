@@ -227,4 +227,10 @@ DecodePlan decode_plan(int B, int Lcap, int hs, int hn, int dv);
 bool encode_tmap_4d_bf16(CUtensorMap *map, const void *base, const uint64_t dims[4],
                          const uint64_t strides_bytes[3], const uint32_t box[4]);
 
+// 3-D map of bytes, dims/box innermost first, strides in bytes for dims 1 and
+// 2; swizzle of 0, 64 or 128 bytes; L2 fetches 64 bytes at a time where
+// `narrow`, else 256.
+bool encode_tmap_3d_u8(CUtensorMap *map, const void *base, const uint64_t dims[3], const uint64_t strides_bytes[2],
+                       const uint32_t box[3], int swizzle, bool narrow);
+
 }  // namespace gda

@@ -672,7 +672,7 @@ size_t gda_block_select_workspace_size(int B, int max_blocks, int h_s, int h_n);
  *   initialisation; calls in flight at the same time need a workspace each.
  * Supported: d in {64, 128}; dv in {64, 128, 256}; h_s + h_n <= 128;
  * B <= 65535; block 16, 32, 64 or 128, dividing page_size (Lcap); Lcap
- * (max_pages * page_size) at most 2^31 - 16; at most 2^32 rows in the caches;
+ * (max_pages * page_size) at most 2^31 - 16; fewer than 2^31 rows in the caches;
  * B times Lcap (sparse: times keep * block, itself at most 2^31 - 16) at most
  * 2^34.
  */
