@@ -262,7 +262,7 @@ int decode_fp8_block(DecodeFp8BlockArgs &a, size_t workspace_bytes, gda_stream_t
     if (!(a.d == 64 || a.d == 128) || !(a.dv == 64 || a.dv == 128 || a.dv == 256)) return GDA_ERR_UNSUPPORTED;
     if (heads_above(a.hs, a.hn, 128) || a.B > 65535) return GDA_ERR_UNSUPPORTED;
     if (rows > 2147483647.0) return GDA_ERR_UNSUPPORTED;   // a row is a coordinate of the copies
-    // positions are 32 bits wide and stepped by 16; a range (an 11th of the batch's at most) is counted in 32 bits too
+    // positions of a sequence, and tiles of 16 of all sequences, are counted in 32 bits
     const long long reach = a.list ? static_cast<long long>(a.keep) * a.block : Lcap;
     if (Lcap > 0x7ffffff0 || reach > 0x7ffffff0 || a.B * reach > 1LL << 34) return GDA_ERR_UNSUPPORTED;
     for (const void *p : ptrs)

@@ -50,7 +50,6 @@ namespace gda {
 namespace {
 
 constexpr int kTile = 16;              // positions of a tile
-constexpr int kMinRange = 16;          // fewest positions of a range
 constexpr float kWeightBits = 15.f;    // weights carry a factor 2^15: the largest is within f16, the smallest far from its end
 constexpr float kLowest = -3.0e38f;    // a maximum over no position
 
@@ -123,66 +122,67 @@ struct Params {
     int splits, parts;                       // ranges; parts of a noise head's group
     const int *block_table;
     int page_size, max_pages, num_pages;
-    int shift;                               // log2 of a block's tokens
+    int shift;                               // log2 of a block's tiles
+    uint32_t page_factor;                    // tile / (tiles of a page) = tile * page_factor >> page_shift, below 2^31
+    int page_shift;
     const int *list, *count;                 // [B][hn][keep], [B], or nullptr: all blocks
     int keep;
 };
 
-// Length of sequence b; one outside [0, Lcap] is clamped and reported.
-__device__ __forceinline__ int length_of(const Params &p, int b) {
-    const int len = p.lens[b];
-    if (len >= 0 && len <= p.Lcap) return len;
-    atomicOr(p.err, GDA_DEVERR_BAD_LENGTH);
-    return len < 0 ? 0 : p.Lcap;
+// A sequence: its length, and its tiles along the axis that is cut into ranges.
+struct Span {
+    int len, tiles;
+};
+
+// A length outside [0, Lcap] and a count outside [0, keep] are clamped and reported.
+template <bool LISTED>
+__device__ __forceinline__ Span span_of(const Params &p, int b) {
+    const int len = p.lens[b], count = LISTED ? p.count[b] : 0;
+    const int l = min(max(len, 0), p.Lcap), c = LISTED ? min(max(count, 0), p.keep) : 0;
+    if (l != len || c != count) atomicOr(p.err, GDA_DEVERR_BAD_LENGTH);
+    return {l, LISTED ? (l == 0 ? 0 : c << p.shift) : (l + kTile - 1) / kTile};
 }
 
-// Positions of sequence b along the axis that is cut into ranges: a multiple of 16.
-__device__ __forceinline__ int positions_of(const Params &p, int b) {
-    const int len = length_of(p, b);
-    if (p.list == nullptr) return (len + kTile - 1) / kTile * kTile;
-    int count = p.count[b];
-    if (count < 0 || count > p.keep) {
-        atomicOr(p.err, GDA_DEVERR_BAD_LENGTH);
-        count = count < 0 ? 0 : p.keep;
-    }
-    return len == 0 ? 0 : count << p.shift;
+__device__ __forceinline__ int positions_of(const Params &p, int b) {    // for the joining kernel: 0 if there are none
+    return (p.list != nullptr ? span_of<true>(p, b) : span_of<false>(p, b)).tiles;
 }
 
-// The range [start, end) of a split in the concatenated positions, and where it begins.
+// The tiles [start, end) of a split on the axis of all sequences, and where it begins.  (There are fewer than 2^31.)
 struct Range {
-    long long start, end, per, before;   // before: positions of the sequences ahead of b
+    int start, end, per, before;         // before: tiles of the sequences ahead of b
     int b;
+    Span span;                           // of b
 };
 
 // Computed by a whole warp; false if the split has nothing to do.
+template <bool LISTED>
 __device__ __forceinline__ bool range_of(const Params &p, int split, Range &r) {
     const int lane = threadIdx.x & 31;
-    long long total = 0;
+    int total = 0;
 #pragma unroll 4
-    for (int b = lane; b < p.B; b += 32) total += positions_of(p, b);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    r.per = max(static_cast<long long>(kMinRange), (total + p.splits - 1) / p.splits);
-    r.per = (r.per + kTile - 1) / kTile * kTile;
+    for (int b = lane; b < p.B; b += 32) total += span_of<LISTED>(p, b).tiles;
+    total = __reduce_add_sync(0xffffffffu, total);
+    r.per = max(1, (total + p.splits - 1) / p.splits);
+    if (static_cast<long long>(split) * r.per >= total) return false;
     r.start = split * r.per;
     r.end = min(total, r.start + r.per);
-    if (r.start >= total) return false;
-    long long carry = 0;
+    int carry = 0;
     for (int base = 0; base < p.B; base += 32) {
         const int b = base + lane;
-        const long long len = b < p.B ? positions_of(p, b) : 0;
-        long long incl = len;
+        const Span span = b < p.B ? span_of<LISTED>(p, b) : Span{0, 0};
+        int incl = span.tiles;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += y;
         }
-        const long long before = carry + incl - len;
-        const unsigned hit = __ballot_sync(0xffffffffu, before <= r.start && r.start < before + len);
+        const int before = carry + incl - span.tiles;
+        const unsigned hit = __ballot_sync(0xffffffffu, before <= r.start && r.start < before + span.tiles);
         if (hit) {
             const int src = __ffs(hit) - 1;
             r.b = base + src;
             r.before = __shfl_sync(0xffffffffu, before, src);
+            r.span = {__shfl_sync(0xffffffffu, span.len, src), __shfl_sync(0xffffffffu, span.tiles, src)};
             return true;
         }
         carry += __shfl_sync(0xffffffffu, incl, 31);
@@ -191,15 +191,16 @@ __device__ __forceinline__ bool range_of(const Params &p, int split, Range &r) {
 }
 
 // Notes the first and last range of every sequence that begins in range r of split `split`, for the joining kernel.
+template <bool LISTED>
 __device__ __forceinline__ void note_sequences(const Params &p, const Range &r, int split) {
-    long long before = r.before;
+    int before = r.before;
     for (int b = r.b; before < r.end; ++b) {
-        const int len = positions_of(p, b);
-        if (len > 0 && before >= r.start && (threadIdx.x & 31) == 0) {
+        const int tiles = span_of<LISTED>(p, b).tiles;
+        if (tiles > 0 && before >= r.start && (threadIdx.x & 31) == 0) {
             p.ws_seg[2 * b] = split;
-            p.ws_seg[2 * b + 1] = static_cast<int>((before + len - 1) / r.per);
+            p.ws_seg[2 * b + 1] = (before + tiles - 1) / r.per;
         }
-        before += len;
+        before += tiles;
     }
 }
 
@@ -238,55 +239,58 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// A place in a warp's range: sequence b, positions [pos, hi) of it, and the positions of the range after those.
+// A place in a warp's range: sequence b, tiles [tile, hi) of it, and the tiles of the range after those.
 struct Cursor {
-    int b, pos, hi, left;
+    int b, tile, hi, left;
 };
 
-__device__ __forceinline__ void enter(Cursor &c, int pos, int len) {
-    const int n = min(len - pos, c.left);
-    c.pos = pos;
-    c.hi = pos + n;
+__device__ __forceinline__ void enter(Cursor &c, int tile, int tiles) {
+    const int n = min(tiles - tile, c.left);
+    c.tile = tile;
+    c.hi = tile + n;
     c.left -= n;
 }
 
-// To the next sequence with positions; there is one while left > 0.
-__device__ __forceinline__ void next_sequence(const Params &p, Cursor &c) {
-    int len = 0;
-    do len = positions_of(p, ++c.b);
-    while (len == 0);
-    enter(c, 0, len);
+// To the next sequence with tiles; there is one while left > 0.  Returns its length.
+template <bool LISTED>
+__device__ __forceinline__ int next_sequence(const Params &p, Cursor &c) {
+    Span span;
+    do span = span_of<LISTED>(p, ++c.b);
+    while (span.tiles == 0);
+    enter(c, 0, span.tiles);
+    return span.len;
 }
 
-// A tile in the cache: its page, its first row there, and how many of its 16 positions exist.
+// A tile in the cache: its page, its place there in tiles, and how many of its 16 positions exist.
 struct Place {
-    int page, offset, n;
+    int page, tile, n;
 };
 
-// The tile at position pos (along the axis of ranges) of sequence b, whose length is len.  A page outside the pool is
-// read as page 0 and reported.  (The caches have 2^32 rows at most.)
+// Tile `tile` (along the axis of ranges) of sequence b, whose length is len.
 template <bool LISTED>
-__device__ __forceinline__ Place place_of(const Params &p, int b, int g, int pos, int len) {
+__device__ __forceinline__ Place place_of(const Params &p, int b, int g, int tile, int len) {
     // no branch on what is loaded: the loads are waited for when the tile's copies are started, a step later
-    long long at = pos;
+    bool exists = true;
     if constexpr (LISTED) {
-        const int id = p.list[(static_cast<size_t>(b) * p.hn + g) * p.keep + (pos >> p.shift)];
-        at = (static_cast<long long>(id) << p.shift) + (pos & ((1 << p.shift) - 1));
+        const int id = p.list[(static_cast<size_t>(b) * p.hn + g) * p.keep + (tile >> p.shift)];
+        exists = static_cast<unsigned>(id) <= static_cast<unsigned>(len / kTile >> p.shift);   // negative ones are not
+        tile = exists ? (id << p.shift) + (tile & ((1 << p.shift) - 1)) : 0;
+        exists = exists && tile * kTile < len;
+        tile = exists ? tile : 0;
     }
-    const bool exists = at >= 0 && at < len;
-    const int i = exists ? static_cast<int>(at) : 0, pg = i / p.page_size;
+    const int pg = static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(tile)) * p.page_factor >> p.page_shift);
     const int phys = p.block_table != nullptr ? p.block_table[static_cast<size_t>(b) * p.max_pages + pg] : b;
-    return {phys, i - pg * p.page_size, exists ? min(kTile, len - i) : 0};
+    return {phys, tile - pg * (p.page_size / kTile), exists ? min(kTile, len - tile * kTile) : 0};
 }
 
-// Cache row that a tile begins at.
-__device__ __forceinline__ uint32_t row_of(const Params &p, const Place &at) {
+// Cache row that a tile begins at.  A page outside the pool is read as page 0 and reported.  (Rows are below 2^31.)
+__device__ __forceinline__ int row_of(const Params &p, const Place &at) {
     int phys = at.page;
-    if (phys < 0 || phys >= p.num_pages) {
+    if (static_cast<unsigned>(phys) >= static_cast<unsigned>(p.num_pages)) {
         if (at.n > 0) atomicOr(p.err, GDA_DEVERR_BAD_PAGE);
         phys = 0;
     }
-    return static_cast<uint32_t>(phys) * p.page_size + at.offset;
+    return phys * p.page_size + at.tile * kTile;
 }
 
 // Places in a warp's shared memory, in bytes; a stage holds K of one tile and V of the tile before it.
@@ -308,53 +312,50 @@ struct Maps {
     CUtensorMap k1, k2, v;
 };
 
-// Starts the loads of the scales of a tile: lanes 0 .. RH of K, 4 .. RH + 3 of V; the eighth word is the number of positions.
-template <int RH>
-__device__ __forceinline__ void issue_scales(const Params &p, uint32_t dst, uint32_t row, int n, uint32_t h0, uint32_t g) {
-    const uint32_t lane = threadIdx.x & 31, hs = p.hs, hn = p.hn, blk = row >> p.shift, j = lane & 3;
-    const float *src = lane < 4 ? (j < RH ? p.k1s + static_cast<size_t>(blk) * hs + h0 + j : p.k2s + static_cast<size_t>(blk) * hn + g)
-                                : p.vs + static_cast<size_t>(blk) * hs + h0 + min(j, RH - 1u);
-    if (lane < 7) copy_async4(dst + lane * 4, src, n > 0);
-    if (lane == 7) asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + 28), "r"(n) : "memory");
-}
-
 template <typename V>
 __device__ __forceinline__ V at(const uint8_t *smem) { return *reinterpret_cast<const V *>(smem); }
 
-// The query rows of the warp's heads as f16 in shared memory, scaled by a
-// power of two that brings their largest element to [2^14, 2^15) (f16 then
-// holds all of bf16's digits down to 2^-31 of that).  Returns this lane's
-// factor from a product of codes to exp2 units: that of head lane % 4.
+// The query rows of a warp's heads.
 template <int D, int RH>
-__device__ __forceinline__ float load_queries(const Params &p, uint8_t *dst, int b, int h0, int g) {
-    const int lane = threadIdx.x & 31;
-    float mine = 0.f;
-    uint32_t words[RH + 1][D / 64];                      // all on their way before the first is used
+struct Queries {
+    uint32_t words[RH + 1][D / 64];
+
+    __device__ __forceinline__ void fetch(const Params &p, int b, int h0, int g) {
+        const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int j = 0; j <= RH; ++j) {
-        const __nv_bfloat16 *q = j == RH ? p.q2 + (static_cast<size_t>(b) * p.hn + g) * D
-                                         : p.q1 + (static_cast<size_t>(b) * p.hs + h0 + j) * D;
+        for (int j = 0; j <= RH; ++j) {
+            const __nv_bfloat16 *q = j == RH ? p.q2 + (static_cast<size_t>(b) * p.hn + g) * D
+                                             : p.q1 + (static_cast<size_t>(b) * p.hs + h0 + j) * D;
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i) words[j][i] = reinterpret_cast<const uint32_t *>(q)[lane + 32 * i];
+            for (int i = 0; i < D / 64; ++i) words[j][i] = reinterpret_cast<const uint32_t *>(q)[lane + 32 * i];
+        }
     }
+
+    // As f16 to shared memory, scaled by a power of two that brings a row's largest element to [2^14, 2^15) (f16 then
+    // holds all of bf16's digits down to 2^-31 of that).  Returns this lane's factor from a product of codes to exp2
+    // units: that of head lane % 4.
+    __device__ __forceinline__ float place(const Params &p, uint8_t *dst) const {
+        const int lane = threadIdx.x & 31;
+        float mine = 0.f;
 #pragma unroll
-    for (int j = 0; j <= RH; ++j) {
-        const uint32_t(&w)[D / 64] = words[j];
-        uint32_t most = 0;
+        for (int j = 0; j <= RH; ++j) {
+            const uint32_t(&w)[D / 64] = words[j];
+            uint32_t most = 0;
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i) most = max(most, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
-        most = __reduce_max_sync(0xffffffffu, most);
-        const int up = min(268 - static_cast<int>(most >> 7), 253);       // biased exponent of the factor (254 has no inverse)
-        const float f = __uint_as_float(static_cast<uint32_t>(up) << 23);
+            for (int i = 0; i < D / 64; ++i) most = max(most, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+            most = __reduce_max_sync(0xffffffffu, most);
+            const int up = min(268 - static_cast<int>(most >> 7), 253);   // biased exponent of the factor (254 has no inverse)
+            const float f = __uint_as_float(static_cast<uint32_t>(up) << 23);
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i)
-            reinterpret_cast<uint32_t *>(dst + j * D * 2)[lane + 32 * i] =
-                pack_half2(bf16_lo(w[i]) * f, bf16_hi(w[i]) * f);
-        const float back = __uint_as_float(static_cast<uint32_t>(254 - up) << 23);
-        if ((lane & 3) == j) mine = p.scale_log2 * back;
+            for (int i = 0; i < D / 64; ++i)
+                reinterpret_cast<uint32_t *>(dst + j * D * 2)[lane + 32 * i] =
+                    pack_half2(bf16_lo(w[i]) * f, bf16_hi(w[i]) * f);
+            const float back = __uint_as_float(static_cast<uint32_t>(254 - up) << 23);
+            if ((lane & 3) == j) mine = p.scale_log2 * back;
+        }
+        return mine;
     }
-    return mine;
-}
+};
 
 // One warp: split u / units of the range, unit u % units = (noise head, part of its group).
 template <int D, int DV, int RH, bool LISTED>
@@ -377,45 +378,54 @@ __global__ void __launch_bounds__(32, (Stage<D, DV, RH>::warps)) gda_decode_fp8_
     __syncwarp();
     asm volatile("griddepcontrol.wait;" ::: "memory");
     Range range;
-    if (!range_of(p, split, range)) return;
-    if (u % units == 0) note_sequences(p, range, split);
+    if (!range_of<LISTED>(p, split, range)) return;
 
-    Cursor use{range.b, 0, 0, static_cast<int>(range.end - range.start)};
-    enter(use, static_cast<int>(range.start - range.before), positions_of(p, range.b));
+    Cursor use{range.b, 0, 0, range.end - range.start};
+    enter(use, range.start - range.before, range.span.tiles);
     Cursor get = use;                                    // the copies' place, ahead of the arithmetic's
-    int get_len = length_of(p, get.b);
-    Place next{0, 0, 0};
-    uint32_t last = 0;
-    int to = 0;
-    bool more = true, ready = false, pending = false;    // positions are left; K of `next`, V of the tile at row `last` are to be copied
+    int get_len = range.span.len;
+    Place next = place_of<LISTED>(p, get.b, g, get.tile, get_len);
+    Queries<D, RH> q;
+    q.fetch(p, use.b, h0, g);
+    if (u % units == 0) note_sequences<LISTED>(p, range, split);
+
+    // scales of a tile: lanes 0 .. RH of K, 4 .. RH + 3 of V
+    const int j_of = lane & 3, which = lane >= 4 ? 2 : (j_of < RH ? 0 : 1);
+    const float *const scale_base = which == 0 ? p.k1s + h0 + j_of : (which == 1 ? p.k2s + g : p.vs + h0 + min(j_of, RH - 1));
+    const uint32_t scale_pitch = which == 1 ? p.hn : p.hs;
+    int last = 0, to = 0, counts[A + 1] = {};            // counts: positions of the last tiles copied, the latest at the end
+    bool ready = true, pending = false;                  // K of `next`, V of the tile at row `last` are to be copied
     auto copy = [&]() {
         const uint32_t stage = ring + to * S::bytes, bar = ring + S::bars + to * 8;
-        if (lane == 0 && (ready || pending))
+        const int row = row_of(p, next), before = last;
+        if (lane == 0 && (ready || pending)) {
             mbar_arrive_expect_tx(reinterpret_cast<uint64_t *>(smem + S::bars) + to,
                                   (ready ? S::k_bytes : 0) + (pending ? S::v_bytes : 0));
-        if (pending && lane == 0) load_box(stage + S::v, maps.v, bar, static_cast<int>(last), h0 * (DV < 128 ? 1 : DV / 128));
-        pending = ready;
-        if (ready) {
-            last = row_of(p, next);
-            if (lane == 0) {
-                load_box(stage + S::k, maps.k1, bar, static_cast<int>(last), h0);
-                load_box(stage + S::k + RH * kTile * D, maps.k2, bar, static_cast<int>(last), g);
-            }
-            issue_scales<RH>(p, ring + S::scales + to * 32, last, next.n, h0, g);
-            get.pos += kTile;
-            if (get.pos >= get.hi) {
-                if (get.left > 0) {
-                    next_sequence(p, get);
-                    get_len = length_of(p, get.b);
-                } else {
-                    more = false;
-                }
+            if (pending) load_box(stage + S::v, maps.v, bar, before, h0 * (DV < 128 ? 1 : DV / 128));
+            if (ready) {
+                load_box(stage + S::k, maps.k1, bar, row, h0);
+                load_box(stage + S::k + RH * kTile * D, maps.k2, bar, row, g);
             }
         }
-        ready = more;
-        if (more) next = place_of<LISTED>(p, get.b, g, get.pos, get_len);
+        if (lane < 7 && ready)
+            copy_async4(ring + S::scales + to * 32 + lane * 4,
+                        scale_base + static_cast<size_t>(static_cast<uint32_t>(row) / kTile >> p.shift) * scale_pitch, next.n > 0);
         asm volatile("cp.async.commit_group;" ::: "memory");
+        last = row;
+#pragma unroll
+        for (int i = 0; i < A; ++i) counts[i] = counts[i + 1];
+        counts[A] = next.n;
+        pending = ready;
         to = to == A ? 0 : to + 1;
+        if (!ready) return;
+        if (++get.tile >= get.hi) {
+            if (get.left == 0) {
+                ready = false;
+                return;
+            }
+            get_len = next_sequence<LISTED>(p, get);
+        }
+        next = place_of<LISTED>(p, get.b, g, get.tile, get_len);
     };
 
     uint8_t *const queries = smem + S::queries, *const weights = smem + S::weights;
@@ -458,7 +468,7 @@ __global__ void __launch_bounds__(32, (Stage<D, DV, RH>::warps)) gda_decode_fp8_
             if (t == j) sc0 = c[0], sc1 = c[2];
         }
         const float ks = at<float>(scales + 4 * t), vs = at<float>(scales + 16 + 4 * t);
-        have = at<int>(scales + 28);
+        have = counts[0];
         sc0 = sc0 * factor * ks, sc1 = sc1 * factor * ks;
         if (quad >= have) sc0 = -INFINITY;
         if (quad + 8 >= have) sc1 = -INFINITY;
@@ -553,13 +563,13 @@ __global__ void __launch_bounds__(32, (Stage<D, DV, RH>::warps)) gda_decode_fp8_
             }
         }
     };
-    // Leaves what the part that lies in sequence use.b has come to.
-    auto leave = [&]() {
+    // Leaves what the part that lies in sequence b has come to.
+    auto leave = [&](int b) {
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
         l *= 0x1p-15f;
         const float mn = __shfl_sync(0xffffffffu, m, RH), ln = __shfl_sync(0xffffffffu, l, RH);
-        const size_t slot = static_cast<size_t>(split) + use.b;
+        const size_t slot = static_cast<size_t>(split) + b;
 #pragma unroll
         for (int j = 0; j < RH; ++j) {
             const float mj = __shfl_sync(0xffffffffu, m, j), lj = __shfl_sync(0xffffffffu, l, j);
@@ -579,9 +589,10 @@ __global__ void __launch_bounds__(32, (Stage<D, DV, RH>::warps)) gda_decode_fp8_
     // Step g: the values of tile g - 1, what ends with it and begins with tile g, and the scores of tile g.  Every piece
     // of the work stands in one place: a kernel starts with cold instructions, and what a first and a last step had of
     // their own cost more than the order of the pieces gains.
-    int from = 1, ahead = A + 1;                         // the first step copies nothing; steps until the first tile is there
+    int from = 0, ahead = A;                             // steps until the first tile is there
     uint32_t parity = 0;                                 // of each stage's barrier
-    bool first = true, ending = true;                    // no tile has been scored; the last one scored was its part's last
+    int part_of = -1;                                    // the sequence of the part that is under way
+    bool ending = true, over = false;                    // the tile scored last was its part's last; the range's last
     for (;;) {
         __syncwarp();                                    // the readers of the stage to be written are done
         copy();
@@ -601,26 +612,29 @@ __global__ void __launch_bounds__(32, (Stage<D, DV, RH>::warps)) gda_decode_fp8_
         uint8_t *const stage = smem + from * S::bytes;
         const uint8_t *const scales = smem + S::scales + from * 32;
         from = from == A ? 0 : from + 1;
-        if (!first) {
+        if (part_of >= 0) {
             if (have < kTile) drop_rows(stage);
             values_of(stage);
         }
         if (ending) {
-            if (!first) {
-                leave();
-                if (use.left == 0) return;
-                next_sequence(p, use);
-            }
-            factor = load_queries<D, RH>(p, queries, use.b, h0, g);
+            if (part_of >= 0) leave(part_of);
+            if (over) return;
+            factor = q.place(p, queries);
             clear();
             m = kLowest, l = 0.f, v_most = 0.f, v_inverse = 0.f;
-            first = false;
+            part_of = use.b;
         }
         __syncwarp();                                    // the weights have been read, the queries are there
         scores_of(stage, scales);
         rescale();
-        use.pos += kTile;
-        ending = use.pos >= use.hi;
+        ending = ++use.tile >= use.hi;
+        if (ending) {
+            over = use.left == 0;
+            if (!over) {
+                next_sequence<LISTED>(p, use);
+                q.fetch(p, use.b, h0, g);
+            }
+        }
     }
 }
 
@@ -678,8 +692,11 @@ size_t decode_fp8_block_workspace_bytes(int B, int hs, int hn, int d, int dv) { 
 int launch_decode_fp8_block(const DecodeFp8BlockArgs &a, cudaStream_t stream) {
     const Plan pl = plan_of(a.B, a.hs, a.hn, a.d, a.dv);
     char *ws = static_cast<char *>(a.workspace);
-    int shift = 4;
-    while (1 << shift < a.block) ++shift;
+    int shift = 0, page_shift = 31;
+    while (kTile << shift < a.block) ++shift;
+    const uint32_t page_tiles = a.page_size / kTile;     // factor = 2^(31 + l) / page_tiles, rounded up, 2^l >= page_tiles
+    while (1ull << (page_shift - 31) < page_tiles) ++page_shift;
+    const uint32_t page_factor = static_cast<uint32_t>(((1ull << page_shift) + page_tiles - 1) / page_tiles);
     const Params p{static_cast<const __nv_bfloat16 *>(a.q1),
                    static_cast<const __nv_bfloat16 *>(a.q2),
                    a.k1c, a.k2c, a.vc, a.k1s, a.k2s, a.vs, a.lens, a.lambda,
@@ -690,7 +707,7 @@ int launch_decode_fp8_block(const DecodeFp8BlockArgs &a, cudaStream_t stream) {
                    a.dev_err, a.lambda_init, a.eps,
                    static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(a.d))),
                    a.B, a.Lcap, a.hs, a.hn, pl.splits, pl.heads.parts, a.block_table, a.page_size, a.max_pages,
-                   a.num_pages, shift, a.list, a.count, a.keep};
+                   a.num_pages, shift, page_factor, page_shift, a.list, a.count, a.keep};
     cudaError_t e = cudaErrorInvalidValue;
     switch (a.d * 1000 + a.dv) {
         case 64064: e = launch_split<64, 64>(p, pl.heads.each, stream); break;

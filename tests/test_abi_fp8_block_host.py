@@ -157,19 +157,6 @@ def test_decode_workspace_sizes(lib):
             assert size(65536, 1, 1, d, dv) == 0 and size(1, 127, 2, d, dv) == 0 and size(1, 6, 4, d, dv) == 0
 
 
-def test_ranges_of_the_longest_batch_fit_32_bits(lib):
-    """The decode counts a range's positions in 32 bits: the fewest ranges of any supported shape against the most
-    positions.  The workspace has (ranges + B) slots of h_s (2 dv + 4) floats, so its size gives the ranges."""
-    fewest = 1 << 30
-    for d in (64, 128):
-        for dv in (64, 128, 256):
-            for hn in range(1, 65):
-                for hs in range(hn, 129 - hn, hn):
-                    slots = lib.gda_attn_decode_fp8_block_workspace_size(1, hs, hn, d, dv) / (4 * hs * (2 * dv + 4))
-                    fewest = min(fewest, int(slots) - 1)
-    assert fewest >= 11 - 1 and (1 << 34) / 10 + 16 < 1 << 31
-
-
 def test_sizes_past_32_bits_are_refused_by_the_binding(lib):
     import grouped_differential_attention_gb300 as gda
     for big in (1 << 31, (1 << 32) + 4, -(1 << 32) + 4):
