@@ -51,7 +51,9 @@ __device__ __forceinline__ size_t pool_block(const BlockSelectArgs &a, int b, in
     return static_cast<size_t>(phys) * per + (j - pg * per);
 }
 
-constexpr int kChunk = 16;              // blocks of tokens that a warp scores
+// Blocks of tokens that a warp scores.  us of both kernels with 8 / 16 / 32, cold: 64 sequences of 64 to 128 blocks, 12 +
+// 4 heads 22.7 / 23.7 / 27.8; one of 2048, 24 + 8 heads 28.8 / 31.9 / 35.0.
+constexpr int kChunk = 8;
 constexpr int kScoreWarps = 4;
 
 // Bytes of four whole numbers.
@@ -263,8 +265,7 @@ __global__ void __launch_bounds__(THREADS) gda_block_select_kernel(const BlockSe
 
 template <int THREADS>
 cudaError_t launch_select(const BlockSelectArgs &a, int most, cudaStream_t stream) {
-    const cudaError_t e = cudaFuncSetAttribute(gda_block_select_kernel<THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kBlockSelectMaxBlocks * 4);
+    const cudaError_t e = allow_shared_memory<gda_block_select_kernel<THREADS>>(kBlockSelectMaxBlocks * 4);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(a.hn, a.B);
@@ -289,7 +290,8 @@ int launch_block_select(const BlockSelectArgs &a, cudaStream_t stream) {
     else gda_block_score_kernel<128><<<grid, kScoreWarps * 32, 0, stream>>>(a, most);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return record_cuda_error(e);
-    e = most > 512 ? launch_select<1024>(a, most, stream) : launch_select<256>(a, most, stream);
+    // 2048 blocks, us of both kernels, cold: 31.9 with 1024 threads, 27.8 with 512 or 256
+    e = most > 512 ? launch_select<512>(a, most, stream) : launch_select<256>(a, most, stream);
     return e == cudaSuccess ? GDA_OK : record_cuda_error(e);
 }
 

@@ -371,7 +371,8 @@ int launch_cache_append_fp8_block(const CacheFp8BlockArgs &a, cudaStream_t strea
     const int per = static_cast<int>(std::min<long long>(kMaxRows, std::max<long long>(1, a.T / 256)));
     const dim3 grid(static_cast<unsigned>((a.T + per - 1) / per), groups);
     const auto kern = scan ? gda_cache_append_fp8_block_kernel<true> : gda_cache_append_fp8_block_kernel<false>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kWarps * kPieces);
+    cudaError_t e = scan ? allow_shared_memory<gda_cache_append_fp8_block_kernel<true>>(kWarps * kPieces)
+                         : allow_shared_memory<gda_cache_append_fp8_block_kernel<false>>(kWarps * kPieces);
     if (e != cudaSuccess) return record_cuda_error(e);
     if (!scan) {
         gda_cache_index_kernel<<<static_cast<unsigned>((a.T + kThreads - 1) / kThreads), kThreads, 0, stream>>>(a);

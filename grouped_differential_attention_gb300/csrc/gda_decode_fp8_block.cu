@@ -650,19 +650,17 @@ bool encode(CUtensorMap *map, const uint8_t *base, int n, int heads, long long r
     return encode_tmap_3d_u8(map, base, dims, strides, shape, swizzle, listed);
 }
 
-template <int D, int DV, int RH>
+template <int D, int DV, int RH, bool LISTED>
 cudaError_t launch_split(const Params &p, cudaStream_t stream) {
     using S = Stage<D, DV, RH>;
-    const auto kern = p.list != nullptr ? gda_decode_fp8_block_split_kernel<D, DV, RH, true>
-                                        : gda_decode_fp8_block_split_kernel<D, DV, RH, false>;
+    constexpr auto kern = gda_decode_fp8_block_split_kernel<D, DV, RH, LISTED>;
     Maps maps;
     const long long rows = static_cast<long long>(p.num_pages) * p.page_size;
-    const bool listed = p.list != nullptr;
     constexpr int KS = D == 64 ? 0 : 128, VS = DV == 64 ? 64 : 128;
-    if (!encode(&maps.k1, p.k1c, D, p.hs, rows, RH, KS, listed) || !encode(&maps.k2, p.k2c, D, p.hn, rows, 1, KS, listed) ||
-        !encode(&maps.v, p.vc, DV, p.hs, rows, RH, VS, listed))
+    if (!encode(&maps.k1, p.k1c, D, p.hs, rows, RH, KS, LISTED) || !encode(&maps.k2, p.k2c, D, p.hn, rows, 1, KS, LISTED) ||
+        !encode(&maps.v, p.vc, DV, p.hs, rows, RH, VS, LISTED))
         return cudaErrorInvalidValue;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::total);
+    const cudaError_t e = allow_shared_memory<kern>(S::total);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(p.splits * p.hn * p.parts);
@@ -675,6 +673,11 @@ cudaError_t launch_split(const Params &p, cudaStream_t stream) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, p, maps);
+}
+
+template <int D, int DV, int RH>
+cudaError_t launch_split(const Params &p, cudaStream_t stream) {
+    return p.list != nullptr ? launch_split<D, DV, RH, true>(p, stream) : launch_split<D, DV, RH, false>(p, stream);
 }
 
 template <int D, int DV>

@@ -4,6 +4,7 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -173,6 +174,21 @@ struct DecodeFp8BlockArgs {
 // Remembers `e` as this thread's last CUDA error (see gda_last_cuda_error),
 // clears the runtime's sticky-free error state and returns GDA_ERR_CUDA.
 int record_cuda_error(cudaError_t e);
+
+// Lets `kernel` have this much dynamic shared memory on the current device, asked once for a device (half a microsecond
+// of a call's six).
+template <auto kernel>
+cudaError_t allow_shared_memory(int bytes) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // Checks the current device (GB300, compute capability 10.3) once and
 // returns a gda_status plus the address of its device error word.
