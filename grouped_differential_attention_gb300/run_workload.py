@@ -5,9 +5,12 @@
     python -m grouped_differential_attention_gb300.run_workload decode --launches 3
     python -m grouped_differential_attention_gb300.run_workload decode_fp8 --launches 3
     python -m grouped_differential_attention_gb300.run_workload decode_fp4 --launches 3
+    python -m grouped_differential_attention_gb300.run_workload decode_fp8_block --launches 3
+    python -m grouped_differential_attention_gb300.run_workload decode_sparse --launches 3
     python -m grouped_differential_attention_gb300.run_workload norm_rope --launches 3
     python -m grouped_differential_attention_gb300.run_workload norm_rope_backward --launches 3
     python -m grouped_differential_attention_gb300.run_workload serving_step --launches 3
+    python -m grouped_differential_attention_gb300.run_workload sparse_serving_step --launches 3
     python -m grouped_differential_attention_gb300.run_workload backward --launches 1
     python -m grouped_differential_attention_gb300.run_workload backward_bf16 --launches 3
     python -m grouped_differential_attention_gb300.run_workload prefill2pass --launches 3
@@ -29,8 +32,9 @@ from grouped_differential_attention_gb300 import workloads as W
 
 def main(argv=None):
     ap = argparse.ArgumentParser()
-    ap.add_argument("kind", choices=["prefill", "prefill2pass", "decode", "decode_fp8", "decode_fp4", "backward",
-                                     "backward_bf16", "norm_rope", "norm_rope_backward", "serving_step"])
+    ap.add_argument("kind", choices=["prefill", "prefill2pass", "decode", "decode_fp8", "decode_fp4", "decode_fp8_block",
+                                     "decode_sparse", "backward", "backward_bf16", "norm_rope", "norm_rope_backward",
+                                     "serving_step", "sparse_serving_step"])
     ap.add_argument("workload", nargs="?", default=None)
     ap.add_argument("--launches", type=int, default=3)
     ap.add_argument("--flags", type=int, default=0, help="gda_attn_fwd_ex flags for the prefill kind")
@@ -95,6 +99,25 @@ def main(argv=None):
 
         def launch():
             gda.gda_attn_decode_fp4(q1, q2, *cache, lens, lam, w.lambda_init, eps=w.eps, out=out, workspace=ws)
+    elif args.kind in ("decode_fp8_block", "decode_sparse"):
+        # 8-bit caches with a scale for 64 tokens; sparse: 16 blocks of each sequence, chosen in each launch
+        w, block, keep = W.GDA3_DECODE_B64, 64, 16
+        q1, q2, k1c, k2c, vc, lens, lam = [t.to(dev) for t in W.make_decode_inputs(w)]
+        cache, bounds = W.empty_fp8_block_cache(w.B, w.Lcap, block, w.h_s, w.h_n, w.d, w.dv, dev)
+        gda.gda_cache_append_fp8_block(*(t.flatten(0, 1) for t in (k1c, k2c, vc)),
+                                       torch.arange(w.B * w.Lcap, dtype=torch.int32, device=dev), *cache,
+                                       k_sig_bounds=bounds[0], k_noise_bounds=bounds[1])
+        out = torch.empty((w.B, w.h_s, w.dv), dtype=torch.bfloat16, device=dev)
+        ws = torch.empty(gda.gda_attn_decode_fp8_block_workspace_size(w.B, w.h_s, w.h_n, w.d, w.dv), dtype=torch.uint8,
+                         device=dev)
+        if args.kind == "decode_fp8_block":
+            def launch():
+                gda.gda_attn_decode_fp8_block(q1, q2, *cache, lens, lam, w.lambda_init, eps=w.eps, out=out, workspace=ws)
+        else:
+            def launch():
+                lists = gda.gda_block_select(q1, q2, *bounds, *cache[3:5], lens, block, keep)
+                gda.gda_attn_decode_sparse_fp8_block(q1, q2, *cache, *lists, lens, lam, w.lambda_init, eps=w.eps, out=out,
+                                                     workspace=ws)
     elif args.kind in ("norm_rope", "norm_rope_backward"):
         # the projections of a prefill workload (default: the 3:1 B=4 L=2048 one) before its attention
         w = W.PREFILL_WORKLOADS[args.workload or W.GDA3_PREFILL_L2048.name]
@@ -116,9 +139,10 @@ def main(argv=None):
 
             def launch():
                 gda.gda_qk_norm_rope_bwd(*x, weight, pos, freq, *dy, grads=grads, workspace=ws)
-    elif args.kind == "serving_step":
+    elif args.kind in ("serving_step", "sparse_serving_step"):
         # one new token for each sequence of the decode workload: its page and slot, norm and rotation, the row into a
-        # paged 4-bit cache, and the decode over it (the cache's values are whatever zeroed pages hold)
+        # paged cache of 4 bits, and the decode over it; sparse: of 8 bits with a scale for a page, the choice of 16 pages
+        # and the decode over those (the cache's values are whatever zeroed pages hold)
         w, page = W.GDA3_DECODE_B64, 64
         rows = [t.to(dev) for t in W.make_prefill_inputs(W.GDA3_PREFILL_L2048, B=w.B, L=1, h_s=w.h_s, h_n=w.h_n, d=w.d,
                                                          dv=w.dv)]
@@ -127,7 +151,11 @@ def main(argv=None):
         lens = torch.randint(w.len_range[0], w.len_range[1] - args.launches, (w.B,),
                              generator=torch.Generator().manual_seed(w.seed)).to(torch.int32).to(dev)
         per = -(-w.Lcap // page)
-        cache = W.empty_fp4_cache(w.B * per, page, w.h_s, w.h_n, w.d, w.dv, dev)
+        sparse = args.kind == "sparse_serving_step"
+        if sparse:
+            cache, bounds = W.empty_fp8_block_cache(w.B * per, page, page, w.h_s, w.h_n, w.d, w.dv, dev)
+        else:
+            cache = W.empty_fp4_cache(w.B * per, page, w.h_s, w.h_n, w.d, w.dv, dev)
         table = torch.arange(w.B * per, dtype=torch.int32, device=dev).view(w.B, per)
         held = (lens.cpu() + page - 1) // page
         free = torch.cat([table[b, n:].cpu() for b, n in enumerate(held.tolist())]).to(dev)
@@ -137,16 +165,22 @@ def main(argv=None):
         weight = torch.ones((4, w.d), device=dev)
         freq = (10000.0 ** (-torch.arange(0, w.d, 2, dtype=torch.float64) / w.d)).float().to(dev)
         out = torch.empty((w.B, w.h_s, w.dv), dtype=torch.bfloat16, device=dev)
-        ws = torch.empty(gda.gda_attn_decode_fp4_workspace_size(w.B, w.h_s, w.h_n, w.d, w.dv), dtype=torch.uint8,
-                         device=dev)
+        size = gda.gda_attn_decode_fp8_block_workspace_size if sparse else gda.gda_attn_decode_fp4_workspace_size
+        ws = torch.empty(size(w.B, w.h_s, w.h_n, w.d, w.dv), dtype=torch.uint8, device=dev)
 
         def launch():
             slot, pos, *_ = gda.gda_block_tables(lens, ones, table, free, count, page, w.B * per, w.B,
                                                  out=(*step, lens, count))
             a1, b1, a2, b2 = gda.gda_qk_norm_rope(q1, k1, q2, k2, weight, pos, freq, eps=w.eps)
-            gda.gda_cache_append_fp4(b1, b2, v, slot, *cache)
-            gda.gda_attn_decode_paged_fp4(a1, a2, *cache, table, lens, lam, w.lambda_init, eps=w.eps, out=out,
-                                          workspace=ws)
+            if sparse:
+                gda.gda_cache_append_fp8_block(b1, b2, v, slot, *cache, k_sig_bounds=bounds[0], k_noise_bounds=bounds[1])
+                lists = gda.gda_block_select(a1, a2, *bounds, *cache[3:5], lens, page, 16, block_table=table)
+                gda.gda_attn_decode_sparse_fp8_block(a1, a2, *cache, *lists, lens, lam, w.lambda_init, block_table=table,
+                                                     eps=w.eps, out=out, workspace=ws)
+            else:
+                gda.gda_cache_append_fp4(b1, b2, v, slot, *cache)
+                gda.gda_attn_decode_paged_fp4(a1, a2, *cache, table, lens, lam, w.lambda_init, eps=w.eps, out=out,
+                                              workspace=ws)
     else:
         w = W.GDA3_DECODE_B64
         inp = [t.to(dev) for t in W.make_decode_inputs(w)]

@@ -209,6 +209,20 @@ def empty_fp4_cache(pages: int, page_size: int, h_s: int, h_n: int, d: int, dv: 
     return (*codes, *blocks, *(torch.ones(h, dtype=torch.float32, device=device) for h, _ in dims))
 
 
+def empty_fp8_block_cache(pages: int, page_size: int, block: int, h_s: int, h_n: int, d: int, dv: int, device):
+    """A zeroed 8-bit cache with a scale for ``block`` tokens and head, and the bounds of its keys.
+
+    ((k_sig, k_noise, v) codes [pages, page_size, heads, dim] and their scales [pages, page_size / block, heads], six
+    tensors in the order the entry points take them; (k_sig, k_noise) bounds [pages, page_size / block, heads, 2, d]).
+    """
+    dims, per = ((h_s, d), (h_n, d), (h_s, dv)), page_size // block
+    codes = [torch.zeros(pages, page_size, h, n, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+             for h, n in dims]
+    scales = [torch.zeros(pages, per, h, dtype=torch.float32, device=device) for h, _ in dims]
+    bounds = tuple(torch.zeros(pages, per, h, 2, d, dtype=torch.int8, device=device) for h in (h_s, h_n))
+    return (*codes, *scales), bounds
+
+
 def page_caches(k1c, k2c, vc, page_size: int, seed: int = 0, spare_pages: int = 3):
     """Scatter contiguous caches [B, Lcap, heads, dim] into page pools.
 
