@@ -1126,6 +1126,7 @@ def gda_cache_read_fp8_block(slot_map, k_sig_pool, k_noise_pool, v_pool, k_sig_s
     if slot_map.dim() != 1 or k_sig_pool.dim() != 4 or k_noise_pool.dim() != 4 or v_pool.dim() != 4:
         raise ValueError("slot_map must be 1-D and pools [num_pages, page_size, heads, dim]")
     T = slot_map.numel()
+    _int32(T)
     _, _, hs, d = k_sig_pool.shape
     hn, dv = k_noise_pool.shape[2], v_pool.shape[3]
     cache, size, pages, block = _fp8_block_cache((k_sig_pool, k_noise_pool, v_pool), (k_sig_scale, k_noise_scale, v_scale),

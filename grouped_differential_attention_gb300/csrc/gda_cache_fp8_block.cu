@@ -22,7 +22,14 @@
 // of a block writes all of it; to find the others, a call of few rows looks
 // through the slot map, one of many takes a launch before that notes in
 // index[slot] which row has that slot.  An entry counts only if that row's slot
-// is this slot, so what else the workspace holds does no harm.
+// is this slot, so what else the workspace holds does no harm.  A row that is
+// alone in its block (a decode step) is 256 elements to a warp; several are
+// held by a thread block in shared memory between the two passes over them.
+//
+// Measured (kernels; 12 + 4 heads of 64/128, blocks of 64): 64 rows of as many
+// sequences 5 us, 256 10.5, 1024 22; 8192 rows of a prompt 2.5 + 20 (63 MB, 9.3
+// at the copy rate of 6793 GB/s: two waves of thread blocks, each a chain of
+// looking up, loading and writing); reading 8192 rows 12.7 (63 MB).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <algorithm>
@@ -82,6 +89,7 @@ struct Shared {
     int place[kMaxBlock];              // the call's row of each place of the block of tokens, or -1
     int slots[kMaxRows];
     unsigned some[kMaxRows / 32];
+    int one[kMaxRows], more[kMaxRows], ones, mores;   // the rows that write a block: alone, and with others
     uint32_t most[kWarps];
     uint32_t top[kWarps][64], low[kWarps][64];   // pairs of a key's channels
 };
@@ -257,12 +265,147 @@ __device__ __forceinline__ void write_heads(const CacheFp8BlockArgs &a, int tens
     *reinterpret_cast<uint2 *>(bounds + n) = make_uint2(nl[0], nl[1]);
 }
 
-// grid (groups of `per` rows of the call, groups of heads).  SCAN: members are looked for in the slot map.
+// 256 elements of a row that is the only one of its block, 8 to a lane (a head is n / 8 lanes): what is read of them.
+struct Piece {
+    uint4 w;
+    uint2 old_top, old_low;
+    float old;
+    int tensor, slot, head, ch;
+    bool here;
+};
+
+__device__ __forceinline__ Piece fetch_piece(const CacheFp8BlockArgs &a, long long t, int slot, int piece) {
+    Piece p{};
+    for (; p.tensor < 2; ++p.tensor) {
+        const int of = (a.heads[p.tensor] * a.dims[p.tensor] + 255) / 256;
+        if (piece < of) break;
+        piece -= of;
+    }
+    const int n = a.dims[p.tensor], e = piece * 256 + (threadIdx.x & 31) * 8;
+    p.slot = slot;
+    p.head = e / n, p.ch = e & (n - 1);
+    p.here = p.head < a.heads[p.tensor];
+    if (!p.here) return p;
+    p.w = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.rows[p.tensor]) + t * a.ld[p.tensor] + e);
+    if ((slot & (a.block - 1)) == 0) return p;               // the block begins: nothing of it is read
+    const size_t place = static_cast<size_t>(slot / a.block) * a.heads[p.tensor] + p.head;
+    p.old = a.scale[p.tensor][place];
+    if (p.tensor == 2 || a.bounds[0] == nullptr) return p;
+    const int8_t *bounds = a.bounds[p.tensor] + place * 2 * n + p.ch;
+    p.old_top = *reinterpret_cast<const uint2 *>(bounds);
+    p.old_low = *reinterpret_cast<const uint2 *>(bounds + n);
+    return p;
+}
+
+// The greatest and the least of bounds, for 8 channels: those before, brought to the scale, and codes of one row.
+__device__ __forceinline__ void join_bounds(uint2 &top, uint2 &low, const uint32_t (&c)[4], float shift, bool fresh) {
+    uint32_t nt[2] = {0u, 0u}, nl[2] = {0u, 0u};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float2 pair = half2_bits_to_float2(e4m3x2_to_half2(c[k / 2]));
+        const float v = k & 1 ? pair.y : pair.x;
+        float t = v == v ? ceilf(v * 0.25f) : -128.f, l = v == v ? floorf(v * 0.25f) : 127.f;
+        if (!fresh) {
+            const uint32_t ot = (k < 4 ? top.x : top.y) >> 8 * (k & 3), ol = (k < 4 ? low.x : low.y) >> 8 * (k & 3);
+            t = fmaxf(t, ceilf(static_cast<float>(static_cast<int8_t>(ot)) * shift));
+            l = fminf(l, floorf(static_cast<float>(static_cast<int8_t>(ol)) * shift));
+        }
+        nt[k / 4] |= (static_cast<uint32_t>(static_cast<int>(t)) & 0xffu) << 8 * (k & 3);
+        nl[k / 4] |= (static_cast<uint32_t>(static_cast<int>(l)) & 0xffu) << 8 * (k & 3);
+    }
+    top = make_uint2(nt[0], nt[1]), low = make_uint2(nl[0], nl[1]);
+}
+
+__device__ __forceinline__ void write_piece(const CacheFp8BlockArgs &a, Piece &p) {
+    const int n = a.dims[p.tensor], in_block = p.slot & (a.block - 1);
+    const bool fresh = in_block == 0;
+    const uint32_t v[4] = {p.w.x, p.w.y, p.w.z, p.w.w};
+    uint32_t no[4], both = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) no[k] = not_finite(v[k]), both = __vmaxu2(both, v[k] & 0x7fff7fffu & ~no[k]);
+    uint32_t most = max(both & 0xffffu, both >> 16);
+    for (int o = 1; o < n / 8; o <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+    const float scale = fmaxf(p.old, fp8_scale_of(most << 16)), r = __frcp_rn(scale);
+    const float shift = fresh ? 1.f : __fdiv_rn(p.old, scale), most_code = fminf(448.f, __fdiv_rn(0x1.ep127f, scale));
+    if (!p.here) return;
+    uint32_t c[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)                              // the limits make numbers of what is none
+        c[k] = codes_of(bf16_lo(v[k]), bf16_hi(v[k]), r, most_code) | (no[k] & 0x7fu) | (no[k] >> 16 & 0x7f00u);
+    const size_t pitch = static_cast<size_t>(a.heads[p.tensor]) * n, blk = p.slot / a.block;
+    uint8_t *const codes = a.codes[p.tensor] + blk * a.block * pitch + p.head * n + p.ch;
+    *reinterpret_cast<uint2 *>(codes + in_block * pitch) =
+        make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
+    if (p.ch == 0) a.scale[p.tensor][blk * a.heads[p.tensor] + p.head] = scale;
+    if (shift != 1.f) {                                      // the rows that are there already
+        for (int base = 0; base < a.block; base += 8) {
+            uint2 was[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) was[i] = *reinterpret_cast<const uint2 *>(codes + (base + i) * pitch);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t x[2] = {was[i].x, was[i].y};
+                uint32_t o[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint2 h = e4m3x4_to_half2x2(x[k]);
+                    const float2 y = half2_bits_to_float2(h.x), z = half2_bits_to_float2(h.y);
+                    o[k] = float2_to_e4m3x2(y.x * shift, y.y * shift) | float2_to_e4m3x2(z.x * shift, z.y * shift) << 16;
+                }
+                if (base + i != in_block) *reinterpret_cast<uint2 *>(codes + (base + i) * pitch) = make_uint2(o[0], o[1]);
+            }
+        }
+    }
+    if (p.tensor == 2 || a.bounds[0] == nullptr) return;
+    join_bounds(p.old_top, p.old_low, c, shift, fresh);
+    int8_t *const bounds = a.bounds[p.tensor] + (blk * a.heads[p.tensor] + p.head) * 2 * n + p.ch;
+    *reinterpret_cast<uint2 *>(bounds) = p.old_top;
+    *reinterpret_cast<uint2 *>(bounds + n) = p.old_low;
+}
+
+// The rows of a call in the block of tokens from slot `first` on, a bit for each place; a whole warp.  `wins`: row t is
+// the one that is written to its place.  SCAN: they are looked for in the slot map.
+template <bool SCAN>
+__device__ __forceinline__ void members_of(const CacheFp8BlockArgs &a, int first, int in_block, long long t, uint32_t (&m)[4],
+                                           int (&rows)[4], bool &wins) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) m[w] = 0;
+    wins = false;
+    if constexpr (SCAN) {
+        int last = -1;                                       // of two rows with one slot the later one is written
+#pragma unroll 4
+        for (int i = lane; i < a.T; i += 32) {
+            const unsigned at = static_cast<unsigned>(a.slot_map[i]) - static_cast<unsigned>(first);
+            if (at < static_cast<unsigned>(a.block)) {
+#pragma unroll
+                for (int w = 0; w < 4; ++w) m[w] |= static_cast<int>(at >> 5) == w ? 1u << (at & 31) : 0u;
+                if (static_cast<int>(at) == in_block) last = i;
+            }
+        }
+#pragma unroll
+        for (int w = 0; w < 4; ++w) m[w] = __reduce_or_sync(0xffffffffu, m[w]);
+        wins = __reduce_max_sync(0xffffffffu, last) == t;
+    } else {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const int at = 32 * w + lane;
+            const int i = at < a.block ? a.index[first + at] : -1;
+            const bool there = i >= 0 && i < a.T && a.slot_map[i] == first + at;
+            rows[w] = there ? i : -1;                        // of this lane's places
+            m[w] = __ballot_sync(0xffffffffu, there);
+            wins |= __any_sync(0xffffffffu, there && at == in_block && i == t);
+        }
+    }
+}
+
+// grid (groups of `per` rows of the call, groups of heads).
 template <bool SCAN>
 __global__ void __launch_bounds__(kThreads) gda_cache_append_fp8_block_kernel(const CacheFp8BlockArgs a, int per) {
     __shared__ Shared sh;
     extern __shared__ __align__(16) uint8_t pieces[];        // [kWarps][kKeep][32][16]
     const long long t0 = static_cast<long long>(blockIdx.x) * per;
+    const int warp = threadIdx.x >> 5;
     if constexpr (!SCAN) asm volatile("griddepcontrol.wait;" ::: "memory");   // the index is written
     if (threadIdx.x < kMaxRows) {                            // the rows that may have the lowest slot of a block
         const long long t = t0 + threadIdx.x;
@@ -272,35 +415,81 @@ __global__ void __launch_bounds__(kThreads) gda_cache_append_fp8_block_kernel(co
         if (slot >= a.slots && blockIdx.y == 0) atomicOr(a.dev_err, GDA_DEVERR_BAD_PAGE);
         // most rows of a prompt have the slot after that of the row before
         if (may && (slot & (a.block - 1)) != 0 && t > 0 && a.slot_map[t - 1] == slot - 1) may = false;
+        if constexpr (!SCAN) {
+            // and some other row has it where the rows come in any order
+            if (may && (slot & (a.block - 1)) != 0) {
+                const int i = a.index[slot - 1];
+                if (i >= 0 && i < a.T && a.slot_map[i] == slot - 1) may = false;
+            }
+        }
         sh.slots[threadIdx.x] = slot;
         const unsigned mask = __ballot_sync(0xffffffffu, may);
         if (threadIdx.x % 32 == 0) sh.some[threadIdx.x / 32] = mask;
+        if (threadIdx.x == 0) sh.ones = sh.mores = 0;
     }
     __syncthreads();
-    const uint64_t some = sh.some[0] | static_cast<uint64_t>(sh.some[1]) << 32;
-    for (uint64_t rest = some; rest != 0; rest &= rest - 1) {    // a step is the same for the whole thread block
-        const int step = __ffsll(static_cast<long long>(rest)) - 1, slot = sh.slots[step];
-        const long long t = t0 + step;
-        const int in_block = slot & (a.block - 1), first = slot - in_block, blk = slot / a.block;
-        if (rest != some) __syncthreads();                   // the readers of `sh` are done
-        if constexpr (SCAN) {
-            if (threadIdx.x < kMaxBlock) sh.place[threadIdx.x] = -1;
-            __syncthreads();
-            for (int i = threadIdx.x; i < a.T; i += kThreads) {
-                const unsigned other = static_cast<unsigned>(a.slot_map[i]) - static_cast<unsigned>(first);
-                if (other < static_cast<unsigned>(a.block)) atomicMax(&sh.place[other], i);
+    int nth = 0;                                             // which of them have it, a warp to a row
+    for (uint64_t rest = sh.some[0] | static_cast<uint64_t>(sh.some[1]) << 32; rest != 0; rest &= rest - 1) {
+        if (nth++ % kWarps != warp) continue;
+        const int step = __ffsll(static_cast<long long>(rest)) - 1, slot = sh.slots[step], in_block = slot & (a.block - 1);
+        uint32_t m[4];
+        int rows[4];
+        bool wins;
+        members_of<SCAN>(a, slot - in_block, in_block, t0 + step, m, rows, wins);
+        const int w = in_block >> 5;
+        const uint32_t below = (w > 0 ? m[0] : 0u) | (w > 1 ? m[1] : 0u) | (w > 2 ? m[2] : 0u) |
+                               ((w == 0 ? m[0] : (w == 1 ? m[1] : (w == 2 ? m[2] : m[3]))) & ((1u << (in_block & 31)) - 1));
+        if (!wins || below != 0) continue;
+        const bool alone = __popc(m[0]) + __popc(m[1]) + __popc(m[2]) + __popc(m[3]) == 1;
+        int k = 0;
+        if ((threadIdx.x & 31) == 0) {
+            k = atomicAdd(alone ? &sh.ones : &sh.mores, 1);
+            (alone ? sh.one : sh.more)[k] = step;
+        }
+        k = __shfl_sync(0xffffffffu, k, 0);
+        if (!SCAN && !alone && k == 0) {                     // the first one's rows are known already
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sh.place[32 * i + (threadIdx.x & 31)] = rows[i];
+        }
+    }
+    __syncthreads();
+
+    // rows that are alone in their blocks, as in a decode step: a warp to 256 elements, the next ones on their way
+    int total = 0;
+    for (int t = 0; t < 3; ++t) total += (a.heads[t] * a.dims[t] + 255) / 256;
+    const int lo = total * static_cast<int>(blockIdx.y) / static_cast<int>(gridDim.y);
+    const int own = total * (static_cast<int>(blockIdx.y) + 1) / static_cast<int>(gridDim.y) - lo, tasks = sh.ones * own;
+    auto fetch = [&](int i) {
+        const int step = sh.one[i / own];
+        return fetch_piece(a, t0 + step, sh.slots[step], lo + i % own);
+    };
+    if (warp < tasks) {
+        Piece now = fetch(warp);
+        for (int i = warp; i < tasks; i += kWarps) {
+            Piece next{};
+            if (i + kWarps < tasks) next = fetch(i + kWarps);
+            write_piece(a, now);
+            now = next;
+        }
+    }
+
+    for (int k = 0; k < sh.mores; ++k) {                     // the same for the whole thread block
+        const int slot = sh.slots[sh.more[k]], in_block = slot & (a.block - 1), first = slot - in_block, blk = slot / a.block;
+        if (SCAN || k > 0) {
+            if (k > 0) __syncthreads();                      // the readers of `place` are done
+            if constexpr (SCAN) {
+                if (threadIdx.x < kMaxBlock) sh.place[threadIdx.x] = -1;
+                __syncthreads();
+                for (int i = threadIdx.x; i < a.T; i += kThreads) {
+                    const unsigned other = static_cast<unsigned>(a.slot_map[i]) - static_cast<unsigned>(first);
+                    if (other < static_cast<unsigned>(a.block)) atomicMax(&sh.place[other], i);
+                }
+            } else if (threadIdx.x < a.block) {
+                const int i = a.index[first + threadIdx.x];
+                sh.place[threadIdx.x] = i >= 0 && i < a.T && a.slot_map[i] == first + static_cast<int>(threadIdx.x) ? i : -1;
             }
-        } else if (threadIdx.x < a.block) {
-            const int i = a.index[first + threadIdx.x];
-            sh.place[threadIdx.x] = i >= 0 && i < a.T && a.slot_map[i] == first + static_cast<int>(threadIdx.x) ? i : -1;
+            __syncthreads();
         }
-        __syncthreads();
-        bool lower = false;
-        if (threadIdx.x <= in_block) {                       // two rows with one slot: one of them is written
-            const int i = sh.place[threadIdx.x];
-            lower = threadIdx.x < in_block ? i >= 0 : i != t;
-        }
-        if (__syncthreads_or(lower)) continue;
         const bool fresh = sh.place[0] >= 0;
         int group = blockIdx.y, tensor = 0;
         for (; tensor < 2; ++tensor) {
@@ -367,8 +556,11 @@ int launch_cache_append_fp8_block(const CacheFp8BlockArgs &a, cudaStream_t strea
     unsigned groups = 0;
     for (int t = 0; t < 3; ++t) groups += groups_of(a.heads[t], a.block, a.dims[t]);
     const bool scan = a.T <= kCacheScanRows;
-    // rows of a thread block: the rows of a prompt but one in a block are passed over at once
-    const int per = static_cast<int>(std::min<long long>(kMaxRows, std::max<long long>(1, a.T / 256)));
+    // Rows of a thread block: the rows of a prompt but one in a block are passed over at once, so there are more where
+    // blocks are longer.  us of the call with a divisor of 8192 / 16384 / 32768: 8192 rows of a prompt, blocks of 64 22.8 /
+    // 24.9 / 28.9; nine pieces of 227, blocks of 16, with the rows read back 33 / 46 / 46; 256 rows of 256 blocks 10.5 /
+    // 14.7 / 14.6.
+    const int per = static_cast<int>(std::min<long long>(kMaxRows, std::max<long long>(1, a.T * a.block / 8192)));
     const dim3 grid(static_cast<unsigned>((a.T + per - 1) / per), groups);
     const auto kern = scan ? gda_cache_append_fp8_block_kernel<true> : gda_cache_append_fp8_block_kernel<false>;
     cudaError_t e = scan ? allow_shared_memory<gda_cache_append_fp8_block_kernel<true>>(kWarps * kPieces)
