@@ -557,10 +557,11 @@ int launch_cache_append_fp8_block(const CacheFp8BlockArgs &a, cudaStream_t strea
     for (int t = 0; t < 3; ++t) groups += groups_of(a.heads[t], a.block, a.dims[t]);
     const bool scan = a.T <= kCacheScanRows;
     // Rows of a thread block: the rows of a prompt but one in a block are passed over at once, so there are more where
-    // blocks are longer.  us of the call with a divisor of 8192 / 16384 / 32768: 8192 rows of a prompt, blocks of 64 22.8 /
-    // 24.9 / 28.9; nine pieces of 227, blocks of 16, with the rows read back 33 / 46 / 46; 256 rows of 256 blocks 10.5 /
-    // 14.7 / 14.6.
-    const int per = static_cast<int>(std::min<long long>(kMaxRows, std::max<long long>(1, a.T * a.block / 8192)));
+    // blocks are longer.  us of the call with T block / 8192, / 16384, / 32768: 8192 rows of a prompt, blocks of 64 22.8 /
+    // 24.9 / 28.9; 256 rows of 256 blocks 10.5 / 14.7 / 14.6; nine pieces of 227 rows, blocks of 16, with the rows read
+    // back, 33 with the first (three rows) and 29 with T / 256.
+    const int per = static_cast<int>(
+        std::min<long long>(kMaxRows, std::max<long long>(1, std::max<long long>(a.T / 256, a.T * a.block / 8192))));
     const dim3 grid(static_cast<unsigned>((a.T + per - 1) / per), groups);
     const auto kern = scan ? gda_cache_append_fp8_block_kernel<true> : gda_cache_append_fp8_block_kernel<false>;
     cudaError_t e = scan ? allow_shared_memory<gda_cache_append_fp8_block_kernel<true>>(kWarps * kPieces)
