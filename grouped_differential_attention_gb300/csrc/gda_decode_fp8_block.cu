@@ -31,9 +31,17 @@
 //     to the largest such scale so far: a larger one shrinks the accumulators,
 //     as a larger score does.
 // Step g of the loop copies K of tile g + A and V of the tile before that one,
-// scores tile g and adds the values of tile g - 1 in one run of instructions:
-// the chain from scores to weights has the values' work beside it, and no more
-// than a tile is held while it is used.
+// adds the values of tile g - 1 and scores tile g, so that no more than a tile
+// is held while it is used.
+//
+// Measured (both kernels; of the 6793 GB/s of a copy): 64 sequences of 4096 to
+// 8192, 12 + 4 heads of 64/128, 1007 MB: 157 us (95 %); one of 131072, 24 + 8
+// heads, 671 MB: 109 us (91 %); 16 of up to 8191, 16 + 4 heads of 128/256, 437
+// MB: 73 us (88 %); 16 listed blocks of 64 of each of the 64 sequences, 168 MB:
+// 38 us (66 %).  About 10 us of each are fixed: the chain of lengths, list, table
+// and first tile (3), the joining (3), and two launches.  Copies alone take 95 %
+// of the time.  By cp.async, a lane's 16 bytes each, the first two took 166 and
+// 115 us: their issue was what the warps waited for.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <algorithm>
@@ -57,7 +65,10 @@ constexpr float kLowest = -3.0e38f;    // a maximum over no position
 // (two at dv = 256).  Every part reads and scores the noise head for itself, and
 // where the parts do not divide the group the last one does a head again, so a
 // part costs about its heads and one more; the fewest of those are taken, of as
-// many the smaller parts.
+// many the smaller parts.  us of a call, 4 noise heads of 64/128, sequences of
+// 4096 to 8192: groups of three as 3 166, as 2 + 2 234; of four as 2 + 2 209,
+// as ones 307; of five as 3 + 3 195, as 2 + 2 + 2 232.  16 sequences of up to
+// 8191, of 128/256: groups of four as 2 + 2 77, as ones 79.
 struct Heads {
     int parts, each;   // parts of a group; signal heads of a part
 };
@@ -81,10 +92,15 @@ __host__ __device__ constexpr int stages_with(int warps, int rh, int d, int dv) 
     const int fit = (227 * 1024 / warps - 2048 - other_bytes(rh, d)) / tile_bytes(rh, d, dv);
     return fit > kMaxStages ? kMaxStages : fit;
 }
-// Warps that share an SM: eight, or as many as leave each two stages.
+// Warps that share an SM: the more signal heads a warp has, the more bytes it has in flight and the fewer warps it takes;
+// as many on each of the four schedulers, and two stages for each.  us of a call, 8 / 12 / 16 warps: one signal head, 64
+// sequences of 4096 to 8192, 4 + 4 heads of 64/128 86 / 76 / 72, 8 + 8 of 64/64 146 / 119 / 109; 32 of 8 + 8 of 128/128 104
+// / 98 (as many as fit); two, 8 + 4 of 64/128 120 / 123, 16 + 4 209 / 218, but 28 + 4, four parts to a group, 205 / 177; 16
+// + 4 of 64/64 175 / 159 / 160.  Three of 64/128, 12 + 4: 160 with eight, 167 with six of three stages, 173 with nine.
+// Two of 128/256, 16 + 4: 76 with seven, 83 with four of three stages.
 __host__ __device__ constexpr int warps_per_sm(int rh, int d, int dv) {
-    int warps = 8;
-    while (warps > 1 && stages_with(warps, rh, d, dv) < 2) --warps;
+    int warps = rh == 1 ? 16 : (rh == 2 && dv == 64 ? 12 : 8);
+    while (warps > 1 && stages_with(warps, rh, d, dv) < 2) warps -= warps > 8 ? 4 : 1;
     return warps;
 }
 __host__ __device__ constexpr int stages_of(int rh, int d, int dv) { return stages_with(warps_per_sm(rh, d, dv), rh, d, dv); }
