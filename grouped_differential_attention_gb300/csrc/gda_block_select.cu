@@ -1,7 +1,7 @@
 // The blocks of tokens that a query is to attend, by a cheap score over the
 // bounds that gda_cache_append_fp8_block keeps of every block's keys.
 //
-// For head h with query q, q8 = rint(q * (127 / amax)), amax = max |q|; a block
+// For head h with query q, q8 = rint(q * (127 * (1 / amax))), amax = max |q|; a block
 // b whose keys lie between lo and hi in every channel has, whatever its keys,
 // a dot product of at most
 //   ub_h(b) = sum over channels of q8 * hi where q8 > 0, of q8 * lo where q8 < 0
@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) gda_block_score_kernel(const
     for (int o = 1; o < LANES; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     const float amax = __uint_as_float(top);
     const bool ok = top < 0x7f800000u && amax >= 0x1p-100f;
-    const float r = ok ? __fdiv_rn(127.f, amax) : 0.f;
+    const float r = ok ? __fmul_rn(127.f, __frcp_rn(amax)) : 0.f;   // q / amax is often k + 1/2: each rounding counts
     uint32_t part[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {

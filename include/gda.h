@@ -615,7 +615,8 @@ size_t gda_cache_append_fp8_block_workspace_size(int T, int num_pages, int page_
 /*
  * The blocks that a decode step is to attend, chosen by a bound on their
  * logits, for gda_attn_decode_sparse_fp8_block.  For every head h, with
- * q8 = rint(q * (127 / amax)), amax = max |q| (float32):
+ * q8 = rint(q * (127 * (1 / amax))), amax = max |q| (float32, each operation
+ * rounded):
  *   x_h(block) = (sum over channels of max(q8 * greatest, q8 * least)) * scale_h(block) * amax
  * from the block's bounds and key scale, a bound on its logits up to a factor;
  * with t = (x_h(block) - max over the sequence's blocks of x_h) * 4 / (127 ln 2

@@ -226,7 +226,7 @@ def block_select(q1, q2, bounds, scales, table, lens, block, keep, first, last):
                 amax = f32(np.abs(x).max())
                 if not (np.isfinite(x).all() and amax >= 2.0 ** -100):
                     continue
-                q8 = np.rint((x * (f32(127) / amax)).astype(f32)).astype(np.int64)
+                q8 = np.rint((x * f32(f32(127) * (f32(1) / amax))).astype(f32)).astype(np.int64)
                 v = np.empty(n, dtype=f32)
                 for j, place in enumerate(at):
                     hi, lo = bounds[i][place][h].astype(np.int64)

@@ -73,6 +73,20 @@ def test_equal_scores_go_to_the_lowest(keep):
           first=min(1, keep - 1))
 
 
+@pytest.mark.parametrize("amax", [1.0, 1.0546875, 1.2734375, 1.875, 1.8671875 * 2.0 ** -60, 1.4296875 * 2.0 ** 100])
+def test_queries_between_two_whole_numbers(amax):
+    """Elements that are odd multiples of amax / 254: q8 goes by the rounding of 127 * (1 / amax), in few blocks that
+    differ in one unit of it."""
+    c = make(1, 64, 3, 1, 64, 16, [64 * 16], seed=6, coarse=True)
+    for i, q in enumerate(c["q"]):
+        half = torch.tensor([amax, amax / 2, -amax / 2, amax / 4]).bfloat16().repeat(16)
+        c["q"][i] = half.expand_as(q).clone()
+        g = torch.Generator().manual_seed(i)
+        c["bounds"][i] = torch.randint(-1, 2, c["bounds"][i].shape, generator=g).to(torch.int8)
+    for keep in (5, 20):
+        check(c, keep)
+
+
 def test_many_blocks():
     c = make(2, 5000, 3, 1, 64, 16, [5000 * 16, 4097 * 16 - 5], seed=4)
     for keep in (3, 300, 4999):
