@@ -13,8 +13,8 @@
 // group (the signal heads that share a noise head, and that) that wants it
 // most: the score is the largest share.  (The bounds themselves cannot be
 // compared between heads: one whose logits are flat would outweigh one that
-// attends to few blocks.)  A head whose amax is below 2^-100 or not finite takes
-// no part.  Kept are the first and last blocks that the caller names, then the
+// attends to few blocks.)  A head whose amax is below 2^-100 or not finite, or
+// whose largest x is past float32, takes no part.  Kept are the first and last blocks that the caller names, then the
 // highest scores, of equal ones the lowest index.  The sums are over whole
 // numbers, w in units of 2^-40, and the roundings have one order, so the choice
 // is the same everywhere.
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(THREADS) gda_block_select_kernel(const BlockSe
         __syncthreads();
         if (here && member == 0 && lane == 0) {
             for (int k = 1; k < team; ++k) total += part_sum[warp + k];
-            best[i] = m, inverse[i] = m > -INFINITY ? __frcp_rn(__fmul_rn(__ull2float_rn(total), 0x1p-40f)) : 0.f;
+            best[i] = m, inverse[i] = m > -INFINITY && m < INFINITY ? __frcp_rn(__fmul_rn(__ull2float_rn(total), 0x1p-40f)) : 0.f;
         }
     }
     __syncthreads();

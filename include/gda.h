@@ -623,7 +623,8 @@ size_t gda_cache_append_fp8_block_workspace_size(int T, int num_pages, int page_
  * sqrt(d)) and w_h = 2^floor(t) (1 + t - floor(t)), about 2^t, the block's share
  * of head h is w_h / (sum of w_h over the blocks), and its score the largest
  * share among the heads of a noise head's group (its signal heads and itself).
- * A head whose amax is below 2^-100 or not finite takes no part.  A sequence
+ * A head whose amax is below 2^-100 or not finite, or whose largest x is past
+ * float32's range, takes no part.  A sequence
  * of n = ceil(cache_lens[b] / block) blocks keeps all of them if n <= keep,
  * else its first `first` and last `last` ones and the highest scores up to
  * keep, of equal scores the lower block.

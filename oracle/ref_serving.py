@@ -231,7 +231,10 @@ def block_select(q1, q2, bounds, scales, table, lens, block, keep, first, last):
                 for j, place in enumerate(at):
                     hi, lo = bounds[i][place][h].astype(np.int64)
                     ub = int((np.maximum(q8, 0) * hi + np.minimum(q8, 0) * lo).sum())
-                    v[j] = f32(f32(ub) * scales[i][place][h]) * amax
+                    with np.errstate(over="ignore"):
+                        v[j] = f32(f32(ub) * scales[i][place][h]) * amax
+                if np.isinf(v.max()):
+                    continue
                 unit = f32(4 / 127 / np.log(2) / np.sqrt(x.size))
                 t = np.maximum(((v - v.max()).astype(f32) * unit).astype(f32), f32(-126))
                 e = np.floor(t)

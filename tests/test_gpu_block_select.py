@@ -120,6 +120,17 @@ def test_heads_without_a_score():
     assert run(c, 4, first=0, last=1)[0][3, 0].tolist() == [0, 1, 2, 59]
 
 
+def test_bounds_past_float32():
+    """A head whose bounds on some block are infinite takes no part, one with blocks at minus infinity does."""
+    c = make(2, 60, 3, 1, 64, 16, [60 * 16] * 2, seed=10)
+    c["q"][0][0, 1] *= 2.0 ** 125
+    c["q"][0][1, 2] = 2.0 ** 120
+    c["bounds"][0][1, 5:, 2] = -100
+    c["bounds"][0][1, :5, 2] = 0
+    check(c, 9)
+    check(c, 4, 0, 0)
+
+
 def test_bad_lengths_and_pages_are_reported():
     c = make(3, 12, 3, 1, 64, 16, [12 * 16, 12 * 16 + 1, -4], seed=8, page=48)
     gda.gda_device_error(clear=True)
