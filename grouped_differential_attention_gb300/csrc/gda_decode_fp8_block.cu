@@ -448,7 +448,10 @@ __global__ void __launch_bounds__(32, (Stage<D, DV, RH>::warps)) gda_decode_fp8_
     float factor = 0.f;
     float acc[RH][SLABS * WORDS][4];                     // [w]: of tiles 2 w + t / 2 and map t % 2, see values_of
     float m = kLowest, l = 0.f;                          // of head t (both its lanes' positions; l of this lane's only)
-    float v_most = 0.f, v_inverse = 0.f;                 // of head t: the largest scale of V so far, and 1 over it
+    // of head t: the largest scale of V so far, and 1 over it.  From 2^-126 on, whose inverse is finite: smaller scales
+    // (or 0) are relative to that
+    constexpr float kLeast = 0x1p-126f;
+    float v_most = kLeast, v_inverse = 1.f / kLeast;
     float shrink = 1.f, v_shrink = 1.f;                  // of what was added before the last tile scored
     auto clear = [&]() {
 #pragma unroll
@@ -637,7 +640,7 @@ __global__ void __launch_bounds__(32, (Stage<D, DV, RH>::warps)) gda_decode_fp8_
             if (over) return;
             factor = q.place(p, queries);
             clear();
-            m = kLowest, l = 0.f, v_most = 0.f, v_inverse = 0.f;
+            m = kLowest, l = 0.f, v_most = kLeast, v_inverse = 1.f / kLeast;
             part_of = use.b;
         }
         __syncwarp();                                    // the weights have been read, the queries are there

@@ -238,6 +238,18 @@ def test_scales_far_apart_and_zero():
     check(run(c), c)
 
 
+def test_scales_without_a_finite_inverse():
+    """Scales below 2^-128, whose inverse is past float32: beside ordinary blocks, and alone."""
+    c = make(3, 256, 6, 2, 64, 128, [256, 200, 129], seed=13, block=32)
+    v = c["scales"][2]
+    v[:2, ::2] = 2.0 ** -149
+    v[2] = 2.0 ** -140
+    c["scales"][0][:, 3] = 2.0 ** -145
+    out = run(c)
+    check(out[:2], {**c, **{k: c[k][:2] for k in ("q1", "q2", "lens")}})
+    assert (out[2].abs() <= 2.0 ** -120).all()
+
+
 def test_large_queries_and_scores():
     c = make(2, 512, 3, 1, 128, 128, [512, 300], seed=8, block=64)
     c["q1"] *= 3e4
