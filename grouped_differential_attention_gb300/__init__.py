@@ -1204,9 +1204,14 @@ def gda_block_select(q_sig, q_noise, k_sig_bounds, k_noise_bounds, k_sig_scale, 
                     (out[1], "block_count", i32, (B,)))
     if not table:
         at.insert(6, None)
-    workspace = _workspace(workspace, _bytes_of("gda_block_select_workspace_size", B, max_pages * per, hs, hn), dev)
+    need = _bytes_of("gda_block_select_workspace_size", B, max_pages * per, hs, hn)
+    if workspace is not None or need:
+        workspace = _workspace(workspace, need, dev)
+        space = (workspace.data_ptr(), workspace.numel())
+    else:
+        space = (None, 0)
     _enqueue(_load().gda_block_select, "gda block selection", dev, *at, B, max_pages, per * block, pages, block, keep,
-             first, last, hs, hn, d, workspace.data_ptr(), workspace.numel())
+             first, last, hs, hn, d, *space)
     return tuple(out)
 
 

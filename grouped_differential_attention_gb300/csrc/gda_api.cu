@@ -931,7 +931,7 @@ int gda_cache_read_fp8_block(const int *slot_map, const void *k_sig_pool, const 
 size_t gda_block_select_workspace_size(int B, int max_blocks, int h_s, int h_n) {
     if (B < 1 || max_blocks < 1 || h_s < 1 || h_n < 1 || h_s % h_n != 0) return 0;
     if (B > 65535 || max_blocks > kBlockSelectMaxBlocks || heads_above(h_s, h_n, 128)) return 0;
-    return static_cast<size_t>(B) * max_blocks * (h_s + h_n) * sizeof(float);
+    return block_select_workspace_bytes(B, max_blocks, h_s, h_n);
 }
 
 int gda_block_select(const void *q_sig, const void *q_noise, const int8_t *k_sig_bounds, const int8_t *k_noise_bounds,
@@ -956,9 +956,8 @@ int gda_block_select(const void *q_sig, const void *q_noise, const int8_t *k_sig
         return GDA_ERR_MISALIGNED;
     if (!aligned4({k_sig_scale, k_noise_scale, block_table, cache_lens, block_list, block_count}))
         return GDA_ERR_MISALIGNED;
-    if (!workspace || !aligned16(workspace) ||
-        workspace_bytes < gda_block_select_workspace_size(B, static_cast<int>(most), h_s, h_n))
-        return GDA_ERR_WORKSPACE;
+    const size_t need = block_select_workspace_bytes(B, static_cast<int>(most), h_s, h_n);
+    if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return GDA_ERR_WORKSPACE;
     BlockSelectArgs a{q_sig, q_noise, k_sig_bounds, k_noise_bounds, k_sig_scale, k_noise_scale, block_table, cache_lens,
                       block_list, block_count, B, max_pages, page_size, num_pages, block, keep, first, last, h_s, h_n, d,
                       static_cast<float>(4.0 / 127.0 / std::log(2.0) / std::sqrt(static_cast<double>(d))),

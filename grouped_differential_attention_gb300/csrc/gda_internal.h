@@ -226,6 +226,7 @@ size_t decode_fp4_workspace_bytes(int B, int hs, int hn, int d, int dv);
 int launch_cache_append_fp8_block(const CacheFp8BlockArgs &a, cudaStream_t stream);
 int launch_cache_read_fp8_block(const CacheFp8BlockArgs &a, cudaStream_t stream);
 int launch_block_select(const BlockSelectArgs &a, cudaStream_t stream);
+size_t block_select_workspace_bytes(int B, int most, int hs, int hn);
 int launch_decode_fp8_block(const DecodeFp8BlockArgs &a, cudaStream_t stream);
 size_t decode_fp8_block_workspace_bytes(int B, int hs, int hn, int d, int dv);
 

@@ -636,8 +636,10 @@ size_t gda_cache_append_fp8_block_workspace_size(int T, int num_pages, int page_
  *   block) that each noise head keeps, ascending, then -1.
  *   block_count [B] int32: min(n, keep).
  *   workspace: gda_block_select_workspace_size(B, max_pages * page_size /
- *   block, h_s, h_n) bytes, 16-byte aligned, owned by the caller, needs no
- *   initialisation; calls in flight at the same time need a workspace each.
+ *   block, h_s, h_n) bytes (0, and then it may be NULL, where a group's
+ *   bounds of a sequence fit on chip: at 3 signal heads to a noise head up to
+ *   30000 blocks, at 24 up to 10000), 16-byte aligned, owned by the caller, needs no initialisation; calls in flight at
+ *   the same time need a workspace each.
  * A length outside [0, max_pages * page_size] is clamped and reported
  * (GDA_DEVERR_BAD_LENGTH), a page outside the pool is read as page 0 and
  * reported (GDA_DEVERR_BAD_PAGE).  The result does not depend on the order of

@@ -85,14 +85,18 @@ def test_select_refuses(lib):
     for bad in (dict(d=96), dict(hs=128, hn=1), dict(B=65536), dict(block=8), dict(mp=32768, ps=32, block=16),
                 dict(mp=32769, ps=32), dict(pages=2 ** 31 - 1)):
         assert select(lib, **bad) == UNSUPPORTED
-    assert select(lib, ws=None) == WORKSPACE and select(lib, ws=A + 8) == WORKSPACE
-    assert select(lib, ws_bytes=3 * 8 * 8 * 4 - 1) == WORKSPACE
+    many = dict(mp=8192, ps=32, pages=1, hs=80)             # x of 40 heads of a group does not fit
+    assert select(lib, ws=None, **many) == WORKSPACE and select(lib, ws=A + 8, **many) == WORKSPACE
+    assert select(lib, ws_bytes=3 * 8192 * 82 * 4 - 1, **many) == WORKSPACE
     if not torch.cuda.is_available():
         assert select(lib) == CUDA and select(lib, p=ptrs(10, p6=None), mp=1, pages=3) == CUDA
         assert select(lib, mp=32768, ps=32, pages=1) == CUDA            # the most blocks
+        assert select(lib, ws=None) == CUDA and select(lib, **many) == CUDA
     size = lib.gda_block_select_workspace_size
-    assert size(3, 8, 6, 2) == 768 and size(0, 8, 6, 2) == 0 and size(3, 32769, 6, 2) == 0 and size(3, 8, 6, 4) == 0
-    assert size(65536, 8, 6, 2) == 0 and size(3, 8, 127, 2) == 0
+    assert size(3, 8, 6, 2) == 0 and size(3, 30000, 6, 2) == 0 and size(3, 10000, 24, 1) == 0
+    assert size(3, 8192, 80, 2) == 3 * 8192 * 82 * 4 and size(1, 32768, 127, 1) == 32768 * 128 * 4
+    assert size(0, 8192, 80, 2) == 0 and size(3, 32769, 80, 2) == 0 and size(3, 8192, 80, 3) == 0
+    assert size(65536, 8192, 80, 2) == 0 and size(3, 8192, 127, 2) == 0
 
 
 def decode(lib, p=None, kind="whole", B=4, Lcap=64, block=32, hs=6, hn=2, d=64, dv=128, lam0=0.8, eps=1e-5, ws=A,

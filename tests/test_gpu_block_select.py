@@ -93,6 +93,18 @@ def test_many_blocks():
         check(c, keep, 1, 2)
 
 
+@pytest.mark.parametrize("hs,hn,d,most,lens", [
+    (24, 1, 64, 3000, [48000, 16 * 2500 + 1]),     # x of all heads fits eight thread blocks
+    (100, 1, 64, 4000, [16 * 3999 + 5]),           # and does not: two launches
+    (6, 2, 128, 300, [4800, 4097, 16, 0, 4000]), (3, 1, 64, 1100, [16 * 1100, 16 * 9, 16 * 257, 16 * 256]),
+    (6, 2, 64, 12, [192] * 90),
+])
+def test_every_way_through(hs, hn, d, most, lens):
+    c = make(len(lens), most, hs, hn, d, 16, lens, seed=hs + most, page=48 if most < 1000 else 0)
+    for keep in (1, 8, 200):
+        check(c, keep, min(1, keep - 1), min(2, keep - 1) if keep > 2 else 0)
+
+
 def test_the_most_blocks_of_a_sequence():
     """32768 blocks; keys chosen so that block j's share grows with a known order, above that of a flat noise head."""
     n = 32768
@@ -151,7 +163,7 @@ def test_outputs_of_the_caller_replayed_over_any_workspace():
     c = make(5, 50, 6, 2, 64, 32, [50 * 32, 3, 0, 49 * 32, 700], seed=9, page=64)
     dev = [t.cuda() for t in (*c["q"], *c["bounds"], *c["scales"], c["lens"], c["table"])]
     out = (torch.empty(5, 2, 8, dtype=torch.int32, device="cuda"), torch.empty(5, dtype=torch.int32, device="cuda"))
-    ws = torch.full((gda.gda_block_select_workspace_size(5, 50, 6, 2),), 0xFF, dtype=torch.uint8, device="cuda")
+    ws = torch.full((5 * 50 * 8 * 4,), 0xFF, dtype=torch.uint8, device="cuda")
     want = [t.clone() for t in run(c, 8)]
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
