@@ -197,22 +197,29 @@ __device__ __forceinline__ void list_highest(const uint32_t *keys, int n, int ke
                                              uint2 (&sums)[THREADS / 32]) {
     constexpr int WARPS = THREADS / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (n <= kCountKeys) {                                   // few: a thread to a key, which counts those ahead of its own
-        const int j = threadIdx.x;
-        const uint32_t own = j < n ? keys[j] : 0u;
-        int ahead = 0;
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-            const uint32_t k = keys[i];
-            ahead += k > own || (k == own && i < j);
+    if (n <= kCountKeys) {                                   // few: EACH lanes to a key count those ahead of it
+        constexpr int EACH = THREADS / kCountKeys;
+        const int j = threadIdx.x / EACH;
+        uint32_t lanes = 0;
+        if (warp * (32 / EACH) < n) {
+            const uint32_t own = keys[min(j, n - 1)];
+            int ahead = 0;
+#pragma unroll 8
+            for (int i = lane % EACH; i < n; i += EACH) {
+                const uint32_t k = keys[i];
+                ahead += k > own || (k == own && i < j);
+            }
+#pragma unroll
+            for (int o = 1; o < EACH; o <<= 1) ahead += __shfl_xor_sync(0xffffffffu, ahead, o);
+            lanes = __ballot_sync(0xffffffffu, j < n && ahead < kept && lane % EACH == 0);
+            if (lane == 0) sums[warp].x = __popc(lanes);
         }
-        const bool mine = j < n && ahead < kept;
-        const uint32_t lanes = __ballot_sync(0xffffffffu, mine);
-        if (lane == 0) sums[warp].x = __popc(lanes);
         __syncthreads();
-        int at = __popc(lanes & ((1u << lane) - 1));
-        for (int w = 0; w < warp; ++w) at += sums[w].x;
-        if (mine) list[at] = j;
+        if (lanes >> lane & 1u) {
+            int at = __popc(lanes & ((1u << lane) - 1));
+            for (int w = 0; w < warp; ++w) at += sums[w].x;
+            list[at] = j;
+        }
         return;
     }
     // the kept-th highest key, eight bits at a time, a histogram to a warp: most keys share their first digits
@@ -374,21 +381,9 @@ __global__ void __launch_bounds__(kThreads) gda_block_select_fused_kernel(const 
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks_));
     const int rank = static_cast<int>(rank_), ranks = static_cast<int>(ranks_);
     const int g = blockIdx.x / ranks, b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LANES;
-    const int n = (length_of(a, b) + a.block - 1) / a.block, kept = min(n, a.keep), r = a.hs / a.hn, heads = r + 1;
-    int *list = a.list + (static_cast<size_t>(b) * a.hn + g) * a.keep;
-    if (rank == 0) {
-        if (g == 0 && threadIdx.x == 0) a.count[b] = kept;
-        for (int i = threadIdx.x + (n <= a.keep ? 0 : kept); i < a.keep; i += kThreads) list[i] = i < kept ? i : -1;
-    }
-    if (n <= a.keep) return;                                 // the whole cluster
-    const int per = (n + ranks - 1) / ranks, j0 = min(n, rank * per), own = min(n, j0 + per) - j0;   // per <= part
+    const int r = a.hs / a.hn, heads = r + 1;
     uint4 *const parts = reinterpret_cast<uint4 *>(raw);     // [heads][LANES]
-    int *const places = reinterpret_cast<int *>(raw + heads * 256);
-    float *const x = reinterpret_cast<float *>(places + part);   // [heads][part]
-    uint32_t *const keys = reinterpret_cast<uint32_t *>(x + heads * part);
-
-    for (int j = threadIdx.x; j < own; j += kThreads) places[j] = static_cast<int>(pool_block(a, b, j0 + j));
-    for (int h = warp; h < heads; h += WARPS) {
+    for (int h = WARPS - 1 - warp; h < heads; h += WARPS) {   // while the first warps look up places
         const uint4 *q = reinterpret_cast<const uint4 *>(
             h == r ? static_cast<const __nv_bfloat16 *>(a.q2) + (static_cast<size_t>(b) * a.hn + g) * D
                    : static_cast<const __nv_bfloat16 *>(a.q1) + (static_cast<size_t>(b) * a.hs + g * r + h) * D);
@@ -396,6 +391,19 @@ __global__ void __launch_bounds__(kThreads) gda_block_select_fused_kernel(const 
         if (lane < LANES) parts[h * LANES + sub] = make_uint4(part8.w[0], part8.w[1], part8.w[2], part8.w[3]);
         if (lane == 0) amax[h] = part8.ok ? part8.amax : -1.f;
     }
+    const int n = (length_of(a, b) + a.block - 1) / a.block, kept = min(n, a.keep);
+    int *list = a.list + (static_cast<size_t>(b) * a.hn + g) * a.keep;
+    if (rank == 0) {
+        if (g == 0 && threadIdx.x == 0) a.count[b] = kept;
+        for (int i = threadIdx.x + (n <= a.keep ? 0 : kept); i < a.keep; i += kThreads) list[i] = i < kept ? i : -1;
+    }
+    if (n <= a.keep) return;                                 // the whole cluster
+    const int per = (n + ranks - 1) / ranks, j0 = min(n, rank * per), own = min(n, j0 + per) - j0;   // per <= part
+    int *const places = reinterpret_cast<int *>(raw + heads * 256);
+    float *const x = reinterpret_cast<float *>(places + part);   // [heads][part]
+    uint32_t *const keys = reinterpret_cast<uint32_t *>(x + heads * part);
+
+    for (int j = threadIdx.x; j < own; j += kThreads) places[j] = static_cast<int>(pool_block(a, b, j0 + j));
     __syncthreads();
 
     // (block, head) pairs, a block's heads side by side as their bounds are
