@@ -26,10 +26,12 @@
 // alone in its block (a decode step) is 256 elements to a warp; several are
 // held by a thread block in shared memory between the two passes over them.
 //
-// Measured (kernels; 12 + 4 heads of 64/128, blocks of 64): 64 rows of as many
-// sequences 5 us, 256 10.5, 1024 22; 8192 rows of a prompt 2.5 + 20 (63 MB, 9.3
-// at the copy rate of 6793 GB/s: two waves of thread blocks, each a chain of
-// looking up, loading and writing); reading 8192 rows 12.7 (63 MB).
+// Measured (graph replay; 12 + 4 heads of 64/128, blocks of 64): 64 rows of as
+// many sequences 6.3 us, 256 10.3, 1024 22; 8192 rows of a prompt 20.5 (63 MB,
+// 9.3 at the copy rate of 6793 GB/s: noting the slots 2.5, then a wave and a half
+// of thread blocks, each a chain of looking up, loading and writing); reading
+// 8192 rows 12.4 (63 MB).  Rows prefetched into L2 while the slots are noted:
+// 22.6 with the rows there already, 25.7 for 28.8 with them in HBM, not kept.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <algorithm>
@@ -43,8 +45,8 @@
 namespace gda {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kMaxBlock = 128;
+constexpr int kThreads = 256;          // of reading, and of noting slots
+constexpr int kMaxBlock = 128;         // (a thread block has as many threads at least)
 constexpr int kMaxRows = 64;           // rows of the call that a thread block looks at
 constexpr int kKeep = 16;              // pieces of 8 elements that a lane holds
 
@@ -81,17 +83,18 @@ __device__ __forceinline__ uint32_t codes_of(float lo, float hi, float r, float 
 __host__ __device__ constexpr int warps_of(int block, int n) {
     return block * n <= kKeep * 8 * 32 ? 1 : block * n / (kKeep * 8 * 32);
 }
-__host__ __device__ constexpr int groups_of(int heads, int block, int n) {   // thread blocks for the heads of a tensor
-    return (heads * warps_of(block, n) + kWarps - 1) / kWarps;
+__host__ __device__ constexpr int groups_of(int heads, int block, int n, int warps) {   // thread blocks for a tensor's heads
+    return (heads * warps_of(block, n) + warps - 1) / warps;
 }
 
+template <int WARPS>
 struct Shared {
     int place[kMaxBlock];              // the call's row of each place of the block of tokens, or -1
     int slots[kMaxRows];
     unsigned some[kMaxRows / 32];
     int one[kMaxRows], more[kMaxRows], ones, mores;   // the rows that write a block: alone, and with others
-    uint32_t most[kWarps];
-    uint32_t top[kWarps][64], low[kWarps][64];   // pairs of a key's channels
+    uint32_t most[WARPS];
+    uint32_t top[WARPS][64], low[WARPS][64];   // pairs of a key's channels
 };
 constexpr int kPieces = kKeep * 512;   // bytes of a warp's pieces
 
@@ -107,11 +110,12 @@ __device__ __forceinline__ void copies_landed() { asm volatile("cp.async.wait_al
 // go through shared memory, where no other thread reads them: that many loads are in flight without as many registers,
 // in loops that need not be unrolled (a call of few rows runs once through cold instructions: unrolled over registers 64
 // rows took 18 us and 8192 rows 50).
-__device__ __forceinline__ void write_heads(const CacheFp8BlockArgs &a, int tensor, int group, int blk, Shared &sh,
+template <int WARPS>
+__device__ __forceinline__ void write_heads(const CacheFp8BlockArgs &a, int tensor, int group, int blk, Shared<WARPS> &sh,
                                             uint8_t *pieces, bool fresh) {
     const int n = a.dims[tensor], log = n == 64 ? 3 : (n == 128 ? 4 : 5), lanes = 1 << log, step = 32 >> log;
     const int share = warps_of(a.block, n), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int head = (group * kWarps + warp) / share, member = warp % share;
+    const int head = (group * WARPS + warp) / share, member = warp % share;
     const bool here = head < a.heads[tensor];
     const int ch = (lane & (lanes - 1)) * 8, row0 = member * step + (lane >> log), stride = share * step;   // this lane's places
     const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(a.rows[tensor]) + head * n + ch;
@@ -400,10 +404,10 @@ __device__ __forceinline__ void members_of(const CacheFp8BlockArgs &a, int first
 }
 
 // grid (groups of `per` rows of the call, groups of heads).
-template <bool SCAN>
-__global__ void __launch_bounds__(kThreads) gda_cache_append_fp8_block_kernel(const CacheFp8BlockArgs a, int per) {
-    __shared__ Shared sh;
-    extern __shared__ __align__(16) uint8_t pieces[];        // [kWarps][kKeep][32][16]
+template <bool SCAN, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32) gda_cache_append_fp8_block_kernel(const CacheFp8BlockArgs a, int per) {
+    __shared__ Shared<WARPS> sh;
+    extern __shared__ __align__(16) uint8_t pieces[];        // [WARPS][kKeep][32][16]
     const long long t0 = static_cast<long long>(blockIdx.x) * per;
     const int warp = threadIdx.x >> 5;
     if constexpr (!SCAN) asm volatile("griddepcontrol.wait;" ::: "memory");   // the index is written
@@ -430,7 +434,7 @@ __global__ void __launch_bounds__(kThreads) gda_cache_append_fp8_block_kernel(co
     __syncthreads();
     int nth = 0;                                             // which of them have it, a warp to a row
     for (uint64_t rest = sh.some[0] | static_cast<uint64_t>(sh.some[1]) << 32; rest != 0; rest &= rest - 1) {
-        if (nth++ % kWarps != warp) continue;
+        if (nth++ % WARPS != warp) continue;
         const int step = __ffsll(static_cast<long long>(rest)) - 1, slot = sh.slots[step], in_block = slot & (a.block - 1);
         uint32_t m[4];
         int rows[4];
@@ -465,9 +469,9 @@ __global__ void __launch_bounds__(kThreads) gda_cache_append_fp8_block_kernel(co
     };
     if (warp < tasks) {
         Piece now = fetch(warp);
-        for (int i = warp; i < tasks; i += kWarps) {
+        for (int i = warp; i < tasks; i += WARPS) {
             Piece next{};
-            if (i + kWarps < tasks) next = fetch(i + kWarps);
+            if (i + WARPS < tasks) next = fetch(i + WARPS);
             write_piece(a, now);
             now = next;
         }
@@ -480,7 +484,7 @@ __global__ void __launch_bounds__(kThreads) gda_cache_append_fp8_block_kernel(co
             if constexpr (SCAN) {
                 if (threadIdx.x < kMaxBlock) sh.place[threadIdx.x] = -1;
                 __syncthreads();
-                for (int i = threadIdx.x; i < a.T; i += kThreads) {
+                for (int i = threadIdx.x; i < a.T; i += WARPS * 32) {
                     const unsigned other = static_cast<unsigned>(a.slot_map[i]) - static_cast<unsigned>(first);
                     if (other < static_cast<unsigned>(a.block)) atomicMax(&sh.place[other], i);
                 }
@@ -493,7 +497,7 @@ __global__ void __launch_bounds__(kThreads) gda_cache_append_fp8_block_kernel(co
         const bool fresh = sh.place[0] >= 0;
         int group = blockIdx.y, tensor = 0;
         for (; tensor < 2; ++tensor) {
-            const int of = groups_of(a.heads[tensor], a.block, a.dims[tensor]);
+            const int of = groups_of(a.heads[tensor], a.block, a.dims[tensor], WARPS);
             if (group < of) break;
             group -= of;
         }
@@ -550,38 +554,47 @@ dim3 read_grid(const CacheFp8BlockArgs &a, unsigned *tokens) {
     return dim3(static_cast<unsigned>((a.T + *tokens - 1) / *tokens), (*tokens * per_token + kThreads - 1) / kThreads);
 }
 
-}  // namespace
-
-int launch_cache_append_fp8_block(const CacheFp8BlockArgs &a, cudaStream_t stream) {
+template <bool SCAN, int WARPS>
+cudaError_t launch_append(const CacheFp8BlockArgs &a, cudaStream_t stream) {
     unsigned groups = 0;
-    for (int t = 0; t < 3; ++t) groups += groups_of(a.heads[t], a.block, a.dims[t]);
-    const bool scan = a.T <= kCacheScanRows;
+    for (int t = 0; t < 3; ++t) groups += groups_of(a.heads[t], a.block, a.dims[t], WARPS);
     // Rows of a thread block: the rows of a prompt but one in a block are passed over at once, so there are more where
-    // blocks are longer.  us of the call with T block / 8192, / 16384, / 32768: 8192 rows of a prompt, blocks of 64 22.8 /
-    // 24.9 / 28.9; 256 rows of 256 blocks 10.5 / 14.7 / 14.6; nine pieces of 227 rows, blocks of 16, with the rows read
-    // back, 33 with the first (three rows) and 29 with T / 256.
+    // blocks are longer.  us of the call with T block / 8192, / 16384: 8192 rows of a prompt, blocks of 64 20.5 / 22.6, in
+    // any order 36.6 / 31.1; 256 rows of 256 blocks 10.4 / 12.4.  Nine pieces of 227 rows, blocks of 16, with the rows read
+    // back: 33 with the first (three rows) and 29 with T / 256.
     const int per = static_cast<int>(
         std::min<long long>(kMaxRows, std::max<long long>(1, std::max<long long>(a.T / 256, a.T * a.block / 8192))));
-    const dim3 grid(static_cast<unsigned>((a.T + per - 1) / per), groups);
-    const auto kern = scan ? gda_cache_append_fp8_block_kernel<true> : gda_cache_append_fp8_block_kernel<false>;
-    cudaError_t e = scan ? allow_shared_memory<gda_cache_append_fp8_block_kernel<true>>(kWarps * kPieces)
-                         : allow_shared_memory<gda_cache_append_fp8_block_kernel<false>>(kWarps * kPieces);
-    if (e != cudaSuccess) return record_cuda_error(e);
-    if (!scan) {
-        gda_cache_index_kernel<<<static_cast<unsigned>((a.T + kThreads - 1) / kThreads), kThreads, 0, stream>>>(a);
-        if ((e = cudaGetLastError()) != cudaSuccess) return record_cuda_error(e);
-    }
+    constexpr auto kern = gda_cache_append_fp8_block_kernel<SCAN, WARPS>;
+    const cudaError_t e = allow_shared_memory<kern>(WARPS * kPieces);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kWarps * kPieces;
+    cfg.gridDim = dim3(static_cast<unsigned>((a.T + per - 1) / per), groups);
+    cfg.blockDim = dim3(WARPS * 32);
+    cfg.dynamicSmemBytes = WARPS * kPieces;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = scan ? 0 : 1;                             // after the index kernel only: others may write what is read here
-    e = cudaLaunchKernelEx(&cfg, kern, a, per);
+    cfg.numAttrs = SCAN ? 0 : 1;                             // after the index kernel only: others may write what is read here
+    return cudaLaunchKernelEx(&cfg, kern, a, per);
+}
+
+}  // namespace
+
+int launch_cache_append_fp8_block(const CacheFp8BlockArgs &a, cudaStream_t stream) {
+    const bool scan = a.T <= kCacheScanRows;
+    if (!scan) {
+        gda_cache_index_kernel<<<static_cast<unsigned>((a.T + kThreads - 1) / kThreads), kThreads, 0, stream>>>(a);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return record_cuda_error(e);
+    }
+    // Warps of a thread block: four, unless more share a head (blocks of 128 at dim 256).  us of the call with four / eight:
+    // 8192 rows of a prompt, blocks of 64 20.5 / 22.6, of 16 25.0 / 31.0; nine pieces of 227 rows of 128/256 18.9 / 20.8;
+    // 8192 rows of as many blocks 102 / 97.
+    const bool four = warps_of(a.block, std::max(a.dims[0], a.dims[2])) <= 4;
+    const cudaError_t e = four ? (scan ? launch_append<true, 4>(a, stream) : launch_append<false, 4>(a, stream))
+                               : (scan ? launch_append<true, 8>(a, stream) : launch_append<false, 8>(a, stream));
     return e == cudaSuccess ? GDA_OK : record_cuda_error(e);
 }
 
