@@ -367,9 +367,16 @@ __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+__device__ __forceinline__ int product(uint4 a, uint4 b, int c) {       // of 16 whole numbers each, added to c
+    c = __dp4a(static_cast<int>(a.x), static_cast<int>(b.x), c);
+    c = __dp4a(static_cast<int>(a.y), static_cast<int>(b.y), c);
+    c = __dp4a(static_cast<int>(a.z), static_cast<int>(b.z), c);
+    return __dp4a(static_cast<int>(a.w), static_cast<int>(b.w), c);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads) gda_block_select_fused_kernel(const BlockSelectArgs a, int part) {
-    constexpr int WARPS = kThreads / 32, LANES = D / 8, PAIRS = 32 / LANES, STEP = WARPS * PAIRS;
+    constexpr int WARPS = kThreads / 32, LANES = D / 16, PAIRS = 32 / LANES, STEP = WARPS * PAIRS;   // 32 bytes to a lane
     extern __shared__ __align__(16) uint8_t raw[];
     __shared__ float amax[128], best[128], own_best[128], inverse[128];
     __shared__ unsigned long long own_sum[128];
@@ -382,13 +389,13 @@ __global__ void __launch_bounds__(kThreads) gda_block_select_fused_kernel(const 
     const int rank = static_cast<int>(rank_), ranks = static_cast<int>(ranks_);
     const int g = blockIdx.x / ranks, b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LANES;
     const int r = a.hs / a.hn, heads = r + 1;
-    uint4 *const parts = reinterpret_cast<uint4 *>(raw);     // [heads][LANES]
+    uint4 *const parts = reinterpret_cast<uint4 *>(raw);     // [heads][D / 8]
     for (int h = WARPS - 1 - warp; h < heads; h += WARPS) {   // while the first warps look up places
         const uint4 *q = reinterpret_cast<const uint4 *>(
             h == r ? static_cast<const __nv_bfloat16 *>(a.q2) + (static_cast<size_t>(b) * a.hn + g) * D
                    : static_cast<const __nv_bfloat16 *>(a.q1) + (static_cast<size_t>(b) * a.hs + g * r + h) * D);
-        const QueryPart<LANES> part8(q, sub);
-        if (lane < LANES) parts[h * LANES + sub] = make_uint4(part8.w[0], part8.w[1], part8.w[2], part8.w[3]);
+        const QueryPart<D / 8> part8(q, lane % (D / 8));
+        if (lane < D / 8) parts[h * (D / 8) + lane] = make_uint4(part8.w[0], part8.w[1], part8.w[2], part8.w[3]);
         if (lane == 0) amax[h] = part8.ok ? part8.amax : -1.f;
     }
     const int n = (length_of(a, b) + a.block - 1) / a.block, kept = min(n, a.keep);
@@ -412,7 +419,7 @@ __global__ void __launch_bounds__(kThreads) gda_block_select_fused_kernel(const 
     const int dj = STEP / heads, dh = STEP % heads;
     while (first < total) {
         constexpr int K = 4;
-        uint4 v[K];
+        uint4 v[K], w[K];
         float s[K];
         int to[K], head[K];
 #pragma unroll
@@ -420,7 +427,8 @@ __global__ void __launch_bounds__(kThreads) gda_block_select_fused_kernel(const 
             const size_t at = static_cast<size_t>(places[min(j, own - 1)]);
             const bool noise = h == r;
             const size_t place = noise ? at * a.hn + g : at * a.hs + g * r + h;
-            v[k] = *reinterpret_cast<const uint4 *>((noise ? a.k2b : a.k1b) + place * 2 * D + sub * 16);
+            const uint4 *bounds = reinterpret_cast<const uint4 *>((noise ? a.k2b : a.k1b) + place * 2 * D) + sub * 2;
+            v[k] = bounds[0], w[k] = bounds[1];
             s[k] = (noise ? a.k2s : a.k1s)[place];
             head[k] = h;
             to[k] = j < own ? h * part + j : -1;
@@ -429,11 +437,9 @@ __global__ void __launch_bounds__(kThreads) gda_block_select_fused_kernel(const 
         }
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const uint4 q8 = parts[head[k] * LANES + sub];
-            int ub = __dp4a(static_cast<int>(v[k].x), static_cast<int>(q8.x), 0);
-            ub = __dp4a(static_cast<int>(v[k].y), static_cast<int>(q8.y), ub);
-            ub = __dp4a(static_cast<int>(v[k].z), static_cast<int>(q8.z), ub);
-            ub = __dp4a(static_cast<int>(v[k].w), static_cast<int>(q8.w), ub);
+            const uint4 *q8 = parts + head[k] * (D / 8) + sub * 2;
+            int ub = product(v[k], q8[0], 0);
+            ub = product(w[k], q8[1], ub);
 #pragma unroll
             for (int o = 1; o < LANES; o <<= 1) ub += __shfl_xor_sync(0xffffffffu, ub, o);
             const float top = amax[head[k]];
