@@ -30,6 +30,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 import threading
 
@@ -1007,22 +1008,36 @@ def gda_attn_decode_paged_fp4(q_sig, q_noise, k_sig_pool, k_noise_pool, v_pool, 
                        block_table, cache_lens, lam, lambda_init, eps, out, workspace)
 
 
-def _addresses(index, device, *wanted):
-    """Checks (tensor, name, dtype, shape) as ``_expect`` does, and returns the tensors' addresses: one pass, as the checks
-    of a small call take as long as its kernels."""
-    out = []
+_shape_of, _dtype_of = operator.attrgetter("shape"), operator.attrgetter("dtype")
+_device_of, _is_dense, _address_of = torch.Tensor.get_device, torch.Tensor.is_contiguous, torch.Tensor.data_ptr
+
+
+def _alike(index, wanted, tensors):
+    """Whether the tensors have the dtypes and shapes of wanted = (names, dtypes, shapes) and are on device ``index``.
+
+    Whole columns at once: the checks of a small call take as long as its kernels."""
     try:
-        for t, _, dtype, shape in wanted:
-            if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
-                break
-            out.append(t.data_ptr())
-        else:
-            return out
-    except AttributeError:
-        pass
-    for t, name, dtype, shape in wanted:
-        _expect(t, name, dtype, shape, device)
-    return [t.data_ptr() for t, _, _, _ in wanted]
+        return (tuple(map(_dtype_of, tensors)) == wanted[1] and tuple(map(_shape_of, tensors)) == wanted[2]
+                and set(map(_device_of, tensors)) == {index})
+    except (AttributeError, TypeError):
+        return False                      # not a tensor: the caller's check names it
+
+
+def _addresses(index, device, wanted, tensors):
+    """Checks tensors against wanted = (names, dtypes, shapes) as ``_expect`` does, and returns their addresses."""
+    if not _alike(index, wanted, tensors) or not all(map(_is_dense, tensors)):
+        for t, name, dtype, shape in zip(tensors, *wanted):
+            _expect(t, name, dtype, shape, device)
+    return list(map(_address_of, tensors))
+
+
+def _token_strides(index, device, wanted, rows):
+    """``_token_stride`` of rows [T, heads, dim]."""
+    if _alike(index, wanted, rows):
+        strides = [t.stride() for t in rows]
+        if all(s[2] == 1 and (s[1] == n or h == 1) for s, (_, h, n) in zip(strides, wanted[2])):
+            return [s[0] if T > 1 else h * n for s, (T, h, n) in zip(strides, wanted[2])]
+    return [_token_stride(t, name, dtype, shape, device) for t, name, dtype, shape in zip(rows, *wanted)]
 
 
 def _cuda_index(t):
@@ -1035,32 +1050,105 @@ def _cuda_index(t):
     return index
 
 
-@functools.lru_cache(maxsize=256)
 def _bytes_of(name, *sizes):
-    """A workspace size of the library, which depends on its arguments alone."""
+    """A workspace size of the library."""
     _int32(*sizes)
     return int(getattr(_load(), name)(*sizes))
 
 
-def _fp8_block_cache(pools, scales, hs, hn, d, dv):
-    """What ``_addresses`` is to check of an 8-bit cache with block scales, the rows of a page, the number of pages and
-    the tokens of a block."""
-    k1, k2, v = pools
-    s1, s2, s3 = scales
-    pages, size, _, _ = k1.shape
-    shape = getattr(s1, "shape", ())
+# What the calls over the 8-bit cache check of their tensors follows from sizes alone: worked out once for each set of
+# them, as (names, dtypes, shapes) with what else the call needs.
+_plan = functools.lru_cache(maxsize=256)
+
+
+def _blocks_of_a_page(scale):
+    shape = getattr(scale, "shape", ())
     if len(shape) != 3:
         raise ValueError("scales must be [num_pages, page_size / block, heads]")
-    per = shape[1]
+    return shape[1]
+
+
+def _fp8_block_cache(pages, size, per, hs, hn, d, dv, code):
+    """(name, dtype, shape) of the six tensors of an 8-bit cache with block scales, and the tokens of a block."""
     if per < 1 or size % per != 0:
         raise ValueError(f"pages of {size} rows do not hold {per} blocks of equal size")
-    if pages > 0x7fffffff or size > 0x7fffffff:
-        _int32(pages, size)
-    code = _FP8 if k1.dtype is _FP8 else torch.uint8
+    _int32(pages, size, hs, hn, d, dv)
     f32, sig, noise = torch.float32, (pages, per, hs), (pages, per, hn)
-    return ((k1, "k_sig codes", code, (pages, size, hs, d)), (k2, "k_noise codes", code, (pages, size, hn, d)),
-            (v, "v codes", code, (pages, size, hs, dv)), (s1, "k_sig_scale", f32, sig),
-            (s2, "k_noise_scale", f32, noise), (s3, "v_scale", f32, sig)), size, pages, size // per
+    return (("k_sig codes", code, (pages, size, hs, d)), ("k_noise codes", code, (pages, size, hn, d)),
+            ("v codes", code, (pages, size, hs, dv)), ("k_sig_scale", f32, sig), ("k_noise_scale", f32, noise),
+            ("v_scale", f32, sig)), size // per
+
+
+def _code_of(pool):
+    return _FP8 if pool.dtype is _FP8 else torch.uint8
+
+
+@_plan
+def _append_fp8_block_plan(T, hs, hn, d, dv, pages, size, per, code, bounds):
+    cache, block = _fp8_block_cache(pages, size, per, hs, hn, d, dv, code)
+    bf, i8 = torch.bfloat16, torch.int8
+    rows = (("k_sig", bf, (T, hs, d)), ("k_noise", bf, (T, hn, d)), ("v", bf, (T, hs, dv)))
+    rest = (("slot_map", torch.int32, (T,)), *cache)
+    if bounds:
+        rest += (("k_sig_bounds", i8, (pages, per, hs, 2, d)), ("k_noise_bounds", i8, (pages, per, hn, 2, d)))
+    return tuple(zip(*rows)), tuple(zip(*rest)), block, _bytes_of("gda_cache_append_fp8_block_workspace_size", T, pages, size)
+
+
+@_plan
+def _read_fp8_block_plan(T, hs, hn, d, dv, pages, size, per, code):
+    cache, block = _fp8_block_cache(pages, size, per, hs, hn, d, dv, code)
+    _int32(T)
+    bf = torch.bfloat16
+    out = (("out k_sig", bf, (T, hs, d)), ("out k_noise", bf, (T, hn, d)), ("out v", bf, (T, hs, dv)))
+    return tuple(zip(("slot_map", torch.int32, (T,)), *cache, *out)), block
+
+
+def _pages_of_sequences(block_table):
+    """The pages of a sequence, or None: contiguous caches are a page for each."""
+    if block_table is None:
+        return None
+    shape = getattr(block_table, "shape", None)
+    if shape is None:
+        raise TypeError("block_table must be a torch.Tensor")
+    if len(shape) != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    return shape[1]
+
+
+def _block_table(B, pages, max_pages):
+    """(name, dtype, shape) of a block table, or of none."""
+    if max_pages is not None:
+        _int32(max_pages)
+        return (("block_table", torch.int32, (B, max_pages)),)
+    if pages != B:
+        raise ValueError(f"caches hold {pages} sequences, expected {B}")
+    return ()
+
+
+@_plan
+def _block_select_plan(B, hs, hn, d, pages, per, max_pages, block, keep, first, last):
+    bf, i8, i32, f32 = torch.bfloat16, torch.int8, torch.int32, torch.float32
+    table = _block_table(B, pages, max_pages)
+    most = per * (max_pages if table else 1)
+    _int32(pages, per * block, keep, first, last, most, d)
+    wanted = (("q_sig", bf, (B, hs, d)), ("q_noise", bf, (B, hn, d)), ("k_sig_bounds", i8, (pages, per, hs, 2, d)),
+              ("k_noise_bounds", i8, (pages, per, hn, 2, d)), ("k_sig_scale", f32, (pages, per, hs)),
+              ("k_noise_scale", f32, (pages, per, hn)), *table, ("cache_lens", i32, (B,)),
+              ("block_list", i32, (B, hn, keep)), ("block_count", i32, (B,)))
+    return tuple(zip(*wanted)), _bytes_of("gda_block_select_workspace_size", B, most, hs, hn)
+
+
+@_plan
+def _decode_fp8_block_plan(B, hs, hn, d, dv, pages, size, per, code, max_pages, keep):
+    cache, block = _fp8_block_cache(pages, size, per, hs, hn, d, dv, code)
+    bf, i32 = torch.bfloat16, torch.int32
+    lists = ()
+    if keep is not None:
+        _int32(keep)
+        lists = (("block_list", i32, (B, hn, keep)), ("block_count", i32, (B,)))
+    wanted = (("q_sig", bf, (B, hs, d)), ("q_noise", bf, (B, hn, d)), *cache, *_block_table(B, pages, max_pages), *lists,
+              ("cache_lens", i32, (B,)), ("lam", torch.float32, (hs,)), ("out", bf, (B, hs, dv)))
+    return tuple(zip(*wanted)), block, _bytes_of("gda_attn_decode_fp8_block_workspace_size", B, hs, hn, d, dv)
 
 
 def gda_cache_append_fp8_block_workspace_size(T: int, num_pages: int, page_size: int) -> int:
@@ -1085,24 +1173,19 @@ def gda_cache_append_fp8_block(k_sig, k_noise, v, slot_map, k_sig_pool, k_noise_
     dev = k_sig.device
     if k_sig.dim() != 3 or k_noise.dim() != 3 or v.dim() != 3 or k_sig_pool.dim() != 4:
         raise ValueError("rows must be [T, heads, dim] and pools [num_pages, page_size, heads, dim]")
+    if (k_sig_bounds is None) != (k_noise_bounds is None):
+        raise ValueError("k_sig_bounds and k_noise_bounds are given both or not at all")
     T, hs, d = k_sig.shape
     hn, dv = k_noise.shape[1], v.shape[2]
-    bf = torch.bfloat16
-    strides = [_token_stride(t, n, bf, (T, h, dim), dev)
-               for t, n, h, dim in ((k_sig, "k_sig", hs, d), (k_noise, "k_noise", hn, d), (v, "v", hs, dv))]
-    cache, size, pages, block = _fp8_block_cache((k_sig_pool, k_noise_pool, v_pool), (k_sig_scale, k_noise_scale, v_scale),
-                                                 hs, hn, d, dv)
-    bounds = ()
-    if k_sig_bounds is not None and k_noise_bounds is not None:
-        i8, per = torch.int8, size // block
-        bounds = ((k_sig_bounds, "k_sig_bounds", i8, (pages, per, hs, 2, d)),
-                  (k_noise_bounds, "k_noise_bounds", i8, (pages, per, hn, 2, d)))
-    elif k_sig_bounds is not None or k_noise_bounds is not None:
-        raise ValueError("k_sig_bounds and k_noise_bounds are given both or not at all")
-    at = _addresses(index, dev, (slot_map, "slot_map", torch.int32, (T,)), *cache, *bounds)
+    pages, size, _, _ = k_sig_pool.shape
+    bounds = () if k_sig_bounds is None else (k_sig_bounds, k_noise_bounds)
+    rows, rest, block, need = _append_fp8_block_plan(T, hs, hn, d, dv, pages, size, _blocks_of_a_page(k_sig_scale),
+                                                     _code_of(k_sig_pool), len(bounds))
+    strides = _token_strides(index, dev, rows, (k_sig, k_noise, v))
+    at = _addresses(index, dev, rest, (slot_map, k_sig_pool, k_noise_pool, v_pool, k_sig_scale, k_noise_scale, v_scale,
+                                       *bounds))
     if not bounds:
         at += (None, None)
-    need = _bytes_of("gda_cache_append_fp8_block_workspace_size", T, pages, size)
     if workspace is not None or need:
         workspace = _workspace(workspace, need, dev)
         space = (workspace.data_ptr(), workspace.numel())
@@ -1126,40 +1209,20 @@ def gda_cache_read_fp8_block(slot_map, k_sig_pool, k_noise_pool, v_pool, k_sig_s
     if slot_map.dim() != 1 or k_sig_pool.dim() != 4 or k_noise_pool.dim() != 4 or v_pool.dim() != 4:
         raise ValueError("slot_map must be 1-D and pools [num_pages, page_size, heads, dim]")
     T = slot_map.numel()
-    _int32(T)
-    _, _, hs, d = k_sig_pool.shape
+    pages, size, hs, d = k_sig_pool.shape
     hn, dv = k_noise_pool.shape[2], v_pool.shape[3]
-    cache, size, pages, block = _fp8_block_cache((k_sig_pool, k_noise_pool, v_pool), (k_sig_scale, k_noise_scale, v_scale),
-                                                 hs, hn, d, dv)
-    bf = torch.bfloat16
-    k1, k2, v = (T, hs, d), (T, hn, d), (T, hs, dv)
+    wanted, block = _read_fp8_block_plan(T, hs, hn, d, dv, pages, size, _blocks_of_a_page(k_sig_scale),
+                                         _code_of(k_sig_pool))
     if out is None:
-        out = (torch.empty(k1, dtype=bf, device=dev), torch.empty(k2, dtype=bf, device=dev),
-               torch.empty(v, dtype=bf, device=dev))
+        bf = torch.bfloat16
+        out = (torch.empty((T, hs, d), dtype=bf, device=dev), torch.empty((T, hn, d), dtype=bf, device=dev),
+               torch.empty((T, hs, dv), dtype=bf, device=dev))
     else:
         out = _given(out, 3, "out")
-    at = _addresses(index, dev, (slot_map, "slot_map", torch.int32, (T,)), *cache, (out[0], "out k_sig", bf, k1),
-                    (out[1], "out k_noise", bf, k2), (out[2], "out v", bf, v))
+    at = _addresses(index, dev, wanted, (slot_map, k_sig_pool, k_noise_pool, v_pool, k_sig_scale, k_noise_scale, v_scale,
+                                         *out))
     _enqueue(_load().gda_cache_read_fp8_block, "gda 8-bit block cache read", dev, *at, T, pages, size, block, hs, hn, d, dv)
     return tuple(out)
-
-
-def _pages_of_sequences(block_table, pages, B):
-    """What ``_addresses`` is to check of a block table, and its pages a sequence; contiguous caches are a page for each
-    sequence."""
-    if block_table is None:
-        if pages != B:
-            raise ValueError(f"caches hold {pages} sequences, expected {B}")
-        return (), 1
-    shape = getattr(block_table, "shape", None)
-    if shape is None:
-        raise TypeError("block_table must be a torch.Tensor")
-    if len(shape) != 2:
-        raise ValueError("block_table must be [B, max_pages]")
-    max_pages = shape[1]
-    if max_pages > 0x7fffffff:
-        _int32(max_pages)
-    return ((block_table, "block_table", torch.int32, (B, max_pages)),), max_pages
 
 
 def gda_block_select_workspace_size(B: int, max_blocks: int, h_s: int, h_n: int) -> int:
@@ -1188,29 +1251,24 @@ def gda_block_select(q_sig, q_noise, k_sig_bounds, k_noise_bounds, k_sig_scale, 
     B, hs, d = q_sig.shape
     hn = q_noise.shape[1]
     pages, per, _, _, _ = k_sig_bounds.shape
-    bf, i8, i32, f32 = torch.bfloat16, torch.int8, torch.int32, torch.float32
-    table, max_pages = _pages_of_sequences(block_table, pages, B)
-    _int32(pages, per * block, keep, first, last, max_pages * per)
+    max_pages = _pages_of_sequences(block_table)
+    wanted, need = _block_select_plan(B, hs, hn, d, pages, per, max_pages, block, keep, first, last)
     if out is None:
+        i32 = torch.int32
         out = (torch.empty((B, hn, keep), dtype=i32, device=dev), torch.empty((B,), dtype=i32, device=dev))
     else:
         out = _given(out, 2, "out")
-    at = _addresses(index, dev, (q_sig, "q_sig", bf, (B, hs, d)), (q_noise, "q_noise", bf, (B, hn, d)),
-                    (k_sig_bounds, "k_sig_bounds", i8, (pages, per, hs, 2, d)),
-                    (k_noise_bounds, "k_noise_bounds", i8, (pages, per, hn, 2, d)),
-                    (k_sig_scale, "k_sig_scale", f32, (pages, per, hs)),
-                    (k_noise_scale, "k_noise_scale", f32, (pages, per, hn)), *table,
-                    (cache_lens, "cache_lens", i32, (B,)), (out[0], "block_list", i32, (B, hn, keep)),
-                    (out[1], "block_count", i32, (B,)))
+    table = () if block_table is None else (block_table,)
+    at = _addresses(index, dev, wanted, (q_sig, q_noise, k_sig_bounds, k_noise_bounds, k_sig_scale, k_noise_scale, *table,
+                                         cache_lens, *out))
     if not table:
         at.insert(6, None)
-    need = _bytes_of("gda_block_select_workspace_size", B, max_pages * per, hs, hn)
     if workspace is not None or need:
         workspace = _workspace(workspace, need, dev)
         space = (workspace.data_ptr(), workspace.numel())
     else:
         space = (None, 0)
-    _enqueue(_load().gda_block_select, "gda block selection", dev, *at, B, max_pages, per * block, pages, block, keep,
+    _enqueue(_load().gda_block_select, "gda block selection", dev, *at, B, max_pages if table else 1, per * block, pages, block, keep,
              first, last, hs, hn, d, *space)
     return tuple(out)
 
@@ -1227,23 +1285,21 @@ def _decode_fp8_block(q_sig, q_noise, pools, scales, block_table, lists, cache_l
         raise ValueError("bad ranks: q [B, heads, d], caches [.., .., heads, dim]")
     B, hs, d = q_sig.shape
     hn, dv = q_noise.shape[1], pools[2].shape[3]
-    bf, i32 = torch.bfloat16, torch.int32
-    cache, size, pages, block = _fp8_block_cache(pools, scales, hs, hn, d, dv)
-    table, max_pages = _pages_of_sequences(block_table, pages, B)
-    if out is None:
-        out = torch.empty((B, hs, dv), dtype=bf, device=dev)
-    keep = 0
+    pages, size, _, _ = pools[0].shape
+    max_pages = _pages_of_sequences(block_table)
+    keep = None
     if lists is not None:
         shape = getattr(lists[0], "shape", ())
         if len(shape) != 3:
             raise ValueError("block_list must be [B, h_n, keep]")
         keep = shape[2]
-        _int32(keep)
-        lists = ((lists[0], "block_list", i32, (B, hn, keep)), (lists[1], "block_count", i32, (B,)))
-    at = _addresses(index, dev, (q_sig, "q_sig", bf, (B, hs, d)), (q_noise, "q_noise", bf, (B, hn, d)), *cache, *table,
-                    *(lists or ()), (cache_lens, "cache_lens", i32, (B,)), (lam, "lam", torch.float32, (hs,)),
-                    (out, "out", bf, (B, hs, dv)))
-    workspace = _workspace(workspace, _bytes_of("gda_attn_decode_fp8_block_workspace_size", B, hs, hn, d, dv), dev)
+    wanted, block, need = _decode_fp8_block_plan(B, hs, hn, d, dv, pages, size, _blocks_of_a_page(scales[0]),
+                                                 _code_of(pools[0]), max_pages, keep)
+    if out is None:
+        out = torch.empty((B, hs, dv), dtype=torch.bfloat16, device=dev)
+    table = () if block_table is None else (block_table,)
+    at = _addresses(index, dev, wanted, (q_sig, q_noise, *pools, *scales, *table, *(lists or ()), cache_lens, lam, out))
+    workspace = _workspace(workspace, need, dev)
     at.insert(-1, float(lambda_init))
     tail = (hs, hn, d, dv, float(eps), workspace.data_ptr(), workspace.numel())
     what = "gda decode (8-bit block cache)"
@@ -1251,7 +1307,8 @@ def _decode_fp8_block(q_sig, q_noise, pools, scales, block_table, lists, cache_l
     if lists is not None:
         if not table:
             at.insert(8, None)
-        _enqueue(lib.gda_attn_decode_sparse_fp8_block, what, dev, *at, B, max_pages, size, pages, block, keep, *tail)
+        _enqueue(lib.gda_attn_decode_sparse_fp8_block, what, dev, *at, B, max_pages if table else 1, size, pages,
+                 block, keep, *tail)
     elif not table:
         _enqueue(lib.gda_attn_decode_fp8_block, what, dev, *at, B, size, block, *tail)
     else:
