@@ -564,7 +564,8 @@ size_t gda_attn_decode_fp4_workspace_size(int B, int h_s, int h_n, int d, int dv
  * written here are powers of two.
  *   bounds [slots / block, heads, 2, d] int8, of K_sig and K_noise: the
  *     greatest of ceil(code / 4) and the least of floor(code / 4) over the
- *     rows written to the block, for every channel (-128 and 127: none).
+ *     rows written to the block, for every channel (-128 and 127: none; a
+ *     growing scale rounds these outwards like the others).
  *
  * gda_cache_append_fp8_block writes T tokens' rows (bf16, `*_stride` elements
  * between tokens, a multiple of 8) to the slots slot_map[T] (int32; negative:
