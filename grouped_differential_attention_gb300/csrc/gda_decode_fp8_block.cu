@@ -2,13 +2,14 @@
 // for each block of tokens and head (one new query token per sequence; format
 // in gda_fp8_block.cuh), contiguous or paged, over all positions of a sequence
 // or over the blocks that a list names; split over the cache length, plus a
-// pass that joins the parts.
+// pass that joins the parts.  Short sequences take one launch: a cluster of
+// thread blocks to each and unit of heads, joined through shared memory.
 //
 // The batch's positions, sequence after sequence, each rounded up to whole
 // tiles of 16 (of a list: count * block), are cut into equal contiguous
 // ranges.  A warp, which is a block of threads of its own, takes one range for
 // one noise head and up to RH signal heads that share it: it copies a tile at a
-// time into a ring in shared memory (cp.async) and keeps the online softmax of
+// time into a ring in shared memory (TMA) and keeps the online softmax of
 // all its maps and the accumulators O1, O2 in registers.  A tile lies in one
 // block of tokens, so its rows follow one another in the cache and every head
 // has one scale.  Each part of a range that lies in one sequence leaves (m, l)
@@ -37,12 +38,14 @@
 // Measured (both kernels; of the 6793 GB/s of a copy): 64 sequences of 4096 to
 // 8192, 12 + 4 heads of 64/128, 1007 MB: 157 us (95 %); one of 131072, 24 + 8
 // heads, 671 MB: 109 us (91 %); 16 of up to 8191, 16 + 4 heads of 128/256, 437
-// MB: 73 us (88 %); 16 listed blocks of 64 of each of the 64 sequences, 168 MB:
-// 38 us (66 %).  About 10 us of each are fixed: the chain of lengths, list, table
-// and first tile (3), the joining (3), and two launches.  Copies alone take 95 %
-// of the time.  By cp.async, a lane's 16 bytes each, the first two took 166 and
-// 115 us: their issue was what the warps waited for.
+// MB: 73 us (88 %); 16 listed blocks of 64 of each of the 64 sequences, 168 MB,
+// one launch: 33 us (77 %; in two launches 38).  About 10 us of two launches are
+// fixed: the chain of lengths, list, table and first tile (3), the joining (3),
+// and the launches.  Copies alone take 95 % of the time.  By cp.async, a lane's
+// 16 bytes each, the first two took 166 and 115 us: their issue was what the
+// warps waited for.
 #include <cuda_bf16.h>
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <algorithm>
 #include <cmath>
@@ -54,11 +57,14 @@
 #include "gda_fp8_block.cuh"
 #include "gda_internal.h"
 
+namespace cg = cooperative_groups;
+
 namespace gda {
 namespace {
 
 constexpr int kTile = 16;              // positions of a tile
 constexpr float kWeightBits = 15.f;    // weights carry a factor 2^15: the largest is within f16, the smallest far from its end
+constexpr int kOneWarps = 8;           // at most, of a sequence in one launch
 constexpr float kLowest = -3.0e38f;    // a maximum over no position
 
 // Signal heads of a warp: a noise head's group in equal parts of at most three
@@ -320,6 +326,8 @@ struct Stage {
     static_assert(count >= 2 && NH <= 4, "a tile is copied while another is used; four scales of K, three of V");
     static constexpr int queries = count * bytes, weights = queries + NH * D * 2, scales = weights + RH * 128;
     static constexpr int bars = scales + kMaxStages * 32, total = bars + kMaxStages * 8 + 1024;
+    static constexpr int pitch = (bars + kMaxStages * 8 + 1023) / 1024 * 1024;   // of the warps of one block of threads
+    static_assert(RH * (2 * DV * 4 + 16) <= count * bytes, "what a warp leaves has room in its ring");
     static constexpr int warps = warps_per_sm(RH, D, DV);
 };
 
@@ -373,29 +381,21 @@ struct Queries {
     }
 };
 
-// One warp: split u / units of the range, unit u % units = (noise head, part of its group).
-template <int D, int DV, int RH, bool LISTED>
-__global__ void __launch_bounds__(32, (Stage<D, DV, RH>::warps)) gda_decode_fp8_block_split_kernel(
-    const Params p, const __grid_constant__ Maps maps) {
+// What a warp of RH heads from h0 on has come to, in its shared memory: sums [RH][2][DV], then m1, l1, m2, l2 of each.
+template <int DV, int RH>
+__device__ __forceinline__ float *left_sums(uint8_t *smem) { return reinterpret_cast<float *>(smem); }
+template <int DV, int RH>
+__device__ __forceinline__ float4 *left_stats(uint8_t *smem) { return reinterpret_cast<float4 *>(smem + RH * 2 * DV * 4); }
+
+// The tiles of `range` (one at least) for noise head g and the signal heads from h0 on, `done` of which others do too.
+// ONE: they are of one sequence, and what they come to is left in shared memory, else in slot split + sequence.
+template <int D, int DV, int RH, bool LISTED, bool ONE>
+__device__ __forceinline__ void run_range(const Params &p, const Maps &maps, const Range &range, uint8_t *const smem,
+                                          const int split, const int g, const int h0, const int done) {
     using S = Stage<D, DV, RH>;
     constexpr int NH = S::NH, SLABS = DV < 128 ? 1 : DV / 128, WORDS = DV < 128 ? 2 : 4, A = S::count - 1;
-    extern __shared__ __align__(1024) uint8_t raw[];
-    uint8_t *const smem = raw + (-smem_u32(raw) & 1023u);
-    const int lane = threadIdx.x, quad = lane >> 2, t = lane & 3;
+    const int lane = threadIdx.x & 31, quad = lane >> 2, t = lane & 3;
     const uint32_t ring = smem_u32(smem);
-    const int units = p.hn * p.parts, u = blockIdx.x;
-    const int split = u / units, g = (u % units) / p.parts, part = u % p.parts;
-    // every part is RH heads: the last begins early where they do not divide the group, and leaves what the parts
-    // before it have done unwritten
-    const int r = p.hs / p.hn, begin = min(part * RH, r - RH), done = part * RH - begin, h0 = g * r + begin;
-    // a programmatic dependent of whatever is ahead in the stream: nothing is read or written before that has completed
-    if (lane < S::count) mbar_init(reinterpret_cast<uint64_t *>(smem + S::bars) + lane, 1);
-    fence_mbar_init();
-    __syncwarp();
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    Range range;
-    if (!range_of<LISTED>(p, split, range)) return;
-
     Cursor use{range.b, 0, 0, range.end - range.start};
     enter(use, range.start - range.before, range.span.tiles);
     Cursor get = use;                                    // the copies' place, ahead of the arithmetic's
@@ -403,7 +403,6 @@ __global__ void __launch_bounds__(32, (Stage<D, DV, RH>::warps)) gda_decode_fp8_
     Place next = place_of<LISTED>(p, get.b, g, get.tile, get_len);
     Queries<D, RH> q;
     q.fetch(p, use.b, h0, g);
-    if (u % units == 0) note_sequences<LISTED>(p, range, split);
 
     // scales of a tile: lanes 0 .. RH of K, 4 .. RH + 3 of V
     const int j_of = lane & 3, which = lane >= 4 ? 2 : (j_of < RH ? 0 : 1);
@@ -584,6 +583,7 @@ __global__ void __launch_bounds__(32, (Stage<D, DV, RH>::warps)) gda_decode_fp8_
     };
     // Leaves what the part that lies in sequence b has come to.
     auto leave = [&](int b) {
+        if constexpr (ONE) __syncwarp();                 // it goes to where the tiles were
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
         l *= 0x1p-15f;
@@ -595,8 +595,10 @@ __global__ void __launch_bounds__(32, (Stage<D, DV, RH>::warps)) gda_decode_fp8_
             const float v = __shfl_sync(0xffffffffu, v_most, j) * 0x1p-15f;
             if (j < done) continue;
             const size_t place = slot * p.hs + h0 + j;
-            if (lane == 0) reinterpret_cast<float4 *>(p.ws_ml)[place] = make_float4(mj, lj, mn, ln);
-            float *o = p.ws_o + (place * 2 + (t & 1)) * DV + 4 * WORDS * quad + 2 * (t >> 1);
+            float4 *const stats = ONE ? left_stats<DV, RH>(smem) + j : reinterpret_cast<float4 *>(p.ws_ml) + place;
+            if (lane == 0) *stats = make_float4(mj, lj, mn, ln);
+            float *const o = (ONE ? left_sums<DV, RH>(smem) + j * 2 * DV : p.ws_o + place * 2 * DV) + (t & 1) * DV +
+                             4 * WORDS * quad + 2 * (t >> 1);
 #pragma unroll
             for (int i = 0; i < SLABS * WORDS; ++i) {
                 const float(&c)[4] = acc[j][i];
@@ -657,6 +659,167 @@ __global__ void __launch_bounds__(32, (Stage<D, DV, RH>::warps)) gda_decode_fp8_
     }
 }
 
+// One warp: split u / units of the range, unit u % units = (noise head, part of its group).
+template <int D, int DV, int RH, bool LISTED>
+__global__ void __launch_bounds__(32, (Stage<D, DV, RH>::warps)) gda_decode_fp8_block_split_kernel(
+    const Params p, const __grid_constant__ Maps maps) {
+    using S = Stage<D, DV, RH>;
+    extern __shared__ __align__(1024) uint8_t raw[];
+    uint8_t *const smem = raw + (-smem_u32(raw) & 1023u);
+    const int lane = threadIdx.x, units = p.hn * p.parts, u = blockIdx.x;
+    const int split = u / units, g = (u % units) / p.parts, part = u % p.parts;
+    // every part is RH heads: the last begins early where they do not divide the group, and leaves what the parts
+    // before it have done unwritten
+    const int r = p.hs / p.hn, begin = min(part * RH, r - RH), done = part * RH - begin, h0 = g * r + begin;
+    // a programmatic dependent of whatever is ahead in the stream: nothing is read or written before that has completed
+    if (lane < S::count) mbar_init(reinterpret_cast<uint64_t *>(smem + S::bars) + lane, 1);
+    fence_mbar_init();
+    __syncwarp();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    Range range;
+    if (!range_of<LISTED>(p, split, range)) return;
+    if (u % units == 0) note_sequences<LISTED>(p, range, split);
+    run_range<D, DV, RH, LISTED, false>(p, maps, range, smem, split, g, h0, done);
+}
+
+// The statistics and sums of parts joined one after the other: a warp to a head, COLS of each map's columns to a lane.
+template <int COLS>
+struct Joined {
+    float4 stats = make_float4(kLowest, 0.f, kLowest, 0.f);
+    float o1[COLS] = {}, o2[COLS] = {};
+
+    // sums: this lane's columns of the first map, those of the second DV behind them
+    __device__ __forceinline__ void add(const float4 s, const float *sums, int dv) {
+        const float t1 = fmaxf(stats.x, s.x), t2 = fmaxf(stats.z, s.z);
+        const float f1 = fast_exp2(stats.x - t1), g1 = fast_exp2(s.x - t1), f2 = fast_exp2(stats.z - t2), g2 = fast_exp2(s.z - t2);
+        stats = make_float4(t1, fmaf(s.y, g1, stats.y * f1), t2, fmaf(s.w, g2, stats.w * f2));
+#pragma unroll
+        for (int i = 0; i < COLS; i += 2) {
+            const float2 x = *reinterpret_cast<const float2 *>(sums + i), y = *reinterpret_cast<const float2 *>(sums + dv + i);
+            o1[i] = fmaf(x.x, g1, o1[i] * f1), o1[i + 1] = fmaf(x.y, g1, o1[i + 1] * f1);
+            o2[i] = fmaf(y.x, g2, o2[i] * f2), o2[i + 1] = fmaf(y.y, g2, o2[i + 1] * f2);
+        }
+    }
+};
+
+// The row of sequence b and head h, by a whole warp.
+template <int COLS>
+__device__ __forceinline__ void write_row(const Params &p, Joined<COLS> &sum, int b, int h) {
+    constexpr int DV = 32 * COLS;
+    const int lane = threadIdx.x & 31;
+    uint32_t *const out = reinterpret_cast<uint32_t *>(p.out + (static_cast<size_t>(b) * p.hs + h) * DV) + lane * COLS / 2;
+    if (sum.stats.y == 0.f) {                                // no position (a NaN is not 0)
+#pragma unroll
+        for (int i = 0; i < COLS; i += 2) out[i / 2] = 0u;
+        return;
+    }
+    const float i1 = 1.f / sum.stats.y, i2 = p.lambda[h] / sum.stats.w;
+    float v[COLS], ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < COLS; ++i) v[i] = sum.o1[i] * i1 - sum.o2[i] * i2, ss = fmaf(v[i], v[i], ss);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float y = (1.f - p.lambda_init) * rsqrtf(ss * (1.f / DV) + p.eps);
+#pragma unroll
+    for (int i = 0; i < COLS; i += 2) out[i / 2] = pack_bf16x2(v[i] * y, v[i + 1] * y);
+}
+
+// grid (units x ranks, B): a cluster of `ranks` blocks of threads to a sequence and unit, their warps to equal parts of
+// the tiles, joined in shared memory, first within a block and then by the cluster's first.  One launch instead of two,
+// for short sequences.
+template <int D, int DV, int RH, bool LISTED>
+__global__ void __launch_bounds__(32 * kOneWarps, 1) gda_decode_fp8_block_one_kernel(const Params p,
+                                                                                     const __grid_constant__ Maps maps) {
+    using S = Stage<D, DV, RH>;
+    constexpr int COLS = DV / 32;                            // of a lane, in joining
+    extern __shared__ __align__(1024) uint8_t raw[];
+    __shared__ __align__(16) float joined[RH][2 * DV];
+    __shared__ float4 joined_stats[RH];
+    const cg::cluster_group cluster = cg::this_cluster();
+    const int rank = static_cast<int>(cluster.block_rank()), ranks = static_cast<int>(cluster.num_blocks());
+    uint8_t *const all = raw + (-smem_u32(raw) & 1023u);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, b = blockIdx.y;
+    const int u = blockIdx.x / ranks, g = u / p.parts, part = u % p.parts;
+    const int r = p.hs / p.hn, begin = min(part * RH, r - RH), done = part * RH - begin, h0 = g * r + begin;
+    uint8_t *const smem = all + warp * S::pitch;
+    if (lane < S::count) mbar_init(reinterpret_cast<uint64_t *>(smem + S::bars) + lane, 1);
+    fence_mbar_init();
+    __syncwarp();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Span span = span_of<LISTED>(p, b);
+    const int per = (span.tiles + warps * ranks - 1) / (warps * ranks);
+    const int first = rank * warps * per, used = per > 0 ? min(warps, max(0, (span.tiles - first + per - 1) / per)) : 0;
+    if (warp < used) {
+        const int start = first + warp * per;
+        const Range range{start, min(span.tiles, start + per), per, 0, b, span};
+        run_range<D, DV, RH, LISTED, true>(p, maps, range, smem, 0, g, h0, done);
+    }
+    __syncthreads();
+    for (int j = done + warp; j < RH; j += warps) {          // (four warps at least: one round)
+        Joined<COLS> sum;
+        for (int c = 0; c < used; ++c) {
+            uint8_t *const left = all + c * S::pitch;
+            sum.add(left_stats<DV, RH>(left)[j], left_sums<DV, RH>(left) + j * 2 * DV + lane * COLS, DV);
+        }
+        if (ranks > 1) {
+            if (lane == 0) joined_stats[j] = sum.stats;
+#pragma unroll
+            for (int i = 0; i < COLS; i += 2) {
+                *reinterpret_cast<float2 *>(&joined[j][lane * COLS + i]) = make_float2(sum.o1[i], sum.o1[i + 1]);
+                *reinterpret_cast<float2 *>(&joined[j][DV + lane * COLS + i]) = make_float2(sum.o2[i], sum.o2[i + 1]);
+            }
+            continue;
+        }
+        write_row<COLS>(p, sum, b, h0 + j);
+    }
+    if (ranks == 1) return;
+    cluster.sync();
+    if (rank == 0)
+        for (int j = done + warp; j < RH; j += warps) {
+            Joined<COLS> sum;
+#pragma unroll 4
+            for (int c = 0; c < ranks; ++c)
+                sum.add(*cluster.map_shared_rank(&joined_stats[j], c), cluster.map_shared_rank(&joined[j][lane * COLS], c), DV);
+            write_row<COLS>(p, sum, b, h0 + j);
+        }
+    cluster.sync();                                          // no block goes while its sums are read
+}
+
+// Blocks of threads of a cluster and warps of a block for a sequence in one launch; ranks = 0: two launches.  `fit`: warps
+// that an SM holds.
+//
+// Both are estimated in us, from the room in the block table or the lists, as the lengths are on the device (lists are
+// taken to be full, caches for three quarters): two launches cost kTwoFixed and kStep for each step of their equal
+// ranges; one costs kOneFixed, kWave for each further wave of blocks of threads, and for each step of a warp kOneStep, its
+// tile's latency, or what the bytes take if that is more.  2 us of kTwoFixed stand for the host's 4 to 5.  us of a call from Python (graph replay, inputs in HBM), one / two
+// launches, 12 + 4 heads of 64/128: one sequence of 256 23 (13.4) / 27 (14.5); 16 of 512 24 (17.5) / 29 (19.6), of 2048 23
+// (30) / 28 (32); 64 of 256 23 (20) / 27 (24), of 512 24 (28) / 27 (32), of 1 to 1024 28 (36) / 27 (34), of 2048 57 (75) /
+// 61 (81); 256 of 512 74 (87) / 67 (87); lists of 16 blocks of 64 for 64 sequences 32.6 (46) / 37.8 (54).  Sixteen clusters
+// of eight do not run at once: four sequences of 1024 took 21.6 with those and 17.5 with two launches.
+constexpr double kTwoFixed = 12.3, kOneFixed = 7.5, kOneCluster = 1.0, kWave = 2.0, kStep = 1.9, kOneStep = 1.5;
+struct OneLaunch {
+    int ranks = 0, warps = 0;
+};
+OneLaunch one_launch(const Params &p, int fit) {
+    const long long reach = p.list != nullptr ? static_cast<long long>(p.keep) << p.shift : (p.Lcap + kTile - 1) / kTile;
+    const long long blocks = static_cast<long long>(p.hn) * p.parts * p.B;
+    const double bytes = kStep * (p.list != nullptr ? 1.0 : 0.75) * static_cast<double>(blocks) * reach / (kSms * fit);
+    OneLaunch best;
+    double least = kTwoFixed + bytes;
+    for (int ranks = 1; ranks <= 8; ranks *= 2) {
+        if (ranks > 1 && blocks * ranks > (ranks == 8 ? 64 : 128)) break;
+        for (const int warps : {4, std::min(fit, kOneWarps)}) {
+            if (warps < 4 || warps > fit) continue;
+            const long long at_once = static_cast<long long>(kSms) * (fit / warps);
+            const long long waves = (blocks * ranks + at_once - 1) / at_once, steps = (reach + warps * ranks - 1) / (warps * ranks);
+            const double us = kOneFixed + (ranks > 1 ? kOneCluster : 0.0) + kWave * static_cast<double>(waves - 1) +
+                              std::max(kOneStep * static_cast<double>(waves * steps), bytes);
+            if (us < least) least = us, best = {ranks, warps};
+        }
+    }
+    return best;
+}
+
 // Rows of `heads` heads of n bytes each, in boxes of (at most 128 bytes) x 16 cache rows x `box` of those.
 // Where noise heads list blocks of their own, no other warp reads what lies beside a head's part of a row, so L2 is to
 // fetch no more than that.
@@ -670,41 +833,59 @@ bool encode(CUtensorMap *map, const uint8_t *base, int n, int heads, long long r
 }
 
 template <int D, int DV, int RH, bool LISTED>
-cudaError_t launch_split(const Params &p, cudaStream_t stream) {
+cudaError_t launch(const Params &p, cudaStream_t stream) {
     using S = Stage<D, DV, RH>;
-    constexpr auto kern = gda_decode_fp8_block_split_kernel<D, DV, RH, LISTED>;
+    constexpr auto split = gda_decode_fp8_block_split_kernel<D, DV, RH, LISTED>;
+    constexpr auto one = gda_decode_fp8_block_one_kernel<D, DV, RH, LISTED>;
     Maps maps;
     const long long rows = static_cast<long long>(p.num_pages) * p.page_size;
     constexpr int KS = D == 64 ? 0 : 128, VS = DV == 64 ? 64 : 128;
     if (!encode(&maps.k1, p.k1c, D, p.hs, rows, RH, KS, LISTED) || !encode(&maps.k2, p.k2c, D, p.hn, rows, 1, KS, LISTED) ||
         !encode(&maps.v, p.vc, DV, p.hs, rows, RH, VS, LISTED))
         return cudaErrorInvalidValue;
-    const cudaError_t e = allow_shared_memory<kern>(S::total);
-    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(p.splits * p.hn * p.parts);
-    cfg.blockDim = dim3(32);
-    cfg.dynamicSmemBytes = S::total;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, p, maps);
+    if (const OneLaunch w = one_launch(p, S::warps); w.ranks > 0) {
+        constexpr int most = S::warps < kOneWarps ? S::warps : kOneWarps;
+        static_assert(most * S::pitch + 1024 + RH * (2 * DV * 4 + 16) + 64 <= 227 * 1024, "a block of threads fits an SM");
+        const cudaError_t e = allow_shared_memory<one>(most * S::pitch + 1024);
+        if (e != cudaSuccess) return e;
+        cfg.gridDim = dim3(p.hn * p.parts * w.ranks, p.B);
+        cfg.blockDim = dim3(32 * w.warps);
+        cfg.dynamicSmemBytes = w.warps * S::pitch + 1024;
+        if (w.ranks > 1) {
+            attr[1].id = cudaLaunchAttributeClusterDimension;
+            attr[1].val.clusterDim.x = w.ranks;
+            attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+            cfg.numAttrs = 2;
+        }
+        return cudaLaunchKernelEx(&cfg, one, p, maps);
+    }
+    cudaError_t e = allow_shared_memory<split>(S::total);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(p.splits * p.hn * p.parts);
+    cfg.blockDim = dim3(32);
+    cfg.dynamicSmemBytes = S::total;
+    e = cudaLaunchKernelEx(&cfg, split, p, maps);
+    return e == cudaSuccess ? launch_join<DV>(p, stream) : e;
 }
 
 template <int D, int DV, int RH>
-cudaError_t launch_split(const Params &p, cudaStream_t stream) {
-    return p.list != nullptr ? launch_split<D, DV, RH, true>(p, stream) : launch_split<D, DV, RH, false>(p, stream);
+cudaError_t launch(const Params &p, cudaStream_t stream) {
+    return p.list != nullptr ? launch<D, DV, RH, true>(p, stream) : launch<D, DV, RH, false>(p, stream);
 }
 
 template <int D, int DV>
-cudaError_t launch_split(const Params &p, int rh, cudaStream_t stream) {
-    if (rh == 1) return launch_split<D, DV, 1>(p, stream);
+cudaError_t launch(const Params &p, int rh, cudaStream_t stream) {
+    if (rh == 1) return launch<D, DV, 1>(p, stream);
     if constexpr (DV < 256)
-        if (rh == 3) return launch_split<D, DV, 3>(p, stream);
-    return launch_split<D, DV, 2>(p, stream);
+        if (rh == 3) return launch<D, DV, 3>(p, stream);
+    return launch<D, DV, 2>(p, stream);
 }
 
 }  // namespace
@@ -732,18 +913,14 @@ int launch_decode_fp8_block(const DecodeFp8BlockArgs &a, cudaStream_t stream) {
                    a.num_pages, shift, page_factor, page_shift, a.list, a.count, a.keep};
     cudaError_t e = cudaErrorInvalidValue;
     switch (a.d * 1000 + a.dv) {
-        case 64064: e = launch_split<64, 64>(p, pl.heads.each, stream); break;
-        case 64128: e = launch_split<64, 128>(p, pl.heads.each, stream); break;
-        case 64256: e = launch_split<64, 256>(p, pl.heads.each, stream); break;
-        case 128064: e = launch_split<128, 64>(p, pl.heads.each, stream); break;
-        case 128128: e = launch_split<128, 128>(p, pl.heads.each, stream); break;
-        case 128256: e = launch_split<128, 256>(p, pl.heads.each, stream); break;
+        case 64064: e = launch<64, 64>(p, pl.heads.each, stream); break;
+        case 64128: e = launch<64, 128>(p, pl.heads.each, stream); break;
+        case 64256: e = launch<64, 256>(p, pl.heads.each, stream); break;
+        case 128064: e = launch<128, 64>(p, pl.heads.each, stream); break;
+        case 128128: e = launch<128, 128>(p, pl.heads.each, stream); break;
+        case 128256: e = launch<128, 256>(p, pl.heads.each, stream); break;
         default: return GDA_ERR_UNSUPPORTED;
     }
-    if (e != cudaSuccess) return record_cuda_error(e);
-    e = a.dv == 64    ? launch_join<64>(p, stream)
-        : a.dv == 128 ? launch_join<128>(p, stream)
-                      : launch_join<256>(p, stream);
     return e == cudaSuccess ? GDA_OK : record_cuda_error(e);
 }
 

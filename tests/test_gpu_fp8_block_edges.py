@@ -109,3 +109,27 @@ def test_the_most_sequences():
     check_select(one, 2)
     again = gda.gda_block_select(few["q1"], few["q2"], *bounds, *c["scales"][:2], few["lens"], 16, 2, block_table=few["table"])
     assert torch.equal(again[0], lists[0][some]) and torch.equal(again[1], lists[1][some])
+
+
+@pytest.mark.parametrize("d,dv", [(64, 64), (64, 128), (64, 256), (128, 64), (128, 128), (128, 256)])
+@pytest.mark.parametrize("hs,hn", [(1, 1), (3, 1), (4, 2), (12, 4), (5, 1), (7, 7), (16, 4)])
+def test_short_lengths_in_caches_that_may_be_long(hs, hn, d, dv):
+    """The same rows where the block table and the lists leave room for many more: what is chosen by the room alone."""
+    lens = [1, 0, 15, 16, 17, 33, 64, 128, 200, 7]
+    c = make(len(lens), 208, hs, hn, d, dv, lens, seed=hs + d + dv, page=48, powers=hs != 4)
+    room = {"table": torch.cat((c["table"], torch.zeros(len(lens), 3000, dtype=torch.int32, device="cuda")), 1).contiguous()}
+    check(run(c | room), c)
+    ids, counts = pick(c, 5, seed=hs)
+    wide = torch.cat((ids, torch.full((*ids.shape[:2], 9000), -1, dtype=torch.int32, device="cuda")), 2).contiguous()
+    check(run(c | {"lists": (wide, counts)}), c | {"lists": (ids, counts)})
+    check(run(c | {"lists": (ids, counts)}), c | {"lists": (ids, counts)})
+
+
+@pytest.mark.parametrize("B,Lcap", [(1, 128), (1, 1100), (1, 3000), (3, 700), (5, 2100), (17, 600), (40, 1000), (130, 300), (300, 100)])
+def test_lengths_up_to_the_room(B, Lcap):
+    """Batches from one sequence to many, whole and over lists, as one launch or two would take them."""
+    lens = [Lcap - (13 * b) % Lcap for b in range(B)]
+    c = make(B, Lcap, 6, 2, 64, 128, lens, seed=B, block=16)
+    check(run(c), c)
+    c["lists"] = pick(c, -(-Lcap // 32), seed=B)
+    check(run(c), c)
