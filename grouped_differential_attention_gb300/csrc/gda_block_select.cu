@@ -55,6 +55,7 @@ __device__ __forceinline__ size_t pool_block(const BlockSelectArgs &a, int b, in
 // 4 heads 22.7 / 23.7 / 27.8; one of 2048, 24 + 8 heads 28.8 / 31.9 / 35.0.
 constexpr int kChunk = 8;
 constexpr int kScoreWarps = 4;
+constexpr int kThreads = 512;          // of a block that selects
 
 // Bytes of four whole numbers.
 __device__ __forceinline__ uint32_t bytes_of(const int (&v)[4]) {
@@ -192,13 +193,12 @@ __device__ __forceinline__ uint3 bin_of(const uint32_t *hist, uint32_t k) {
 constexpr int kCountKeys = 256;        // at most the threads of a block
 
 // The indices of the `kept` < n highest of n keys in shared memory, of equal ones the lowest, ascending; a whole block.
-template <int THREADS>
-__device__ __forceinline__ void list_highest(const uint32_t *keys, int n, int kept, int *list, uint32_t (&hist)[THREADS / 32][256],
-                                             uint2 (&sums)[THREADS / 32]) {
-    constexpr int WARPS = THREADS / 32;
+__device__ __forceinline__ void list_highest(const uint32_t *keys, int n, int kept, int *list, uint32_t (&hist)[kThreads / 32][256],
+                                             uint2 (&sums)[kThreads / 32]) {
+    constexpr int WARPS = kThreads / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (n <= kCountKeys) {                                   // few: EACH lanes to a key count those ahead of it
-        constexpr int EACH = THREADS / kCountKeys;
+        constexpr int EACH = kThreads / kCountKeys;
         const int j = threadIdx.x / EACH;
         uint32_t lanes = 0;
         if (warp * (32 / EACH) < n) {
@@ -227,7 +227,7 @@ __device__ __forceinline__ void list_highest(const uint32_t *keys, int n, int ke
     for (int at = 24; at >= 0; at -= 8) {
         for (int i = lane; i < 256; i += 32) hist[warp][i] = 0;
         __syncthreads();
-        for (int j = threadIdx.x; j < n; j += THREADS) {
+        for (int j = threadIdx.x; j < n; j += kThreads) {
             const uint32_t k = keys[j];
             if (at == 24 || k >> (at + 8) == prefix >> (at + 8)) atomicAdd(&hist[warp][k >> at & 255u], 1u);
         }
@@ -248,7 +248,7 @@ __device__ __forceinline__ void list_highest(const uint32_t *keys, int n, int ke
         }
     }
     // all keys above it, and the first `need` equal to it, in order
-    const int per = (n + THREADS - 1) / THREADS, j0 = min(n, static_cast<int>(threadIdx.x) * per), j1 = min(n, j0 + per);
+    const int per = (n + kThreads - 1) / kThreads, j0 = min(n, static_cast<int>(threadIdx.x) * per), j1 = min(n, j0 + per);
     uint2 mine = make_uint2(0u, 0u);
     for (int j = j0; j < j1; ++j) mine.x += keys[j] > prefix, mine.y += keys[j] == prefix;
     uint2 incl = mine;
@@ -268,9 +268,8 @@ __device__ __forceinline__ void list_highest(const uint32_t *keys, int n, int ke
 }
 
 // grid (hn, B): keeps the blocks of one (sequence, noise head).
-template <int THREADS>
-__global__ void __launch_bounds__(THREADS) gda_block_select_kernel(const BlockSelectArgs a, int most) {
-    constexpr int WARPS = THREADS / 32;
+__global__ void __launch_bounds__(kThreads) gda_block_select_kernel(const BlockSelectArgs a, int most) {
+    constexpr int WARPS = kThreads / 32;
     extern __shared__ uint32_t keys[];
     __shared__ float best[128], inverse[128];                // of the heads: the largest x, 1 / the sum of w
     __shared__ float part_most[WARPS];
@@ -283,7 +282,7 @@ __global__ void __launch_bounds__(THREADS) gda_block_select_kernel(const BlockSe
     const int n = (length_of(a, b) + a.block - 1) / a.block, kept = min(n, a.keep), r = a.hs / a.hn;
     int *list = a.list + (static_cast<size_t>(b) * a.hn + g) * a.keep;
     if (g == 0 && threadIdx.x == 0) a.count[b] = kept;
-    for (int i = threadIdx.x + (n <= a.keep ? 0 : kept); i < a.keep; i += THREADS) list[i] = i < kept ? i : -1;
+    for (int i = threadIdx.x + (n <= a.keep ? 0 : kept); i < a.keep; i += kThreads) list[i] = i < kept ? i : -1;
     if (n <= a.keep) return;
     const float *x = a.scores + static_cast<size_t>(b) * (a.hs + a.hn) * most;
     auto row_of = [&](int i) { return x + static_cast<size_t>(i == r ? a.hs + g : g * r + i) * most; };
@@ -317,23 +316,22 @@ __global__ void __launch_bounds__(THREADS) gda_block_select_kernel(const BlockSe
         }
     }
     __syncthreads();
-    for (int j = threadIdx.x; j < n; j += THREADS) {
+    for (int j = threadIdx.x; j < n; j += kThreads) {
         float s = 0.f;
 #pragma unroll 4
         for (int i = 0; i <= r; ++i) s = fmaxf(s, __fmul_rn(weight(row_of(i)[j], best[i], a.unit), inverse[i]));
         keys[j] = key_of(a, s, j, n);
     }
     __syncthreads();
-    list_highest<THREADS>(keys, n, kept, list, hist, sums);
+    list_highest(keys, n, kept, list, hist, sums);
 }
 
-template <int THREADS>
 cudaError_t launch_select(const BlockSelectArgs &a, int most, cudaStream_t stream) {
-    const cudaError_t e = allow_shared_memory<gda_block_select_kernel<THREADS>>(kBlockSelectMaxBlocks * 4);
+    const cudaError_t e = allow_shared_memory<gda_block_select_kernel>(kBlockSelectMaxBlocks * 4);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(a.hn, a.B);
-    cfg.blockDim = dim3(THREADS);
+    cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = most * 4;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -341,7 +339,7 @@ cudaError_t launch_select(const BlockSelectArgs &a, int most, cudaStream_t strea
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, gda_block_select_kernel<THREADS>, a, most);
+    return cudaLaunchKernelEx(&cfg, gda_block_select_kernel, a, most);
 }
 
 // ---- one launch ----
@@ -352,7 +350,6 @@ cudaError_t launch_select(const BlockSelectArgs &a, int most, cudaStream_t strea
 // empty launch, 4 the bounds and 2 the ranking; one of 2048, 24 + 8 heads, 9 MB 16.6 (20.7), 4 the bounds and 4 the
 // search.  It is bound by its chain of short phases, not by the bytes (1.9 and 1.3 us).  256 / 512 threads: 11.9 / 12.5
 // and 16.6 / 16.6, but 17.6 / 16.5 and 23.7 / 20.6 with the bounds in HBM.
-constexpr int kThreads = 512;
 constexpr int kMaxCluster = 8;
 constexpr int kSharedLimit = 200 * 1024;
 
@@ -500,7 +497,7 @@ __global__ void __launch_bounds__(kThreads) gda_block_select_fused_kernel(const 
     }
     if (ranks > 1) cluster_barrier();
     else __syncthreads();
-    if (rank == 0) list_highest<kThreads>(keys, n, kept, list, hist, sums);
+    if (rank == 0) list_highest(keys, n, kept, list, hist, sums);
 }
 
 // Thread blocks of a cluster: as many as it takes to keep the SMs busy, not fewer than 128 blocks of tokens each, and not
@@ -552,8 +549,7 @@ int launch_block_select(const BlockSelectArgs &a, cudaStream_t stream) {
     else gda_block_score_kernel<128><<<grid, kScoreWarps * 32, 0, stream>>>(a, most);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return record_cuda_error(e);
-    // 2048 blocks, us of both kernels, cold: 31.9 with 1024 threads, 27.8 with 512 or 256
-    e = most > 512 ? launch_select<512>(a, most, stream) : launch_select<256>(a, most, stream);
+    e = launch_select(a, most, stream);
     return e == cudaSuccess ? GDA_OK : record_cuda_error(e);
 }
 

@@ -133,3 +133,49 @@ def test_lengths_up_to_the_room(B, Lcap):
     check(run(c), c)
     c["lists"] = pick(c, -(-Lcap // 32), seed=B)
     check(run(c), c)
+
+
+def with_room(c, listed=False):
+    """The same call over a block table (or lists) with room for many more."""
+    table = torch.cat((c["table"], torch.zeros(c["table"].shape[0], 3000, dtype=torch.int32, device="cuda")), 1).contiguous()
+    if not listed:
+        return c | {"table": table}
+    ids, counts = c["lists"]
+    return c | {"table": table, "lists": (torch.cat((ids, torch.full((*ids.shape[:2], 9000), -1, dtype=torch.int32,
+                                                                     device="cuda")), 2).contiguous(), counts)}
+
+
+@pytest.mark.parametrize("listed", [False, True])
+def test_bad_rows_pages_and_workspaces_where_there_is_room(listed):
+    lens = [1, 0, 15, 17, 96, 130, 47]
+    c = make(len(lens), 160, 6, 2, 64, 128, lens, seed=5, page=32, block=16)
+    if listed:
+        c["lists"] = pick(c, 4, seed=5)
+    ws = torch.full((gda.gda_attn_decode_fp8_block_workspace_size(7, 6, 2, 64, 128),), 0xFF, dtype=torch.uint8, device="cuda")
+    want = run(with_room(c, listed), workspace=ws).clone()
+    check(want, c)
+    assert torch.equal(run(with_room(c, listed), workspace=ws), want) and torch.equal(run(with_room(c, listed)), want)
+    used = torch.zeros(c["pools"][0].shape[:2], dtype=torch.bool, device="cuda")
+    for b, n in enumerate(lens):
+        for j in range(n):
+            used[c["table"][b, j // 32].long(), j % 32] = True
+    clean = [t.clone() for t in (*c["pools"], *c["scales"])]
+    for p, s in zip(c["pools"], c["scales"]):
+        p[~used] = 0x7F
+        s[~used.view(used.shape[0], -1, 16).any(-1)] = float("nan")
+    assert torch.equal(run(with_room(c, listed)), want)
+    c["pools"], c["scales"] = clean[:3], clean[3:]
+    gda.gda_device_error(clear=True)
+    c["lens"][4] = -4
+    out = run(with_room(c, listed))
+    assert gda.gda_device_error(clear=True) == gda.GDA_DEVERR_BAD_LENGTH
+    c["lens"][4] = 0
+    check(out, c)
+    c["lens"][4], c["table"][5, 1], c["table"][4, 0] = 96, 10 ** 9, -1
+    if listed:                                               # the pages in question are among the chosen ones
+        c["lists"][0][4:6] = torch.tensor([0, 1, 2, 3], dtype=torch.int32, device="cuda")
+        c["lists"][1][4:6] = 4
+    out = run(with_room(c, listed))
+    assert gda.gda_device_error(clear=True) == gda.GDA_DEVERR_BAD_PAGE
+    pages = c["pools"][0].shape[0]
+    check(out, c | {"table": torch.where((c["table"] >= 0) & (c["table"] < pages), c["table"], 0)})
