@@ -179,3 +179,14 @@ def test_bad_rows_pages_and_workspaces_where_there_is_room(listed):
     assert gda.gda_device_error(clear=True) == gda.GDA_DEVERR_BAD_PAGE
     pages = c["pools"][0].shape[0]
     check(out, c | {"table": torch.where((c["table"] >= 0) & (c["table"] < pages), c["table"], 0)})
+
+
+@pytest.mark.parametrize("d,dv", [(64, 64), (64, 128), (64, 256), (128, 64), (128, 128), (128, 256)])
+@pytest.mark.parametrize("hs,hn", [(1, 1), (2, 1), (3, 1), (5, 1), (8, 4)])
+def test_one_sequence_of_each_shape(hs, hn, d, dv):
+    """The largest clusters, with the most shared memory."""
+    for n in (16 * 128, 1999):
+        c = make(1, 2048, hs, hn, d, dv, [n], seed=n, block=32)
+        check(run(c), c)
+        c["lists"] = pick(c, 40, seed=n)
+        check(run(c), c)
