@@ -238,15 +238,6 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap &map, u
                  "r"(head), "r"(bar) : "memory");
 }
 
-// Waits, for a second at most, until the barrier's phase of this parity has completed.
-__device__ __forceinline__ bool landed(uint32_t bar, uint32_t parity) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
-    while (!mbar_try_wait(bar, parity))
-        if (global_timer_ns() - t0 > kWaitTimeoutNs) return false;
-    return true;
-}
-
 // a * b + c: 16 x 16 (f16) times 16 x 8 (f16).
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1) {
@@ -622,10 +613,10 @@ __device__ __forceinline__ void run_range(const Params &p, const Maps &maps, con
             continue;
         }
         asm volatile("cp.async.wait_group %0;" ::"n"(A) : "memory");
-        if (!landed(ring + S::bars + from * 8, parity >> from & 1u)) {
+        if (!mbar_wait_warp(ring + S::bars + from * 8, parity >> from & 1u)) {
             // it gives up; the copies of the other stages are waited for, as long again
             atomicOr(p.err, GDA_DEVERR_DECODE_TIMEOUT);
-            for (int i = 0; i < S::count; ++i) landed(ring + S::bars + i * 8, parity >> i & 1u);
+            for (int i = 0; i < S::count; ++i) mbar_wait_warp(ring + S::bars + i * 8, parity >> i & 1u);
             return;
         }
         parity ^= 1u << from;

@@ -95,6 +95,21 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, unsign
     }
 }
 
+// Waits, for `limit` ns at most, until the barrier's phase of this parity has
+// completed; a whole warp.  Its lanes look at the clock each for itself, so
+// the outcome is voted on: some may run out of time right before the others
+// see the phase complete, and a warp that parts there would wait for itself
+// at its next barrier.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, uint64_t limit = kWaitTimeoutNs) {
+    bool ok = mbar_try_wait(bar, parity);
+    if (!ok) {
+        const uint64_t t0 = global_timer_ns();
+        do ok = mbar_try_wait(bar, parity);
+        while (!ok && global_timer_ns() - t0 <= limit);
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
 // -------------------------------------------------------------------- TMA --
 
 // 4-D tiled TMA load into shared memory; completion is signalled on `bar`
