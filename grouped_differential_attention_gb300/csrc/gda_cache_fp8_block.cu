@@ -16,7 +16,8 @@
 // Bounds of a block's keys, for gda_block_select, in fours of the scale:
 //   max over rows of ceil(code / 4), min of floor(code / 4), one int8 each for
 // every channel (|code| <= 448, so at most 112), -128 and 127 if there is none.
-// ceil(ceil(x / 4) / 2^k) = ceil(x / 4 / 2^k), so a growing scale keeps them exact.
+// ceil(ceil(x / 4) / 2^k) = ceil(x / 4 / 2^k), so a growing scale keeps them exact.  A scale of the caller's own need be no
+// power of two: codes brought from it are rounded up as well as down, and the bounds follow to where 4 bound would be.
 //
 // The rows of a block may be anywhere in the call.  The row with the lowest slot
 // of a block writes all of it; to find the others, a call of few rows looks
@@ -105,6 +106,26 @@ __device__ __forceinline__ void copy_async8(uint32_t dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copies_landed() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Eight channels' bounds of codes that are brought to a scale 1 / shift as large, where shift is no power of two: rounded
+// outwards, and at least as far as the code 4 bound would come, since codes are rounded to the nearest (their order stays).
+__device__ __forceinline__ void bring_bounds(uint2 &top, uint2 &low, float shift) {
+    uint2 nt = {}, nl = {};
+#pragma unroll 1
+    for (int at = 0; at < 32; at += 8) {
+        auto bring = [&](uint32_t word_t, uint32_t word_l, uint32_t &to_t, uint32_t &to_l) {
+            const float t = static_cast<float>(static_cast<int8_t>(word_t >> at)), l = static_cast<float>(static_cast<int8_t>(word_l >> at));
+            const uint32_t codes = float2_to_e4m3x2(__fmul_rn(4.f * t, shift), __fmul_rn(4.f * l, shift));
+            const float2 far = half2_bits_to_float2(e4m3x2_to_half2(codes));
+            to_t |= (static_cast<uint32_t>(static_cast<int>(fmaxf(ceilf(t * shift), ceilf(far.x * 0.25f)))) & 0xffu) << at;
+            to_l |= (static_cast<uint32_t>(static_cast<int>(fminf(floorf(l * shift), floorf(far.y * 0.25f)))) & 0xffu) << at;
+        };
+        bring(top.x, low.x, nt.x, nl.x);
+        bring(top.y, low.y, nt.y, nl.y);
+    }
+    top = nt, low = nl;
+}
+__device__ __forceinline__ bool power_of_two(float x) { return (__float_as_uint(x) & 0x7fffffu) == 0; }
 
 // One block of tokens, the heads of this thread block: `share` warps to a head, n / 8 lanes to a row.  A lane's pieces
 // go through shared memory, where no other thread reads them: that many loads are in flight without as many registers,
@@ -248,6 +269,9 @@ __device__ __forceinline__ void write_heads(const CacheFp8BlockArgs &a, int tens
                 }
     }
     if (!here || member != 0 || lane >= lanes) return;
+    const bool odd_shift = !fresh && !power_of_two(shift);
+    if (odd_shift) bring_bounds(old_top, old_low, shift);
+    const float by = odd_shift ? 1.f : shift;
     uint32_t nt[2] = {0u, 0u}, nl[2] = {0u, 0u};
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -259,8 +283,8 @@ __device__ __forceinline__ void write_heads(const CacheFp8BlockArgs &a, int tens
         if (!fresh) {
             const uint32_t ot = (k < 4 ? old_top.x : old_top.y) >> 8 * (k & 3);
             const uint32_t ol = (k < 4 ? old_low.x : old_low.y) >> 8 * (k & 3);
-            t = fmaxf(t, ceilf(static_cast<float>(static_cast<int8_t>(ot)) * shift));
-            l = fminf(l, floorf(static_cast<float>(static_cast<int8_t>(ol)) * shift));
+            t = fmaxf(t, ceilf(static_cast<float>(static_cast<int8_t>(ot)) * by));
+            l = fminf(l, floorf(static_cast<float>(static_cast<int8_t>(ol)) * by));
         }
         nt[k / 4] |= (static_cast<uint32_t>(static_cast<int>(t)) & 0xffu) << 8 * (k & 3);
         nl[k / 4] |= (static_cast<uint32_t>(static_cast<int>(l)) & 0xffu) << 8 * (k & 3);
@@ -303,6 +327,7 @@ __device__ __forceinline__ Piece fetch_piece(const CacheFp8BlockArgs &a, long lo
 
 // The greatest and the least of bounds, for 8 channels: those before, brought to the scale, and codes of one row.
 __device__ __forceinline__ void join_bounds(uint2 &top, uint2 &low, const uint32_t (&c)[4], float shift, bool fresh) {
+    if (!fresh && !power_of_two(shift)) bring_bounds(top, low, shift), shift = 1.f;
     uint32_t nt[2] = {0u, 0u}, nl[2] = {0u, 0u};
 #pragma unroll
     for (int k = 0; k < 8; ++k) {

@@ -561,11 +561,13 @@ size_t gda_attn_decode_fp4_workspace_size(int B, int h_s, int h_n, int d, int dv
  *   scale [slots / block, heads]        float32, of `block` consecutive slots
  * and stands for code * scale.  block: 16, 32, 64 or 128; page_size (Lcap) is
  * a multiple of it.  Any finite scales >= 0 may be read; those that are
- * written here are powers of two.
+ * made here are powers of two (a larger one of the caller's own, of any form,
+ * is kept).
  *   bounds [slots / block, heads, 2, d] int8, of K_sig and K_noise: the
  *     greatest of ceil(code / 4) and the least of floor(code / 4) over the
- *     rows written to the block, for every channel (-128 and 127: none; a
- *     growing scale rounds these outwards like the others).
+ *     rows written to the block, for every channel (-128 and 127: none).  A
+ *     growing scale brings them along, rounded outwards, so that they stay
+ *     bounds of the codes, whatever scale those were written at.
  *
  * gda_cache_append_fp8_block writes T tokens' rows (bf16, `*_stride` elements
  * between tokens, a multiple of 8) to the slots slot_map[T] (int32; negative:

@@ -194,7 +194,10 @@ def append_fp8_block(x, slots, codes, scale, bounds=None):
             if fresh:
                 top, low = np.full_like(top, -128), np.full_like(low, 127)
             else:
+                far = [round_e4m3((f32(4) * b.astype(f32) * shift).astype(f32)) / 4 for b in (top, low)]
                 top, low = np.ceil(top * shift), np.floor(low * shift)
+                if np.frexp(shift)[0] != 0.5:               # codes are rounded both ways: as far as 4 * bound goes
+                    top, low = np.maximum(top, np.ceil(far[0])), np.minimum(low, np.floor(far[1]))
             known = np.isfinite(y)
             top = np.maximum(top, np.where(known, np.ceil(y / 4), -128).max(0))
             low = np.minimum(low, np.where(known, np.floor(y / 4), 127).min(0))

@@ -1,0 +1,59 @@
+"""The 8-bit block cache at scales of any size and form."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import ref_serving as R
+from tests.test_gpu_cache_fp8_block import Cache
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from grouped_differential_attention_gb300 import build
+    build.build()
+
+
+# ---- bounds ----
+
+def with_bounds(scale, seed, block=32):
+    """Two blocks of codes, with scales of the caller's own and exactly their bounds."""
+    c = Cache(1, 2 * block, block, 3, 1, 64, 64, seed=seed)
+    for i in range(3):
+        c.ref[0][i] &= 0xF7                                           # no NaN codes (bit 3 of 0x7F and 0xFF)
+        c.ref[1][i][:] = scale
+        if i < 2:
+            v = R.e4m3_value(c.ref[0][i]).reshape(2, block, *c.ref[0][i].shape[1:]) / 4
+            c.ref[2][i][:] = np.stack((np.ceil(v.max(1)), np.floor(v.min(1))), 2)
+        for k in range(3):
+            if k < 2 or i < 2:
+                c.dev[k][i].copy_(torch.from_numpy(c.ref[k][i]).view(c.dev[k][i].shape))
+    return c
+
+
+def assert_bounds_hold(c):
+    for i in range(2):
+        code = R.e4m3_value(c.dev[0][i].cpu().numpy()[0])             # [slots, heads, n]
+        code = code.reshape(2, -1, *code.shape[1:])
+        top, low = (c.dev[2][i].cpu().numpy()[0, :, :, k].astype(np.float64) for k in range(2))
+        assert (code.max(1) <= 4 * top).all(), (i, float((code.max(1) - 4 * top).max()))
+        assert (code.min(1) >= 4 * low).all(), (i, float((4 * low - code.min(1)).max()))
+
+
+@pytest.mark.parametrize("alone", [True, False])
+@pytest.mark.parametrize("scale", [1.366, 0.75, 3.0, 1.9999999, 1.0, 0.3 * 2.0 ** -126])
+def test_bounds_stay_bounds_when_a_scale_of_the_callers_own_grows(scale, alone):
+    """Codes that are brought to a new scale are rounded to e4m3, upwards too, by up to half a step of 32."""
+    for seed in range(3):
+        c = with_bounds(scale, seed)
+        assert_bounds_hold(c)
+        g = torch.Generator().manual_seed(seed)
+        slots = torch.tensor([5, 40] if alone else [5, 40, 9, 3, 63, 33], dtype=torch.int32)
+        for times in (448 * 1.01, 448 * 1.3, 448 * 2.9, 448 * 64.0, 448 * 5e4):   # of the scale: it grows each time
+            rows = [(x.float().sign() * times * scale).bfloat16() for x in c.rows(slots.numel(), g)]
+            for x in rows:
+                x[:, :, ::2] *= 0.01
+            c.append(rows, slots)
+            assert_bounds_hold(c)
+            c.check()
