@@ -530,6 +530,14 @@ __global__ void __launch_bounds__(WARPS * 32) gda_cache_append_fp8_block_kernel(
     }
 }
 
+// c * s towards zero, the last digit set where digits are lost: rounded to bf16 after that, the product is rounded once.
+// (A code's 4 digits and a scale's 24 are more than float32 has; with scales that are powers of two nothing is lost.  8192
+// rows in a row of graph nodes 10.3 us without it, 10.4 with a branch around the loop, 10.6 with one inside.)
+__device__ __forceinline__ float product_to_odd(float c, float s) {
+    const float p = __fmul_rz(c, s), rest = __fmaf_ru(fabsf(c), s, -fabsf(p));
+    return rest > 0.f ? __uint_as_float(__float_as_uint(p) | 1u) : p;
+}
+
 // A thread's token and its 16 elements of the token's row: `tokens` tokens to a thread block (32-bit division).
 __global__ void __launch_bounds__(kThreads) gda_cache_read_fp8_block_kernel(const CacheFp8BlockArgs a, unsigned tokens) {
     const unsigned n0 = a.heads[0] * a.dims[0] / 16, n1 = a.heads[1] * a.dims[1] / 16, n2 = a.heads[2] * a.dims[2] / 16;
@@ -551,12 +559,22 @@ __global__ void __launch_bounds__(kThreads) gda_cache_read_fp8_block_kernel(cons
         const float s = a.scale[tensor][static_cast<size_t>(static_cast<unsigned>(slot) / static_cast<unsigned>(a.block)) *
                                         a.heads[tensor] + (in_row >> shift)];
         const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+        if (__builtin_expect(power_of_two(s), 1)) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint2 h = e4m3x4_to_half2x2(w[k]);
-            const float2 p = half2_bits_to_float2(h.x), q = half2_bits_to_float2(h.y);
-            o[2 * k] = pack_bf16x2(__fmul_rn(p.x, s), __fmul_rn(p.y, s));
-            o[2 * k + 1] = pack_bf16x2(__fmul_rn(q.x, s), __fmul_rn(q.y, s));
+            for (int k = 0; k < 4; ++k) {
+                const uint2 h = e4m3x4_to_half2x2(w[k]);
+                const float2 p = half2_bits_to_float2(h.x), q = half2_bits_to_float2(h.y);
+                o[2 * k] = pack_bf16x2(__fmul_rn(p.x, s), __fmul_rn(p.y, s));
+                o[2 * k + 1] = pack_bf16x2(__fmul_rn(q.x, s), __fmul_rn(q.y, s));
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint2 h = e4m3x4_to_half2x2(w[k]);
+                const float2 p = half2_bits_to_float2(h.x), q = half2_bits_to_float2(h.y);
+                o[2 * k] = pack_bf16x2(product_to_odd(p.x, s), product_to_odd(p.y, s));
+                o[2 * k + 1] = pack_bf16x2(product_to_odd(q.x, s), product_to_odd(q.y, s));
+            }
         }
     }
     uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(const_cast<void *>(a.rows[tensor])) +

@@ -593,9 +593,9 @@ size_t gda_attn_decode_fp4_workspace_size(int B, int h_s, int h_n, int d, int dv
  *   time need a workspace each.
  *
  * gda_cache_read_fp8_block is the reverse: rows of the slots as dense bf16
- * [T, heads, dim], rounded once (exact for scales that are powers of two; zero
- * rows for slots that append leaves out): the keys and values of a cached
- * prefix for gda_attn_fwd_chunk.
+ * [T, heads, dim], rounded once, to the nearest, ties to even (exact for scales
+ * that are powers of two from 2^-124 on; zero rows for slots that append leaves
+ * out): the keys and values of a cached prefix for gda_attn_fwd_chunk.
  *
  * Supported: d in {64, 128}; dv in {64, 128, 256}; h_s + h_n <= 128; fewer
  * than 2^31 slots.  Pointers 16-byte aligned, slot_map and scales 4-byte.

@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 import torch
 
+import grouped_differential_attention_gb300 as gda
 from oracle import ref_serving as R
 from tests.test_gpu_cache_fp8_block import Cache
 
@@ -57,3 +58,33 @@ def test_bounds_stay_bounds_when_a_scale_of_the_callers_own_grows(scale, alone):
             c.append(rows, slots)
             assert_bounds_hold(c)
             c.check()
+
+
+# ---- reading ----
+
+def bf16_once(x):
+    """float64 x to bf16, rounded once (torch goes through float32)."""
+    x = np.asarray(x, dtype=np.float64)
+    with np.errstate(all="ignore"):
+        e = np.floor(np.log2(np.maximum(np.abs(x), 2.0 ** -126)))
+        step = np.exp2(e - 7)
+        y = np.rint(x / step) * step
+    return torch.from_numpy(np.where(np.abs(y) >= 2.0 ** 128, np.copysign(np.inf, x), y)).float().bfloat16()
+
+
+@pytest.mark.parametrize("low,high", [(0.0, 1.0), (-126.0, -118.0), (-149.0, -126.0), (116.0, 127.99)])
+def test_rows_of_any_scale_are_rounded_once(low, high):
+    c = Cache(64, 32, 16, 4, 2, 64, 128, seed=11)
+    g = torch.Generator().manual_seed(int(high))
+    for s in c.dev[1]:
+        s.copy_(torch.exp2(low + (high - low) * torch.rand(s.shape, generator=g)))
+    c.dev[1][0][0, 0, 0], c.dev[1][0][0, 0, 1], c.dev[1][2][5, 1, 2] = 1.2881944, 0.0, 1.5
+    c.ref[1] = [s.flatten(0, 1).cpu().numpy() for s in c.dev[1]]
+    slots = torch.arange(64 * 32, dtype=torch.int32)
+    back = gda.gda_cache_read_fp8_block(slots.cuda(), *c.dev[0], *c.dev[1])
+    for i, y in enumerate(back):
+        want = bf16_once(c.value(i, slots.numpy()).numpy())
+        y = y.cpu()
+        assert torch.equal(torch.isnan(y), torch.isnan(want))
+        diff = torch.nan_to_num(y.float(), nan=7.0) != torch.nan_to_num(want.float(), nan=7.0)
+        assert not diff.any(), (i, int(diff.sum()))
