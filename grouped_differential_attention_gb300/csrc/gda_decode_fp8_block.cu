@@ -705,12 +705,17 @@ __device__ __forceinline__ void write_row(const Params &p, Joined<COLS> &sum, in
         return;
     }
     const float i1 = 1.f / sum.stats.y, i2 = p.lambda[h] / sum.stats.w;
-    float v[COLS], ss = 0.f;
+    float v[COLS], ss, early = 1.f, late = 1.f;
+    for (int round = 0;; ++round) {
+        const float e1 = i1 * early, e2 = i2 * early;
+        ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < COLS; ++i) v[i] = sum.o1[i] * i1 - sum.o2[i] * i2, ss = fmaf(v[i], v[i], ss);
+        for (int i = 0; i < COLS; ++i) v[i] = (sum.o1[i] * e1 - sum.o2[i] * e2) * late, ss = fmaf(v[i], v[i], ss);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float y = (1.f - p.lambda_init) * rsqrtf(ss * (1.f / DV) + p.eps);
+        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (round > 0 || norm_in_range(ss, p.eps, early, late)) break;
+    }
+    const float y = norm_factor(ss, DV, p.eps, p.lambda_init, early, late);
 #pragma unroll
     for (int i = 0; i < COLS; i += 2) out[i / 2] = pack_bf16x2(v[i] * y, v[i + 1] * y);
 }

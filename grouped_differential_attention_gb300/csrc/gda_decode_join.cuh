@@ -15,6 +15,23 @@ namespace {
 
 constexpr int kSms = 152;              // SMs that the plans of the split decodes count on
 
+// Whether a row's sum of squares is of use for its norm.  Those of elements from about 2^64 on are past float32, and those
+// below 2^-63 are lost, which tells where eps is as small.  The row is then taken once more, times early in the two maps'
+// sums and late in their difference, powers of two that the norm takes out again: its squares are then at most 2^124, and at
+// least 2^-118 for an element of 2^-149.
+__device__ __forceinline__ bool norm_in_range(float squares, float eps, float &early, float &late) {
+    if (squares <= 0x1p100f && (squares >= 0x1p-80f || eps >= 0x1p-60f)) return true;
+    if (squares < 1.f) late = 0x1p90f;
+    else early = 0x1p-70f;                 // (a NaN stays one)
+    return false;
+}
+
+// The factor of a row that was taken times early * late.
+__device__ __forceinline__ float norm_factor(float squares, int dv, float eps, float lambda_init, float early, float late) {
+    const float f = early * late;
+    return (1.f - lambda_init) * rsqrtf(squares * (1.f / dv) + eps * f * f);
+}
+
 // grid (h_s, B): joins the parts of one (sequence, head).  DV / 2 threads
 // hold the DV + DV columns of (O1, O2), four each, with the maximum and sum of
 // their map; THREADS / (DV / 2) such groups share the parts, each joining its
@@ -82,18 +99,24 @@ __global__ void __launch_bounds__(THREADS) gda_decode_join_kernel(const Params p
         return;
     }
     const float i1 = 1.f / L1, i2 = p.lambda[h] / L2;
-    const float v[4] = {a.x * i1 - d.x * i2, a.y * i1 - d.y * i2, a.z * i1 - d.z * i2, a.w * i1 - d.w * i2};
-    float ss = v[0] * v[0] + v[1] * v[1] + v[2] * v[2] + v[3] * v[3];
     constexpr unsigned mask = HALF >= 32 ? 0xffffffffu : 0xffffu;
+    float v[4], ss, early = 1.f, late = 1.f;
+    for (int round = 0;; ++round) {        // the same for all threads: they have the same sum
+        const float e1 = i1 * early, e2 = i2 * early;
+        v[0] = (a.x * e1 - d.x * e2) * late, v[1] = (a.y * e1 - d.y * e2) * late;
+        v[2] = (a.z * e1 - d.z * e2) * late, v[3] = (a.w * e1 - d.w * e2) * late;
+        ss = v[0] * v[0] + v[1] * v[1] + v[2] * v[2] + v[3] * v[3];
 #pragma unroll
-    for (int off = (HALF >= 32 ? 32 : HALF) / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(mask, ss, off);
-    if constexpr (HALF > 32) {             // DV = 256: two warps
-        __shared__ float both[2];
-        if (lane == 0) both[warp] = ss;
-        named_bar_sync(1, HALF);
-        ss = both[0] + both[1];
+        for (int off = (HALF >= 32 ? 32 : HALF) / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(mask, ss, off);
+        if constexpr (HALF > 32) {         // DV = 256: two warps
+            __shared__ float both[2][2];
+            if (lane == 0) both[round][warp] = ss;
+            named_bar_sync(1, HALF);
+            ss = both[round][0] + both[round][1];
+        }
+        if (round > 0 || norm_in_range(ss, p.eps, early, late)) break;
     }
-    const float y = (1.f - p.lambda_init) * rsqrtf(ss * (1.f / DV) + p.eps);
+    const float y = norm_factor(ss, DV, p.eps, p.lambda_init, early, late);
     reinterpret_cast<uint2 *>(out)[col] = make_uint2(pack_bf16x2(v[0] * y, v[1] * y), pack_bf16x2(v[2] * y, v[3] * y));
 }
 

@@ -6,6 +6,7 @@ import torch
 import grouped_differential_attention_gb300 as gda
 from oracle import ref_serving as R
 from tests.test_gpu_cache_fp8_block import Cache
+from tests.test_gpu_decode_fp8_block import check, make, run
 
 pytestmark = pytest.mark.gpu
 
@@ -88,3 +89,19 @@ def test_rows_of_any_scale_are_rounded_once(low, high):
         assert torch.equal(torch.isnan(y), torch.isnan(want))
         diff = torch.nan_to_num(y.float(), nan=7.0) != torch.nan_to_num(want.float(), nan=7.0)
         assert not diff.any(), (i, int(diff.sum()))
+
+
+# ---- values of any size ----
+
+@pytest.mark.parametrize("power", [100, 65, 64, 63, 50, -40, -75, -100, -118])
+@pytest.mark.parametrize("B,L,hs,hn,d,dv,page", [(3, 200, 6, 2, 64, 128, 48), (1, 20000, 3, 1, 64, 64, 0),
+                                                 (40, 2100, 4, 2, 128, 256, 0), (2, 300, 1, 1, 64, 256, 0)])
+def test_values_of_any_size(B, L, hs, hn, d, dv, page, power):
+    """V near both ends of float32: the norm's squares are past it."""
+    lens = [max(1, L - 37 * b) for b in range(B)]
+    c = make(B, L, hs, hn, d, dv, lens, seed=power + 200, page=page, powers=power % 2 == 0)
+    c["scales"][2] *= 2.0 ** power
+    for s in c["scales"][:2]:
+        s *= 0.25                                                     # flat maps: sums of many weights near one
+    eps = 1e-5 if power > 0 else 0.0
+    check(run(c, eps=eps), c, eps=eps)
