@@ -583,11 +583,14 @@ __device__ __forceinline__ void run_range(const Params &p, const Maps &maps, con
 #pragma unroll
         for (int j = 0; j < RH; ++j) {
             const float mj = __shfl_sync(0xffffffffu, m, j), lj = __shfl_sync(0xffffffffu, l, j);
-            const float v = __shfl_sync(0xffffffffu, v_most, j) * 0x1p-15f;
+            // sums over values from 2^64 on could leave float32: they and the sum of weights are left 2^64 smaller, and the
+            // maximum, in powers of two, as much larger, which is the same to whoever joins the parts
+            const float most = __shfl_sync(0xffffffffu, v_most, j);
+            const float up = most > 0x1p64f ? 64.f : 0.f, down = most > 0x1p64f ? 0x1p-64f : 1.f, v = most * down * 0x1p-15f;
             if (j < done) continue;
             const size_t place = slot * p.hs + h0 + j;
             float4 *const stats = ONE ? left_stats<DV, RH>(smem) + j : reinterpret_cast<float4 *>(p.ws_ml) + place;
-            if (lane == 0) *stats = make_float4(mj, lj, mn, ln);
+            if (lane == 0) *stats = make_float4(mj + up, lj * down, mn + up, ln * down);
             float *const o = (ONE ? left_sums<DV, RH>(smem) + j * 2 * DV : p.ws_o + place * 2 * DV) + (t & 1) * DV +
                              4 * WORDS * quad + 2 * (t >> 1);
 #pragma unroll

@@ -93,6 +93,12 @@ def test_rows_of_any_scale_are_rounded_once(low, high):
 
 # ---- values of any size ----
 
+def check_numbers(got, c, eps=1e-5):
+    """The bound of tests/test_gpu_decode_fp8_block.py, which NaN would pass."""
+    assert torch.isfinite(got).all()
+    check(got, c, eps)
+
+
 @pytest.mark.parametrize("power", [100, 65, 64, 63, 50, -40, -75, -100, -118])
 @pytest.mark.parametrize("B,L,hs,hn,d,dv,page", [(3, 200, 6, 2, 64, 128, 48), (1, 20000, 3, 1, 64, 64, 0),
                                                  (40, 2100, 4, 2, 128, 256, 0), (2, 300, 1, 1, 64, 256, 0)])
@@ -104,4 +110,27 @@ def test_values_of_any_size(B, L, hs, hn, d, dv, page, power):
     for s in c["scales"][:2]:
         s *= 0.25                                                     # flat maps: sums of many weights near one
     eps = 1e-5 if power > 0 else 0.0
-    check(run(c, eps=eps), c, eps=eps)
+    check_numbers(run(c, eps=eps), c, eps)
+
+
+@pytest.mark.parametrize("power", [110, 118, 125])
+@pytest.mark.parametrize("B,L,hs,hn,d,dv,page", [(3, 200, 6, 2, 64, 128, 48), (1, 20000, 3, 1, 64, 64, 0),
+                                                 (40, 2100, 4, 2, 128, 256, 0), (2, 300, 1, 1, 64, 256, 0)])
+def test_sums_of_large_values(B, L, hs, hn, d, dv, page, power):
+    """V up to the end of float32, whose sums over hundreds of equal weights are past it."""
+    lens = [max(1, L - 37 * b) for b in range(B)]
+    c = make(B, L, hs, hn, d, dv, lens, seed=power, page=page, powers=power % 2 == 0)
+    c["scales"][2] *= 2.0 ** power
+    c["pools"][2] &= 0x7F                                             # of one sign
+    for s in c["scales"][:2]:
+        s *= 0.25
+    check_numbers(run(c), c)
+
+
+def test_values_of_one_sequence_at_both_ends():
+    """Parts of a sequence whose sums are held by different powers of two are joined."""
+    c = make(1, 40000, 3, 1, 64, 128, [40000], seed=3, block=64)
+    c["scales"][2] *= 2.0 ** 60
+    c["scales"][2][:, ::7] *= 2.0 ** 12
+    c["scales"][2][:, 300:] *= 2.0 ** 3
+    check_numbers(run(c), c)
