@@ -27,10 +27,12 @@
 //   - values: A = codes of 16 dims x 16 positions, B = four columns of weights,
 //     the upper and the lower part of both maps', the other four zero, so that
 //     two tiles of dims share one set of accumulators.  A weight is two f16
-//     numbers, so that it keeps 22 bits down to 2^-18 of its map's largest and
-//     2^-40 of that below.  The block's scale of V is in the weights, relative
-//     to the largest such scale so far: a larger one shrinks the accumulators,
-//     as a larger score does.
+//     numbers, and the block's scale of V is in it, relative to a reference R of
+//     its map, so that it keeps 22 bits down to 2^-18 R and 2^-40 R below that.
+//     R is the largest such scale so far, but at most 2^12 times the largest
+//     product of a scale and a weight, so that a scale far above the others'
+//     whose keys have no weight does not take their digits; another R shrinks
+//     the accumulators, as a larger score does.
 // Step g of the loop copies K of tile g + A and V of the tile before that one,
 // adds the values of tile g - 1 and scores tile g, so that no more than a tile
 // is held while it is used.
@@ -66,6 +68,7 @@ constexpr int kTile = 16;              // positions of a tile
 constexpr float kWeightBits = 15.f;    // weights carry a factor 2^15: the largest is within f16, the smallest far from its end
 constexpr int kOneWarps = 8;           // at most, of a sequence in one launch
 constexpr float kLowest = -3.0e38f;    // a maximum over no position
+constexpr float kBand = 4096.f;        // a map's reference is at most that many times its largest product of scale and weight
 
 // Signal heads of a warp: a noise head's group in equal parts of at most three
 // (two at dv = 256).  Every part reads and scores the noise head for itself, and
@@ -438,11 +441,16 @@ __device__ __forceinline__ void run_range(const Params &p, const Maps &maps, con
     float factor = 0.f;
     float acc[RH][SLABS * WORDS][4];                     // [w]: of tiles 2 w + t / 2 and map t % 2, see values_of
     float m = kLowest, l = 0.f;                          // of head t (both its lanes' positions; l of this lane's only)
-    // of head t: the largest scale of V so far, and 1 over it.  From 2^-126 on, whose inverse is finite: smaller scales
-    // (or 0) are relative to that
+    // of head t's two maps: what the scales of V in the weights are relative to, and 1 over it.  From 2^-126 on, whose
+    // inverse is finite: smaller scales (or 0) are relative to that
     constexpr float kLeast = 0x1p-126f;
-    float v_most = kLeast, v_inverse = 1.f / kLeast;
-    float shrink = 1.f, v_shrink = 1.f;                  // of what was added before the last tile scored
+    float ref1 = 1.f, ref2 = 1.f, inverse1 = 1.f, inverse2 = 1.f;
+    auto multiply = [](float (&a)[SLABS * WORDS][4], float f) {
+#pragma unroll
+        for (int i = 0; i < SLABS * WORDS; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) a[i][k] *= f;
+    };
     auto clear = [&]() {
 #pragma unroll
         for (int j = 0; j < RH; ++j)
@@ -451,10 +459,21 @@ __device__ __forceinline__ void run_range(const Params &p, const Maps &maps, con
 #pragma unroll
                 for (int k = 0; k < 4; ++k) acc[j][i][k] = 0.f;
     };
+    // Where a tile's scale of V is above a map's reference or far below it: far above a tile the reference comes down as
+    // what was added before has shrunk, and it goes up to the scale, or as far as the tile's largest weight `top` is worth.
+    // (Where neither is looked at, R is at most kBand times the scale of a tile that raises the maximum.)  Powers of two
+    // stay such where scales are within kBand of one another.
+    auto refer = [](float &ref, float &inverse, float vs, float top, float by) {
+        const float before = ref, worth = __uint_as_float(__float_as_uint(vs * (top * kBand)) & 0x7f800000u);
+        ref = fmaxf(fmaxf(vs * kBand < ref ? ref * by : ref, top * kBand < 1.f ? worth : vs), kLeast);
+        inverse = __frcp_rn(ref);
+        return ref == before ? 1.f : fminf(before * inverse, 0x1p126f);   // (times `by` it is at most 1)
+    };
     int have = kTile;                                    // positions of the tile scored last
     auto scores_of = [&](const uint8_t *const stage, const uint8_t *const scales) {
         // lane (quad, t) ends up with positions quad, quad + 8 of head t
         float sc0 = 0.f, sc1 = 0.f;
+        const float ks = at<float>(scales + 4 * t), vs = at<float>(scales + 16 + 4 * t);
 #pragma unroll
         for (int j = 0; j < NH; ++j) {
             float c[4] = {0.f, 0.f, 0.f, 0.f};
@@ -476,27 +495,37 @@ __device__ __forceinline__ void run_range(const Params &p, const Maps &maps, con
             }
             if (t == j) sc0 = c[0], sc1 = c[2];
         }
-        const float ks = at<float>(scales + 4 * t), vs = at<float>(scales + 16 + 4 * t);
         have = counts[0];
         sc0 = sc0 * factor * ks, sc1 = sc1 * factor * ks;
         if (quad >= have) sc0 = -INFINITY;
         if (quad + 8 >= have) sc1 = -INFINITY;
-        float mt = max3f(m, sc0, sc1);
+        float tile = fmaxf(sc0, sc1);                    // the tile's largest score
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
-        shrink = fast_exp2(m - mt);
+        for (int o = 4; o < 32; o <<= 1) tile = fmaxf(tile, __shfl_xor_sync(0xffffffffu, tile, o));
+        const float mt = fmaxf(m, tile);
+        const float shrink = fast_exp2(m - mt);
         const float p0 = fast_exp2(sc0 - mt + kWeightBits), p1 = fast_exp2(sc1 - mt + kWeightBits);
         m = mt;
         l = fmaf(l, shrink, p0 + p1);
-        v_shrink = 1.f;
-        if (vs > v_most) {
-            v_shrink = __fdiv_rn(v_most, vs);
-            v_most = vs;
-            v_inverse = __frcp_rn(vs);
+        // what was added before shrinks by its scores, and by its references where this tile's scale of V is off them
+        const bool off = t < RH && (vs > fminf(ref1, ref2) || vs * kBand < fmaxf(ref1, ref2));
+        if (__any_sync(0xffffffffu, shrink != 1.f || off)) {
+#pragma unroll
+            for (int j = 0; j < RH; ++j) multiply(acc[j], __shfl_sync(0xffffffffu, shrink, t & 1 ? RH : j));
+            if (__any_sync(0xffffffffu, off)) {
+                const float top = fast_exp2(tile - mt);
+                const float shrink1 = refer(ref1, inverse1, vs, top, shrink);
+                const float shrink2 = refer(ref2, inverse2, vs, __shfl_sync(0xffffffffu, top, RH), __shfl_sync(0xffffffffu, shrink, RH));
+#pragma unroll
+                for (int j = 0; j < RH; ++j) {
+                    const float by1 = __shfl_sync(0xffffffffu, shrink1, j), by2 = __shfl_sync(0xffffffffu, shrink2, j);
+                    multiply(acc[j], t & 1 ? by2 : by1);
+                }
+            }
         }
-        const float ratio = vs * v_inverse;
-        const float n0 = __shfl_sync(0xffffffffu, p0, (lane & ~3) | RH) * ratio, n1 = __shfl_sync(0xffffffffu, p1, (lane & ~3) | RH) * ratio;
-        const float s0 = p0 * ratio, s1 = p1 * ratio;
+        const float ratio1 = vs * inverse1, ratio2 = vs * inverse2;
+        const float n0 = __shfl_sync(0xffffffffu, p0, (lane & ~3) | RH) * ratio2, n1 = __shfl_sync(0xffffffffu, p1, (lane & ~3) | RH) * ratio2;
+        const float s0 = p0 * ratio1, s1 = p1 * ratio1;
         const uint32_t sh = pack_half2(s0, s1), nh = pack_half2(n0, n1);
         const float2 sf = half2_bits_to_float2(sh), nf = half2_bits_to_float2(nh);
         if (t < RH)
@@ -560,18 +589,6 @@ __device__ __forceinline__ void run_range(const Params &p, const Maps &maps, con
         fence_proxy_async_smem();
         __syncwarp();
     };
-    auto rescale = [&]() {
-        if (__any_sync(0xffffffffu, shrink != 1.f || v_shrink != 1.f)) {
-#pragma unroll
-            for (int j = 0; j < RH; ++j) {
-                const float f = __shfl_sync(0xffffffffu, shrink, t & 1 ? RH : j) * __shfl_sync(0xffffffffu, v_shrink, j);
-#pragma unroll
-                for (int i = 0; i < SLABS * WORDS; ++i)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) acc[j][i][k] *= f;
-            }
-        }
-    };
     // Leaves what the part that lies in sequence b has come to.
     auto leave = [&](int b) {
         if constexpr (ONE) __syncwarp();                 // it goes to where the tiles were
@@ -585,12 +602,14 @@ __device__ __forceinline__ void run_range(const Params &p, const Maps &maps, con
             const float mj = __shfl_sync(0xffffffffu, m, j), lj = __shfl_sync(0xffffffffu, l, j);
             // sums over values from 2^64 on could leave float32: they and the sum of weights are left 2^64 smaller, and the
             // maximum, in powers of two, as much larger, which is the same to whoever joins the parts
-            const float most = __shfl_sync(0xffffffffu, v_most, j);
-            const float up = most > 0x1p64f ? 64.f : 0.f, down = most > 0x1p64f ? 0x1p-64f : 1.f, v = most * down * 0x1p-15f;
+            const float r1 = __shfl_sync(0xffffffffu, ref1, j), r2 = __shfl_sync(0xffffffffu, ref2, j);
+            const float down1 = r1 > 0x1p64f ? 0x1p-64f : 1.f, up1 = r1 > 0x1p64f ? 64.f : 0.f;
+            const float down2 = r2 > 0x1p64f ? 0x1p-64f : 1.f, up2 = r2 > 0x1p64f ? 64.f : 0.f;
+            const float v = (t & 1 ? r2 * down2 : r1 * down1) * 0x1p-15f;
             if (j < done) continue;
             const size_t place = slot * p.hs + h0 + j;
             float4 *const stats = ONE ? left_stats<DV, RH>(smem) + j : reinterpret_cast<float4 *>(p.ws_ml) + place;
-            if (lane == 0) *stats = make_float4(mj + up, lj * down, mn + up, ln * down);
+            if (lane == 0) *stats = make_float4(mj + up1, lj * down1, mn + up2, ln * down2);
             float *const o = (ONE ? left_sums<DV, RH>(smem) + j * 2 * DV : p.ws_o + place * 2 * DV) + (t & 1) * DV +
                              4 * WORDS * quad + 2 * (t >> 1);
 #pragma unroll
@@ -636,12 +655,13 @@ __device__ __forceinline__ void run_range(const Params &p, const Maps &maps, con
             if (over) return;
             factor = q.place(p, queries);
             clear();
-            m = kLowest, l = 0.f, v_most = kLeast, v_inverse = 1.f / kLeast;
+            m = kLowest, l = 0.f;
+            ref1 = ref2 = fmaxf(at<float>(scales + 16 + 4 * t), kLeast);   // its largest weights are 1
+            inverse1 = inverse2 = __frcp_rn(ref1);
             part_of = use.b;
         }
         __syncwarp();                                    // the weights have been read, the queries are there
         scores_of(stage, scales);
-        rescale();
         ending = ++use.tile >= use.hi;
         if (ending) {
             over = use.left == 0;

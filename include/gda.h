@@ -667,6 +667,9 @@ size_t gda_block_select_workspace_size(int B, int max_blocks, int h_s, int h_n);
  * and noise head only, both softmax maps normalised over those.
  *   Queries, lambda, out, cache_lens, their clamping and the errors of block
  *   tables as in gda_attn_decode_fp4: a length of 0 gives a zero row.
+ *   The V scales of a sequence may lie any distance apart: a weight times its
+ *   block's scale keeps 22 bits, and is within 2^-28 of its map's largest such
+ *   product where it is smaller than that.
  *   block_list [B, h_n, keep], block_count [B] (sparse), as gda_block_select
  *   gives them: the first block_count[b] entries of a list are attended;
  *   negative ones are passed over, positions from cache_lens[b] on do not

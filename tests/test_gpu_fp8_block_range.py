@@ -1,4 +1,6 @@
 """The 8-bit block cache at scales of any size and form."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -6,7 +8,7 @@ import torch
 import grouped_differential_attention_gb300 as gda
 from oracle import ref_serving as R
 from tests.test_gpu_cache_fp8_block import Cache
-from tests.test_gpu_decode_fp8_block import check, make, run
+from tests.test_gpu_decode_fp8_block import LAM0, check, make, run
 
 pytestmark = pytest.mark.gpu
 
@@ -134,3 +136,92 @@ def test_values_of_one_sequence_at_both_ends():
     c["scales"][2][:, ::7] *= 2.0 ** 12
     c["scales"][2][:, 300:] *= 2.0 ** 3
     check_numbers(run(c), c)
+
+
+# ---- scales far apart ----
+
+def far_apart(order, gap, apart, RH, seed=0, noise_too=True, B=2):
+    """Blocks of V scales 2^apart and 1 whose keys' scores lie `gap` powers of two below and at the top, in an order that
+    repeats; several of them to a warp (eight noise heads share the warps of the GPU, 240 tiles to a sequence)."""
+    block, hs, hn, d, dv = 16, 8 * RH, 8, 64, 128
+    order = order * (240 // len(order))
+    n = len(order) * block
+    c = make(B, n, hs, hn, d, dv, [n] * B, seed=seed, block=block)
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    for q, p, s in ((c["q1"], c["pools"][0], c["scales"][0]), (c["q2"], c["pools"][1], c["scales"][1])):
+        unit = q.float().abs().sum(-1) / d ** 0.5 / math.log(2)       # score of sign(q), in powers of two
+        code = (q.float().sign() * 8)[:, None] * (1 + 0.125 * torch.randint(0, 2, (B, n, 1, 1), generator=g, device="cuda"))
+        p.copy_(code.expand(p.shape).to(torch.float8_e4m3fn).view(torch.uint8))
+        for i, big in enumerate(order):
+            sign = -1.0 if big and (noise_too or q is c["q1"]) else 1.0
+            p.view(torch.float8_e4m3fn)[:, i * block:(i + 1) * block] = \
+                (sign * p.view(torch.float8_e4m3fn)[:, i * block:(i + 1) * block].float()).to(torch.float8_e4m3fn)
+        s.copy_((gap / 2 / (8 * unit))[:, None].expand(s.shape))
+    for i, big in enumerate(order):
+        c["scales"][2][:, i] = 2.0 ** apart if big else 1.0
+    return c
+
+
+def check_far_apart(got, c):
+    """Bound of tests/test_gpu_decode_fp8_block.py with the weights' steps taken of the largest product of a weight and a
+    V scale: they are 2^-39 (f16's smallest, where the largest is 2^15) of a number that is at most 2^12 times that."""
+    hs, d = c["q1"].shape[1:]
+    bl, r = c["block"], hs // c["q2"].shape[1]
+    assert torch.isfinite(got).all()
+    worst = 0.0
+    for b, n in enumerate(c["lens"].tolist()):
+        pos = torch.arange(n, device="cuda")
+
+        def value(i, h):
+            code = c["pools"][i][b, :n, h].view(torch.float8_e4m3fn).float().double()
+            return code, c["scales"][i][b].double()[pos // bl, h][:, None]
+
+        def softmax(i, q, h):
+            code, s = value(i, h)
+            k = code * s
+            return torch.softmax(k @ q.double() / d ** 0.5, 0), (k.abs() @ q.double().abs()).max() / d ** 0.5
+
+        for h in range(hs):
+            a2, s2 = softmax(1, c["q2"][b, h // r], h // r)
+            a1, s1 = softmax(0, c["q1"][b, h], h)
+            code, vs = value(2, h)
+            v, lam = code * vs, c["lam"][h].double()
+            o, off = (a1 - lam * a2) @ v, 0
+            for a, w, s in ((a1, 1.0, s1), (a2, lam.abs(), s2)):
+                off = off + w * (2.0 ** -18 * (1 + s / math.log(2)) * (a @ v.abs())
+                                 + n * 2.0 ** -27 * (a[:, None] * vs).max() * code.abs().max())
+            f = (1 - LAM0) / torch.sqrt((o * o).mean() + 1e-5)
+            ref = f * o
+            rms = torch.sqrt((off * off).mean())
+            bound = 2.0 ** -8 * ref.abs() + f * off + ref.abs() * rms / torch.sqrt((o * o).mean() + 1e-5)
+            worst = max(worst, float(((got[b, h].double() - ref).abs() / bound).max()))
+    assert worst <= 1.0, worst
+
+
+@pytest.mark.parametrize("RH", [1, 2, 3])
+@pytest.mark.parametrize("gap,apart", [(20, 18), (20, 24), (45, 40), (60, 40), (60, 58), (100, 90), (3, 30)])
+@pytest.mark.parametrize("order", [(1, 0), (0, 1), (0, 1, 0, 1, 1, 0), (1, 1, 1, 0, 0, 1)])
+def test_scales_far_apart_with_the_weight_on_the_small(order, gap, apart, RH):
+    c = far_apart(order, gap, apart, RH)
+    check_far_apart(run(c), c)
+
+
+@pytest.mark.parametrize("order", [(1, 0), (0, 1), (0, 1, 0, 1, 1, 0)])
+def test_scales_far_apart_in_one_map_only(order):
+    c = far_apart(order, 60, 40, 3, noise_too=False)
+    check_far_apart(run(c), c)
+
+
+@pytest.mark.parametrize("step,apart", [(0.9, 30), (1.6, 40), (2.5, 90)])
+def test_scales_far_apart_with_scores_that_rise_slowly(step, apart):
+    """Saw teeth of 40 tiles: the first four have the large V scale, and the scores rise by `step` powers of two a tile."""
+    tiles, block, hn, d, dv = 6400, 16, 8, 64, 64
+    n = tiles * block
+    c = make(1, n, hn, hn, d, dv, [n], seed=1, block=block)
+    tooth = torch.arange(tiles, device="cuda") % 40
+    for q, p, s in ((c["q1"], c["pools"][0], c["scales"][0]), (c["q2"], c["pools"][1], c["scales"][1])):
+        unit = 8 * q.float().abs().sum(-1) / d ** 0.5 / math.log(2)   # score of 8 sign(q), in powers of two
+        p.copy_((q.float().sign() * 8)[:, None].expand(p.shape).to(torch.float8_e4m3fn).view(torch.uint8))
+        s.copy_(step * tooth[None, :, None] / unit[:, None])
+    c["scales"][2].copy_(torch.where(tooth < 4, 2.0 ** apart, 1.0)[None, :, None].expand(c["scales"][2].shape))
+    check_far_apart(run(c), c)
