@@ -267,8 +267,7 @@ int decode_fp8_block(DecodeFp8BlockArgs &a, size_t workspace_bytes, gda_stream_t
     if (Lcap > 0x7ffffff0 || reach > 0x7ffffff0 || a.B * reach > 1LL << 34) return GDA_ERR_UNSUPPORTED;
     for (const void *p : ptrs)
         if (!aligned16(p)) return GDA_ERR_MISALIGNED;
-    if (!aligned16(a.lens) || !aligned16(a.lambda)) return GDA_ERR_MISALIGNED;
-    if (!aligned4({a.k1s, a.k2s, a.vs, a.block_table, a.list, a.count})) return GDA_ERR_MISALIGNED;
+    if (!aligned4({a.k1s, a.k2s, a.vs, a.lens, a.lambda, a.block_table, a.list, a.count})) return GDA_ERR_MISALIGNED;
     if (!a.workspace || !aligned16(a.workspace) ||
         workspace_bytes < decode_fp8_block_workspace_bytes(a.B, a.hs, a.hn, a.d, a.dv))
         return GDA_ERR_WORKSPACE;

@@ -667,6 +667,8 @@ size_t gda_block_select_workspace_size(int B, int max_blocks, int h_s, int h_n);
  * and noise head only, both softmax maps normalised over those.
  *   Queries, lambda, out, cache_lens, their clamping and the errors of block
  *   tables as in gda_attn_decode_fp4: a length of 0 gives a zero row.
+ *   Queries, caches and out 16-byte aligned, the rest (scales, lambda, lengths,
+ *   tables, lists) 4-byte: slices of longer tensors, as gda_block_select takes.
  *   The V scales of a sequence may lie any distance apart: a weight times its
  *   block's scale keeps 22 bits, and is within 2^-28 of its map's largest such
  *   product where it is smaller than that.

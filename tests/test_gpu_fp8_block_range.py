@@ -225,3 +225,30 @@ def test_scales_far_apart_with_scores_that_rise_slowly(step, apart):
         s.copy_(step * tooth[None, :, None] / unit[:, None])
     c["scales"][2].copy_(torch.where(tooth < 4, 2.0 ** apart, 1.0)[None, :, None].expand(c["scales"][2].shape))
     check_far_apart(run(c), c)
+
+
+# ---- slices ----
+
+@pytest.mark.parametrize("page", [0, 64])
+@pytest.mark.parametrize("at", [1, 2, 3])
+def test_lengths_and_lambda_from_longer_tensors(page, at):
+    """The lengths and scales that one call of a step takes, the others take: 4-byte aligned slices."""
+    c = make(3, 192, 6, 2, 64, 128, [192, 5, 130], seed=at, page=page, block=64)
+    want = run(c).clone()
+
+    def slice_of(t):
+        longer = torch.zeros(t.numel() + 8, dtype=t.dtype, device="cuda")
+        longer[at:at + t.numel()] = t.flatten()
+        return longer[at:at + t.numel()].view(t.shape)
+
+    bounds = [torch.randint(-112, 113, (*p.shape[:1], p.shape[1] // 64, p.shape[2], 2, 64), device="cuda").to(torch.int8)
+              for p in c["pools"][:2]]
+    choose = lambda c: gda.gda_block_select(c["q1"], c["q2"], *bounds, *c["scales"][:2], c["lens"], 64, 2, block_table=c["table"])
+    lists = choose(c)
+    some = run(c | {"lists": lists}).clone()
+    cut = c | {"lens": slice_of(c["lens"]), "lam": slice_of(c["lam"]), "scales": [slice_of(s) for s in c["scales"]],
+               "table": None if c["table"] is None else slice_of(c["table"])}
+    assert cut["lens"].data_ptr() % 16 == 4 * at
+    assert torch.equal(run(cut), want)
+    assert all(torch.equal(a, b) for a, b in zip(choose(cut), lists))
+    assert torch.equal(run(cut | {"lists": tuple(map(slice_of, lists))}), some)
