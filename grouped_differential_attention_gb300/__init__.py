@@ -23,7 +23,7 @@ positions of a serving step), and a 4-bit cache (``gda_cache_append_fp4``,
 An 8-bit cache with a scale for each block of tokens and head
 (``gda_cache_append_fp8_block``, ``gda_cache_read_fp8_block``), decodes over all
 of it (``gda_attn_decode_fp8_block``, ``gda_attn_decode_paged_fp8_block``), and
-over the blocks that a bound on their logits keeps (``gda_block_select``,
+over the blocks that an estimate of their logits keeps (``gda_block_select``,
 ``gda_attn_decode_sparse_fp8_block``).
 """
 from __future__ import annotations
@@ -1231,7 +1231,7 @@ def gda_block_select_workspace_size(B: int, max_blocks: int, h_s: int, h_n: int)
 
 def gda_block_select(q_sig, q_noise, k_sig_bounds, k_noise_bounds, k_sig_scale, k_noise_scale, cache_lens, block: int,
                      keep: int, *, block_table=None, first: int = 1, last: int = 1, out=None, workspace=None):
-    """The ``keep`` blocks of each sequence that its queries are to attend, by a bound on their logits.
+    """The ``keep`` blocks of each sequence that its queries are to attend, by an estimate of their largest logits.
 
     q_sig [B, h_s, d], q_noise [B, h_n, d] bf16 (as the decode takes them);
     bounds and key scales as ``gda_cache_append_fp8_block`` keeps them for

@@ -5,11 +5,13 @@
 // b whose keys lie between lo and hi in every channel has, whatever its keys,
 // a dot product of at most
 //   ub_h(b) = sum over channels of q8 * hi where q8 > 0, of q8 * lo where q8 < 0
-// (a whole number), and x_h(b) = ub * scale_h(b) * amax is that bound on the
-// logit up to one factor for all heads.  With t = (x_h(b) - max x_h) * 4 / (127
+// (a whole number), and x_h(b) = ub * scale_h(b) * amax that bound in the units of
+// a logit, up to one factor for all heads.  It bounds the products with q8: a
+// channel of q below amax / 254 is 0 there, and where a block's keys are large
+// in such channels its logits may be above it.  With t = (x_h(b) - max x_h) * 4 / (127
 // ln 2 sqrt d) and w = 2^floor(t) (1 + t - floor(t)), 2^t with straight lines
 // between the powers, block b has the share w / sum of w of head h if every
-// block is as good as its bound.  A block counts as much as for the head of the
+// block is as good as its x.  A block counts as much as for the head of the
 // group (the signal heads that share a noise head, and that) that wants it
 // most: the score is the largest share.  (The bounds themselves cannot be
 // compared between heads: one whose logits are flat would outweigh one that
@@ -51,9 +53,10 @@ __device__ __forceinline__ size_t pool_block(const BlockSelectArgs &a, int b, in
     return static_cast<size_t>(phys) * per + (j - pg * per);
 }
 
-// Blocks of tokens that a warp scores.  us of both kernels with 8 / 16 / 32, cold: 64 sequences of 64 to 128 blocks, 12 +
-// 4 heads 22.7 / 23.7 / 27.8; one of 2048, 24 + 8 heads 28.8 / 31.9 / 35.0.
-constexpr int kChunk = 8;
+// Blocks of tokens that a warp scores, in the two launches.  us of both with 8 / 16 / 32, in graphs: one sequence of 32768
+// blocks, 3 + 1 heads of 64 138.8 / 137.9 / 138.2, 24 + 8 heads 164 / 161 / 157; four, 12 + 4 heads 199 / 192 / 191; one of
+// 16384, 48 + 2 heads of 128 389 / 381 / 377.
+constexpr int kChunk = 16;
 constexpr int kScoreWarps = 4;
 constexpr int kThreads = 512;          // of a block that selects
 

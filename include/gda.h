@@ -616,12 +616,14 @@ int gda_cache_read_fp8_block(const int *slot_map, const void *k_sig_pool, const 
 size_t gda_cache_append_fp8_block_workspace_size(int T, int num_pages, int page_size);
 
 /*
- * The blocks that a decode step is to attend, chosen by a bound on their
- * logits, for gda_attn_decode_sparse_fp8_block.  For every head h, with
+ * The blocks that a decode step is to attend, chosen by an estimate of their
+ * largest logits, for gda_attn_decode_sparse_fp8_block.  For every head h, with
  * q8 = rint(q * (127 * (1 / amax))), amax = max |q| (float32, each operation
  * rounded):
  *   x_h(block) = (sum over channels of max(q8 * greatest, q8 * least)) * scale_h(block) * amax
- * from the block's bounds and key scale, a bound on its logits up to a factor;
+ * from the block's bounds and key scale: up to a factor, a bound on its logits
+ * with q8 in place of q (channels of q below amax / 254 are 0 there, so a block
+ * whose keys are large in those may have a logit above it);
  * with t = (x_h(block) - max over the sequence's blocks of x_h) * 4 / (127 ln 2
  * sqrt(d)) and w_h = 2^floor(t) (1 + t - floor(t)), about 2^t, the block's share
  * of head h is w_h / (sum of w_h over the blocks), and its score the largest
