@@ -40,8 +40,8 @@
 // Measured (both kernels; of the 6793 GB/s of a copy): 64 sequences of 4096 to
 // 8192, 12 + 4 heads of 64/128, 1007 MB: 157 us (95 %); one of 131072, 24 + 8
 // heads, 671 MB: 109 us (91 %); 16 of up to 8191, 16 + 4 heads of 128/256, 437
-// MB: 73 us (88 %); 16 listed blocks of 64 of each of the 64 sequences, 168 MB,
-// one launch: 33 us (77 %; in two launches 38).  About 10 us of two launches are
+// MB: 74 us (88 %); 16 listed blocks of 64 of each of the 64 sequences, 168 MB,
+// one launch: 33.6 us (74 %; in two launches 38).  About 10 us of two launches are
 // fixed: the chain of lengths, list, table and first tile (3), the joining (3),
 // and the launches.  Copies alone take 95 % of the time.  By cp.async, a lane's
 // 16 bytes each, the first two took 166 and 115 us: their issue was what the
@@ -810,11 +810,13 @@ __global__ void __launch_bounds__(32 * kOneWarps, 1) gda_decode_fp8_block_one_ke
 // Both are estimated in us, from the room in the block table or the lists, as the lengths are on the device (lists are
 // taken to be full, caches for three quarters): two launches cost kTwoFixed and kStep for each step of their equal
 // ranges; one costs kOneFixed, kWave for each further wave of blocks of threads, and for each step of a warp kOneStep, its
-// tile's latency, or what the bytes take if that is more.  2 us of kTwoFixed stand for the host's 4 to 5.  us of a call from Python (graph replay, inputs in HBM), one / two
-// launches, 12 + 4 heads of 64/128: one sequence of 256 23 (13.4) / 27 (14.5); 16 of 512 24 (17.5) / 29 (19.6), of 2048 23
-// (30) / 28 (32); 64 of 256 23 (20) / 27 (24), of 512 24 (28) / 27 (32), of 1 to 1024 28 (36) / 27 (34), of 2048 57 (75) /
-// 61 (81); 256 of 512 74 (87) / 67 (87); lists of 16 blocks of 64 for 64 sequences 32.6 (46) / 37.8 (54).  Sixteen clusters
-// of eight do not run at once: four sequences of 1024 took 21.6 with those and 17.5 with two launches.
+// tile's latency, or what the bytes take if that is more.  2 us of kTwoFixed stand for the host's 4 to 5.  us of a call from
+// Python (graph replay, inputs in HBM), one / two launches, 12 + 4 heads of 64/128: one sequence of 256 23 (13.4) / 27
+// (14.5); 16 of 512 24 (17.5) / 29 (19.6), of 2048 23 (30) / 28 (32); 64 of 256 23 (20) / 27 (24), of 512 24 (28) / 27 (32),
+// of 1 to 1024 28 (36) / 27 (34), where the estimates are equal, of 2048 57 (75) / 61 (81), where they are 55.5 and 50.7, so
+// that the slower two are taken; 256 of 512 74 (87) / 67 (87); lists of 16 blocks of 64 for 64 sequences 33.6 (46) / 37.8
+// (54).  Sixteen clusters of eight do not run at once: four sequences of 1024 took 21.6 with those and 17.5 with two
+// launches.
 constexpr double kTwoFixed = 12.3, kOneFixed = 7.5, kOneCluster = 1.0, kWave = 2.0, kStep = 1.9, kOneStep = 1.5;
 struct OneLaunch {
     int ranks = 0, warps = 0;
